@@ -206,7 +206,9 @@ def prepare(case, seed):
         elif op in ("norm", "norm_grad"):
             st["handle"] = moe.MoeBlockNorm(
                 case["T"], case["d"], dtype=TYPES[case["act"]],
-                residual_dtype=TYPES[case["res"]], alpha=case["alpha"], eps=EPS)
+                residual_dtype=TYPES[case["res"]], alpha=case["alpha"], eps=EPS,
+                gate={"none": moe.MOE_GATE_NONE, "channel": moe.MOE_GATE_CHANNEL,
+                      "token": moe.MOE_GATE_TOKEN}[case["gate"]])
         else:
             st["handle"] = moe.MoePlan(case["T"], case["d"], case["I"], case["E"], case["k"],
                                        precision=moe.MOE_PREC_NVFP4, flags=0)
