@@ -243,7 +243,7 @@ def _route(st):
         s = torch.where(on, 1.0 / (1.0 + torch.exp(-l)), zero)
         total = s.sum(1)
         p = torch.where(on, s / total[:, None], zero)
-        stat, z = total, torch.zeros(T, device=DEV)
+        stat, z = torch.log(total), torch.zeros(T, device=DEV)
         part = torch.where(taken, 1.0 / (1.0 + torch.exp(-c)), zero)
     else:
         top = torch.where(on, l.amax(1, keepdim=True), zero)
@@ -277,7 +277,7 @@ def _route_grad(st):
     E, k, scoring = case["E"], case["k"], case["scoring"]
     l = st["logits"].float()
     stat = st["row_stat"][:, None]
-    on = stat > (0.0 if scoring == "sigmoid" else -math.inf)
+    on = stat > -math.inf
     zero = torch.zeros((), device=DEV)
     nf = st["counts"][E].float().clamp(min=1.0)
     gp = st["d_losses"][0] * (E / k) * st["counts"][:E].float() / (nf * nf)
@@ -286,8 +286,9 @@ def _route_grad(st):
     ds = torch.where(taken, st["d_scores"], zero)
     if scoring == "sigmoid":
         s = torch.where(on, 1.0 / (1.0 + torch.exp(-l)), zero)
-        p = torch.where(on, s / stat, zero)
-        gs = torch.where(on, (gp - (gp * p).sum(1, keepdim=True)) / stat, zero)
+        total = torch.exp(stat)
+        p = torch.where(on, s / total, zero)
+        gs = torch.where(on, (gp - (gp * p).sum(1, keepdim=True)) / total, zero)
         part = torch.where(taken, 1.0 / (1.0 + torch.exp(-c)), zero)
         total = part.sum(1, keepdim=True)
         part = torch.where(total > 0, part / total, zero)
@@ -447,7 +448,7 @@ def _exact_probabilities(l, live, scoring):
     if scoring == "sigmoid":
         s = torch.sigmoid(l)
         total = s.sum(1)
-        p, stat = s / total[:, None], torch.where(live, total, 0.0)
+        p, stat = s / total[:, None], torch.where(live, total.log(), -math.inf)
     else:
         stat = torch.logsumexp(l, 1)
         p, stat = torch.softmax(l, 1), torch.where(live, stat, -math.inf)
