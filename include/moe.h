@@ -550,6 +550,155 @@ size_t moe_gemm_scratch_bytes(int M, int K);
 int moe_gemm_bf16(int mode, const void* A, const void* B, void* C, int M, int N, int K,
                   void* scratch, void* stream);
 
+/* ---- element types of the entry points that take one ------------------------ */
+#define MOE_DTYPE_BF16  0
+#define MOE_DTYPE_FP32  1
+
+/*
+ * Router: top-k expert ids and scores from logits, per-expert counts, the balance
+ * and z losses, and their gradient.  It makes the ids and scores that moe_forward
+ * takes, and takes the dscores that moe_backward makes.
+ *   E experts (1..256), k of them per token (1..E)
+ *   dtype    MOE_DTYPE_* of the logits and of their gradient
+ *   scoring  how the scores follow from the logits l of the chosen experts:
+ *     MOE_ROUTER_SOFTMAX_TOPK  softmax over the chosen
+ *     MOE_ROUTER_SOFTMAX       their share of the softmax over all experts
+ *     MOE_ROUTER_SIGMOID       sigmoid(l), divided by the chosen experts' sum
+ *   scale    factor on the scores (finite)
+ */
+#define MOE_ROUTER_SOFTMAX_TOPK 0
+#define MOE_ROUTER_SOFTMAX      1
+#define MOE_ROUTER_SIGMOID      2
+typedef struct moe_router_desc {
+  int E, k;
+  int dtype;
+  int scoring;
+  float scale;
+} moe_router_desc;
+
+/*
+ * Bytes of device workspace for T tokens (0 for an invalid description).  It is
+ * scratch: its contents mean nothing before or after a call.  Calls that may
+ * overlap on the GPU need one each.
+ */
+size_t moe_router_workspace_bytes(const moe_router_desc* desc, int T);
+
+/*
+ * Router forward.  Inputs (device):
+ *   logits      [T, E] of dtype, rows ld elements apart (ld >= E)
+ *   bias        [E] fp32 or NULL: added to the logits (in fp32) for the choice
+ *               only; scores and probabilities do not see it
+ *   token_mask  [T] uint8 or NULL: 0 marks a padding token, whose logits are not
+ *               read; it gets the ids (t*k + j) % E and scores 0
+ * Outputs (device, overwritten):
+ *   ids       [T, k] int32: the k largest of l + bias, largest first, ties to the
+ *             lowest index; a NaN ranks below every number
+ *   scores    [T, k] fp32
+ *   counts    [E+1] int32: how often each expert was chosen, and in counts[E] the
+ *             number of live tokens
+ *   prob_sum  [E] fp32: sum over live tokens of p, the softmax over all experts
+ *             (MOE_ROUTER_SIGMOID: sigmoid(l) divided by its sum over all experts)
+ *   losses    [2] fp32: balance = E / (k N^2) * sum_e counts[e] * prob_sum[e] (N =
+ *             counts[E]; 1 when perfectly balanced) and z = mean of
+ *             logsumexp(l)^2 (0 for MOE_ROUTER_SIGMOID)
+ *   row_stat  [T] fp32: logsumexp(l), or for MOE_ROUTER_SIGMOID the logarithm of
+ *             the sum of the sigmoids; what moe_router_backward needs of the forward
+ * A token is live when it is not padding and some logit is above -inf.  A logit of
+ * -inf switches its expert off: it is chosen only when nothing else is left, with
+ * score 0 and without being counted.  A row of -inf only has scores 0 and row_stat
+ * -inf, as padding has.  NaN and +inf logits give NaN
+ * where the formulas do.  Sums run in a fixed order, so results repeat bit for bit.
+ * T >= 0, T*k < 2^31; T = 0 writes counts, prob_sum and losses as zeros.
+ */
+int moe_router_forward(const moe_router_desc* desc, int T, const void* logits, long long ld,
+                       const float* bias, const uint8_t* token_mask, int32_t* ids,
+                       float* scores, int32_t* counts, float* prob_sum, float* losses,
+                       float* row_stat, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Router backward: the gradient of
+ *   sum d_scores * scores + d_losses[0] * balance + d_losses[1] * z
+ * with respect to the logits (the choice and the counts are constants).  logits,
+ * ids, counts and row_stat are the forward's; d_scores [T, k] fp32 (dscores of
+ * moe_backward) and d_losses [2] fp32 (device) may each be NULL for zeros.
+ *   d_logits  [T, E] of dtype, rows ld_d elements apart, overwritten; rows of
+ *             tokens that are not live become 0.  May be logits itself (same ld).
+ */
+int moe_router_backward(const moe_router_desc* desc, int T, const void* logits, long long ld,
+                        const int32_t* ids, const int32_t* counts, const float* row_stat,
+                        const float* d_scores, const float* d_losses, void* d_logits,
+                        long long ld_d, void* stream);
+
+/*
+ * The norms around a block with its gate and residual scale.  On rows of d
+ * elements, with rms(v) = sqrt(mean(v^2) + eps):
+ *   n   = y / rms(y) * w_post             (n = y where w_post is NULL)
+ *   out = residual + alpha * gate * n
+ *   u   = out / rms(out) * w_pre
+ * y is the block's output (as y of moe_forward), out the residual stream after it
+ * and u the next block's input.  y = NULL leaves the first two lines out (u is the
+ * norm of residual); u = w_pre = NULL leaves the last one out.
+ *   d               row width, 1..16384
+ *   dtype           MOE_DTYPE_* of y, u and their gradients
+ *   residual_dtype  of the residual stream and its gradients (MOE_DTYPE_FP32 if
+ *                   dtype is)
+ *   param_dtype     of w_post, w_pre and gate (their gradients are fp32)
+ *   gate            MOE_GATE_NONE, MOE_GATE_CHANNEL (gate [d]) or MOE_GATE_TOKEN
+ *                   (gate [T])
+ *   alpha           the residual scale
+ * Arithmetic is fp32, rounded once on the way out; u follows from the unrounded
+ * out.  Every [T, d] tensor comes with the distance of its rows in elements
+ * (ld >= d) and needs no alignment beyond its elements' (16-byte aligned rows of a
+ * width that 8 divides run faster).
+ */
+#define MOE_GATE_NONE    0
+#define MOE_GATE_CHANNEL 1
+#define MOE_GATE_TOKEN   2
+typedef struct moe_block_norm_desc {
+  int d;
+  int dtype, residual_dtype, param_dtype;
+  int gate;
+  float alpha, eps;
+} moe_block_norm_desc;
+
+/* Bytes of scratch moe_block_norm_backward needs for T rows (0 if desc is invalid). */
+size_t moe_block_norm_workspace_bytes(const moe_block_norm_desc* desc, int T);
+
+/*
+ * Forward.  residual_out (needed with y) may be residual itself and u may be y
+ * itself (same ld).  gate is given exactly when desc->gate is not MOE_GATE_NONE
+ * and y is given; w_pre exactly when u is.  T >= 0.
+ */
+int moe_block_norm_forward(const moe_block_norm_desc* desc, int T, const void* residual,
+                           long long ld_residual, const void* y, long long ld_y,
+                           const void* w_post, const void* gate, const void* w_pre,
+                           void* residual_out, long long ld_out, void* u, long long ld_u,
+                           void* stream);
+
+/*
+ * Backward.  residual_out is the stream after the block (for y = NULL: the
+ * residual that was normed), y, w_post, gate, w_pre as in the forward; the row
+ * statistics are computed again, nothing is kept from the forward.
+ *   d_residual_out  [T, d] gradient at residual_out from what reads it later, or
+ *                   NULL for zeros
+ *   d_u             [T, d] gradient at u, or NULL with w_pre = NULL
+ * Outputs:
+ *   d_residual  [T, d] gradient at residual, overwritten (may be d_residual_out)
+ *   dy          [T, d] gradient at y, overwritten (may be d_u), or NULL
+ *   dw_post [d], dw_pre [d], dgate [d] or [T]: fp32, overwritten, or added to with
+ *               accumulate = 1; each may be NULL
+ * Sums over rows run in a fixed order.  workspace: 16-byte aligned, at least
+ * moe_block_norm_workspace_bytes(desc, T); calls that may overlap need one each.
+ */
+int moe_block_norm_backward(const moe_block_norm_desc* desc, int T, const void* residual_out,
+                            long long ld_out, const void* y, long long ld_y,
+                            const void* d_residual_out, long long ld_dout, const void* d_u,
+                            long long ld_du, const void* w_post, const void* gate,
+                            const void* w_pre, void* d_residual, long long ld_dres, void* dy,
+                            long long ld_dy, float* dw_post, float* dgate, float* dw_pre,
+                            int accumulate, void* workspace, size_t workspace_bytes,
+                            void* stream);
+
 #ifdef __cplusplus
 }
 #endif

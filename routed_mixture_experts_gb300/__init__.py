@@ -11,6 +11,8 @@ built library and a CUDA device and raises otherwise.
 
 from .binding import (  # noqa: F401
     MOE_BUF,
+    MOE_DTYPE_BF16,
+    MOE_DTYPE_FP32,
     MOE_ERR_BAD_IDS,
     MOE_ERR_CUDA,
     MOE_ERR_INVALID_ARG,
@@ -18,14 +20,24 @@ from .binding import (  # noqa: F401
     MOE_ERR_TIMEOUT,
     MOE_ERR_UNSUPPORTED,
     MOE_ERR_WORKSPACE,
+    MOE_GATE_CHANNEL,
+    MOE_GATE_NONE,
+    MOE_GATE_TOKEN,
     MOE_OK,
     MOE_PREC_BF16,
     MOE_PREC_MXFP8,
     MOE_PREC_NVFP4,
+    MOE_ROUTER_SIGMOID,
+    MOE_ROUTER_SOFTMAX,
+    MOE_ROUTER_SOFTMAX_TOPK,
     MOE_WS_HOST_STAGING,
     MOE_WS_TRAINING,
+    BlockNormGrads,
+    MoeBlockNorm,
     MoeError,
     MoePlan,
+    MoeRouter,
+    RouterResult,
     amax_bf16,
     gemm_bf16,
     lib,

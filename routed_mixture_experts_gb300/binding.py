@@ -1,5 +1,6 @@
 """ctypes binding of include/moe.h (argument marshalling only)."""
 
+import collections
 import ctypes
 import os
 import threading
@@ -24,8 +25,30 @@ MOE_BUF = dict(m_indptr=0, off_pad=1, row_of=2, token_of=3, score_of=4, xe=5, a=
                dye=9, dA=10, hs=11, dxe=12, xq=13, xsf=14, hq=15, hsf=16, xqT=17, xqTsf=18,
                dAq=19, dAsf=20, dAqT=21, dAqTsf=22, hsqT=23, hsqTsf=24)
 
+MOE_DTYPE_BF16 = 0
+MOE_DTYPE_FP32 = 1
+MOE_ROUTER_SOFTMAX_TOPK = 0
+MOE_ROUTER_SOFTMAX = 1
+MOE_ROUTER_SIGMOID = 2
+MOE_GATE_NONE = 0
+MOE_GATE_CHANNEL = 1
+MOE_GATE_TOKEN = 2
+
 _lock = threading.Lock()
 _lib = None
+
+
+class RouterDesc(ctypes.Structure):
+    """moe_router_desc"""
+    _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("scoring", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class BlockNormDesc(ctypes.Structure):
+    """moe_block_norm_desc"""
+    _fields_ = [("d", ctypes.c_int), ("dtype", ctypes.c_int), ("residual_dtype", ctypes.c_int),
+                ("param_dtype", ctypes.c_int), ("gate", ctypes.c_int), ("alpha", ctypes.c_float),
+                ("eps", ctypes.c_float)]
 
 
 class MoeError(RuntimeError):
@@ -80,6 +103,19 @@ def _declare(L):
     L.moe_plan_num_sms.restype = i32
     L.moe_plan_launch_count.argtypes = [vp]
     L.moe_plan_launch_count.restype = ctypes.c_longlong
+    i64x = ctypes.c_longlong
+    L.moe_router_workspace_bytes.argtypes = [vp, i32]
+    L.moe_router_workspace_bytes.restype = sz
+    L.moe_router_forward.argtypes = [vp, i32, vp, i64x] + [vp] * 9 + [sz, vp]
+    L.moe_router_backward.argtypes = [vp, i32, vp, i64x] + [vp] * 6 + [i64x, vp]
+    L.moe_block_norm_workspace_bytes.argtypes = [vp, i32]
+    L.moe_block_norm_workspace_bytes.restype = sz
+    L.moe_block_norm_forward.argtypes = [vp, i32] + [vp, i64x] * 2 + [vp] * 3 + [vp, i64x] * 2 + [vp]
+    L.moe_block_norm_backward.argtypes = ([vp, i32] + [vp, i64x] * 4 + [vp] * 3 + [vp, i64x] * 2 +
+                                          [vp] * 3 + [i32, vp, sz, vp])
+    for name in ("moe_router_forward", "moe_router_backward", "moe_block_norm_forward",
+                 "moe_block_norm_backward"):
+        getattr(L, name).restype = i32
     for name in ("moe_plan_set_swiglu_clamp", "moe_plan_set_workspace", "moe_forward",
                  "moe_forward_routed",
                  "moe_backward", "moe_step_host", "moe_quantize_mxfp8", "moe_plan_check",
@@ -373,3 +409,232 @@ def gemm_bf16(mode, A, B, C, M, N, K, stream=None):
     _check(L.moe_gemm_bf16(mode, _p(A), _p(B), _p(C), M, N, K, _p(scratch), _stream(stream)),
            "gemm_bf16")
     return C
+
+
+# ---- the operators around the experts -----------------------------------------
+
+
+def _raw_stream(stream):
+    import torch
+
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+def _dtype_code(dtype, what):
+    import torch
+
+    if dtype == torch.bfloat16:
+        return MOE_DTYPE_BF16
+    if dtype == torch.float32:
+        return MOE_DTYPE_FP32
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: dtype %s (bfloat16 or float32)" % (what, dtype))
+
+
+def _want(t, what, dtype, shape):
+    """t: a contiguous CUDA tensor of this dtype and shape (its address)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: want contiguous %s %s on the GPU, got %s %s" % (
+            what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    return t.data_ptr()
+
+
+def _maybe(t, what, dtype, shape):
+    return None if t is None else _want(t, what, dtype, shape)
+
+
+def _rows(t, what, dtype, shape):
+    """t: a CUDA [T, n] tensor whose rows may lie further apart (address, row distance)."""
+    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %s %s on the GPU, got %s %s" % (
+            what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    T, n = shape
+    apart, inner = t.stride()
+    if T <= 1:
+        apart = n
+    if (inner != 1 and n > 1) or apart < n:
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: rows have to be dense and apart, got strides %s" % (
+            what, t.stride()))
+    return t.data_ptr(), apart
+
+
+RouterResult = collections.namedtuple(
+    "RouterResult", "ids scores counts prob_sum losses row_stat")
+
+
+class MoeRouter:
+    """Top-k routing with the balance and z losses (moe_router_* in moe.h).
+
+    max_tokens sizes the scratch; a call takes any T up to it.  One MoeRouter per
+    concurrent stream."""
+
+    def __init__(self, max_tokens, E, k, scoring=MOE_ROUTER_SOFTMAX_TOPK, scale=1.0, dtype=None,
+                 device="cuda"):
+        import torch
+
+        L = lib()
+        self.max_tokens, self.E, self.k = max_tokens, E, k
+        self.dtype = dtype if dtype is not None else torch.float32
+        self.desc = RouterDesc(E, k, _dtype_code(self.dtype, "MoeRouter"), scoring, scale)
+        self._desc = ctypes.addressof(self.desc)
+        nbytes = L.moe_router_workspace_bytes(self._desc, max_tokens)
+        if not nbytes:
+            raise MoeError(MOE_ERR_INVALID_ARG, "MoeRouter(%d,%d,%d)" % (max_tokens, E, k))
+        self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
+        self._ws = (self.workspace.data_ptr(), nbytes)
+
+    def outputs(self, T):
+        """Fresh output tensors of a forward over T tokens."""
+        import torch
+
+        dev = self.workspace.device
+        f = torch.empty(2 + self.E + T * (self.k + 1), dtype=torch.float32, device=dev)
+        i = torch.empty(self.E + 1 + T * self.k, dtype=torch.int32, device=dev)
+        E, k = self.E, self.k
+        losses, prob_sum, row_stat, scores = f.split([2, E, T, T * k])
+        counts, ids = i.split([E + 1, T * k])
+        return RouterResult(ids.view(T, k), scores.view(T, k), counts, prob_sum, losses, row_stat)
+
+    def forward(self, logits, bias=None, token_mask=None, out=None, stream=None):
+        """logits [T, E] -> RouterResult(ids, scores, counts, prob_sum, losses, row_stat);
+        `out`: an earlier result (or outputs(T)) to overwrite."""
+        import torch
+
+        T, E, k = logits.shape[0], self.E, self.k
+        if T > self.max_tokens:
+            raise MoeError(MOE_ERR_INVALID_ARG, "router: %d tokens, made for %d" % (
+                T, self.max_tokens))
+        lp, ld = _rows(logits, "logits", self.dtype, (T, E))
+        bp = _maybe(bias, "bias", torch.float32, (E,))
+        mp = _maybe(token_mask, "token_mask", torch.uint8, (T,))
+        if out is None:
+            out = self.outputs(T)
+        f32, i32 = torch.float32, torch.int32
+        _check(lib().moe_router_forward(
+            self._desc, T, lp, ld, bp, mp, _want(out.ids, "ids", i32, (T, k)),
+            _want(out.scores, "scores", f32, (T, k)), _want(out.counts, "counts", i32, (E + 1,)),
+            _want(out.prob_sum, "prob_sum", f32, (E,)), _want(out.losses, "losses", f32, (2,)),
+            _want(out.row_stat, "row_stat", f32, (T,)), *self._ws, _raw_stream(stream)),
+            "router forward")
+        return out
+
+    def backward(self, logits, ids, counts, row_stat, d_scores=None, d_losses=None,
+                 d_logits=None, stream=None):
+        """Gradient at the logits of sum(d_scores * scores) + sum(d_losses * losses)."""
+        import torch
+
+        T, E, k = logits.shape[0], self.E, self.k
+        f32 = torch.float32
+        lp, ld = _rows(logits, "logits", self.dtype, (T, E))
+        if d_logits is None:
+            d_logits = torch.empty(T, E, dtype=self.dtype, device=logits.device)
+        dp, ld_d = _rows(d_logits, "d_logits", self.dtype, (T, E))
+        _check(lib().moe_router_backward(
+            self._desc, T, lp, ld, _maybe(ids, "ids", torch.int32, (T, k)),
+            _want(counts, "counts", torch.int32, (E + 1,)),
+            _want(row_stat, "row_stat", f32, (T,)), _maybe(d_scores, "d_scores", f32, (T, k)),
+            _maybe(d_losses, "d_losses", f32, (2,)), dp, ld_d, _raw_stream(stream)),
+            "router backward")
+        return d_logits
+
+
+BlockNormGrads = collections.namedtuple("BlockNormGrads", "d_residual dy dw_post dgate dw_pre")
+
+
+class MoeBlockNorm:
+    """The norms around a block with its gate and residual scale (moe_block_norm_*
+    in moe.h).  max_tokens sizes the backward's scratch; one MoeBlockNorm per
+    concurrent stream.
+
+    dtype: of y, u; residual_dtype: of the residual stream; param_dtype: of w_post,
+    w_pre and gate ([d] with MOE_GATE_CHANNEL, [T] with MOE_GATE_TOKEN)."""
+
+    def __init__(self, max_tokens, d, dtype=None, residual_dtype=None, param_dtype=None,
+                 gate=MOE_GATE_NONE, alpha=1.0, eps=1e-6, device="cuda"):
+        import torch
+
+        self.max_tokens, self.d, self.gate = max_tokens, d, gate
+        self.dtype = dtype if dtype is not None else torch.bfloat16
+        self.residual_dtype = residual_dtype if residual_dtype is not None else self.dtype
+        self.param_dtype = param_dtype if param_dtype is not None else torch.float32
+        self.desc = BlockNormDesc(d, _dtype_code(self.dtype, "dtype"),
+                                  _dtype_code(self.residual_dtype, "residual_dtype"),
+                                  _dtype_code(self.param_dtype, "param_dtype"), gate, alpha, eps)
+        self._desc = ctypes.addressof(self.desc)
+        self._ws_bytes = lib().moe_block_norm_workspace_bytes(self._desc, max_tokens)
+        if not self._ws_bytes:
+            raise MoeError(MOE_ERR_INVALID_ARG, "MoeBlockNorm(%d,%d)" % (max_tokens, d))
+        self.device, self.workspace = device, None     # scratch: from the first backward on
+
+    def _params(self, T, w_post, gate, w_pre):
+        """Addresses of w_post, gate and w_pre, and the gate's shape."""
+        pt, d = self.param_dtype, (self.d,)
+        shape = (T,) if self.gate == MOE_GATE_TOKEN else d
+        return (_maybe(w_post, "w_post", pt, d), _maybe(gate, "gate", pt, shape),
+                _maybe(w_pre, "w_pre", pt, d), shape)
+
+    def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, residual_out=None,
+                u=None, stream=None):
+        """-> (residual_out, u); without y the first is residual, without w_pre u is None."""
+        import torch
+
+        T = residual.shape[0]
+        shape = (T, self.d)
+        rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape)
+        wp, gp, wq, _ = self._params(T, w_post, gate, w_pre)
+        yp = op = up = None
+        ld_y = ld_o = ld_u = 0
+        if y is not None:
+            yp, ld_y = _rows(y, "y", self.dtype, shape)
+            if residual_out is None:
+                residual_out = torch.empty(shape, dtype=self.residual_dtype,
+                                           device=residual.device)
+            op, ld_o = _rows(residual_out, "residual_out", self.residual_dtype, shape)
+        if w_pre is not None:
+            if u is None:
+                u = torch.empty(shape, dtype=self.dtype, device=residual.device)
+            up, ld_u = _rows(u, "u", self.dtype, shape)
+        _check(lib().moe_block_norm_forward(self._desc, T, rp, ld_r, yp, ld_y, wp, gp, wq, op, ld_o,
+                                            up, ld_u, _raw_stream(stream)), "block norm forward")
+        return (residual if y is None else residual_out), (None if w_pre is None else u)
+
+    def backward(self, residual_out, d_residual_out=None, d_u=None, y=None, w_post=None, gate=None,
+                 w_pre=None, d_residual=None, dy=None, dw_post=None, dgate=None, dw_pre=None,
+                 accumulate=False, stream=None):
+        """-> BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre); entries of absent
+        inputs are None.  accumulate adds to the given dw_post, dgate and dw_pre."""
+        import torch
+
+        T, dev, f32 = residual_out.shape[0], residual_out.device, torch.float32
+        if T > self.max_tokens:
+            raise MoeError(MOE_ERR_INVALID_ARG, "block norm: %d rows, made for %d" % (
+                T, self.max_tokens))
+        shape = (T, self.d)
+        act, res = self.dtype, self.residual_dtype
+        rp, ld_r = _rows(residual_out, "residual_out", res, shape)
+        wp, gp, wq, gshape = self._params(T, w_post, gate, w_pre)
+        none = (None, 0)
+        yp, ld_y = none if y is None else _rows(y, "y", act, shape)
+        gr, ld_gr = none if d_residual_out is None else _rows(d_residual_out, "d_residual_out",
+                                                              res, shape)
+        gu, ld_gu = none if d_u is None else _rows(d_u, "d_u", act, shape)
+        new = torch.zeros if accumulate else torch.empty
+        if d_residual is None:
+            d_residual = torch.empty(shape, dtype=res, device=dev)
+        if dy is None and y is not None:
+            dy = torch.empty(shape, dtype=act, device=dev)
+        if dw_post is None and w_post is not None:
+            dw_post = new(self.d, dtype=f32, device=dev)
+        if dgate is None and gate is not None:
+            dgate = new(gshape, dtype=f32, device=dev)
+        if dw_pre is None and w_pre is not None:
+            dw_pre = new(self.d, dtype=f32, device=dev)
+        if self.workspace is None:
+            self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        op, ld_o = _rows(d_residual, "d_residual", res, shape)
+        dp, ld_d = none if dy is None else _rows(dy, "dy", act, shape)
+        _check(lib().moe_block_norm_backward(
+            self._desc, T, rp, ld_r, yp, ld_y, gr, ld_gr, gu, ld_gu, wp, gp, wq, op, ld_o, dp, ld_d,
+            _maybe(dw_post, "dw_post", f32, (self.d,)), _maybe(dgate, "dgate", f32, gshape),
+            _maybe(dw_pre, "dw_pre", f32, (self.d,)), 1 if accumulate else 0,
+            self.workspace.data_ptr(), self._ws_bytes, _raw_stream(stream)), "block norm backward")
+        return BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre)

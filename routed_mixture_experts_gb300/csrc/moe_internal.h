@@ -8,8 +8,33 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
+#include <stdio.h>
+
+#include "../../include/moe.h"
 
 namespace moe {
+
+// SMs of the current device (looked up once per device; 148 if the query fails).
+inline int num_sms() {
+  static std::atomic<int> known[64];
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 148;
+  const bool keep = dev >= 0 && dev < 64;
+  if (keep && (n = known[dev].load(std::memory_order_relaxed)) > 0) return n;
+  if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1)
+    return 148;
+  if (keep) known[dev].store(n, std::memory_order_relaxed);
+  return n;
+}
+
+// A launch's status as a MOE_* code (an error is printed with the entry point).
+inline int cuda_result(cudaError_t e, const char* what) {
+  if (e == cudaSuccess) return MOE_OK;
+  fprintf(stderr, "moe_gb300: CUDA error %s (%s)\n", cudaGetErrorString(e), what);
+  return MOE_ERR_CUDA;
+}
+
+constexpr int kNormMaxWidth = 16384;   // widest row of moe_block_norm_*
 
 // Launch with programmatic stream serialization (see pdl_wait / pdl_trigger in
 // moe_device.cuh): the kernel may be scheduled while the previous kernel of the

@@ -1,0 +1,95 @@
+"""Host-side argument checks of the router and block-norm entry points (CPU only)."""
+
+import ctypes
+
+import pytest
+
+OK, INVALID, WORKSPACE = 0, 1, 2
+A, ODD = ctypes.c_void_p(1 << 20), ctypes.c_void_p((1 << 20) + 1)
+
+
+@pytest.fixture(scope="module")
+def B():
+    from routed_mixture_experts_gb300 import build as b
+
+    b.build()
+    from routed_mixture_experts_gb300 import binding
+
+    binding.lib()
+    return binding
+
+
+def test_router_checks(B):
+    L = B.lib()
+    good = B.RouterDesc(128, 8, 1, 0, 1.0)
+    p = ctypes.addressof(good)
+    assert L.moe_router_workspace_bytes(p, 8192) > 0
+    for bad in [(0, 1, 1, 0, 1.0), (257, 1, 1, 0, 1.0), (8, 9, 1, 0, 1.0), (8, 0, 1, 0, 1.0),
+                (8, 2, 2, 0, 1.0), (8, 2, 1, 3, 1.0), (8, 2, 1, 0, float("inf"))]:
+        s = B.RouterDesc(*bad)
+        assert L.moe_router_workspace_bytes(ctypes.addressof(s), 64) == 0, bad
+    assert L.moe_router_workspace_bytes(None, 64) == 0
+    assert L.moe_router_workspace_bytes(p, -1) == 0
+    assert L.moe_router_workspace_bytes(p, 1 << 28) == 0                   # T*k = 2^31
+
+    def forward(T=4096, logits=A, ld=128, ids=A, scores=A, counts=A, prob=A, losses=A, stat=A,
+                ws=A, nbytes=1 << 30, desc=p):
+        return L.moe_router_forward(desc, T, logits, ld, None, None, ids, scores, counts, prob,
+                                    losses, stat, ws, nbytes, None)
+
+    for bad in (dict(desc=None), dict(T=-1), dict(logits=None), dict(ld=127), dict(ids=None),
+                dict(scores=None), dict(counts=None), dict(prob=None), dict(losses=None),
+                dict(stat=None), dict(logits=ODD), dict(ids=ODD), dict(ws=ODD)):
+        assert forward(**bad) == INVALID, bad
+    assert forward(ws=None) == WORKSPACE
+    assert forward(nbytes=16) == WORKSPACE
+
+    def backward(T=64, logits=A, ld=128, ids=A, counts=A, stat=A, ds=A, dl=A, out=A, ld_d=128):
+        return L.moe_router_backward(p, T, logits, ld, ids, counts, stat, ds, dl, out, ld_d, None)
+
+    for bad in (dict(T=-1), dict(logits=None), dict(ld=1), dict(ids=None), dict(counts=None),
+                dict(stat=None), dict(out=None), dict(ld_d=127), dict(out=ODD), dict(ds=ODD)):
+        assert backward(**bad) == INVALID, bad
+    assert backward(T=0) == OK
+
+
+def test_block_norm_checks(B):
+    L = B.lib()
+
+    def desc(d=2048, dtype=0, res=0, param=1, gate=1, alpha=1.0, eps=1e-6):
+        return B.BlockNormDesc(d, dtype, res, param, gate, alpha, eps)
+
+    for bad in (dict(d=0), dict(d=16385), dict(dtype=2), dict(res=-1), dict(param=2),
+                dict(gate=3), dict(eps=-1.0), dict(eps=float("nan")), dict(dtype=1, res=0)):
+        s = desc(**bad)
+        assert L.moe_block_norm_workspace_bytes(ctypes.addressof(s), 64) == 0, bad
+    s = desc()
+    p = ctypes.addressof(s)
+    assert L.moe_block_norm_workspace_bytes(p, 64) > 0
+    assert L.moe_block_norm_workspace_bytes(p, -1) == 0
+
+    def forward(T=64, res=A, ldr=2048, y=A, ldy=2048, wp=A, gate=A, wq=A, out=A, ldo=2048, u=A,
+                ldu=2048):
+        return L.moe_block_norm_forward(p, T, res, ldr, y, ldy, wp, gate, wq, out, ldo, u, ldu,
+                                        None)
+
+    for bad in (dict(T=-1), dict(res=None), dict(ldr=2047), dict(y=None), dict(ldy=1),
+                dict(gate=None), dict(wq=None), dict(out=None), dict(u=None), dict(ldu=7),
+                dict(res=ODD), dict(y=ODD), dict(u=ODD), dict(wp=ODD), dict(gate=ODD)):
+        assert forward(**bad) == INVALID, bad
+    assert forward(T=0) == OK
+
+    def backward(T=640, x=A, ldx=2048, y=A, ldy=2048, do=A, lddo=2048, du=A, lddu=2048, wp=A,
+                 gate=A, wq=A, dr=A, lddr=2048, dy=A, lddy=2048, dwp=A, dg=A, dwq=A, acc=0, ws=A,
+                 nbytes=1 << 30):
+        return L.moe_block_norm_backward(p, T, x, ldx, y, ldy, do, lddo, du, lddu, wp, gate, wq,
+                                         dr, lddr, dy, lddy, dwp, dg, dwq, acc, ws, nbytes, None)
+
+    for bad in (dict(T=-1), dict(x=None), dict(y=None), dict(gate=None), dict(wq=None),
+                dict(wp=None), dict(dr=None), dict(du=None), dict(ldx=1), dict(lddo=1),
+                dict(lddu=1), dict(lddr=1), dict(lddy=1), dict(dwp=ODD), dict(dg=ODD),
+                dict(dwq=ODD), dict(do=ODD), dict(ws=ODD)):
+        assert backward(**bad) == INVALID, bad
+    assert backward(ws=None) == WORKSPACE
+    assert backward(nbytes=64) == WORKSPACE
+    assert backward(T=0, acc=1) == OK
