@@ -302,8 +302,8 @@ int moe_prepare_weights_mxfp8_backward(const void* w13, const void* w2, int d, i
  *
  * An NVFP4 plan (precision MOE_PREC_NVFP4; d % 256 == 0, I % 256 == 0) takes
  * only an inference workspace (flags 0; MOE_ERR_UNSUPPORTED for
- * MOE_WS_TRAINING or MOE_WS_HOST_STAGING) and runs moe_forward_nvfp4 only
- * (moe_forward returns MOE_ERR_UNSUPPORTED).
+ * MOE_WS_TRAINING or MOE_WS_HOST_STAGING) and runs moe_forward_nvfp4 and
+ * moe_decode_nvfp4 only (moe_forward returns MOE_ERR_UNSUPPORTED).
  */
 
 /*
@@ -347,6 +347,27 @@ int moe_forward_nvfp4(moe_plan* plan, const void* x, const int32_t* ids, const f
                       const uint8_t* w13_codes, const uint8_t* w13_sf, const float* w13_scale,
                       const uint8_t* w2_codes, const uint8_t* w2_sf, const float* w2_scale,
                       void* y, void* stream);
+
+/*
+ * The routed experts of a few tokens: what moe_forward_nvfp4 is for prompts, for
+ * the single tokens of a decoding loop, on the same prepared weights.  The
+ * activations are not quantised (no activation scales are needed): x stays bf16,
+ * h is rounded to 11 significant bits (relative to the largest of each 128 of its
+ * elements), every sum is fp32, and
+ *   y[t] = bf16( sum_j scores[t,j] * (w2_scale[e] * W2[e] . h) ),
+ *   h = silu(G) * U, (G, U) = w13_scale[e] * W13[e] . x[t] (clipped to the plan's
+ *   clamp), e = ids[t,j], in fixed j order.
+ * tokens: 0 <= tokens <= min(T, MOE_DECODE_MAX_TOKENS) of the plan's T; x [tokens,
+ * d] bf16, ids and scores [tokens, k], y [tokens, d] bf16 (16-byte aligned).  Each
+ * chosen expert is read once for every 8 of its tokens; beyond some tens of tokens
+ * per expert moe_forward_nvfp4 is the faster call.  Bad ids are dropped and
+ * reported as by moe_forward.  Two launches; NVFP4 plans only.
+ */
+#define MOE_DECODE_MAX_TOKENS 256
+int moe_decode_nvfp4(moe_plan* plan, const void* x, const int32_t* ids, const float* scores,
+                     int tokens, const uint8_t* w13_codes, const uint8_t* w13_sf,
+                     const float* w13_scale, const uint8_t* w2_codes, const uint8_t* w2_sf,
+                     const float* w2_scale, void* y, void* stream);
 
 /*
  * amax = max |in[i]| over n bf16 values (device pointers; amax is one fp32 on

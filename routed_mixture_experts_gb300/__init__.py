@@ -11,6 +11,7 @@ built library and a CUDA device and raises otherwise.
 
 from .binding import (  # noqa: F401
     MOE_BUF,
+    MOE_DECODE_MAX_TOKENS,
     MOE_DTYPE_BF16,
     MOE_DTYPE_FP32,
     MOE_ERR_BAD_IDS,

@@ -33,6 +33,7 @@ MOE_ROUTER_SIGMOID = 2
 MOE_GATE_NONE = 0
 MOE_GATE_CHANNEL = 1
 MOE_GATE_TOKEN = 2
+MOE_DECODE_MAX_TOKENS = 256
 
 _lock = threading.Lock()
 _lib = None
@@ -96,6 +97,8 @@ def _declare(L):
     L.moe_nvfp4_weight_bytes.restype = sz
     L.moe_prepare_weights_nvfp4.argtypes = [vp, vp, i32, i32, i32] + [vp] * 7
     L.moe_forward_nvfp4.argtypes = [vp] * 12
+    L.moe_decode_nvfp4.argtypes = [vp] * 4 + [i32] + [vp] * 8
+    L.moe_decode_nvfp4.restype = i32
     L.moe_amax_bf16.argtypes = [vp, ctypes.c_longlong, vp, vp]
     L.moe_plan_set_backward_split.argtypes = [vp, i32]
     L.moe_plan_set_wgrad_interleave.argtypes = [vp, ctypes.c_longlong]
@@ -225,6 +228,24 @@ class MoePlan:
         _check(lib().moe_forward_nvfp4(self.ptr, _p(x), _p(ids), _p(scores), _p(w13q), _p(w13s),
                                        _p(w13c), _p(w2q), _p(w2s), _p(w2c), _p(y),
                                        _stream(stream)), "forward_nvfp4")
+        return y
+
+    def decode_nvfp4(self, x, ids, scores, prepared, y=None, stream=None):
+        """The routed experts of x [tokens, d], tokens <= min(T, MOE_DECODE_MAX_TOKENS);
+        prepared = prepare_weights_nvfp4(w13, w2) (see moe_decode_nvfp4 in moe.h)."""
+        import torch
+
+        n, k = x.shape[0], self.k
+        bf16 = torch.bfloat16
+        xp = _want(x, "x", bf16, (n, self.d))
+        if y is None:
+            y = torch.empty(n, self.d, dtype=bf16, device=x.device)
+        w13q, w13s, w13c, w2q, w2s, w2c = prepared
+        _check(lib().moe_decode_nvfp4(
+            self.ptr, xp, _want(ids, "ids", torch.int32, (n, k)),
+            _want(scores, "scores", torch.float32, (n, k)), n, w13q.data_ptr(), w13s.data_ptr(),
+            w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
+            _want(y, "y", bf16, (n, self.d)), _raw_stream(stream)), "decode_nvfp4")
         return y
 
     def backward(self, dy, w13, w2, dw13, dw2, dx=None, dscores=None, stream=None):

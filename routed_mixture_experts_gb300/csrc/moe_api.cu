@@ -78,6 +78,12 @@ struct moe_plan {
   float nv_x_scale, nv_h_scale;
   CUtensorMap tm_w13nv, tm_w2nv;
   const void *w13nv_cached, *w2nv_cached;
+  // moe_decode_nvfp4: h and ys of up to dec_tokens tokens, which pairs count, and
+  // the arrival counters (zero between calls)
+  int dec_tokens;
+  float *dec_h, *dec_ys;
+  uint8_t* dec_keep;
+  int* dec_arrived;
   int ngr_d, ngr_I;                 // 128-element scale groups along d and along I
   CUtensorMap tm_xq, tm_hq, tm_w13q, tm_w2q;
   const void *w13q_cached, *w2q_cached;
@@ -273,6 +279,12 @@ size_t layout(moe_plan* p, char* base, int flags) {
     p->xsf = reinterpret_cast<uint8_t*>(take((size_t)nv_sf_bytes(RP, (int)d)));
     p->hq = reinterpret_cast<uint8_t*>(take(RP * I / 2));
     p->hsf = reinterpret_cast<uint8_t*>(take((size_t)nv_sf_bytes(RP, (int)I)));
+    p->dec_tokens = p->T < kDecodeMaxTokens ? p->T : kDecodeMaxTokens;
+    const size_t pairs = (size_t)p->dec_tokens * k;
+    p->dec_h = reinterpret_cast<float*>(take(4 * pairs * I));
+    p->dec_ys = reinterpret_cast<float*>(take(4 * pairs * d));
+    p->dec_keep = reinterpret_cast<uint8_t*>(take(pairs));
+    p->dec_arrived = reinterpret_cast<int*>(take(4 * (d / 32)));
   }
   if (mx) {
     p->xq = reinterpret_cast<uint8_t*>(take(RP * d));
@@ -688,6 +700,8 @@ int moe_plan_set_workspace(moe_plan* p, void* ws, size_t bytes, int flags) {
         encode_tmap_bf16(&p->tm_ys, p->ys, RP, p->d, 128))
       return MOE_ERR_CUDA;
     if (flags & MOE_WS_HOST_STAGING) return MOE_ERR_UNSUPPORTED;
+    const int rc = cuda_status(cudaMemset(p->dec_arrived, 0, 4 * (size_t)(p->d / 32)));
+    if (rc != MOE_OK) return rc;
     return reset_error_word(p->err);
   }
   p->w13t_cached = p->w2t_cached = nullptr;
@@ -1422,6 +1436,36 @@ int moe_plan_set_timing_events(moe_plan* p, int which, void* const* events, int 
 }
 
 long long moe_plan_launch_count(const moe_plan* p) { return p ? p->launches : 0; }
+
+// The routed experts of a few tokens: matrix-vector products on the prepared
+// NVFP4 weights (moe_decode.cu), activations not quantised.
+int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float* scores,
+                     int tokens, const uint8_t* w13q, const uint8_t* w13_sf,
+                     const float* w13_scale, const uint8_t* w2q, const uint8_t* w2_sf,
+                     const float* w2_scale, void* y, void* stream_v) {
+  if (!p || tokens < 0) return MOE_ERR_INVALID_ARG;
+  if (p->precision != MOE_PREC_NVFP4) return MOE_ERR_UNSUPPORTED;
+  if (tokens > (p->T < kDecodeMaxTokens ? p->T : kDecodeMaxTokens)) return MOE_ERR_INVALID_ARG;
+  if (!w13q || !w13_sf || !w13_scale || !w2q || !w2_sf || !w2_scale || !aligned16(w13q) ||
+      !aligned16(w2q) || !aligned16(w13_sf) || !aligned16(w2_sf))
+    return MOE_ERR_INVALID_ARG;
+  if (!p->ws) return MOE_ERR_WORKSPACE;
+  if (tokens == 0) return MOE_OK;
+  if (!x || !ids || !scores || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  DecodeCall c = {};
+  c.x = x; c.ids = ids; c.scores = scores;
+  c.T = tokens; c.k = p->k; c.d = p->d; c.I = p->I; c.E = p->E;
+  c.clamp = p->clamp;
+  c.w13 = w13q; c.w13_sf = w13_sf; c.w13_scale = w13_scale;
+  c.w2 = w2q; c.w2_sf = w2_sf; c.w2_scale = w2_scale;
+  c.h = p->dec_h; c.ys = p->dec_ys; c.keep = p->dec_keep; c.arrived = p->dec_arrived;
+  c.y = y;
+  c.err = p->err;
+  const cudaError_t e = launch_decode_nvfp4(c, static_cast<cudaStream_t>(stream_v));
+  if (e != cudaSuccess) return cuda_status(e);
+  p->launches += 2;
+  return MOE_OK;
+}
 
 int moe_plan_check(moe_plan* p, long long* detail) {
   if (!p || !p->ws) return MOE_ERR_INVALID_ARG;

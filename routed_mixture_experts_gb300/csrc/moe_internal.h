@@ -209,6 +209,25 @@ cudaError_t launch_amax_bf16(const void* in, int nmat, long long per, unsigned i
 cudaError_t launch_prepare_nvfp4(const void* w, int E, long long rows_per_expert, int K, int gu_I,
                                  uint8_t* codes, uint8_t* sf, float* scale, cudaStream_t stream);
 
+// The routed experts of a few tokens on NVFP4 weights (moe_decode.cu).
+constexpr int kDecodeMaxTokens = 256;
+struct DecodeCall {
+  const void* x;             // [T, d] bf16
+  const int32_t* ids;        // [T, k]
+  const float* scores;       // [T, k]
+  int T, k, d, I, E;
+  float clamp;
+  const uint8_t *w13, *w13_sf, *w2, *w2_sf;   // prepared weights
+  const float *w13_scale, *w2_scale;          // [E]
+  float* h;                  // [T*k, I] scratch
+  float* ys;                 // [T*k, d] scratch
+  uint8_t* keep;             // [T*k] scratch
+  int* arrived;              // [d / 32], zero between calls
+  void* y;                   // [T, d] bf16
+  DevError* err;
+};
+cudaError_t launch_decode_nvfp4(const DecodeCall& c, cudaStream_t stream);   // two launches
+
 // Launch the CTA-pair grouped GEMM over routed rows (256 x 256 tiles, A K-major;
 // requires expert segments padded to 256 rows and N % 256 == 0).
 cudaError_t launch_gemm_pair(int epi, bool b_mn, const CUtensorMap& ta, const CUtensorMap& tb,
