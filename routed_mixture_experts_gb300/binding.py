@@ -239,9 +239,9 @@ class MoePlan:
         bf16 = torch.bfloat16
         xp = _want(x, "x", bf16, (n, self.d))
         if y is None:
-            y = torch.empty(n, self.d, dtype=bf16, device=x.device)
+            y = torch.empty((n, self.d), dtype=bf16, device=x.device)
         w13q, w13s, w13c, w2q, w2s, w2c = prepared
-        _check(lib().moe_decode_nvfp4(
+        _check(_lib.moe_decode_nvfp4(
             self.ptr, xp, _want(ids, "ids", torch.int32, (n, k)),
             _want(scores, "scores", torch.float32, (n, k)), n, w13q.data_ptr(), w13s.data_ptr(),
             w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
@@ -436,9 +436,14 @@ def gemm_bf16(mode, A, B, C, M, N, K, stream=None):
 
 
 def _raw_stream(stream):
+    """The handle of `stream`, or of the current device's current stream.  (The public
+    torch.cuda.current_stream() builds a Stream object for it, a third of the host
+    time of a small call.)"""
     import torch
 
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _dtype_code(dtype, what):
@@ -453,10 +458,10 @@ def _dtype_code(dtype, what):
 
 def _want(t, what, dtype, shape):
     """t: a contiguous CUDA tensor of this dtype and shape (its address)."""
-    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or not t.is_cuda:
-        raise MoeError(MOE_ERR_INVALID_ARG, "%s: want contiguous %s %s on the GPU, got %s %s" % (
-            what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+        return t.data_ptr()
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want contiguous %s %s on the GPU, got %s %s" % (
+        what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
 
 
 def _maybe(t, what, dtype, shape):
@@ -465,17 +470,17 @@ def _maybe(t, what, dtype, shape):
 
 def _rows(t, what, dtype, shape):
     """t: a CUDA [T, n] tensor whose rows may lie further apart (address, row distance)."""
-    if t.dtype != dtype or t.shape != shape or not t.is_cuda:
-        raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %s %s on the GPU, got %s %s" % (
-            what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
-    T, n = shape
-    apart, inner = t.stride()
-    if T <= 1:
-        apart = n
-    if (inner != 1 and n > 1) or apart < n:
-        raise MoeError(MOE_ERR_INVALID_ARG, "%s: rows have to be dense and apart, got strides %s" % (
-            what, t.stride()))
-    return t.data_ptr(), apart
+    if t.dtype is dtype and t.shape == shape and t.is_cuda:
+        if t.is_contiguous():
+            return t.data_ptr(), shape[1]
+        apart, inner = t.stride()
+        if shape[0] <= 1:
+            apart = shape[1]
+        if (inner == 1 or shape[1] == 1) and apart >= shape[1]:
+            return t.data_ptr(), apart
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %s %s on the GPU, rows dense and apart; got %s "
+                   "%s, strides %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape),
+                                       t.stride()))
 
 
 RouterResult = collections.namedtuple(
@@ -505,37 +510,40 @@ class MoeRouter:
 
     def outputs(self, T):
         """Fresh output tensors of a forward over T tokens."""
-        import torch
+        from torch import empty, float32, int32
 
-        dev = self.workspace.device
-        f = torch.empty(2 + self.E + T * (self.k + 1), dtype=torch.float32, device=dev)
-        i = torch.empty(self.E + 1 + T * self.k, dtype=torch.int32, device=dev)
-        E, k = self.E, self.k
-        losses, prob_sum, row_stat, scores = f.split([2, E, T, T * k])
-        counts, ids = i.split([E + 1, T * k])
-        return RouterResult(ids.view(T, k), scores.view(T, k), counts, prob_sum, losses, row_stat)
+        dev, E, k = self.workspace.device, self.E, self.k
+        return RouterResult(empty((T, k), dtype=int32, device=dev),
+                            empty((T, k), dtype=float32, device=dev),
+                            empty((E + 1,), dtype=int32, device=dev),
+                            empty((E,), dtype=float32, device=dev),
+                            empty((2,), dtype=float32, device=dev),
+                            empty((T,), dtype=float32, device=dev))
 
     def forward(self, logits, bias=None, token_mask=None, out=None, stream=None):
         """logits [T, E] -> RouterResult(ids, scores, counts, prob_sum, losses, row_stat);
         `out`: an earlier result (or outputs(T)) to overwrite."""
         import torch
 
+        f32, i32 = torch.float32, torch.int32
         T, E, k = logits.shape[0], self.E, self.k
         if T > self.max_tokens:
             raise MoeError(MOE_ERR_INVALID_ARG, "router: %d tokens, made for %d" % (
                 T, self.max_tokens))
         lp, ld = _rows(logits, "logits", self.dtype, (T, E))
-        bp = _maybe(bias, "bias", torch.float32, (E,))
+        bp = _maybe(bias, "bias", f32, (E,))
         mp = _maybe(token_mask, "token_mask", torch.uint8, (T,))
         if out is None:
             out = self.outputs(T)
-        f32, i32 = torch.float32, torch.int32
-        _check(lib().moe_router_forward(
-            self._desc, T, lp, ld, bp, mp, _want(out.ids, "ids", i32, (T, k)),
-            _want(out.scores, "scores", f32, (T, k)), _want(out.counts, "counts", i32, (E + 1,)),
-            _want(out.prob_sum, "prob_sum", f32, (E,)), _want(out.losses, "losses", f32, (2,)),
-            _want(out.row_stat, "row_stat", f32, (T,)), *self._ws, _raw_stream(stream)),
-            "router forward")
+            at = [t.data_ptr() for t in out]
+        else:
+            at = (_want(out.ids, "ids", i32, (T, k)), _want(out.scores, "scores", f32, (T, k)),
+                  _want(out.counts, "counts", i32, (E + 1,)),
+                  _want(out.prob_sum, "prob_sum", f32, (E,)),
+                  _want(out.losses, "losses", f32, (2,)),
+                  _want(out.row_stat, "row_stat", f32, (T,)))
+        _check(_lib.moe_router_forward(self._desc, T, lp, ld, bp, mp, *at, *self._ws, _raw_stream(stream)),
+               "router forward")
         return out
 
     def backward(self, logits, ids, counts, row_stat, d_scores=None, d_losses=None,
@@ -547,9 +555,11 @@ class MoeRouter:
         f32 = torch.float32
         lp, ld = _rows(logits, "logits", self.dtype, (T, E))
         if d_logits is None:
-            d_logits = torch.empty(T, E, dtype=self.dtype, device=logits.device)
-        dp, ld_d = _rows(d_logits, "d_logits", self.dtype, (T, E))
-        _check(lib().moe_router_backward(
+            d_logits = torch.empty((T, E), dtype=self.dtype, device=logits.device)
+            dp, ld_d = d_logits.data_ptr(), E
+        else:
+            dp, ld_d = _rows(d_logits, "d_logits", self.dtype, (T, E))
+        _check(_lib.moe_router_backward(
             self._desc, T, lp, ld, _maybe(ids, "ids", torch.int32, (T, k)),
             _want(counts, "counts", torch.int32, (E + 1,)),
             _want(row_stat, "row_stat", f32, (T,)), _maybe(d_scores, "d_scores", f32, (T, k)),
@@ -609,12 +619,16 @@ class MoeBlockNorm:
             if residual_out is None:
                 residual_out = torch.empty(shape, dtype=self.residual_dtype,
                                            device=residual.device)
-            op, ld_o = _rows(residual_out, "residual_out", self.residual_dtype, shape)
+                op, ld_o = residual_out.data_ptr(), self.d
+            else:
+                op, ld_o = _rows(residual_out, "residual_out", self.residual_dtype, shape)
         if w_pre is not None:
             if u is None:
                 u = torch.empty(shape, dtype=self.dtype, device=residual.device)
-            up, ld_u = _rows(u, "u", self.dtype, shape)
-        _check(lib().moe_block_norm_forward(self._desc, T, rp, ld_r, yp, ld_y, wp, gp, wq, op, ld_o,
+                up, ld_u = u.data_ptr(), self.d
+            else:
+                up, ld_u = _rows(u, "u", self.dtype, shape)
+        _check(_lib.moe_block_norm_forward(self._desc, T, rp, ld_r, yp, ld_y, wp, gp, wq, op, ld_o,
                                             up, ld_u, _raw_stream(stream)), "block norm forward")
         return (residual if y is None else residual_out), (None if w_pre is None else u)
 
@@ -653,7 +667,7 @@ class MoeBlockNorm:
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
         op, ld_o = _rows(d_residual, "d_residual", res, shape)
         dp, ld_d = none if dy is None else _rows(dy, "dy", act, shape)
-        _check(lib().moe_block_norm_backward(
+        _check(_lib.moe_block_norm_backward(
             self._desc, T, rp, ld_r, yp, ld_y, gr, ld_gr, gu, ld_gu, wp, gp, wq, op, ld_o, dp, ld_d,
             _maybe(dw_post, "dw_post", f32, (self.d,)), _maybe(dgate, "dgate", f32, gshape),
             _maybe(dw_pre, "dw_pre", f32, (self.d,)), 1 if accumulate else 0,
