@@ -174,7 +174,8 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
   return 1.f / sqrtf(sum_sq / (float)d + eps);
 }
 
-// Forward: one row per group of tpr threads, held in registers.
+// Forward, a row per group of tpr threads and no loop: few rows, wide rows and rows
+// without 16-byte alignment.
 template <typename A, typename R, int V, bool VEC>
 __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   __shared__ float red[2][32];
@@ -241,6 +242,133 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   pdl_trigger();
 }
 
+
+// ---- rows streamed through shared memory ---------------------------------------
+//
+// Rows of up to 4096 aligned columns: persistent CTAs of 512 threads, a thread owning
+// 8 columns of every row of its group.  It copies its own 16-byte pieces of the next
+// rows into its own slots of a ring with cp.async and reads them back itself, so a
+// copy in flight costs no register and needs no barrier; the parameters of its
+// columns stay in registers.
+
+constexpr int kStreamThreads = 512;
+constexpr int kStreamMaxWidth = kStreamThreads * 8;
+constexpr int kStages = 3;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A thread's slots of one tensor of one stage: sizeof(T) / 2 pieces of 16 bytes,
+// each [threads] apart so that a warp reads and writes consecutive pieces.
+template <typename T>
+__host__ __device__ constexpr int slot_bytes() { return kStreamThreads * 8 * (int)sizeof(T); }
+
+template <typename T>
+__device__ __forceinline__ void slot_copy(uint32_t slot, const T* src) {
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
+    cp_async16(slot + (i * kStreamThreads + threadIdx.x) * 16, src + i * (16 / sizeof(T)));
+}
+__device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const uint16_t*) {
+  load_vec8(reinterpret_cast<const uint16_t*>(slot + threadIdx.x * 16), f);
+}
+__device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const float*) {
+  const float4 a = *reinterpret_cast<const float4*>(slot + threadIdx.x * 16);
+  const float4 b = *reinterpret_cast<const float4*>(slot + (kStreamThreads + threadIdx.x) * 16);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+// Forward over streamed rows.
+template <typename A, typename R>
+__global__ void __launch_bounds__(kStreamThreads, 2) k_block_norm_stream(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ float red[2][2][kStreamThreads / 32];
+  constexpr int kStage = slot_bytes<A>() + slot_bytes<R>();
+  pdl_wait();
+  const int tpr = a.tpr, groups = blockDim.x / tpr;
+  const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr;
+  const int d = a.d, c0 = li * 8;
+  const bool in = c0 < d;
+  const long long first = (long long)blockIdx.x * groups + g, hop = (long long)gridDim.x * groups;
+  const uint32_t base = smem_u32(ring);
+  auto fetch = [&](long long row, int stage) {
+    if (in && row < a.T) {
+      if (a.y) slot_copy(base + stage * kStage, static_cast<const A*>(a.y) + row * a.ld_y + c0);
+      slot_copy(base + stage * kStage + slot_bytes<A>(),
+                static_cast<const R*>(a.res) + row * a.ld_res + c0);
+    }
+    cp_async_commit();
+  };
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+  float q[8], w[8];          // alpha * w_post * channel gate, w_pre
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = a.alpha, w[e] = 0.f;
+  if (in) {
+    float v[8];
+    if (a.y && a.w_post) {
+      load8_param<true>(a.w_post, a.param_bf16, 0, li, tpr, d, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] *= v[e];
+    }
+    if (a.y && a.gate_kind == MOE_GATE_CHANNEL) {
+      load8_param<true>(a.gate, a.param_bf16, 0, li, tpr, d, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q[e] *= v[e];
+    }
+    if (a.u) load8_param<true>(a.w_pre, a.param_bf16, 0, li, tpr, d, w);
+  }
+  int stage = 0, flip = 0;
+  for (long long row = first; row < a.T; row += hop) {
+    float x[8], y[8], s[1];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+    float f = 1.f;
+    if (a.y && a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
+    cp_async_wait<kStages - 2>();
+    if (in) {
+      if (a.y) slot_read(ring + stage * kStage, y, static_cast<const A*>(nullptr));
+      slot_read(ring + stage * kStage + slot_bytes<A>(), x, static_cast<const R*>(nullptr));
+    }
+    // into the slots read one row ago
+    fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+    if (a.y) {
+      if (a.w_post) {
+        s[0] = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[0] += y[e] * y[e];
+        group_sum(s, &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g);
+        f *= inv_rms(s[0], d, a.eps);
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += f * (q[e] * y[e]);
+      if (in) store_vec8(static_cast<R*>(a.out) + row * a.ld_out + c0, x);
+    }
+    if (a.u) {
+      s[0] = 0.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[0] += x[e] * x[e];
+      group_sum(s, &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g);
+      const float rs = inv_rms(s[0], d, a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] *= rs * w[e];
+      if (in) store_vec8(static_cast<A*>(a.u) + row * a.ld_u + c0, x);
+    }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    flip ^= 1;
+  }
+  pdl_trigger();
+}
+
 // The column sums' last step: the parameter gradients of column c from
 // P = sum_t du x rs and S = sum_t g_t dr y ry.
 __device__ __forceinline__ void param_grads(const NormArgs& a, int c, float P, float S) {
@@ -253,27 +381,238 @@ __device__ __forceinline__ void param_grads(const NormArgs& a, int c, float P, f
     put(a.dgate, a.alpha * S * (a.w_post ? param(a.w_post, a.param_bf16, c) : 1.f));
 }
 
-constexpr int kGradThreads = 512;
+// ---- gradient --------------------------------------------------------------------
 
-// Gradient: row groups walk the rows; a thread keeps the column sums P and S of
-// its columns in registers, the CTA adds its groups' sums in order and leaves
-// them in `partial` (k_block_norm_finish adds the CTAs').
-template <typename A, typename R, int V, bool VEC>
-__global__ void __launch_bounds__(kGradThreads) k_block_norm_grad(const NormArgs a) {
-  extern __shared__ float sm[];                // [2][d]: w_pre and q; later P and S
-  __shared__ float red[2][kGradThreads / 32 * 6];
+// The six row sums over the tpr threads of a group: each exchange halves the values
+// a lane still adds (9 shuffles instead of 30), a warp's totals go to buf[warp][8]
+// and every thread adds the warps in order.
+__device__ __forceinline__ void group_sum6(float (&s)[6], float (*buf)[8], int li, int tpr,
+                                           int bar) {
+  const int lane = li & 31;
+  const bool b4 = lane & 16, b3 = lane & 8, b2 = lane & 4;
+  float r[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float lo = s[i], hi = i < 2 ? s[4 + i] : 0.f;
+    r[i] = (b4 ? hi : lo) + __shfl_xor_sync(0xffffffffu, b4 ? lo : hi, 16);
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+    r[i] = (b3 ? r[2 + i] : r[i]) + __shfl_xor_sync(0xffffffffu, b3 ? r[i] : r[2 + i], 8);
+  float v = (b2 ? r[1] : r[0]) + __shfl_xor_sync(0xffffffffu, b2 ? r[0] : r[1], 4);
+  v += __shfl_xor_sync(0xffffffffu, v, 2);
+  v += __shfl_xor_sync(0xffffffffu, v, 1);
+  if ((lane & 3) == 0) buf[li >> 5][lane >> 2] = v;     // value 4 b4 + 2 b3 + b2
+  if (tpr == 32) __syncwarp();
+  else group_sync(bar, tpr);
+#pragma unroll
+  for (int i = 0; i < 6; ++i) s[i] = 0.f;
+  for (int w = 0; w < tpr / 32; ++w) {
+    const float4 p = *reinterpret_cast<const float4*>(buf[w]);
+    const float2 q = *reinterpret_cast<const float2*>(buf[w] + 4);
+    s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
+    s[4] += q.x; s[5] += q.y;
+  }
+}
+
+// What a row's elements need of its six sums.
+struct RowFactors {
+  float rs, cx;          // 1/rms(x), rs^3 mean(t x)
+  float ry, cy, gt;      // 1/rms(y), ry^2 mean(q dr y), token gate
+};
+
+__device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float (&s)[6],
+                                                  long long row, bool writer) {
+  const float inv_d = 1.f / (float)a.d;
+  RowFactors f;
+  f.rs = a.du ? inv_rms(s[0], a.d, a.eps) : 0.f;
+  f.cx = f.rs * f.rs * f.rs * (s[1] * inv_d);
+  f.ry = a.w_post ? inv_rms(s[2], a.d, a.eps) : 1.f;
+  const float D = s[3] + f.rs * s[4] - f.cx * s[5];
+  f.gt = 1.f;
+  if (a.y && a.gate_kind == MOE_GATE_TOKEN) {
+    f.gt = param(a.gate, a.param_bf16, row);
+    if (a.dgate && writer) {
+      const float v = f.ry * D;
+      a.dgate[row] = a.accumulate ? a.dgate[row] + v : v;
+    }
+  }
+  f.cy = a.w_post ? f.ry * f.ry * D * inv_d : 0.f;
+  return f;
+}
+
+__device__ __forceinline__ void row_sums(float (&s)[6], const float (&x)[8], const float (&y)[8],
+                                         const float (&dr)[8], const float (&du)[8],
+                                         const float (&wp)[8], const float (&q)[8]) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float t = du[e] * wp[e], qy = q[e] * y[e];
+    s[0] += x[e] * x[e];
+    s[1] += t * x[e];
+    s[2] += y[e] * y[e];
+    s[3] += qy * dr[e];
+    s[4] += qy * t;
+    s[5] += qy * x[e];
+  }
+}
+
+// dr becomes d_residual, y dy; the column sums take the row's terms.
+__device__ __forceinline__ void row_grads(const RowFactors& f, const float (&x)[8], float (&y)[8],
+                                          float (&dr)[8], const float (&du)[8],
+                                          const float (&wp)[8], const float (&q)[8],
+                                          float (&P)[8], float (&S)[8]) {
+  const float gy = f.gt * f.ry;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    P[e] += du[e] * (x[e] * f.rs);
+    dr[e] += f.rs * (du[e] * wp[e]) - f.cx * x[e];
+    S[e] += gy * (dr[e] * y[e]);
+    y[e] = gy * (q[e] * dr[e] - f.cy * y[e]);
+  }
+}
+
+__device__ __forceinline__ bool wants_column_sums(const NormArgs& a) {
+  return a.dw_pre || a.dw_post || (a.dgate && a.gate_kind == MOE_GATE_CHANNEL);
+}
+
+// The CTA's column sums from sm[2][d]: to `partial`, or (one CTA) to the gradients.
+__device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float* sm) {
+  const int d = a.d;
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    if (a.partial) {
+      a.partial[(long long)blockIdx.x * 2 * d + c] = sm[c];
+      a.partial[(long long)blockIdx.x * 2 * d + d + c] = sm[d + c];
+    } else {
+      param_grads(a, c, sm[c], sm[d + c]);
+    }
+  }
+}
+
+// Gradient of rows of up to 4096 columns: row groups walk the rows with the next
+// rows on their way (VEC: through the ring; else in registers), the sums of a
+// thread's 8 columns in registers.
+template <typename A, typename R, bool VEC>
+__global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_stream(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];
+  __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
+  constexpr int kA = slot_bytes<A>(), kR = slot_bytes<R>(), kStage = 2 * kA + 2 * kR;
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
   const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr;
-  const int d = a.d;
-  float* wpre = sm;
-  float* q = sm + d;
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+  const int d = a.d, c0 = li * 8;
+  const bool in = c0 < d;                        // VEC: the thread has columns
+  const long long first = (long long)blockIdx.x * groups + g, hop = (long long)gridDim.x * groups;
+  const A* const y_in = static_cast<const A*>(a.y);
+  const A* const du_in = static_cast<const A*>(a.du);
+  const R* const x_in = static_cast<const R*>(a.res);
+  const R* const dr_in = static_cast<const R*>(a.dres);
+  const uint32_t base = smem_u32(ring);
+  auto fetch = [&](long long row, int stage) {
+    if (in && row < a.T) {
+      const uint32_t at = base + stage * kStage;
+      slot_copy(at, x_in + row * a.ld_res + c0);
+      if (dr_in) slot_copy(at + kR, dr_in + row * a.ld_dres + c0);
+      if (y_in) slot_copy(at + 2 * kR, y_in + row * a.ld_y + c0);
+      if (du_in) slot_copy(at + 2 * kR + kA, du_in + row * a.ld_du + c0);
+    }
+    cp_async_commit();
+  };
+  float x[8], y[8], dr[8], du[8];
+  auto load = [&](long long row, float (&nx)[8], float (&ny)[8], float (&ndr)[8], float (&ndu)[8]) {
+    if (row >= a.T) return;
+    load8<false>(x_in + row * a.ld_res, 0, li, tpr, d, nx);
+    if (dr_in) load8<false>(dr_in + row * a.ld_dres, 0, li, tpr, d, ndr);
+    if (y_in) load8<false>(y_in + row * a.ld_y, 0, li, tpr, d, ny);
+    if (du_in) load8<false>(du_in + row * a.ld_du, 0, li, tpr, d, ndu);
+  };
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = y[e] = dr[e] = du[e] = 0.f;
+  float nx[8], ny[8], ndr[8], ndu[8];
+  if (VEC) {
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) nx[e] = ny[e] = ndr[e] = ndu[e] = 0.f;
+    load(first, nx, ny, ndr, ndu);
+  }
+  float wp[8], q[8], P[8], S[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = col<VEC>(0, e, li, tpr);
+    wp[e] = P[e] = S[e] = 0.f;
+    q[e] = a.alpha;
+    if (c < d) {
+      if (a.du) wp[e] = param(a.w_pre, a.param_bf16, c);
+      if (a.y && a.w_post) q[e] *= param(a.w_post, a.param_bf16, c);
+      if (a.y && a.gate_kind == MOE_GATE_CHANNEL) q[e] *= param(a.gate, a.param_bf16, c);
+    }
+  }
+  int stage = 0, flip = 0;
+  for (long long row = first; row < a.T; row += hop) {
+    if (VEC) {
+      cp_async_wait<kStages - 2>();
+      const uint8_t* at = ring + stage * kStage;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = dr[e] = 0.f;
+      if (in) {
+        slot_read(at, x, x_in);
+        if (dr_in) slot_read(at + kR, dr, x_in);
+        if (y_in) slot_read(at + 2 * kR, y, y_in);
+        if (du_in) slot_read(at + 2 * kR + kA, du, y_in);
+      }
+      fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = nx[e], y[e] = ny[e], dr[e] = ndr[e], du[e] = ndu[e];
+      load(row + hop, nx, ny, ndr, ndu);
+    }
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    row_sums(s, x, y, dr, du, wp, q);
+    group_sum6(s, &red[flip][g * (tpr / 32)], li, tpr, 1 + g);
+    const RowFactors f = row_factors(a, s, row, li == 0);
+    row_grads(f, x, y, dr, du, wp, q, P, S);
+    store8<VEC>(static_cast<R*>(a.out) + row * a.ld_out, 0, li, tpr, d, dr);
+    if (y_in && a.u) store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, 0, li, tpr, d, y);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    flip ^= 1;
+  }
+  pdl_trigger();
+  if (!wants_column_sums(a)) return;
+  cp_async_wait<0>();
+  float* sm = reinterpret_cast<float*>(ring);
+  for (int i = 0; i < groups; ++i) {
+    __syncthreads();
+    if (g == i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<VEC>(0, e, li, tpr);
+        if (c < d) {
+          sm[c] = (i ? sm[c] : 0.f) + P[e];
+          sm[d + c] = (i ? sm[d + c] : 0.f) + S[e];
+        }
+      }
+  }
+  __syncthreads();
+  leave_column_sums(a, sm);
+}
+
+// Gradient of wider rows: a group is the CTA, V pieces of 8 columns a thread, the
+// parameters in shared memory.
+template <typename A, typename R, int V, bool VEC>
+__global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
+  extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
+  __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
+  pdl_wait();
+  const int tpr = a.tpr, li = threadIdx.x, d = a.d;
+  float* wpre = wide_sm;
+  float* qs = wide_sm + d;
+  for (int c = li; c < d; c += tpr) {
     wpre[c] = a.du ? param(a.w_pre, a.param_bf16, c) : 0.f;
     float f = a.alpha;
     if (a.y && a.w_post) f *= param(a.w_post, a.param_bf16, c);
     if (a.y && a.gate_kind == MOE_GATE_CHANNEL) f *= param(a.gate, a.param_bf16, c);
-    q[c] = f;
+    qs[c] = f;
   }
   __syncthreads();
   float P[V][8], S[V][8];
@@ -281,10 +620,8 @@ __global__ void __launch_bounds__(kGradThreads) k_block_norm_grad(const NormArgs
   for (int v = 0; v < V; ++v)
 #pragma unroll
     for (int e = 0; e < 8; ++e) P[v][e] = S[v][e] = 0.f;
-  const float inv_d = 1.f / (float)d;
   int flip = 0;
-  for (long long row = (long long)blockIdx.x * groups + g; row < a.T;
-       row += (long long)gridDim.x * groups, flip ^= 1) {
+  for (long long row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
     float x[V][8], y[V][8], dr[V][8], du[V][8];
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -296,87 +633,46 @@ __global__ void __launch_bounds__(kGradThreads) k_block_norm_grad(const NormArgs
       if (a.dres) load8<VEC>(static_cast<const R*>(a.dres) + row * a.ld_dres, v, li, tpr, d, dr[v]);
       if (a.du) load8<VEC>(static_cast<const A*>(a.du) + row * a.ld_du, v, li, tpr, d, du[v]);
     }
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<VEC>(v, e, li, tpr);
-        if (c < d) {
-          const float t = du[v][e] * wpre[c], qy = q[c] * y[v][e];
-          s[0] += x[v][e] * x[v][e];
-          s[1] += t * x[v][e];
-          s[2] += y[v][e] * y[v][e];
-          s[3] += qy * dr[v][e];
-          s[4] += qy * t;
-          s[5] += qy * x[v][e];
-        }
-      }
-    group_sum(s, &red[flip][g * (tpr / 32) * 6], li, tpr, 1 + g);
-    const float rs = a.du ? inv_rms(s[0], d, a.eps) : 0.f;
-    const float cx = rs * rs * rs * (s[1] * inv_d);
-    const float ry = a.w_post ? inv_rms(s[2], d, a.eps) : 1.f;
-    const float D = s[3] + rs * s[4] - cx * s[5];
-    float gt = 1.f;
-    if (a.y && a.gate_kind == MOE_GATE_TOKEN) {
-      gt = param(a.gate, a.param_bf16, row);
-      if (a.dgate && li == 0) {
-        const float v = ry * D;
-        a.dgate[row] = a.accumulate ? a.dgate[row] + v : v;
-      }
-    }
-    const float cy = a.w_post ? ry * ry * D * inv_d : 0.f;
+    float wp[8], q[8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float o[8];
+      load8<VEC>(wpre, v, li, tpr, d, wp);
+      load8<VEC>(qs, v, li, tpr, d, q);
+      row_sums(s, x[v], y[v], dr[v], du[v], wp, q);
+    }
+    group_sum6(s, red[flip], li, tpr, 1);
+    const RowFactors f = row_factors(a, s, row, li == 0);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<VEC>(v, e, li, tpr);
-        const float wp = c < d ? wpre[c] : 0.f, qc = c < d ? q[c] : 0.f;
-        P[v][e] += du[v][e] * x[v][e] * rs;
-        dr[v][e] += rs * (du[v][e] * wp) - cx * x[v][e];
-        S[v][e] += gt * ry * dr[v][e] * y[v][e];
-        o[e] = ry * gt * (qc * dr[v][e] - cy * y[v][e]);
-      }
+    for (int v = 0; v < V; ++v) {
+      load8<VEC>(wpre, v, li, tpr, d, wp);
+      load8<VEC>(qs, v, li, tpr, d, q);
+      row_grads(f, x[v], y[v], dr[v], du[v], wp, q, P[v], S[v]);
       store8<VEC>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, dr[v]);
-      if (a.y && a.u) store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, o);
+      if (a.y && a.u) store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, y[v]);
     }
   }
   pdl_trigger();
-  if (!a.dw_pre && !a.dw_post && !(a.dgate && a.gate_kind == MOE_GATE_CHANNEL)) return;
-  for (int i = 0; i < groups; ++i) {
-    __syncthreads();
-    if (g == i) {
+  if (!wants_column_sums(a)) return;
+  __syncthreads();
 #pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = col<VEC>(v, e, li, tpr);
-          if (c < d) {
-            wpre[c] = (i ? wpre[c] : 0.f) + P[v][e];
-            q[c] = (i ? q[c] : 0.f) + S[v][e];
-          }
-        }
-    }
+  for (int v = 0; v < V; ++v) {
+    store8<VEC>(wpre, v, li, tpr, d, P[v]);
+    store8<VEC>(qs, v, li, tpr, d, S[v]);
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    if (a.partial) {
-      a.partial[(long long)blockIdx.x * 2 * d + c] = wpre[c];
-      a.partial[(long long)blockIdx.x * 2 * d + d + c] = q[c];
-    } else {
-      param_grads(a, c, wpre[c], q[c]);
-    }
-  }
+  leave_column_sums(a, wide_sm);
 }
 
-// Adds the CTAs' column sums in order: 32 columns per CTA, 8 slices of the CTAs.
-__global__ void __launch_bounds__(256) k_block_norm_finish(const NormArgs a) {
-  __shared__ float part[2][8][32];
+// Adds the CTAs' column sums in order: 32 columns per CTA, 16 slices of the CTAs.
+constexpr int kSlices = 16;
+__global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormArgs a) {
+  __shared__ float part[2][kSlices][32];
   pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
   float P = 0.f, S = 0.f;
   if (c < a.d)
-    for (int i = sl; i < a.n_partial; i += 8) {
+#pragma unroll 4
+    for (int i = sl; i < a.n_partial; i += kSlices) {
       P += a.partial[(long long)i * 2 * a.d + c];
       S += a.partial[(long long)i * 2 * a.d + a.d + c];
     }
@@ -386,7 +682,7 @@ __global__ void __launch_bounds__(256) k_block_norm_finish(const NormArgs a) {
   if (sl == 0 && c < a.d) {
     P = S = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kSlices; ++i) {
       P += part[0][i][threadIdx.x & 31];
       S += part[1][i][threadIdx.x & 31];
     }
@@ -400,9 +696,10 @@ __global__ void __launch_bounds__(256) k_block_norm_finish(const NormArgs a) {
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-int grad_pieces(int d) { return d <= kGradThreads * 16 ? 2 : 4; }
+// Gradient: threads of a row and rows at a time of a CTA.
+int grad_pieces(int d) { return d <= kStreamMaxWidth ? 1 : (d <= 2 * kStreamMaxWidth ? 2 : 4); }
 int grad_tpr(int d) { return round32((d + grad_pieces(d) * 8 - 1) / (grad_pieces(d) * 8)); }
-int grad_groups(int d) { return kGradThreads / grad_tpr(d); }
+int grad_groups(int d) { return kStreamThreads / grad_tpr(d); }
 int grad_grid(int T, int d) {
   const int per = grad_groups(d), want = (T + per - 1) / per, sms = num_sms();
   return want < sms ? want : sms;
@@ -417,6 +714,18 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
 
 template <typename A, typename R>
 cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
+  // many aligned rows: the stream
+  if (vec && a.d <= kStreamMaxWidth && a.T >= 4 * num_sms()) {
+    static std::atomic<unsigned long long> done{0};
+    const int smem = kStages * (slot_bytes<A>() + slot_bytes<R>());
+    cudaError_t e = smem_optin_once(k_block_norm_stream<A, R>, smem, done);
+    if (e != cudaSuccess) return e;
+    a.tpr = round32((a.d + 7) / 8);
+    const int groups = kStreamThreads / a.tpr, want = (a.T + groups - 1) / groups;
+    const int cap = 2 * num_sms();
+    return launch_pdl(k_block_norm_stream<A, R>, dim3(want < cap ? want : cap),
+                      dim3(groups * a.tpr), smem, st, a);
+  }
   // few rows: more threads and fewer columns each; d > 8192 needs two pieces
   const bool one = a.d <= 8192 && a.T < 4 * num_sms();
   a.tpr = round32((a.d + (one ? 7 : 15)) / (one ? 8 : 16));
@@ -424,21 +733,44 @@ cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
   return vec ? launch_fwd<A, R, 2, true>(a, st) : launch_fwd<A, R, 2, false>(a, st);
 }
 
-template <typename A, typename R, int V, bool VEC>
-cudaError_t launch_grad(const NormArgs& a, int grid, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const int smem = 2 * a.d * (int)sizeof(float);
-  cudaError_t e = smem_optin_once(k_block_norm_grad<A, R, V, VEC>, 2 * kNormMaxWidth * 4, done);
+template <typename... KArgs>
+cudaError_t launch_grad(void (*kernel)(KArgs...), std::atomic<unsigned long long>& done,
+                        int max_smem, int smem, const NormArgs& a, int grid, cudaStream_t st) {
+  const cudaError_t e = smem_optin_once(kernel, max_smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_block_norm_grad<A, R, V, VEC>, dim3(grid),
-                    dim3(a.tpr * grad_groups(a.d)), smem, st, a);
+  return launch_pdl(kernel, dim3(grid), dim3(a.tpr * grad_groups(a.d)), smem, st, a);
+}
+
+template <typename A, typename R, bool VEC>
+cudaError_t launch_grad_stream(const NormArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
+  const int ring = kStages * 2 * (slot_bytes<A>() + slot_bytes<R>());
+  const int smem = VEC && ring > sums ? ring : sums;
+  return launch_grad(k_block_norm_grad_stream<A, R, VEC>, done, smem, smem, a, grid, st);
+}
+
+template <typename A, typename R, int V, bool VEC>
+cudaError_t launch_grad_wide(const NormArgs& a, int grid, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  return launch_grad(k_block_norm_grad_wide<A, R, V, VEC>, done,
+                     2 * kNormMaxWidth * (int)sizeof(float), 2 * a.d * (int)sizeof(float), a, grid,
+                     st);
 }
 
 template <typename A, typename R>
 cudaError_t launch_grad_types(const NormArgs& a, bool vec, int grid, cudaStream_t st) {
-  if (grad_pieces(a.d) == 2)
-    return vec ? launch_grad<A, R, 2, true>(a, grid, st) : launch_grad<A, R, 2, false>(a, grid, st);
-  return vec ? launch_grad<A, R, 4, true>(a, grid, st) : launch_grad<A, R, 4, false>(a, grid, st);
+  switch (grad_pieces(a.d)) {
+    case 1:
+      return vec ? launch_grad_stream<A, R, true>(a, grid, st)
+                 : launch_grad_stream<A, R, false>(a, grid, st);
+    case 2:
+      return vec ? launch_grad_wide<A, R, 2, true>(a, grid, st)
+                 : launch_grad_wide<A, R, 2, false>(a, grid, st);
+    default:
+      return vec ? launch_grad_wide<A, R, 4, true>(a, grid, st)
+                 : launch_grad_wide<A, R, 4, false>(a, grid, st);
+  }
 }
 
 int elem(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
@@ -593,6 +925,6 @@ extern "C" int moe_block_norm_backward(
   else
     e = launch_grad_types<uint16_t, uint16_t>(a, vec, grid, st);
   if (e == cudaSuccess && a.partial)
-    e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32), dim3(256), 0, st, a);
+    e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32), dim3(kSlices * 32), 0, st, a);
   return cuda_result(e, "moe_block_norm_backward");
 }
