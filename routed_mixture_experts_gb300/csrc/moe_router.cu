@@ -58,11 +58,15 @@ __device__ __forceinline__ float load_logit(const uint16_t* p) { return bf2f(*p)
 __device__ __forceinline__ void store_logit(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = f2bf(v); }
 
-// fp32 to an unsigned integer of the same order; NaN below every number, -0 = +0.
+// fp32 to an unsigned integer of the same order, above 1; NaN is 1, below every
+// number, and 0 stays free for "not there"; -0 = +0.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 0u;
+  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 1u;
   return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float order_value(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -71,60 +75,50 @@ __device__ __forceinline__ float warp_sum(float v) {
   return v;
 }
 __device__ __forceinline__ float warp_max(float v) {      // NaN only if every lane's is
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kAll, v, o));
-  return v;
+  return order_value(__reduce_max_sync(kAll, order_key(v)));
 }
 
 // A row's weights, before they are divided by their sum: exp(l - top) for the
 // softmax, sigmoid(l) * exp(-top) for the sigmoid, with top the largest logit (the
-// sigmoid: at most 0), so that the sum neither overflows nor underflows.
+// sigmoid: at most 0), so that the sum neither overflows nor underflows.  The
+// hardware exponential errs by a few 2^-23 near the largest logit, where the sum is.
 __device__ __forceinline__ float weight(float l, float top, bool sig) {
-  if (l == -INFINITY) return 0.f;
-  if (!sig) return expf(l - top);
-  return l > 0.f ? 1.f / (1.f + expf(-l)) : expf(l - top) / (1.f + expf(l));
+  if (!sig) return __expf(l - top);                       // l = -inf: 0 (top is not)
+  const float t = __expf(-fabsf(l));
+  return __fdividef(l > 0.f ? 1.f : __expf(l - top), 1.f + t);
 }
 
-// The losses from the whole sums (threads 0..E-1 hold their expert's): one warp
-// sum per warp, the warps added in order by thread 0.
-__device__ __forceinline__ void write_sums(const RouterArgs& a, int count, float prob, int live,
-                                           float z, float* red) {
-  const int e = threadIdx.x;
-  float v = 0.f;
-  if (e < a.E) {
-    a.counts[e] = count;
-    a.prob_sum[e] = prob;
-    v = (float)count * prob;
-  }
+// Sums over the CTA's warps in a fixed order; all threads call it, warp 0 has the sum.
+__device__ __forceinline__ float block_sum(float v, float* buf) {
   v = warp_sum(v);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = v;
   __syncthreads();
-  if (threadIdx.x == 0) {
-    float s = 0.f;
-    for (int w = 0; w < (int)(blockDim.x >> 5); ++w) s += red[w];
-    const float n = live > 0 ? (float)live : 1.f;
-    a.counts[a.E] = live;
-    a.losses[0] = s / n * ((float)a.E / (float)a.k) / n;
-    a.losses[1] = z / n;
-  }
+  return warp_sum((threadIdx.x & 31) < (blockDim.x >> 5) ? buf[threadIdx.x & 31] : 0.f);
+}
+
+__device__ __forceinline__ void write_losses(const RouterArgs& a, float balance, float z,
+                                             int live) {
+  const float n = live > 0 ? (float)live : 1.f;
+  a.counts[a.E] = live;
+  a.losses[0] = balance / n * ((float)a.E / (float)a.k) / n;
+  a.losses[1] = z / n;
 }
 
 // Forward.  L = logits type, NV = slots of 32 experts.
 template <typename L, int NV>
 __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
+  extern __shared__ float psum[];                 // [warps][NV * 32]
   __shared__ int cnt[kMaxE];
-  __shared__ float psum[kMaxE];
-  __shared__ float zsum[32], red[32];
-  __shared__ int nlive;
-  pdl_wait();
+  __shared__ uint8_t sel_id[32][kMaxE];           // a warp's chosen experts, in order
+  __shared__ float wz[32];
+  __shared__ int wlive[32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int E = a.E, k = a.k;
-  for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) {
-    cnt[e] = 0;
-    psum[e] = 0.f;
-  }
-  if (threadIdx.x == 0) nlive = 0;
+  float* const mine = psum + warp * (NV * 32);    // first the row's logits, by expert
+  for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
+  pdl_wait();
+  const bool sig = a.scoring == MOE_ROUTER_SIGMOID;
   float ps[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) ps[i] = 0.f;
@@ -134,7 +128,6 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     const L* row = static_cast<const L*>(a.logits) + t * a.ld;
     int32_t* ids = a.ids + t * k;
     float* scores = a.scores + t * k;
-    const bool sig = a.scoring == MOE_ROUTER_SIGMOID;
     if (a.mask && !a.mask[t]) {
       // padding: the row is not read; ids spread over the experts
       for (int j = lane; j < k; j += 32) {
@@ -146,199 +139,228 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     }
     float l[NV];
     uint32_t key[NV];
+    float mx = -INFINITY;
+    bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
       l[i] = e < E ? load_logit(row + e) : -INFINITY;
-      key[i] = e < E ? order_key(a.bias ? l[i] + a.bias[e] : l[i]) : 0u;
     }
-    // selection; a taken slot's key becomes 0 and its bit in `taken` is set
-    uint32_t taken = 0u;
-    for (int j = 0; j < k; ++j) {
-      uint32_t best = 0u;
-      int at = kMaxE;
-#pragma unroll
-      for (int i = NV - 1; i >= 0; --i) {
-        const bool open = !(taken >> i & 1u) && lane + 32 * i < E;
-        if (open && key[i] >= best) {
-          best = key[i];
-          at = lane + 32 * i;
-        }
-      }
-      const uint32_t top = __reduce_max_sync(kAll, best);
-      const int e = (int)__reduce_min_sync(kAll, best == top ? (unsigned)at : (unsigned)kMaxE);
-      if ((e & 31) == lane) taken |= 1u << (e >> 5);
-      if (lane == 0) ids[j] = e;
-    }
-    float mx = l[0];
-    bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
+      const int e = lane + 32 * i;
+      key[i] = e < E ? order_key(a.bias ? l[i] + a.bias[e] : l[i]) : 0u;
+      mine[e] = l[i];
       mx = fmaxf(mx, l[i]);
       nan |= l[i] != l[i];
     }
+    // the largest key k times; slots are searched in order and lanes within a slot,
+    // so equal keys go to the lowest expert.  A chosen key becomes 0.
+    for (int j = 0; j < k; ++j) {
+      uint32_t best = key[0];
+#pragma unroll
+      for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+      const uint32_t top = __reduce_max_sync(kAll, best);
+      bool open = true;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (open) {
+          const unsigned has = __ballot_sync(kAll, key[i] == top);
+          if (has) {
+            const int at = __ffs(has) - 1;
+            if (lane == at) {
+              key[i] = 0u;
+              sel_id[warp][j] = (uint8_t)(32 * i + at);
+            }
+            open = false;
+          }
+        }
+    }
     mx = warp_max(mx);
     nan = __any_sync(kAll, nan);
-    const bool live = nan || mx > -INFINITY;
-    __syncwarp();                          // lane 0's ids are visible to the warp
-    if (!live) {
-      for (int j = lane; j < k; j += 32) scores[j] = 0.f;
+    __syncwarp();                          // sel_id and the row's logits are written
+    if (!nan && mx == -INFINITY) {         // nothing to choose
+      for (int j = lane; j < k; j += 32) {
+        ids[j] = sel_id[warp][j];
+        scores[j] = 0.f;
+      }
       if (lane == 0) a.row_stat[t] = -INFINITY;
+      __syncwarp();
       continue;
     }
+    if (mx == -INFINITY) mx = 0.f;         // NaN and -inf only: any shift gives NaN
     live_rows += 1;
     const float top = sig ? fminf(mx, 0.f) : mx;
-    float p[NV], total = 0.f;
+    float total = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      p[i] = lane + 32 * i < E ? weight(l[i], top, sig) : 0.f;
-      total += p[i];
+      l[i] = lane + 32 * i < E ? weight(l[i], top, sig) : 0.f;
+      total += l[i];
     }
     total = warp_sum(total);
-    const float stat = top + logf(total);
     const float inv = 1.f / total;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      p[i] *= inv;
-      ps[i] += p[i];
-    }
+    for (int i = 0; i < NV; ++i) ps[i] += l[i] * inv;
+    const float stat = top + logf(total);
     if (lane == 0) a.row_stat[t] = stat;
     if (!sig) z += stat * stat;
-    // the chosen: scores and counts
-    float ctop = top, csum = total;
+    // the chosen: scores and counts.  Without a bias the row's largest logit is among
+    // them, and its shift serves.
+    float ctop = top, cinv = inv;
     if (a.scoring != MOE_ROUTER_SOFTMAX) {
-      ctop = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (taken >> i & 1u) ctop = fmaxf(ctop, l[i]);
-      ctop = warp_max(ctop);
-      if (sig) ctop = fminf(ctop, 0.f);
-      csum = 0.f;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (taken >> i & 1u) csum += weight(l[i], ctop, sig);
-      csum = warp_sum(csum);
+      if (a.bias) {
+        float m = -INFINITY;
+        for (int j = lane; j < k; j += 32) m = fmaxf(m, mine[sel_id[warp][j]]);
+        ctop = warp_max(m);
+        if (sig) ctop = fminf(ctop, 0.f);
+        if (nan && ctop == -INFINITY) ctop = top;
+      }
+      float sum = 0.f;
+      if (ctop != -INFINITY)
+        for (int j = lane; j < k; j += 32) sum += weight(mine[sel_id[warp][j]], ctop, sig);
+      sum = warp_sum(sum);
+      cinv = sum == 0.f ? 0.f : 1.f / sum;
     }
     for (int j = lane; j < k; j += 32) {
-      const int e = ids[j];
-      const float c = load_logit(row + e);
-      const float s = csum == 0.f ? 0.f : weight(c, ctop, sig) / csum;
-      scores[j] = s * a.scale;
+      const int e = sel_id[warp][j];
+      const float c = mine[e];
+      ids[j] = e;
+      scores[j] = ctop == -INFINITY ? 0.f : weight(c, ctop, sig) * cinv * a.scale;
       if (c != -INFINITY) atomicAdd(&cnt[e], 1);
     }
+    __syncwarp();                          // before the next row overwrites them
   }
   pdl_trigger();
   // the warps' sums, added in order
-  for (int w = 0; w < nw; ++w) {
-    __syncthreads();
-    if (warp == w) {
 #pragma unroll
-      for (int i = 0; i < NV; ++i) psum[lane + 32 * i] += ps[i];
-      if (lane == 0) {
-        zsum[w] = z;
-        nlive += live_rows;
-      }
-    }
+  for (int i = 0; i < NV; ++i) mine[lane + 32 * i] = ps[i];
+  if (lane == 0) {
+    wz[warp] = z;
+    wlive[warp] = live_rows;
   }
   __syncthreads();
-  z = 0.f;
-  for (int w = 0; w < nw; ++w) z += zsum[w];
-  if (a.part_prob) {
-    const long long b = blockIdx.x;
-    for (int e = threadIdx.x; e < E; e += blockDim.x) {
-      a.part_prob[b * E + e] = psum[e];
+  float v = 0.f;
+  const long long b = blockIdx.x;
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float P = 0.f;
+    for (int w = 0; w < nw; ++w) P += psum[w * (NV * 32) + e];
+    if (a.part_prob) {
+      a.part_prob[b * E + e] = P;
       a.part_count[b * (E + 1) + e] = cnt[e];
+    } else {
+      a.prob_sum[e] = P;
+      a.counts[e] = cnt[e];
+      v += (float)cnt[e] * P;
     }
+  }
+  z = warp_sum(lane < nw ? wz[lane] : 0.f);
+  const int live = __reduce_add_sync(kAll, lane < nw ? wlive[lane] : 0);
+  if (a.part_prob) {
     if (threadIdx.x == 0) {
-      a.part_count[b * (E + 1) + E] = nlive;
+      a.part_count[b * (E + 1) + E] = live;
       a.part_z[b] = z;
     }
   } else {
-    const int e = threadIdx.x < kMaxE ? threadIdx.x : 0;
-    write_sums(a, cnt[e], psum[e], nlive, z, red);
+    __syncthreads();                       // wz has been read
+    v = block_sum(v, wz);
+    if (threadIdx.x == 0) write_losses(a, v, z, live);
   }
 }
 
-// Adds the CTAs' sums in order: 4 slices of the CTAs per expert.
+// Adds the CTAs' sums: a cluster of one CTA per 32 experts, warp w of it expert w,
+// the balance loss joined through the cluster's shared memory.
 __global__ void __launch_bounds__(1024) k_router_finish(const RouterArgs a) {
-  __shared__ float sp[4][kMaxE];
-  __shared__ int sc[4][kMaxE];
-  __shared__ float red[32];
-  __shared__ float zs[32];
-  __shared__ int ls[32];
+  __shared__ float sp[32][33];
+  __shared__ int sc[32][33];
+  __shared__ float per_warp[32], part[8];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int e = blockIdx.x * 32 + lane;
+  cluster_sync();                          // every CTA's shared memory is there
   pdl_wait();
-  const int e = threadIdx.x & (kMaxE - 1), sl = threadIdx.x / kMaxE;
   float P = 0.f;
   int c = 0;
   if (e < a.E)
-    for (int b = sl; b < a.n_part; b += 4) {
+#pragma unroll 4
+    for (int b = warp; b < a.n_part; b += 32) {
       P += a.part_prob[(long long)b * a.E + e];
       c += a.part_count[(long long)b * (a.E + 1) + e];
     }
-  sp[sl][e] = P;
-  sc[sl][e] = c;
   float z = 0.f;
   int live = 0;
-  for (int b = threadIdx.x; b < a.n_part; b += blockDim.x) {
-    z += a.part_z[b];
-    live += a.part_count[(long long)b * (a.E + 1) + a.E];
-  }
-  z = warp_sum(z);
-  live = __reduce_add_sync(kAll, live);
-  if ((threadIdx.x & 31) == 0) {
-    zs[threadIdx.x >> 5] = z;
-    ls[threadIdx.x >> 5] = live;
+  if (blockIdx.x == 0 && warp == 0)
+    for (int b = lane; b < a.n_part; b += 32) {
+      z += a.part_z[b];
+      live += a.part_count[(long long)b * (a.E + 1) + a.E];
+    }
+  sp[warp][lane] = P;
+  sc[warp][lane] = c;
+  __syncthreads();
+  P = warp_sum(sp[lane][warp]);            // expert blockIdx.x * 32 + warp
+  c = __reduce_add_sync(kAll, sc[lane][warp]);
+  if (lane == 0) {
+    const int mine = blockIdx.x * 32 + warp;
+    if (mine < a.E) {
+      a.prob_sum[mine] = P;
+      a.counts[mine] = c;
+    }
+    per_warp[warp] = (float)c * P;
   }
   __syncthreads();
-  z = 0.f;
-  live = 0;
-  for (int w = 0; w < 32; ++w) {
-    z += zs[w];
-    live += ls[w];
+  if (warp == 0) {
+    const float v = warp_sum(per_warp[lane]);
+    if (lane == 0)
+      asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(
+                       mapa_shared(smem_u32(&part[blockIdx.x]), 0)), "f"(v) : "memory");
+    __syncwarp();
   }
-  P = 0.f;
-  c = 0;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    P += sp[i][e];
-    c += sc[i][e];
+  cluster_sync();
+  if (blockIdx.x == 0 && warp == 0) {
+    z = warp_sum(z);
+    live = __reduce_add_sync(kAll, live);
+    if (lane == 0) {
+      float balance = 0.f;
+      for (int i = 0; i < (int)gridDim.x; ++i) balance += part[i];
+      write_losses(a, balance, z, live);
+    }
   }
-  write_sums(a, c, P, live, z, red);
   pdl_trigger();
 }
 
-// Gradient: a warp per row, as the forward.  `extra` holds the chosen experts'
-// own terms of the warp's row.
+// Gradient: a warp per row, as the forward.  A warp's shared memory holds the row's
+// logits and the chosen experts' own terms.
 constexpr int kGradWarps = 8;
 
 template <typename L, int NV>
 __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArgs a) {
-  __shared__ float extra[kGradWarps][kMaxE];
-  pdl_wait();
+  __shared__ float logits[kGradWarps][NV * 32], extra[kGradWarps][NV * 32];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int E = a.E, k = a.k;
-  const bool sig = a.scoring == MOE_ROUTER_SIGMOID;
-  float* ex = extra[warp];
+  const bool sig = a.scoring == MOE_ROUTER_SIGMOID, in_g = a.scoring == MOE_ROUTER_SOFTMAX;
+  float* const lg = logits[warp];
+  float* const ex = extra[warp];
 #pragma unroll
   for (int i = 0; i < NV; ++i) ex[lane + 32 * i] = 0.f;
+  pdl_wait();
   const int live_n = a.counts[E];
-  const float n = live_n > 0 ? (float)live_n : 1.f;
-  float b[NV];
+  const float inv_n = 1.f / (live_n > 0 ? (float)live_n : 1.f);
+  float b[NV], dz = 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int e = lane + 32 * i;
-    b[i] = (e < E && a.d_losses)
-               ? a.d_losses[0] * ((float)E / (float)k) * (float)a.counts[e] / n / n : 0.f;
+  for (int i = 0; i < NV; ++i) b[i] = 0.f;
+  if (a.d_losses) {
+    const float f = a.d_losses[0] * ((float)E / (float)k) * inv_n;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int e = lane + 32 * i;
+      if (e < E) b[i] = f * ((float)a.counts[e] * inv_n);
+    }
+    if (!sig) dz = a.d_losses[1] * 2.f * inv_n;
   }
-  const float dz = (a.d_losses && !sig) ? a.d_losses[1] * 2.f / n : 0.f;
-  __syncwarp();
   for (long long t = (long long)blockIdx.x * kGradWarps + warp; t < a.T;
        t += (long long)gridDim.x * kGradWarps) {
     const L* row = static_cast<const L*>(a.logits) + t * a.ld;
     L* out = static_cast<L*>(a.d_logits) + t * a.ld_d;
     const float stat = a.row_stat[t];
-    const bool live = stat != -INFINITY;
-    if (!live) {                            // padding, or nothing to choose: no gradient
+    if (stat == -INFINITY) {                // not live: no gradient
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (lane + 32 * i < E) store_logit(out + lane + 32 * i, 0.f);
@@ -353,71 +375,70 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
     if (a.d_scores) {
       const int32_t* ids = a.ids + t * k;
       const float* ds = a.d_scores + t * k;
-      // normalised chosen scores s', their sum C and sum v s'
-      float ctop = -INFINITY, csum = 0.f, vs = 0.f;
-      if (a.scoring != MOE_ROUTER_SOFTMAX) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) lg[lane + 32 * i] = l[i];
+      __syncwarp();
+      // normalised chosen scores s' = weight / csum, and sum v s'
+      float ctop = -INFINITY, cinv = 0.f, vs = 0.f;
+      if (!in_g) {
         for (int j = lane; j < k; j += 32) {
           const int e = ids[j];
-          if (e >= 0 && e < E) ctop = fmaxf(ctop, load_logit(row + e));
+          if (e >= 0 && e < E) ctop = fmaxf(ctop, lg[e]);
         }
         ctop = warp_max(ctop);
         if (sig) ctop = fminf(ctop, 0.f);
-        for (int j = lane; j < k; j += 32) {
-          const int e = ids[j];
-          if (e >= 0 && e < E) csum += weight(load_logit(row + e), ctop, sig);
-        }
-        csum = warp_sum(csum);
-        for (int j = lane; j < k; j += 32) {
-          const int e = ids[j];
-          if (e >= 0 && e < E && csum != 0.f) {
-            const float w = weight(load_logit(row + e), ctop, sig) / csum;
-            if (w != 0.f) vs += ds[j] * a.scale * w;
+        float sum = 0.f;
+        if (ctop != -INFINITY)
+          for (int j = lane; j < k; j += 32) {
+            const int e = ids[j];
+            if (e >= 0 && e < E && lg[e] != -INFINITY) {
+              const float w = weight(lg[e], ctop, sig);
+              sum += w;
+              vs += ds[j] * a.scale * w;
+            }
           }
-        }
-        vs = warp_sum(vs);
+        sum = warp_sum(sum);
+        cinv = sum == 0.f ? 0.f : 1.f / sum;
+        vs = warp_sum(vs) * cinv;
       }
       for (int j = lane; j < k; j += 32) {
         const int e = ids[j];
         if (e < 0 || e >= E) continue;
-        const float c = load_logit(row + e), v = ds[j] * a.scale;
+        const float c = lg[e], v = ds[j] * a.scale;
         float x = 0.f;
-        if (c != -INFINITY) {
-          if (a.scoring == MOE_ROUTER_SOFTMAX)
-            x = v;
-          else if (csum != 0.f)
-            x = weight(c, ctop, sig) / csum * (v - vs);
-        }
+        if (c != -INFINITY)
+          x = in_g ? v : ctop == -INFINITY ? 0.f : weight(c, ctop, sig) * cinv * (v - vs);
         ex[e] = x;
       }
       __syncwarp();
     }
-    float p[NV], gp = 0.f;
-    const bool in_g = a.scoring == MOE_ROUTER_SOFTMAX;
     // p = weight(l, stat): exp(l - lse), or sigmoid(l) / S (for l > 0 divided by S here)
-    const float inv = sig ? expf(-stat) : 1.f;
+    const float inv = sig ? __expf(-stat) : 1.f;
+    float gp = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      p[i] = lane + 32 * i < E ? weight(l[i], stat, sig) : 0.f;
-      if (sig && l[i] > 0.f) p[i] *= inv;
-      gp += p[i] * (b[i] + (in_g ? ex[lane + 32 * i] : 0.f));
+      float p = lane + 32 * i < E ? weight(l[i], stat, sig) : 0.f;
+      float after = 1.f;
+      if (sig) {
+        const float u = __expf(-fabsf(l[i]));
+        after = __fdividef(l[i] > 0.f ? u : 1.f, 1.f + u);       // 1 - sigmoid
+        if (l[i] > 0.f) p *= inv;
+      }
+      const float x = ex[lane + 32 * i];
+      const float g = b[i] + (in_g ? x : 0.f);
+      gp += p * g;
+      // dl = after * (p * (g + dz stat - gp) + own term), without gp for now
+      lg[lane + 32 * i] = after * p;
+      l[i] = after * (p * (g + dz * stat) + (in_g ? 0.f : x));
     }
     gp = warp_sum(gp);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
-      const float x = ex[e];
-      float g = p[i] * (b[i] + (in_g ? x : 0.f) - gp + dz * stat) + (in_g ? 0.f : x);
-      if (sig) g *= l[i] > 0.f ? expf(-l[i]) / (1.f + expf(-l[i])) : 1.f / (1.f + expf(l[i]));
-      if (e < E) store_logit(out + e, g);
+      if (e < E) store_logit(out + e, l[i] - lg[e] * gp);
+      if (a.d_scores) ex[e] = 0.f;          // clear for the next row
     }
-    if (a.d_scores) {                       // clear for the next row
-      __syncwarp();
-      for (int j = lane; j < k; j += 32) {
-        const int e = a.ids[t * k + j];
-        if (e >= 0 && e < E) ex[e] = 0.f;
-      }
-      __syncwarp();
-    }
+    __syncwarp();
   }
   pdl_trigger();
 }
@@ -428,25 +449,51 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
 // Up to this many rows run on one CTA, which also writes the sums (no second
 // launch).
 constexpr int kOneCtaRows = 64;
-constexpr int kFwdWarps = 16;
+
+// warps of a CTA: its chosen experts and per-warp sums take shared memory
+int forward_warps(int T, int grid) { return grid > 1 ? 32 : T > 8 ? 32 : 8; }
 
 int forward_grid(int T) {
   if (T <= kOneCtaRows) return 1;
-  const int want = (T + kFwdWarps - 1) / kFwdWarps, cap = num_sms();
+  const int want = (T + 31) / 32, cap = num_sms();
   return want < cap ? want : cap;
+}
+
+template <typename L, int NV>
+cudaError_t launch_forward_nv(const RouterArgs& a, int grid, cudaStream_t st) {
+  const int warps = forward_warps(a.T, grid), smem = warps * NV * 32 * (int)sizeof(float);
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = smem_optin_once(k_router<L, NV>, 32 * NV * 32 * (int)sizeof(float), done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_router<L, NV>, dim3(grid), dim3(warps * 32), smem, st, a);
 }
 
 template <typename L>
 cudaError_t launch_forward(const RouterArgs& a, int grid, cudaStream_t st) {
-  const int warps = grid > 1 ? kFwdWarps : a.T > 8 ? 32 : 8;
-  const dim3 g(grid), b(warps * 32);
   switch ((a.E + 31) / 32) {
-    case 1: return launch_pdl(k_router<L, 1>, g, b, 0, st, a);
-    case 2: return launch_pdl(k_router<L, 2>, g, b, 0, st, a);
-    case 3: return launch_pdl(k_router<L, 3>, g, b, 0, st, a);
-    case 4: return launch_pdl(k_router<L, 4>, g, b, 0, st, a);
-    default: return launch_pdl(k_router<L, 8>, g, b, 0, st, a);
+    case 1: return launch_forward_nv<L, 1>(a, grid, st);
+    case 2: return launch_forward_nv<L, 2>(a, grid, st);
+    case 3: return launch_forward_nv<L, 3>(a, grid, st);
+    case 4: return launch_forward_nv<L, 4>(a, grid, st);
+    default: return launch_forward_nv<L, 8>(a, grid, st);
   }
+}
+
+cudaError_t launch_finish(const RouterArgs& a, cudaStream_t st) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((a.E + 31) / 32);
+  cfg.blockDim = dim3(1024);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cfg.gridDim.x;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, k_router_finish, a);
 }
 
 template <typename L>
@@ -517,8 +564,7 @@ extern "C" int moe_router_forward(const moe_router_desc* s, int T, const void* l
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e = s->dtype == MOE_DTYPE_FP32 ? launch_forward<float>(a, grid, st)
                                              : launch_forward<uint16_t>(a, grid, st);
-  if (e == cudaSuccess && a.part_prob)
-    e = launch_pdl(k_router_finish, dim3(1), dim3(1024), 0, st, a);
+  if (e == cudaSuccess && a.part_prob) e = launch_finish(a, st);
   return cuda_result(e, "moe_router_forward");
 }
 
