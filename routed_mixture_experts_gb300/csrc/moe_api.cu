@@ -1452,6 +1452,7 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
   if (!p->ws) return MOE_ERR_WORKSPACE;
   if (tokens == 0) return MOE_OK;
   if (!x || !ids || !scores || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (!decode_nvfp4_fits(p->d, p->I, tokens * p->k)) return MOE_ERR_UNSUPPORTED;
   DecodeCall c = {};
   c.x = x; c.ids = ids; c.scores = scores;
   c.T = tokens; c.k = p->k; c.d = p->d; c.I = p->I; c.E = p->E;
@@ -1461,9 +1462,10 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
   c.h = p->dec_h; c.ys = p->dec_ys; c.keep = p->dec_keep; c.arrived = p->dec_arrived;
   c.y = y;
   c.err = p->err;
-  const cudaError_t e = launch_decode_nvfp4(c, static_cast<cudaStream_t>(stream_v));
+  int launches = 0;
+  const cudaError_t e = launch_decode_nvfp4(c, &launches, static_cast<cudaStream_t>(stream_v));
   if (e != cudaSuccess) return cuda_status(e);
-  p->launches += 2;
+  p->launches += launches;
   return MOE_OK;
 }
 

@@ -41,10 +41,10 @@ namespace {
 
 constexpr int kStep = 128;              // K elements per warp step
 constexpr int kCols = 8;                // tokens per pass (MMA columns)
-constexpr int kMaxWarps = 8;
-// shared bytes of a token's step: four 64-byte pieces, and 64 more so that the
-// eight lanes of a quarter-warp load from different banks
-constexpr int kTokStride = 320;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+// Up to this many tokens the last CTA of some rows joins the experts' results.
+constexpr int kArrivalTokens = 4;
 
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t word, int byte) {
   uint32_t r;
@@ -98,17 +98,18 @@ __device__ __forceinline__ void pow2_scale(float amax, float& mul, float& inv) {
   inv = s == 254 ? __uint_as_float(0x00400000u) : __uint_as_float((uint32_t)(254 - s) << 23);
 }
 
-// One lane's operands of a step: 16 code bytes of each of its rows and the scale
-// words of the four rows (blocks of its half K group).
+// One lane's operands of a step: 16 code bytes of each of its four rows, and the
+// scale words of the four rows (blocks of its half K group).
 struct StepA {
   uint4 c[4];
   uint4 s;
 };
 
+// Where they are: the lane's bytes of step 0 in its first row, its scales.  The
+// second row is `gap` bytes further, the third and fourth `far` beyond those.
 struct Rows {
-  const uint8_t* code[4];     // the lane's 16 bytes of step 0 in each row
-  const uint8_t* scale;       // the lane's 16 scale bytes of step 0
-  int half;                   // 16 * (q & 1): which two of a K group's four blocks
+  const uint8_t* code;
+  const uint8_t* scale;
 };
 
 __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
@@ -118,53 +119,47 @@ __device__ __forceinline__ uint4 ldg_stream(const uint8_t* p) {
   return v;
 }
 
-__device__ __forceinline__ void load_step(const Rows& r, int step, StepA& a) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) a.c[i] = ldg_stream(r.code[i] + (long long)step * (kStep / 2));
-  a.s = *reinterpret_cast<const uint4*>(r.scale + (long long)step * 1024);
+__device__ __forceinline__ void load_step(const Rows& r, long long gap, long long far, int step,
+                                          StepA& a) {
+  const uint8_t* p = r.code + step * (kStep / 2);
+  a.c[0] = ldg_stream(p);
+  a.c[1] = ldg_stream(p + gap);
+  a.c[2] = ldg_stream(p + far);
+  a.c[3] = ldg_stream(p + far + gap);
+  a.s = ldg_stream(r.scale + step * 1024);
 }
 
-// acc[tile][..] += (dequantised rows) . (the tokens' step in `xs`), the step's
-// token scales (inverse powers of two) applied to the partial sums.
-__device__ __forceinline__ void mma_step(const StepA& a, int half, const uint8_t* xs,
-                                         const float* inv, int lane, bool have,
-                                         float (&acc)[2][4]) {
-  const int g = lane >> 2, q = lane & 3;
+// acc[..][tile] += (dequantised rows) . (the tokens' step at `xs`, the lane's piece
+// of its token; absent tokens are zero).  Two sums per tile: an MMA waits some 50
+// cycles for the one before it in its sum.
+__device__ __forceinline__ void mma_step(const StepA& a, int half, const uint8_t* xs, bool have,
+                                         float (&acc)[2][2][4]) {
   const uint32_t sw[4] = {a.s.x, a.s.y, a.s.z, a.s.w};
-  uint32_t s0[4], s1[4];
+  uint32_t code[4][4], s0[4], s1[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
+    code[i][0] = a.c[i].x; code[i][1] = a.c[i].y; code[i][2] = a.c[i].z; code[i][3] = a.c[i].w;
     uint32_t h;
     const uint16_t two = (uint16_t)(sw[i] >> half);
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(two));
     s0[i] = __byte_perm(h, h, 0x1010);
     s1[i] = __byte_perm(h, h, 0x3232);
   }
-  float c[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
     uint4 b = make_uint4(0u, 0u, 0u, 0u);
-    if (have) b = *reinterpret_cast<const uint4*>(xs + g * kTokStride + w * 64 + q * 16);
+    if (have) b = *reinterpret_cast<const uint4*>(xs + w * 64);
     uint32_t f[4][4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t word = w == 0 ? a.c[i].x : w == 1 ? a.c[i].y : w == 2 ? a.c[i].z : a.c[i].w;
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int p = 0; p < 4; ++p) f[i][p] = mul_f16x2(e2m1x2_to_f16x2(word, p), w < 2 ? s0[i] : s1[i]);
-    }
+      for (int p = 0; p < 4; ++p)
+        f[i][p] = mul_f16x2(e2m1x2_to_f16x2(code[i][w], p), w < 2 ? s0[i] : s1[i]);
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
-      mma_f16(c[t], f[2 * t][0], f[2 * t + 1][0], f[2 * t][1], f[2 * t + 1][1], b.x, b.y);
-      mma_f16(c[t], f[2 * t][2], f[2 * t + 1][2], f[2 * t][3], f[2 * t + 1][3], b.z, b.w);
+      mma_f16(acc[0][t], f[2 * t][0], f[2 * t + 1][0], f[2 * t][1], f[2 * t + 1][1], b.x, b.y);
+      mma_f16(acc[1][t], f[2 * t][2], f[2 * t + 1][2], f[2 * t][3], f[2 * t + 1][3], b.z, b.w);
     }
-  }
-  const float i0 = inv[2 * q], i1 = inv[2 * q + 1];
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    acc[t][0] += c[t][0] * i0;
-    acc[t][1] += c[t][1] * i1;
-    acc[t][2] += c[t][2] * i0;
-    acc[t][3] += c[t][3] * i1;
   }
 }
 
@@ -173,292 +168,684 @@ struct DecodeArgs {
   const int32_t* ids;         // [T, k]
   const float* scores;        // [T, k]
   int T, k, d, I, E;
-  int slots;                  // gridDim.y: T*k (slot = pair) or E (slot = expert)
+  int cols;                   // tokens per pass
   float clamp;
   const uint8_t *codes, *sf;  // this launch's matrix
   const float* w_scale;
   float* h;                   // [T*k, I]
   float* ys;                  // [T*k, d]
   uint8_t* keep;              // [T*k] 1: the pair counts (valid id, first in its row)
-  int* arrived;               // [d / 32], zero between calls
+  int* arrived;               // [d / 32], zero between calls; NULL: k_decode_combine joins
   uint16_t* y;                // [T, d]
   DevError* err;
 };
 
-struct Shared {
-  int list[kDecodeMaxTokens]; // pairs t*k+j of the CTA's expert
-  int count, first, last;
-  __align__(16) uint8_t xs[kMaxWarps][kCols * kTokStride];
-  float inv[kMaxWarps][kCols];
-  float red[kMaxWarps][32][9];
+// A unit is 32 rows of one chosen expert's matrix (a row set) for one pass of its
+// tokens (up to a.cols of them); the units are numbered pass by pass, expert by
+// expert, and every CTA takes a run of them.  Both are found anew by every CTA from
+// the ids alone: a thread per expert counts, and one scan numbers.
+struct Plan {
+  int2 warp_sums[kThreads / 32];
+  int count[kThreads];        // tokens by expert (E <= 256), later the end of its pairs
+  int start[kThreads];        // its first pair in the list
+  int expert, first, tokens;  // the pass that find_pass() looked for
 };
 
-// The expert of a slot; -1: none.  With a slot per pair the pair's own id.
-__device__ __forceinline__ int slot_expert(const DecodeArgs& a, int slot) {
-  if (a.slots != a.T * a.k) return slot;
-  const int e = a.ids[slot];
-  return e >= 0 && e < a.E ? e : -1;
-}
+// What thread e < 256 keeps of expert e.
+struct Mine {
+  int passes, before;         // its passes, and those of the experts ahead
+  int start, tokens;          // its pairs in the list
+};
+
+// Bytes of a token's row of K fp16 elements in shared memory: 64 more than the row,
+// so that the eight lanes of a quarter-warp load from different banks.
+__host__ __device__ constexpr int row_bytes(int K) { return 2 * K + 64; }
+// Bytes of the pairs' list and of its unordered form.
+__host__ __device__ constexpr int list_bytes(int pairs) { return (4 * pairs + 127) / 128 * 128; }
 
 // True for an id that repeats an earlier one of its row.
 __device__ __forceinline__ bool repeated(const DecodeArgs& a, int p) {
-  const int e = a.ids[p], row = p / a.k * a.k;
-  for (int i = row; i < p; ++i)
-    if (a.ids[i] == e) return true;
-  return false;
+  const int e = a.ids[p];
+  bool same = false;
+#pragma unroll 8
+  for (int i = p / a.k * a.k; i < p; ++i) same |= a.ids[i] == e;     // independent loads
+  return same;
 }
 
-// The pairs that chose expert e, into s.list; false: none, or (a slot per pair)
-// another slot has them.  All threads call it.
-__device__ __forceinline__ bool collect(const DecodeArgs& a, Shared& s, int slot, int e) {
-  if (threadIdx.x == 0) {
-    s.count = 0;
-    s.first = INT_MAX;
+// Counts and numbers; returns the number of passes.  All threads call it; the list is
+// complete after fill_list() and a __syncthreads().
+__device__ __forceinline__ int make_plan(const DecodeArgs& a, Plan& s, Mine& m) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
+    const int e = a.ids[p];
+    if (e >= 0 && e < a.E) atomicAdd(&s.count[e], 1);
   }
   __syncthreads();
-  const int n = a.T * a.k;
-  if (e >= 0)
-    for (int p = threadIdx.x; p < n; p += blockDim.x)
-      if (a.ids[p] == e && !repeated(a, p)) {
-        s.list[atomicAdd(&s.count, 1)] = p;
-        atomicMin(&s.first, p);
-      }
+  m = Mine{0, 0, 0, 0};
+  int2 sum = make_int2(0, 0);                        // inclusive over the warp's experts
+  if (threadIdx.x < kThreads) {
+    m.tokens = s.count[threadIdx.x];
+    m.passes = (m.tokens + a.cols - 1) / a.cols;
+    sum = make_int2(m.passes, m.tokens);
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const int x = __shfl_up_sync(0xffffffffu, sum.x, o), y = __shfl_up_sync(0xffffffffu, sum.y, o);
+      if (lane >= o) sum.x += x, sum.y += y;
+    }
+    if (lane == 31) s.warp_sums[warp] = sum;
+  }
   __syncthreads();
-  return s.count > 0 && (a.slots != n || s.first == slot);
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    const int2 v = s.warp_sums[w];
+    if (w < warp) sum.x += v.x, sum.y += v.y;
+    all += v.x;
+  }
+  if (threadIdx.x < kThreads) {
+    m.before = sum.x - m.passes;
+    m.start = sum.y - m.tokens;
+    s.count[threadIdx.x] = s.start[threadIdx.x] = m.start;
+  }
+  return all;
 }
 
-// Adds the warps' accumulators in order; thread v < 256 returns element
-// (row i, g; column c) = (v / 64, v / 8 % 8, v % 8).
-__device__ __forceinline__ float reduce_warps(Shared& s, const float (&acc)[2][4], int warp,
-                                              int lane, int nw, int v) {
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) s.red[warp][lane][t * 4 + j] = acc[t][j];
-  __syncthreads();
-  float r = 0.f;
-  if (v < 256) {
-    const int i = v >> 6, g = v >> 3 & 7, c = v & 7;
-    const int src = g * 4 + (c >> 1), at = (i >> 1) * 4 + (i & 1) * 2 + (c & 1);
-    for (int w = 0; w < nw; ++w) r += s.red[w][src][at];
+// The pairs t*k+j by expert, ascending, into `list` (complete after the next
+// __syncthreads(); `raw`: as long): every CTA has to come to the same passes.  A pair
+// that repeats an id of its row is computed too, and dropped where the tokens'
+// experts are added.  All threads call it.
+__device__ __forceinline__ void fill_list(const DecodeArgs& a, Plan& s, uint16_t* list,
+                                          uint16_t* raw) {
+  for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
+    const int e = a.ids[p];
+    if (e >= 0 && e < a.E) raw[atomicAdd(&s.count[e], 1)] = (uint16_t)p;
   }
+  __syncthreads();
+  for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
+    const int e = a.ids[p];
+    if (e < 0 || e >= a.E) continue;
+    int at = s.start[e];
+    const int first = at, end = s.count[e];
+    for (int i = first; i < end; ++i) at += raw[i] < p;
+    list[at] = (uint16_t)p;
+  }
+}
+
+// The expert of pass `pass`, its first pair in the list and its tokens, for all
+// threads after a __syncthreads().
+__device__ __forceinline__ void find_pass(const DecodeArgs& a, Plan& s, const Mine& m, int pass) {
+  const int n = pass - m.before;
+  if (n >= 0 && n < m.passes) {
+    s.expert = threadIdx.x;
+    s.first = m.start + n * a.cols;
+    s.tokens = min(a.cols, m.tokens - n * a.cols);
+  }
+}
+
+// This CTA's run of `total` units.
+__device__ __forceinline__ int2 run_of(int total) {
+  const unsigned n = gridDim.x, b = blockIdx.x, q = (unsigned)total / n, r = total - q * n;
+  const int from = (int)(b * q + min(b, r));
+  return make_int2(from, from + (int)(q + (b < r ? 1u : 0u)));
+}
+
+// Eight consecutive activations as they are in memory.
+struct PieceX { uint4 v; };
+struct PieceH { float4 v[2]; };
+__device__ __forceinline__ void load_piece(const uint16_t* p, PieceX& r) {
+  r.v = *reinterpret_cast<const uint4*>(p);
+}
+__device__ __forceinline__ void load_piece(const float* p, PieceH& r) {
+  r.v[0] = __ldcg(reinterpret_cast<const float4*>(p));
+  r.v[1] = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+}
+__device__ __forceinline__ void unpack(const PieceX& r, float (&f)[8]) {
+  const uint32_t u[4] = {r.v.x, r.v.y, r.v.z, r.v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(u[i] << 16);
+    f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ void unpack(const PieceH& r, float (&f)[8]) {
+  f[0] = r.v[0].x; f[1] = r.v[0].y; f[2] = r.v[0].z; f[3] = r.v[0].w;
+  f[4] = r.v[1].x; f[5] = r.v[1].y; f[6] = r.v[1].z; f[7] = r.v[1].w;
+}
+
+template <bool W13>
+struct PieceOf;
+template <>
+struct PieceOf<true> {
+  using type = PieceX;
+  static __device__ const uint16_t* row(const DecodeArgs& a, int pair) {
+    return a.x + (long long)(pair / a.k) * a.d;
+  }
+};
+template <>
+struct PieceOf<false> {
+  using type = PieceH;
+  static __device__ const float* row(const DecodeArgs& a, int pair) {
+    return a.h + (long long)pair * a.I;
+  }
+};
+
+// The staged tokens of a pass.
+struct Tokens {
+  unsigned amax[kCols];       // of a token's row, as bits
+  float inv[kCols];           // inverse of its scale
+  int pair[kCols];
+  float score[kCols];
+};
+
+// The rows of the pass's `nt` tokens as fp16 scaled by a power of two per token, each
+// step's 16 pieces of 8 elements in the order of mma_step: piece 4q+w at 64 w + 16 q.
+// Called by all threads; a group of eight warps stages one pass (nt = 0: none), a
+// token taking as many warps as there are for it and a lane keeping up to KEPT of its
+// pieces between the search for the largest element and the conversion.  The rows are
+// complete after the next __syncthreads().
+template <bool W13, int KEPT>
+__device__ __forceinline__ void stage_tokens(const DecodeArgs& a, Tokens& s, uint8_t* xs,
+                                             const uint16_t* list, int nt) {
+  using Piece = typename PieceOf<W13>::type;
+  const int warp = threadIdx.x >> 5 & 7, lane = threadIdx.x & 31, K = W13 ? a.d : a.I;
+  const int share = nt > 4 ? 1 : nt > 2 ? 2 : nt > 1 ? 4 : 8;    // warps of a token
+  const int c = warp / share, per = K / 8, hop = 32 * share;
+  const int first = lane + 32 * (warp - c * share);
+  if ((threadIdx.x & 255) < kCols) s.amax[threadIdx.x & 255] = 0u;
+  __syncthreads();
+  const bool mine = c < nt;
+  const int pair = mine ? list[c] : 0;
+  const auto* src = PieceOf<W13>::row(a, pair);
+  Piece kept[KEPT];
+  float f[8];
+  if (mine) {
+    float m = 0.f;
+    auto largest = [&](const Piece& p) {
+      unpack(p, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) m = fmaxf(m, fabsf(f[e]));
+    };
+#pragma unroll
+    for (int n = 0; n < KEPT; ++n)
+      if (first + n * hop < per) load_piece(src + (first + n * hop) * 8, kept[n]);
+    if (first == 0) {
+      s.pair[c] = pair;
+      if (!W13) s.score[c] = a.scores[pair];
+    }
+#pragma unroll
+    for (int n = 0; n < KEPT; ++n)
+      if (first + n * hop < per) largest(kept[n]);
+    for (int i = first + KEPT * hop; i < per; i += hop) {
+      Piece p;
+      load_piece(src + i * 8, p);
+      largest(p);
+    }
+    const unsigned top = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+    if (lane == 0) atomicMax(&s.amax[c], top);
+  }
+  __syncthreads();
+  if (!mine) return;
+  float mul, inv;
+  pow2_scale(__uint_as_float(s.amax[c]), mul, inv);
+  if (first == 0) s.inv[c] = inv;
+  uint8_t* const to = xs + c * row_bytes(K);
+  auto convert = [&](const Piece& p, int i) {
+    unpack(p, f);
+    *reinterpret_cast<uint4*>(to + (i >> 4) * 256 + (i & 3) * 64 + (i >> 2 & 3) * 16) =
+        make_uint4(pack_f16x2(f[0] * mul, f[1] * mul), pack_f16x2(f[2] * mul, f[3] * mul),
+                   pack_f16x2(f[4] * mul, f[5] * mul), pack_f16x2(f[6] * mul, f[7] * mul));
+  };
+#pragma unroll
+  for (int n = 0; n < KEPT; ++n)
+    if (first + n * hop < per) convert(kept[n], first + n * hop);
+  for (int i = first + KEPT * hop; i < per; i += hop) {
+    Piece p;
+    load_piece(src + i * 8, p);
+    convert(p, i);
+  }
+}
+
+// Where the lane's rows of unit column `sub` of expert e are.
+template <bool W13>
+__device__ __forceinline__ Rows rows_of(const DecodeArgs& a, int e, int sub) {
+  const int lane = threadIdx.x & 31, g = lane >> 2, q = lane & 3;
+  const int K = W13 ? a.d : a.I, blk = sub >> 2, at = (sub & 3) * 8 + g;
+  const long long row = W13 ? (long long)e * 2 * a.I + blk * 64 + at : (long long)e * a.d + blk * 128 + at;
+  const long long block = W13 ? (long long)e * (a.I / 64) + blk : (long long)e * (a.d / 128) + blk;
+  Rows r;
+  r.code = a.codes + row * (K / 2) + q * 16;
+  r.scale = a.sf + (block * (K / 64) + (q >> 1)) * 512 + at * 16;
   return r;
 }
 
-// W13 x, SwiGLU.  blockIdx.x: 16 columns of h (set s of a 64-column block).
-__global__ void __launch_bounds__(256, 3) k_decode_w13(const DecodeArgs a) {
-  __shared__ Shared s;
-  pdl_wait();
-  pdl_trigger();          // the W2 kernel may start: it reads weights and ids before it waits
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  if (blockIdx.x == 0 && blockIdx.y == 0) {
-    for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
-      const int e = a.ids[p];
-      const bool ok = e >= 0 && e < a.E && !repeated(a, p);
-      a.keep[p] = ok;
-      if (!ok) {
-        atomicCAS(&a.err->code, 0, MOE_ERR_BAD_IDS);
-        atomicMin(&a.err->first_bad, p);
-      }
-    }
+// First of the eight output columns of row i of a unit (rows g = 0..7 follow).
+template <bool W13>
+__device__ __forceinline__ int out_col(int sub, int i) {
+  return W13 ? (sub >> 2) * 64 + i * 32 + (sub & 3) * 8 : (sub >> 2) * 128 + i * 32 + (sub & 3) * 8;
+}
+
+__device__ __forceinline__ float swiglu(const DecodeArgs& a, float G, float U) {
+  if (a.clamp > 0.f) {
+    G = fminf(fmaxf(G, -a.clamp), a.clamp);
+    U = fminf(fmaxf(U, -a.clamp), a.clamp);
   }
-  const int slot = blockIdx.y, e = slot_expert(a, slot);
-  const int blk = blockIdx.x >> 2, set = blockIdx.x & 3;
-  const int steps = a.d / kStep;
-  Rows r;
-  {
-    const long long row = (long long)(e < 0 ? 0 : e) * 2 * a.I + blk * 64 + set * 8 + g;
-    const uint8_t* base = a.codes + q * 16;
-    const long long ld = a.d / 2;
-    r.code[0] = base + row * ld;
-    r.code[1] = base + (row + 32) * ld;
-    r.code[2] = base + (row + a.I) * ld;
-    r.code[3] = base + (row + a.I + 32) * ld;
-    r.scale = a.sf + (((long long)(e < 0 ? 0 : e) * (a.I / 64) + blk) * (a.d / 64) + (q >> 1)) * 512 +
-              (set * 8 + g) * 16;
-    r.half = (q & 1) * 16;
-  }
-  StepA w0;
-  if (warp < steps && e >= 0) load_step(r, warp, w0);
-  if (!collect(a, s, slot, e)) return;
-  const float alpha = a.w_scale[e];
-  const int count = s.count;
-  for (int t0 = 0; t0 < count; t0 += kCols) {
-    const int nt = min(kCols, count - t0);
-    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int step = warp; step < steps; step += nw) {
-      StepA cur;
-      if (step == warp && t0 == 0) cur = w0;
-      else load_step(r, step, cur);
-      // the tokens' 128 elements: 16 lanes a token, 8 elements a lane
-      __syncwarp();
-      if (lane < kCols) s.inv[warp][lane] = 0.f;
-      __syncwarp();
-      for (int c = lane >> 4; c < nt; c += 2) {
-        const int piece = lane & 15;
-        const uint4 v = *reinterpret_cast<const uint4*>(
-            a.x + (long long)(s.list[t0 + c] / a.k) * a.d + step * kStep + piece * 8);
-        const uint32_t u[4] = {v.x, v.y, v.z, v.w};
-        float f[8], amax = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          f[2 * i] = __uint_as_float(u[i] << 16);
-          f[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
-          amax = fmaxf(amax, fmaxf(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
-        }
-        const unsigned half = 0xFFFFu << (lane & 16);
-#pragma unroll
-        for (int o = 8; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(half, amax, o));
-        float mul, inv;
-        pow2_scale(amax, mul, inv);
-        uint4 p;
-        p.x = pack_f16x2(f[0] * mul, f[1] * mul);
-        p.y = pack_f16x2(f[2] * mul, f[3] * mul);
-        p.z = pack_f16x2(f[4] * mul, f[5] * mul);
-        p.w = pack_f16x2(f[6] * mul, f[7] * mul);
-        *reinterpret_cast<uint4*>(&s.xs[warp][c * kTokStride + (piece & 3) * 64 + (piece >> 2) * 16]) = p;
-        if (piece == 0) s.inv[warp][c] = inv;
-      }
-      __syncwarp();
-      mma_step(cur, r.half, s.xs[warp], s.inv[warp], lane, g < nt, acc);
-    }
-    if (t0) __syncthreads();            // the previous pass's sums have been read
-    // gate rows are i = 0, 1, up rows i = 2, 3 of the same column
-    const float v = reduce_warps(s, acc, warp, lane, nw, threadIdx.x);
-    __shared__ float up[128];
-    const int tid = threadIdx.x;
-    if (tid >= 128 && tid < 256) up[tid - 128] = v;
-    __syncthreads();
-    if (tid < 128) {
-      const int i = tid >> 6, col = blk * 64 + i * 32 + set * 8 + (tid >> 3 & 7), c = tid & 7;
-      if (c < nt) {
-        float G = alpha * v, U = alpha * up[tid];
-        if (a.clamp > 0.f) {
-          G = fminf(fmaxf(G, -a.clamp), a.clamp);
-          U = fminf(fmaxf(U, -a.clamp), a.clamp);
-        }
-        a.h[(long long)s.list[t0 + c] * a.I + col] = G / (1.f + __expf(-G)) * U;
-      }
+  return __fdividef(G, 1.f + __expf(-G)) * U;
+}
+
+// Which pairs count, and the first bad id into the error word (one CTA calls it).
+__device__ __forceinline__ void check_ids(const DecodeArgs& a) {
+  for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
+    const int e = a.ids[p];
+    const bool ok = e >= 0 && e < a.E && !repeated(a, p);
+    a.keep[p] = ok;
+    if (!ok) {
+      atomicCAS(&a.err->code, 0, MOE_ERR_BAD_IDS);
+      atomicMin(&a.err->first_bad, p);
     }
   }
 }
 
-// W2 h x score; the CTA that is last of its 32 rows adds the tokens' experts.
-__global__ void __launch_bounds__(256, 3) k_decode_w2(const DecodeArgs a) {
-  __shared__ Shared s;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
-  const int g = lane >> 2, q = lane & 3;
-  const int slot = blockIdx.y, e = slot_expert(a, slot);
-  const int blk = blockIdx.x >> 2, set = blockIdx.x & 3;
-  const int steps = a.I / kStep;
-  Rows r;
-  {
-    const long long row = (long long)(e < 0 ? 0 : e) * a.d + blk * 128 + set * 8 + g;
-    const long long ld = a.I / 2;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) r.code[i] = a.codes + q * 16 + (row + 32 * i) * ld;
-    r.scale = a.sf + (((long long)(e < 0 ? 0 : e) * (a.d / 128) + blk) * (a.I / 64) + (q >> 1)) * 512 +
-              (set * 8 + g) * 16;
-    r.half = (q & 1) * 16;
-  }
-  // weights, ids and scales were there before the W13 kernel started
-  StepA w0;
-  if (warp < steps && e >= 0) load_step(r, warp, w0);
-  const bool mine = collect(a, s, slot, e);
-  const float alpha = mine ? a.w_scale[e] : 0.f;
-  pdl_wait();                            // h is complete
-  pdl_trigger();
-  const int count = mine ? s.count : 0;
-  for (int t0 = 0; t0 < count; t0 += kCols) {
-    const int nt = min(kCols, count - t0);
-    float acc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
-    for (int step = warp; step < steps; step += nw) {
-      StepA cur;
-      if (step == warp && t0 == 0) cur = w0;
-      else load_step(r, step, cur);
-      __syncwarp();
-      if (lane < kCols) s.inv[warp][lane] = 0.f;
-      __syncwarp();
-      // the tokens' 128 elements of h: a warp a token, 4 elements a lane
-      for (int c = 0; c < nt; ++c) {
-        const float4 v = *reinterpret_cast<const float4*>(
-            a.h + (long long)s.list[t0 + c] * a.I + step * kStep + lane * 4);
-        float amax = fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w)));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-        float mul, inv;
-        pow2_scale(amax, mul, inv);
-        const uint2 p = make_uint2(pack_f16x2(v.x * mul, v.y * mul), pack_f16x2(v.z * mul, v.w * mul));
-        *reinterpret_cast<uint2*>(&s.xs[warp][c * kTokStride + (lane >> 1 & 3) * 64 +
-                                              (lane >> 3) * 16 + (lane & 1) * 8]) = p;
-        if (lane == 0) s.inv[warp][c] = inv;
-      }
-      __syncwarp();
-      mma_step(cur, r.half, s.xs[warp], s.inv[warp], lane, g < nt, acc);
-    }
-    if (t0) __syncthreads();
-    for (int v0 = threadIdx.x; v0 < 256; v0 += blockDim.x) {
-      float v;
-      if (v0 == (int)threadIdx.x) {
-        v = reduce_warps(s, acc, warp, lane, nw, v0);
-      } else {
-        const int i = v0 >> 6, gg = v0 >> 3 & 7, c = v0 & 7;
-        v = 0.f;
-        for (int w = 0; w < nw; ++w)
-          v += s.red[w][gg * 4 + (c >> 1)][(i >> 1) * 4 + (i & 1) * 2 + (c & 1)];
-      }
-      const int i = v0 >> 6, c = v0 & 7;
-      if (c < nt) {
-        const int p = s.list[t0 + c];
-        a.ys[(long long)p * a.d + blk * 128 + i * 32 + set * 8 + (v0 >> 3 & 7)] =
-            a.scores[p] * (alpha * v);
-      }
-    }
-  }
-  // arrival: the last CTA of these rows sees every other one's ys
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    __threadfence();
-    s.last = atomicAdd(&a.arrived[blockIdx.x], 1) == a.slots - 1;
-    __threadfence();
-  }
-  __syncthreads();
-  if (!s.last) return;
+// y[t] for the 32 rows of unit column `sub`, from every pair's ys.
+__device__ __forceinline__ void combine_rows(const DecodeArgs& a, int sub) {
   for (int v = threadIdx.x; v < a.T * 32; v += blockDim.x) {
-    const int t = v >> 5, row = blk * 128 + (v >> 3 & 3) * 32 + set * 8 + (v & 7);
+    const int t = v >> 5, row = out_col<false>(sub, v >> 3 & 3) + (v & 7);
     float sum = 0.f;
-    for (int j = 0; j < a.k; ++j) {
+#pragma unroll 8
+    for (int j = 0; j < a.k; ++j) {              // a dropped pair's ys is old: not added
       const int p = t * a.k + j;
-      if (a.keep[p]) sum += __ldcg(a.ys + (long long)p * a.d + row);
+      const float w = __ldcg(a.ys + (long long)p * a.d + row);
+      sum += a.keep[p] ? w : 0.f;
     }
     a.y[(long long)t * a.d + row] = f2bf(sum);
   }
-  if (threadIdx.x == 0) a.arrived[blockIdx.x] = 0;
 }
 
-int warps_for(int K) {
-  const int steps = K / kStep;
-  return steps < kMaxWarps ? steps : kMaxWarps;
+// ---- few units: K split over the warps ------------------------------------------
+//
+// A CTA of eight warps takes one unit at a time, a warp every eighth step, the sums
+// joined in shared memory: a unit is over after d / 1024 steps, and one token's eight
+// experts fill the GPU.
+template <bool W13>
+__global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];       // the pairs' list, the tokens' rows
+  __shared__ Plan s;
+  __shared__ Tokens tok;
+  __shared__ float red[2][kWarps][32][9];
+  __shared__ int last;
+  uint16_t* const list = reinterpret_cast<uint16_t*>(smem);
+  uint8_t* const xs = smem + list_bytes(a.T * a.k);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int K = W13 ? a.d : a.I, per = W13 ? a.I / 16 : a.d / 32;      // units of a pass
+  const int steps = K / kStep, half = (q & 1) * 16;
+  const long long gap = 32LL * (K / 2), far = (long long)(W13 ? a.I : 64) * (K / 2);
+  s.count[threadIdx.x] = 0;
+  __syncthreads();
+  if (W13) {
+    pdl_wait();
+    pdl_trigger();        // the W2 kernel may start: before it waits it reads what was
+  }                       // there before this one: weights and ids
+  Mine m;
+  const int passes = make_plan(a, s, m);
+  int2 run = run_of(passes * per);
+  int pass = run.x / per, sub = run.x - pass * per;
+  if (run.x < run.y) find_pass(a, s, m, pass);
+  __syncthreads();
+  StepA w;
+  if (run.x < run.y && warp < steps) load_step(rows_of<W13>(a, s.expert, sub), gap, far, warp, w);
+  fill_list(a, s, list, list + a.T * a.k);
+  if (!W13) {
+    pdl_wait();           // h is complete
+    pdl_trigger();
+  }
+  __syncthreads();
+  int flip = 0, n = run.y - run.x;
+  while (n > 0) {
+    const int e = s.expert, nt = s.tokens, stop = min(per, sub + n);
+    const float alpha = a.w_scale[e];
+    stage_tokens<W13, W13 ? 4 : 2>(a, tok, xs, list + s.first, nt);
+    __syncthreads();
+    n -= stop - sub;
+    for (; sub < stop; ++sub) {
+      float acc[2][2][4] = {};
+      const Rows r = rows_of<W13>(a, e, sub);
+      const uint8_t* lane_xs = xs + g * row_bytes(K) + q * 16;
+      for (int step = warp; step < steps; step += kWarps) {
+        StepA cur = w;
+        if (step + kWarps < steps) load_step(r, gap, far, step + kWarps, w);
+        else if (sub + 1 < stop) load_step(rows_of<W13>(a, e, sub + 1), gap, far, warp, w);
+        mma_step(cur, half, lane_xs + step * (2 * kStep), g < nt, acc);
+      }
+      float (*sums)[32][9] = red[flip];
+      flip ^= 1;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[warp][lane][t * 4 + j] = acc[0][t][j] + acc[1][t][j];
+      __syncthreads();
+      // element (row i of four, g; column c), the warps added in order
+      auto reduced = [&](int i, int gg, int c) {
+        float v = 0.f;
+#pragma unroll
+        for (int x = 0; x < kWarps; ++x)
+          v += sums[x][gg * 4 + (c >> 1)][(i >> 1) * 4 + (i & 1) * 2 + (c & 1)];
+        return v;
+      };
+      const int gg = threadIdx.x & 7, c = threadIdx.x >> 3 & 7, i = threadIdx.x >> 6;
+      if (c < nt && (!W13 || i < 2)) {
+        const float f = alpha * tok.inv[c];
+        if (W13)
+          a.h[(long long)tok.pair[c] * a.I + out_col<true>(sub, i) + gg] =
+              swiglu(a, f * reduced(i, gg, c), f * reduced(i + 2, gg, c));
+        else
+          a.ys[(long long)tok.pair[c] * a.d + out_col<false>(sub, i) + gg] =
+              tok.score[c] * (f * reduced(i, gg, c));
+      }
+      if (!W13 && a.arrived) {
+        // the CTA that is last of these rows sees every other pass's ys
+        __syncthreads();
+        if (threadIdx.x == 0) {
+          __threadfence();
+          last = atomicAdd(&a.arrived[sub], 1) == passes - 1;
+          __threadfence();
+        }
+        __syncthreads();
+        if (last) {
+          combine_rows(a, sub);
+          if (threadIdx.x == 0) a.arrived[sub] = 0;
+        }
+      }
+    }
+    if (n > 0) {
+      pass += 1;
+      sub = 0;
+      __syncthreads();                   // the pass has been read
+      find_pass(a, s, m, pass);
+      __syncthreads();
+      if (warp < steps) load_step(rows_of<W13>(a, s.expert, 0), gap, far, warp, w);
+    }
+  }
+  if (W13 && blockIdx.x == 0) check_ids(a);
+  if (!W13 && a.arrived && passes == 0)  // nothing but bad ids
+    for (int v = blockIdx.x * kThreads + threadIdx.x; v < a.T * a.d; v += gridDim.x * kThreads)
+      a.y[v] = 0;
+}
+
+// ---- many units: a unit a warp ----------------------------------------------------
+//
+// One CTA of 16 warps an SM.  It stages the tokens of two passes of its run at once;
+// its warps then take the run's units one by one and stream them on their own: each
+// lane copies its own pieces of the next steps (and of the next unit's first) into
+// its own slots of a ring with cp.async and reads them back itself, so that nothing
+// in the stream waits for another warp.  Loads of 64 contiguous bytes a row and step
+// reach 5.8 TB/s here with three steps in flight (6.5 with 512).
+constexpr int kStreamWarps = 16;
+constexpr int kStages = 3;
+constexpr int kStageBytes = kStreamWarps * 5 * 512;        // five 16-byte pieces a lane
+constexpr int kRingBytes = kStages * kStageBytes;
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <bool W13>
+__global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t smem[];       // ring, list, two passes' rows
+  __shared__ Plan s;
+  __shared__ Tokens tok[2];
+  __shared__ int two[2][3];                             // expert, first pair, tokens
+  __shared__ int taken;
+  uint16_t* const list = reinterpret_cast<uint16_t*>(smem + kRingBytes);
+  uint8_t* const xs = smem + kRingBytes + list_bytes(a.T * a.k);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int g = lane >> 2, q = lane & 3;
+  const int K = W13 ? a.d : a.I, per = W13 ? a.I / 16 : a.d / 32;
+  const int steps = K / kStep, half = (q & 1) * 16;
+  const long long gap = 32LL * (K / 2), far = (long long)(W13 ? a.I : 64) * (K / 2);
+  const uint8_t* const slot = smem + warp * (5 * 512) + lane * 16;
+  if (threadIdx.x < kThreads) s.count[threadIdx.x] = 0;
+  __syncthreads();
+  if (W13) {
+    pdl_wait();
+    pdl_trigger();        // as in k_decode_split
+  }
+  Mine m;
+  const int passes = make_plan(a, s, m);
+  int2 run = run_of(passes * per);
+  int pass = run.x / per, sub0 = run.x - pass * per, n = run.y - run.x;
+  bool listed = false;
+  while (n > 0) {
+    // two passes: unit columns [sub0, per) of the first, [0, n - ..) of the second
+    __syncthreads();
+    for (int i = 0; i < 2; ++i) {
+      const int k = pass + i - m.before;
+      if (k >= 0 && k < m.passes) {
+        two[i][0] = threadIdx.x;
+        two[i][1] = m.start + k * a.cols;
+        two[i][2] = min(a.cols, m.tokens - k * a.cols);
+      }
+    }
+    if (threadIdx.x == 0) taken = kStreamWarps;
+    __syncthreads();
+    const int n0 = min(n, per - sub0), n1 = min(n - n0, per), here = n0 + n1;
+    auto rows = [&](int v) {
+      return v < n0 ? rows_of<W13>(a, two[0][0], sub0 + v) : rows_of<W13>(a, two[1][0], v - n0);
+    };
+    // The copies are kStages - 1 steps ahead: step `to_step` of the rows r comes next,
+    // of the warp's unit or (in_next) of the one it takes after that.
+    int unit = warp, next = here, to_step = 0, to_stage = 0;
+    bool more = unit < here, in_next = false;
+    Rows r{nullptr, nullptr};
+    if (more) r = rows(unit);
+    auto fetch = [&]() {
+      if (more) {
+        const uint32_t at = smem_u32(slot) + to_stage * kStageBytes;
+        const uint8_t* p = r.code + to_step * (kStep / 2);
+        cp_async16(at, p);
+        cp_async16(at + 512, p + gap);
+        cp_async16(at + 1024, p + far);
+        cp_async16(at + 1536, p + far + gap);
+        cp_async16(at + 2048, r.scale + to_step * 1024);
+        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
+        if (++to_step == steps) {
+          to_step = 0;
+          more = !in_next && next < here;
+          in_next = true;
+          if (more) r = rows(next);
+        }
+      }
+      cp_async_commit();
+    };
+    auto take = [&]() {
+      int v = 0;
+      if (lane == 0) v = atomicAdd(&taken, 1);
+      return __shfl_sync(0xffffffffu, v, 0);
+    };
+    if (more) next = take();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch();
+    if (!listed) {
+      fill_list(a, s, list, list + a.T * a.k);
+      if (!W13) {
+        pdl_wait();                      // h is complete
+        pdl_trigger();
+      }
+      listed = true;
+      __syncthreads();
+    }
+    {
+      const int i = warp >> 3;
+      stage_tokens<W13, W13 ? 8 : 3>(a, tok[i], xs + i * a.cols * row_bytes(K), list + two[i][1],
+                                     i == 0 || n1 > 0 ? two[i][2] : 0);
+    }
+    __syncthreads();
+    int stage = 0;
+    while (unit < here) {
+      const int i = unit < n0 ? 0 : 1, e = two[i][0], nt = two[i][2];
+      const int sub = i ? unit - n0 : sub0 + unit;
+      const float alpha = a.w_scale[e];
+      const uint8_t* lane_xs = xs + (i * a.cols + g) * row_bytes(K) + q * 16;
+      float acc[2][2][4] = {};
+      for (int step = 0; step < steps; ++step) {
+        cp_async_wait<kStages - 2>();
+        StepA w;
+        const uint8_t* at = slot + stage * kStageBytes;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w.c[j] = *reinterpret_cast<const uint4*>(at + j * 512);
+        w.s = *reinterpret_cast<const uint4*>(at + 2048);
+        stage = stage + 1 == kStages ? 0 : stage + 1;
+        fetch();                         // into the stage read one step ago
+        mma_step(w, half, lane_xs + step * (2 * kStep), g < nt, acc);
+      }
+#pragma unroll
+      for (int c2 = 0; c2 < 2; ++c2) {
+        const int c = 2 * q + c2;
+        if (c >= nt) continue;
+        const float f = alpha * tok[i].inv[c];
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] = f * (acc[0][j >> 1][(j & 1) * 2 + c2] + acc[1][j >> 1][(j & 1) * 2 + c2]);
+        if (W13) {
+          float* h = a.h + (long long)tok[i].pair[c] * a.I + g;
+          h[out_col<true>(sub, 0)] = swiglu(a, v[0], v[2]);
+          h[out_col<true>(sub, 1)] = swiglu(a, v[1], v[3]);
+        } else {
+          float* ys = a.ys + (long long)tok[i].pair[c] * a.d + g;
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ys[out_col<false>(sub, j)] = tok[i].score[c] * v[j];
+        }
+      }
+      unit = next;                       // its first steps are on their way
+      if (unit < here) {
+        next = take();
+        in_next = !more;                 // all of them are (a row of kStages - 1 steps)
+        if (in_next && next < here) {
+          more = true;
+          r = rows(next);
+        }
+      }
+    }
+    cp_async_wait<0>();
+    n -= here;                           // more to do: both passes are over
+    pass += 2;
+    sub0 = 0;
+  }
+  if (W13 && blockIdx.x == 0) check_ids(a);
+  if (!W13 && !listed) {
+    pdl_wait();
+    pdl_trigger();
+  }
+}
+
+// y[t] = the tokens' experts in j order, four columns a thread.
+__global__ void __launch_bounds__(kThreads) k_decode_combine(const DecodeArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const int per = a.d / 4;
+  const long long v = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (v >= (long long)a.T * per) return;
+  const int t = (int)(v / per), c = (int)(v - (long long)t * per) * 4;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int j = 0; j < a.k; ++j) {
+    const int p = t * a.k + j;
+    const bool on = a.keep[p] != 0;              // a dropped pair's ys is old: not added
+    const float4 w = __ldcg(reinterpret_cast<const float4*>(a.ys + (long long)p * a.d + c));
+    sum.x += on ? w.x : 0.f;
+    sum.y += on ? w.y : 0.f;
+    sum.z += on ? w.z : 0.f;
+    sum.w += on ? w.w : 0.f;
+  }
+  *reinterpret_cast<uint2*>(a.y + (long long)t * a.d + c) =
+      make_uint2(pack_bf2(sum.x, sum.y), pack_bf2(sum.z, sum.w));
+}
+
+// ---- host side -------------------------------------------------------------------
+
+// Dynamic shared memory the kernels may take beside their static.
+constexpr int kSplitDynamic = 200 * 1024, kStreamDynamic = 216 * 1024;
+
+// Tokens of a pass: up to 8, fewer where their rows would not fit.
+int split_cols(int K, int pairs, int T) {
+  int room = kSplitDynamic - list_bytes(pairs);
+  if (room > 64 * 1024) room = 64 * 1024;              // three CTAs an SM
+  const int fit = room / row_bytes(K), most = T < kCols ? T : kCols;
+  return fit < most ? fit : most;
+}
+int stream_cols(int K, int pairs, int T) {
+  const int room = kStreamDynamic - kRingBytes - list_bytes(pairs);
+  const int fit = room / 2 / row_bytes(K), most = T < kCols ? T : kCols;
+  return fit < most ? fit : most;
+}
+
+// Units of one launch, and whether it streams: every warp of the GPU gets a unit and
+// passes of four tokens fit.
+template <bool W13>
+long long units_of(const DecodeArgs& a) {
+  const int pairs = a.T * a.k;
+  return (long long)(pairs < a.E ? pairs : a.E) * (W13 ? a.I / 16 : a.d / 32);
+}
+template <bool W13>
+bool streams(const DecodeArgs& a) {
+  return units_of<W13>(a) >= (long long)kStreamWarps * num_sms() &&
+         stream_cols(W13 ? a.d : a.I, a.T * a.k, a.T) >= (a.T < 4 ? a.T : 4);
+}
+
+template <bool W13>
+cudaError_t launch_product(DecodeArgs a, cudaStream_t st) {
+  const int pairs = a.T * a.k, K = W13 ? a.d : a.I, sms = num_sms();
+  if (streams<W13>(a)) {
+    static std::atomic<unsigned long long> done{0};
+    const cudaError_t e = smem_optin_once(k_decode_stream<W13>, kStreamDynamic, done);
+    if (e != cudaSuccess) return e;
+    a.cols = stream_cols(K, pairs, a.T);
+    return launch_pdl(k_decode_stream<W13>, dim3(sms), dim3(kStreamWarps * 32),
+                      kRingBytes + list_bytes(pairs) + 2 * a.cols * row_bytes(K), st, a);
+  }
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = smem_optin_once(k_decode_split<W13>, kSplitDynamic, done);
+  if (e != cudaSuccess) return e;
+  a.cols = split_cols(K, pairs, a.T);
+  const long long units = units_of<W13>(a);
+  return launch_pdl(k_decode_split<W13>, dim3((unsigned)(units < 3LL * sms ? units : 3LL * sms)),
+                    dim3(kThreads), list_bytes(pairs) + a.cols * row_bytes(K), st, a);
 }
 
 }  // namespace
 
-cudaError_t launch_decode_nvfp4(const DecodeCall& c, cudaStream_t stream) {
+bool decode_nvfp4_fits(int d, int I, int pairs) {
+  return split_cols(d, pairs, 1) > 0 && split_cols(I, pairs, 1) > 0;
+}
+
+cudaError_t launch_decode_nvfp4(const DecodeCall& c, int* launches, cudaStream_t stream) {
   DecodeArgs a = {};
   a.x = static_cast<const uint16_t*>(c.x);
   a.ids = c.ids; a.scores = c.scores;
   a.T = c.T; a.k = c.k; a.d = c.d; a.I = c.I; a.E = c.E;
-  a.slots = c.T * c.k < c.E ? c.T * c.k : c.E;
   a.clamp = c.clamp;
-  a.h = c.h; a.ys = c.ys; a.keep = c.keep; a.arrived = c.arrived;
+  a.h = c.h; a.ys = c.ys; a.keep = c.keep;
   a.y = static_cast<uint16_t*>(c.y);
   a.err = c.err;
   a.codes = c.w13; a.sf = c.w13_sf; a.w_scale = c.w13_scale;
-  cudaError_t e = launch_pdl(k_decode_w13, dim3(c.I / 16, a.slots), dim3(256), 0, stream, a);
+  cudaError_t e = launch_product<true>(a, stream);
   if (e != cudaSuccess) return e;
   a.codes = c.w2; a.sf = c.w2_sf; a.w_scale = c.w2_scale;
-  return launch_pdl(k_decode_w2, dim3(c.d / 32, a.slots), dim3(warps_for(c.I) * 32), 0, stream, a);
+  const bool joined = c.T <= kArrivalTokens && !streams<false>(a);
+  a.arrived = joined ? c.arrived : nullptr;
+  e = launch_product<false>(a, stream);
+  *launches = joined ? 2 : 3;
+  if (e != cudaSuccess || joined) return e;
+  const long long threads = (long long)c.T * (c.d / 4);
+  return launch_pdl(k_decode_combine, dim3((unsigned)((threads + kThreads - 1) / kThreads)),
+                    dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace moe

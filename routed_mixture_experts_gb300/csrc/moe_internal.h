@@ -226,7 +226,8 @@ struct DecodeCall {
   void* y;                   // [T, d] bf16
   DevError* err;
 };
-cudaError_t launch_decode_nvfp4(const DecodeCall& c, cudaStream_t stream);   // two launches
+bool decode_nvfp4_fits(int d, int I, int pairs);   // in shared memory
+cudaError_t launch_decode_nvfp4(const DecodeCall& c, int* launches, cudaStream_t stream);
 
 // Launch the CTA-pair grouped GEMM over routed rows (256 x 256 tiles, A K-major;
 // requires expert segments padded to 256 rows and N % 256 == 0).

@@ -100,7 +100,11 @@ SIZES = [dict(T=1, d=256, I=256, E=4, k=2), dict(T=1, d=512, I=768, E=300 // 2, 
          dict(T=16, d=256, I=256, E=32, k=2), dict(T=9, d=256, I=256, E=1, k=1),
          dict(T=33, d=512, I=256, E=8, k=4), dict(T=64, d=256, I=256, E=64, k=8),
          dict(T=256, d=256, I=256, E=7, k=2), dict(T=40, d=256, I=256, E=256, k=20),
-         dict(T=5, d=256, I=1280, E=6, k=2, clamp=0.5)]
+         dict(T=5, d=256, I=1280, E=6, k=2, clamp=0.5),
+         # enough units for a unit a warp, in the first or the second product, with the
+         # shortest rows and several passes of one expert's tokens
+         dict(T=60, d=512, I=768, E=80, k=4), dict(T=100, d=2048, I=256, E=48, k=3),
+         dict(T=150, d=256, I=1280, E=40, k=5)]
 
 
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: ",".join("%s%s" % kv for kv in s.items()))
