@@ -78,12 +78,10 @@ struct moe_plan {
   float nv_x_scale, nv_h_scale;
   CUtensorMap tm_w13nv, tm_w2nv;
   const void *w13nv_cached, *w2nv_cached;
-  // moe_decode_nvfp4: h and ys of up to dec_tokens tokens, which pairs count, and
-  // the arrival counters (zero between calls)
+  // moe_decode_nvfp4: h and ys of up to dec_tokens tokens, and which pairs count
   int dec_tokens;
   float *dec_h, *dec_ys;
   uint8_t* dec_keep;
-  int* dec_arrived;
   int ngr_d, ngr_I;                 // 128-element scale groups along d and along I
   CUtensorMap tm_xq, tm_hq, tm_w13q, tm_w2q;
   const void *w13q_cached, *w2q_cached;
@@ -284,7 +282,6 @@ size_t layout(moe_plan* p, char* base, int flags) {
     p->dec_h = reinterpret_cast<float*>(take(4 * pairs * I));
     p->dec_ys = reinterpret_cast<float*>(take(4 * pairs * d));
     p->dec_keep = reinterpret_cast<uint8_t*>(take(pairs));
-    p->dec_arrived = reinterpret_cast<int*>(take(4 * (d / 32)));
   }
   if (mx) {
     p->xq = reinterpret_cast<uint8_t*>(take(RP * d));
@@ -700,8 +697,6 @@ int moe_plan_set_workspace(moe_plan* p, void* ws, size_t bytes, int flags) {
         encode_tmap_bf16(&p->tm_ys, p->ys, RP, p->d, 128))
       return MOE_ERR_CUDA;
     if (flags & MOE_WS_HOST_STAGING) return MOE_ERR_UNSUPPORTED;
-    const int rc = cuda_status(cudaMemset(p->dec_arrived, 0, 4 * (size_t)(p->d / 32)));
-    if (rc != MOE_OK) return rc;
     return reset_error_word(p->err);
   }
   p->w13t_cached = p->w2t_cached = nullptr;
@@ -1459,7 +1454,7 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
   c.clamp = p->clamp;
   c.w13 = w13q; c.w13_sf = w13_sf; c.w13_scale = w13_scale;
   c.w2 = w2q; c.w2_sf = w2_sf; c.w2_scale = w2_scale;
-  c.h = p->dec_h; c.ys = p->dec_ys; c.keep = p->dec_keep; c.arrived = p->dec_arrived;
+  c.h = p->dec_h; c.ys = p->dec_ys; c.keep = p->dec_keep;
   c.y = y;
   c.err = p->err;
   int launches = 0;

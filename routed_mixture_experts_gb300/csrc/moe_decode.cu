@@ -43,8 +43,6 @@ constexpr int kStep = 128;              // K elements per warp step
 constexpr int kCols = 8;                // tokens per pass (MMA columns)
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-// Up to this many tokens the last CTA of some rows joins the experts' results.
-constexpr int kArrivalTokens = 4;
 
 __device__ __forceinline__ uint32_t e2m1x2_to_f16x2(uint32_t word, int byte) {
   uint32_t r;
@@ -175,7 +173,6 @@ struct DecodeArgs {
   float* h;                   // [T*k, I]
   float* ys;                  // [T*k, d]
   uint8_t* keep;              // [T*k] 1: the pair counts (valid id, first in its row)
-  int* arrived;               // [d / 32], zero between calls; NULL: k_decode_combine joins
   uint16_t* y;                // [T, d]
   DevError* err;
 };
@@ -191,10 +188,11 @@ struct Plan {
   int expert, first, tokens;  // the pass that find_pass() looked for
 };
 
-// What thread e < 256 keeps of expert e.
+// What a thread keeps: of expert threadIdx.x < 256, and the id of pair threadIdx.x.
 struct Mine {
   int passes, before;         // its passes, and those of the experts ahead
   int start, tokens;          // its pairs in the list
+  int id;
 };
 
 // Bytes of a token's row of K fp16 elements in shared memory: 64 more than the row,
@@ -216,12 +214,13 @@ __device__ __forceinline__ bool repeated(const DecodeArgs& a, int p) {
 // complete after fill_list() and a __syncthreads().
 __device__ __forceinline__ int make_plan(const DecodeArgs& a, Plan& s, Mine& m) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  m = Mine{0, 0, 0, 0, -1};
   for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
     const int e = a.ids[p];
+    if (p == threadIdx.x) m.id = e;
     if (e >= 0 && e < a.E) atomicAdd(&s.count[e], 1);
   }
   __syncthreads();
-  m = Mine{0, 0, 0, 0};
   int2 sum = make_int2(0, 0);                        // inclusive over the warp's experts
   if (threadIdx.x < kThreads) {
     m.tokens = s.count[threadIdx.x];
@@ -254,15 +253,15 @@ __device__ __forceinline__ int make_plan(const DecodeArgs& a, Plan& s, Mine& m) 
 // __syncthreads(); `raw`: as long): every CTA has to come to the same passes.  A pair
 // that repeats an id of its row is computed too, and dropped where the tokens'
 // experts are added.  All threads call it.
-__device__ __forceinline__ void fill_list(const DecodeArgs& a, Plan& s, uint16_t* list,
-                                          uint16_t* raw) {
+__device__ __forceinline__ void fill_list(const DecodeArgs& a, Plan& s, const Mine& m,
+                                          uint16_t* list, uint16_t* raw) {
   for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
-    const int e = a.ids[p];
+    const int e = p == threadIdx.x ? m.id : a.ids[p];
     if (e >= 0 && e < a.E) raw[atomicAdd(&s.count[e], 1)] = (uint16_t)p;
   }
   __syncthreads();
   for (int p = threadIdx.x; p < a.T * a.k; p += blockDim.x) {
-    const int e = a.ids[p];
+    const int e = p == threadIdx.x ? m.id : a.ids[p];
     if (e < 0 || e >= a.E) continue;
     int at = s.start[e];
     const int first = at, end = s.count[e];
@@ -445,18 +444,120 @@ __device__ __forceinline__ void check_ids(const DecodeArgs& a) {
   }
 }
 
-// y[t] for the 32 rows of unit column `sub`, from every pair's ys.
-__device__ __forceinline__ void combine_rows(const DecodeArgs& a, int sub) {
-  for (int v = threadIdx.x; v < a.T * 32; v += blockDim.x) {
-    const int t = v >> 5, row = out_col<false>(sub, v >> 3 & 3) + (v & 7);
-    float sum = 0.f;
+// ---- one token ---------------------------------------------------------------------
+//
+// No list is needed: a pair is an expert of its own.  W13: a unit of one pair a CTA,
+// K split over its eight warps as in k_decode_split.  W2: 32 rows a CTA, a warp a pair
+// (k <= 8), its whole row of weights on its way before h is there, and the pairs
+// added in the CTA: no third launch.
+
+// The expert of pair j of the one token; -1 for a bad id or a repeated one.
+__device__ __forceinline__ int expert_of(const DecodeArgs& a, int j) {
+  const int e = a.ids[j];
+  bool ok = e >= 0 && e < a.E;
 #pragma unroll 8
-    for (int j = 0; j < a.k; ++j) {              // a dropped pair's ys is old: not added
-      const int p = t * a.k + j;
-      const float w = __ldcg(a.ys + (long long)p * a.d + row);
-      sum += a.keep[p] ? w : 0.f;
+  for (int i = 0; i < j; ++i) ok &= a.ids[i] != e;
+  return ok ? e : -1;
+}
+
+__global__ void __launch_bounds__(kThreads, 3) k_decode_one_w13(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t xs[];         // the token's row
+  __shared__ Tokens tok;
+  __shared__ uint16_t pair;
+  __shared__ float red[kWarps][32][9];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int per = a.I / 16, steps = a.d / kStep;
+  const int j = blockIdx.x / per, sub = blockIdx.x - j * per;
+  const long long gap = 32LL * (a.d / 2), far = (long long)a.I * (a.d / 2);
+  if (threadIdx.x == 0) pair = (uint16_t)j;
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const int e = expert_of(a, j);
+  StepA w;
+  Rows r{nullptr, nullptr};
+  if (e >= 0) {
+    r = rows_of<true>(a, e, sub);
+    if (warp < steps) load_step(r, gap, far, warp, w);
+  }
+  if (blockIdx.x == 0) check_ids(a);
+  if (e < 0) return;
+  const float alpha = a.w_scale[e];
+  stage_tokens<true, 1>(a, tok, xs, &pair, 1);
+  __syncthreads();
+  float acc[2][2][4] = {};
+  for (int step = warp; step < steps; step += kWarps) {
+    StepA cur = w;
+    if (step + kWarps < steps) load_step(r, gap, far, step + kWarps, w);
+    mma_step(cur, (q & 1) * 16, xs + q * 16 + step * (2 * kStep), g == 0, acc);
+  }
+  if (q == 0)                            // column 0
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      red[warp][g][i] = acc[0][i >> 1][(i & 1) * 2] + acc[1][i >> 1][(i & 1) * 2];
+  __syncthreads();
+  if (threadIdx.x < 16) {
+    const int i = threadIdx.x >> 3, gg = threadIdx.x & 7;
+    float G = 0.f, U = 0.f;
+#pragma unroll
+    for (int x = 0; x < kWarps; ++x) {
+      G += red[x][gg][i];
+      U += red[x][gg][i + 2];
     }
-    a.y[(long long)t * a.d + row] = f2bf(sum);
+    const float f = alpha * tok.inv[0];
+    a.h[(long long)j * a.I + out_col<true>(sub, i) + gg] = swiglu(a, f * G, f * U);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads, 2) k_decode_one_w2(const DecodeArgs a) {
+  extern __shared__ __align__(16) uint8_t xs[];         // the pairs' rows of h
+  __shared__ Tokens tok;
+  __shared__ uint16_t pairs[kCols];
+  __shared__ float red[kWarps][32];
+  __shared__ float factor[kWarps];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, q = lane & 3;
+  const int sub = blockIdx.x, steps = a.I / kStep;
+  const long long gap = 32LL * (a.I / 2), far = 64LL * (a.I / 2);
+  if (threadIdx.x < kCols) pairs[threadIdx.x] = (uint16_t)threadIdx.x;
+  // weights, ids and scales were there before the W13 kernel started
+  const int e = warp < a.k ? expert_of(a, warp) : -1;
+  StepA w[2];
+  Rows r{nullptr, nullptr};
+  if (e >= 0) {
+    r = rows_of<false>(a, e, sub);
+    load_step(r, gap, far, 0, w[0]);
+    load_step(r, gap, far, 1, w[1]);
+  }
+  const float alpha = e >= 0 ? a.w_scale[e] : 0.f;
+  __syncthreads();
+  pdl_wait();                            // h is complete
+  pdl_trigger();
+  stage_tokens<false, 3>(a, tok, xs, pairs, a.k);
+  __syncthreads();
+  if (e >= 0) {
+    float acc[2][2][4] = {};
+    const uint8_t* lane_xs = xs + warp * row_bytes(a.I) + q * 16;
+    for (int step = 0; step < steps; step += 2) {          // steps is even
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const StepA cur = w[b];
+        if (step + b + 2 < steps) load_step(r, gap, far, step + b + 2, w[b]);
+        mma_step(cur, (q & 1) * 16, lane_xs + (step + b) * (2 * kStep), g == 0, acc);
+      }
+    }
+    if (q == 0)                          // column 0
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        red[warp][i * 8 + g] = acc[0][i >> 1][(i & 1) * 2] + acc[1][i >> 1][(i & 1) * 2];
+  } else {
+    red[warp][lane] = 0.f;
+  }
+  if (lane == 0) factor[warp] = e >= 0 ? tok.score[warp] * (alpha * tok.inv[warp]) : 0.f;
+  __syncthreads();
+  if (warp == 0) {
+    float y = 0.f;
+    for (int j = 0; j < a.k; ++j) y += factor[j] * red[j][lane];
+    a.y[out_col<false>(sub, lane >> 3) + (lane & 7)] = f2bf(y);
   }
 }
 
@@ -471,7 +572,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a
   __shared__ Plan s;
   __shared__ Tokens tok;
   __shared__ float red[2][kWarps][32][9];
-  __shared__ int last;
   uint16_t* const list = reinterpret_cast<uint16_t*>(smem);
   uint8_t* const xs = smem + list_bytes(a.T * a.k);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -493,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a
   __syncthreads();
   StepA w;
   if (run.x < run.y && warp < steps) load_step(rows_of<W13>(a, s.expert, sub), gap, far, warp, w);
-  fill_list(a, s, list, list + a.T * a.k);
+  fill_list(a, s, m, list, list + a.T * a.k);
   if (!W13) {
     pdl_wait();           // h is complete
     pdl_trigger();
@@ -541,20 +641,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a
           a.ys[(long long)tok.pair[c] * a.d + out_col<false>(sub, i) + gg] =
               tok.score[c] * (f * reduced(i, gg, c));
       }
-      if (!W13 && a.arrived) {
-        // the CTA that is last of these rows sees every other pass's ys
-        __syncthreads();
-        if (threadIdx.x == 0) {
-          __threadfence();
-          last = atomicAdd(&a.arrived[sub], 1) == passes - 1;
-          __threadfence();
-        }
-        __syncthreads();
-        if (last) {
-          combine_rows(a, sub);
-          if (threadIdx.x == 0) a.arrived[sub] = 0;
-        }
-      }
     }
     if (n > 0) {
       pass += 1;
@@ -566,9 +652,6 @@ __global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a
     }
   }
   if (W13 && blockIdx.x == 0) check_ids(a);
-  if (!W13 && a.arrived && passes == 0)  // nothing but bad ids
-    for (int v = blockIdx.x * kThreads + threadIdx.x; v < a.T * a.d; v += gridDim.x * kThreads)
-      a.y[v] = 0;
 }
 
 // ---- many units: a unit a warp ----------------------------------------------------
@@ -672,7 +755,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch();
     if (!listed) {
-      fill_list(a, s, list, list + a.T * a.k);
+      fill_list(a, s, m, list, list + a.T * a.k);
       if (!W13) {
         pdl_wait();                      // h is complete
         pdl_trigger();
@@ -799,6 +882,20 @@ bool streams(const DecodeArgs& a) {
          stream_cols(W13 ? a.d : a.I, a.T * a.k, a.T) >= (a.T < 4 ? a.T : 4);
 }
 
+cudaError_t launch_one_w13(DecodeArgs a, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = smem_optin_once(k_decode_one_w13, kSplitDynamic, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_decode_one_w13, dim3(a.k * (a.I / 16)), dim3(kThreads), row_bytes(a.d), st, a);
+}
+
+cudaError_t launch_one_w2(DecodeArgs a, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const cudaError_t e = smem_optin_once(k_decode_one_w2, kSplitDynamic, done);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(k_decode_one_w2, dim3(a.d / 32), dim3(kThreads), a.k * row_bytes(a.I), st, a);
+}
+
 template <bool W13>
 cudaError_t launch_product(DecodeArgs a, cudaStream_t st) {
   const int pairs = a.T * a.k, K = W13 ? a.d : a.I, sms = num_sms();
@@ -835,14 +932,15 @@ cudaError_t launch_decode_nvfp4(const DecodeCall& c, int* launches, cudaStream_t
   a.y = static_cast<uint16_t*>(c.y);
   a.err = c.err;
   a.codes = c.w13; a.sf = c.w13_sf; a.w_scale = c.w13_scale;
-  cudaError_t e = launch_product<true>(a, stream);
+  // one token of up to eight experts whose rows fit: two launches
+  const bool one = c.T == 1 && c.k <= kWarps && row_bytes(c.d) <= kSplitDynamic &&
+                   c.k * row_bytes(c.I) <= kSplitDynamic;
+  cudaError_t e = one ? launch_one_w13(a, stream) : launch_product<true>(a, stream);
   if (e != cudaSuccess) return e;
   a.codes = c.w2; a.sf = c.w2_sf; a.w_scale = c.w2_scale;
-  const bool joined = c.T <= kArrivalTokens && !streams<false>(a);
-  a.arrived = joined ? c.arrived : nullptr;
-  e = launch_product<false>(a, stream);
-  *launches = joined ? 2 : 3;
-  if (e != cudaSuccess || joined) return e;
+  e = one ? launch_one_w2(a, stream) : launch_product<false>(a, stream);
+  *launches = one ? 2 : 3;
+  if (e != cudaSuccess || one) return e;
   const long long threads = (long long)c.T * (c.d / 4);
   return launch_pdl(k_decode_combine, dim3((unsigned)((threads + kThreads - 1) / kThreads)),
                     dim3(kThreads), 0, stream, a);

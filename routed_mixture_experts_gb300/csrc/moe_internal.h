@@ -222,7 +222,6 @@ struct DecodeCall {
   float* h;                  // [T*k, I] scratch
   float* ys;                 // [T*k, d] scratch
   uint8_t* keep;             // [T*k] scratch
-  int* arrived;              // [d / 32], zero between calls
   void* y;                   // [T, d] bf16
   DevError* err;
 };

@@ -150,28 +150,23 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sum N values over the tpr threads of a row group (warps summed in order, so
-// every thread of the group gets the same bits).  `buf`: [warps of the group][N].
-template <int N>
-__device__ __forceinline__ void group_sum(float (&s)[N], float* buf, int li, int tpr, int bar) {
+// Sum a value over the tpr threads of a row group: the warps' sums in `buf` (one per
+// warp), then every warp adds them in the same order, so all threads get the same
+// bits.
+__device__ __forceinline__ float group_sum(float s, float* buf, int li, int tpr, int bar) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += __shfl_xor_sync(0xffffffffu, s[i], o);
-  if (tpr == 32) return;
-  if ((li & 31) == 0)
-#pragma unroll
-    for (int i = 0; i < N; ++i) buf[(li >> 5) * N + i] = s[i];
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (tpr == 32) return s;
+  const int lane = li & 31, warps = tpr / 32;
+  if (lane == 0) buf[li >> 5] = s;
   group_sync(bar, tpr);
-#pragma unroll
-  for (int i = 0; i < N; ++i) s[i] = 0.f;
-  for (int w = 0; w < tpr / 32; ++w)
-#pragma unroll
-    for (int i = 0; i < N; ++i) s[i] += buf[w * N + i];
+  s = lane < warps ? buf[lane] : 0.f;
+  for (int o = 1; o < warps; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return __shfl_sync(0xffffffffu, s, 0);
 }
 
 __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
-  return 1.f / sqrtf(sum_sq / (float)d + eps);
+  return rsqrtf(sum_sq * (1.f / (float)d) + eps);
 }
 
 // Forward, a row per group of tpr threads and no loop: few rows, wide rows and rows
@@ -190,18 +185,17 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
     load8<VEC>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
   if (a.y) {
     float y[V][8];
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       load8<VEC>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += y[v][e] * y[v][e];
+      for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
     }
     float f = a.alpha;
     if (a.gate_kind == MOE_GATE_TOKEN) f *= param(a.gate, a.param_bf16, row);
     if (a.w_post) {
-      group_sum(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g);
-      f *= inv_rms(s[0], d, a.eps);
+      f *= inv_rms(group_sum(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
     }
 #pragma unroll
     for (int v = 0; v < V; ++v) {
@@ -223,13 +217,12 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
     }
   }
   if (a.u) {
-    float s[1] = {0.f};
+    float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += x[v][e] * x[v][e];
-    group_sum(s, &red[1][g * (tpr / 32)], li, tpr, 1 + g);
-    const float rs = inv_rms(s[0], d, a.eps);
+      for (int e = 0; e < 8; ++e) s += x[v][e] * x[v][e];
+    const float rs = inv_rms(group_sum(s, &red[1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float w[8];
@@ -329,7 +322,7 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_norm_stream(const N
   }
   int stage = 0, flip = 0;
   for (long long row = first; row < a.T; row += hop) {
-    float x[8], y[8], s[1];
+    float x[8], y[8], s;
 #pragma unroll
     for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
     float f = 1.f;
@@ -343,22 +336,20 @@ __global__ void __launch_bounds__(kStreamThreads, 2) k_block_norm_stream(const N
     fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
     if (a.y) {
       if (a.w_post) {
-        s[0] = 0.f;
+        s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[0] += y[e] * y[e];
-        group_sum(s, &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g);
-        f *= inv_rms(s[0], d, a.eps);
+        for (int e = 0; e < 8; ++e) s += y[e] * y[e];
+        f *= inv_rms(group_sum(s, &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] += f * (q[e] * y[e]);
       if (in) store_vec8(static_cast<R*>(a.out) + row * a.ld_out + c0, x);
     }
     if (a.u) {
-      s[0] = 0.f;
+      s = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s[0] += x[e] * x[e];
-      group_sum(s, &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g);
-      const float rs = inv_rms(s[0], d, a.eps);
+      for (int e = 0; e < 8; ++e) s += x[e] * x[e];
+      const float rs = inv_rms(group_sum(s, &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[e] *= rs * w[e];
       if (in) store_vec8(static_cast<A*>(a.u) + row * a.ld_u + c0, x);
@@ -385,7 +376,7 @@ __device__ __forceinline__ void param_grads(const NormArgs& a, int c, float P, f
 
 // The six row sums over the tpr threads of a group: each exchange halves the values
 // a lane still adds (9 shuffles instead of 30), a warp's totals go to buf[warp][8]
-// and every thread adds the warps in order.
+// and every warp adds them in the same order.
 __device__ __forceinline__ void group_sum6(float (&s)[6], float (*buf)[8], int li, int tpr,
                                            int bar) {
   const int lane = li & 31;
@@ -402,17 +393,18 @@ __device__ __forceinline__ void group_sum6(float (&s)[6], float (*buf)[8], int l
   float v = (b2 ? r[1] : r[0]) + __shfl_xor_sync(0xffffffffu, b2 ? r[0] : r[1], 4);
   v += __shfl_xor_sync(0xffffffffu, v, 2);
   v += __shfl_xor_sync(0xffffffffu, v, 1);
-  if ((lane & 3) == 0) buf[li >> 5][lane >> 2] = v;     // value 4 b4 + 2 b3 + b2
-  if (tpr == 32) __syncwarp();
-  else group_sync(bar, tpr);
-#pragma unroll
-  for (int i = 0; i < 6; ++i) s[i] = 0.f;
-  for (int w = 0; w < tpr / 32; ++w) {
-    const float4 p = *reinterpret_cast<const float4*>(buf[w]);
-    const float2 q = *reinterpret_cast<const float2*>(buf[w] + 4);
-    s[0] += p.x; s[1] += p.y; s[2] += p.z; s[3] += p.w;
-    s[4] += q.x; s[5] += q.y;
+  const int warps = tpr / 32;
+  if (warps > 1) {
+    if ((lane & 3) == 0) buf[li >> 5][lane >> 2] = v;     // value 4 b4 + 2 b3 + b2
+    group_sync(bar, tpr);
+    // lane: value lane / 4, of every fourth warp from lane % 4 on
+    v = 0.f;
+    for (int w = lane & 3; w < warps; w += 4) v += buf[w][lane >> 2];
+    v += __shfl_xor_sync(0xffffffffu, v, 1);
+    v += __shfl_xor_sync(0xffffffffu, v, 2);
   }
+#pragma unroll
+  for (int i = 0; i < 6; ++i) s[i] = __shfl_sync(0xffffffffu, v, 4 * i);
 }
 
 // What a row's elements need of its six sums.
@@ -518,23 +510,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_stream(co
     cp_async_commit();
   };
   float x[8], y[8], dr[8], du[8];
-  auto load = [&](long long row, float (&nx)[8], float (&ny)[8], float (&ndr)[8], float (&ndu)[8]) {
+  // the next row as it is in memory: a conversion would wait for the load
+  R nx[8], ndr[8];
+  A ny[8], ndu[8];
+  auto load = [&](long long row) {
     if (row >= a.T) return;
-    load8<false>(x_in + row * a.ld_res, 0, li, tpr, d, nx);
-    if (dr_in) load8<false>(dr_in + row * a.ld_dres, 0, li, tpr, d, ndr);
-    if (y_in) load8<false>(y_in + row * a.ld_y, 0, li, tpr, d, ny);
-    if (du_in) load8<false>(du_in + row * a.ld_du, 0, li, tpr, d, ndu);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int c = col<false>(0, e, li, tpr);
+      if (c < d) {
+        nx[e] = x_in[row * a.ld_res + c];
+        if (dr_in) ndr[e] = dr_in[row * a.ld_dres + c];
+        if (y_in) ny[e] = y_in[row * a.ld_y + c];
+        if (du_in) ndu[e] = du_in[row * a.ld_du + c];
+      }
+    }
   };
 #pragma unroll
   for (int e = 0; e < 8; ++e) x[e] = y[e] = dr[e] = du[e] = 0.f;
-  float nx[8], ny[8], ndr[8], ndu[8];
   if (VEC) {
 #pragma unroll
     for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) nx[e] = ny[e] = ndr[e] = ndu[e] = 0.f;
-    load(first, nx, ny, ndr, ndu);
+    for (int e = 0; e < 8; ++e) nx[e] = ndr[e] = 0, ny[e] = ndu[e] = 0;
+    load(first);
   }
   float wp[8], q[8], P[8], S[8];
 #pragma unroll
@@ -564,8 +564,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_stream(co
       fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = nx[e], y[e] = ny[e], dr[e] = ndr[e], du[e] = ndu[e];
-      load(row + hop, nx, ny, ndr, ndu);
+      for (int e = 0; e < 8; ++e)
+        x[e] = to_f(nx[e]), y[e] = to_f(ny[e]), dr[e] = to_f(ndr[e]), du[e] = to_f(ndu[e]);
+      load(row + hop);
     }
     float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     row_sums(s, x, y, dr, du, wp, q);
