@@ -259,25 +259,32 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's slots of one tensor of one stage: sizeof(T) / 2 pieces of 16 bytes,
-// each [threads] apart so that a warp reads and writes consecutive pieces.
-template <typename T>
-__host__ __device__ constexpr int slot_bytes() { return kStreamThreads * 8 * (int)sizeof(T); }
+// A thread's slots of one tensor of one stage (TH threads): sizeof(T) / 2 pieces of
+// 16 bytes, TH pieces apart so that a warp reads and writes consecutive pieces.
+template <typename T, int TH = kStreamThreads>
+__host__ __device__ constexpr int slot_bytes() { return TH * 8 * (int)sizeof(T); }
 
-template <typename T>
+template <int TH = kStreamThreads, typename T>
 __device__ __forceinline__ void slot_copy(uint32_t slot, const T* src) {
 #pragma unroll
   for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    cp_async16(slot + (i * kStreamThreads + threadIdx.x) * 16, src + i * (16 / sizeof(T)));
+    cp_async16(slot + (i * TH + threadIdx.x) * 16, src + i * (16 / sizeof(T)));
 }
+template <int TH = kStreamThreads>
 __device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const uint16_t*) {
   load_vec8(reinterpret_cast<const uint16_t*>(slot + threadIdx.x * 16), f);
 }
+template <int TH = kStreamThreads>
 __device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const float*) {
   const float4 a = *reinterpret_cast<const float4*>(slot + threadIdx.x * 16);
-  const float4 b = *reinterpret_cast<const float4*>(slot + (kStreamThreads + threadIdx.x) * 16);
+  const float4 b = *reinterpret_cast<const float4*>(slot + (TH + threadIdx.x) * 16);
   f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
   f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+template <int TH>
+__device__ __forceinline__ void slot_write(uint8_t* slot, const float (&f)[8]) {
+  *reinterpret_cast<float4*>(slot + threadIdx.x * 16) = make_float4(f[0], f[1], f[2], f[3]);
+  *reinterpret_cast<float4*>(slot + (TH + threadIdx.x) * 16) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
 // Forward over streamed rows.
@@ -399,7 +406,9 @@ __device__ __forceinline__ void group_sum6(float (&s)[6], float (*buf)[8], int l
     group_sync(bar, tpr);
     // lane: value lane / 4, of every fourth warp from lane % 4 on
     v = 0.f;
-    for (int w = lane & 3; w < warps; w += 4) v += buf[w][lane >> 2];
+#pragma unroll
+    for (int w = 0; w < kStreamThreads / 32; w += 4)
+      if (w + (lane & 3) < warps) v += buf[w + (lane & 3)][lane >> 2];
     v += __shfl_xor_sync(0xffffffffu, v, 1);
     v += __shfl_xor_sync(0xffffffffu, v, 2);
   }
@@ -413,23 +422,25 @@ struct RowFactors {
   float ry, cy, gt;      // 1/rms(y), ry^2 mean(q dr y), token gate
 };
 
+// ALL: w_pre and w_post are given and there is no gate of a value a token.
+template <bool ALL>
 __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float (&s)[6],
-                                                  long long row, bool writer) {
-  const float inv_d = 1.f / (float)a.d;
+                                                  float inv_d, long long row, bool writer) {
+  const bool post = ALL || a.w_post;
   RowFactors f;
-  f.rs = a.du ? inv_rms(s[0], a.d, a.eps) : 0.f;
+  f.rs = ALL || a.du ? rsqrtf(s[0] * inv_d + a.eps) : 0.f;
   f.cx = f.rs * f.rs * f.rs * (s[1] * inv_d);
-  f.ry = a.w_post ? inv_rms(s[2], a.d, a.eps) : 1.f;
+  f.ry = post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
   const float D = s[3] + f.rs * s[4] - f.cx * s[5];
   f.gt = 1.f;
-  if (a.y && a.gate_kind == MOE_GATE_TOKEN) {
+  if (!ALL && a.y && a.gate_kind == MOE_GATE_TOKEN) {
     f.gt = param(a.gate, a.param_bf16, row);
     if (a.dgate && writer) {
       const float v = f.ry * D;
       a.dgate[row] = a.accumulate ? a.dgate[row] + v : v;
     }
   }
-  f.cy = a.w_post ? f.ry * f.ry * D * inv_d : 0.f;
+  f.cy = post ? f.ry * f.ry * D * inv_d : 0.f;
   return f;
 }
 
@@ -480,117 +491,271 @@ __device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float
   }
 }
 
-// Gradient of rows of up to 4096 columns: row groups walk the rows with the next
-// rows on their way (VEC: through the ring; else in registers), the sums of a
-// thread's 8 columns in registers.
-template <typename A, typename R, bool VEC>
-__global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_stream(const NormArgs a) {
-  extern __shared__ __align__(16) uint8_t ring[];
+// Pairs of fp32 values and the two-wide arithmetic on them: half the instructions of
+// the scalar forms, which is what bounds the row loop.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 make_f2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_f2(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum_f2(f2 v) {
+  float lo, hi;
+  split_f2(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ void to_f2(const float (&f)[8], f2 (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = make_f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_f2(p[i], f[2 * i], f[2 * i + 1]);
+}
+
+// Gradient of rows of up to 4096 columns: row groups walk the rows, the next row on
+// its way (VEC: through the ring; else in registers), the sums of a thread's 8 V
+// columns in registers, its parameters in slots of its own.  V = 2 halves what a row
+// costs beside its elements (the reduction, the factors, the addresses).  ALL: every
+// tensor is given and no gate of a value a token.
+template <int V>
+constexpr int kGradThreads = V == 2 ? 384 : kStreamThreads;
+constexpr int kGradStages = 2;
+
+template <typename A, typename R, int V, bool VEC>
+__host__ __device__ constexpr int grad_ring_bytes() {
+  return VEC ? kGradStages * V * 2 * (slot_bytes<A, kGradThreads<V>>() + slot_bytes<R, kGradThreads<V>>())
+             : 0;
+}
+template <int V>
+__host__ __device__ constexpr int grad_param_bytes() {
+  return 2 * V * slot_bytes<float, kGradThreads<V>>();
+}
+
+template <typename A, typename R, int V, bool VEC, bool ALL>
+__global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(const NormArgs a) {
+  extern __shared__ __align__(16) uint8_t ring[];       // ring, then the parameters' slots
   __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
-  constexpr int kA = slot_bytes<A>(), kR = slot_bytes<R>(), kStage = 2 * kA + 2 * kR;
+  static_assert(VEC || V == 1, "rows in registers: one piece a thread");
+  constexpr int TH = kGradThreads<V>;
+  constexpr int kA = slot_bytes<A, TH>(), kR = slot_bytes<R, TH>(), kF = slot_bytes<float, TH>();
+  constexpr int kPiece = 2 * kA + 2 * kR, kStage = V * kPiece;
+  uint8_t* const params = ring + grad_ring_bytes<A, R, V, VEC>();
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
-  const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr;
-  const int d = a.d, c0 = li * 8;
-  const bool in = c0 < d;                        // VEC: the thread has columns
-  const long long first = (long long)blockIdx.x * groups + g, hop = (long long)gridDim.x * groups;
-  const A* const y_in = static_cast<const A*>(a.y);
-  const A* const du_in = static_cast<const A*>(a.du);
-  const R* const x_in = static_cast<const R*>(a.res);
-  const R* const dr_in = static_cast<const R*>(a.dres);
+  const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
+  const bool has_y = ALL || a.y, has_du = ALL || a.du, has_dr = ALL || a.dres;
+  const long long first = (long long)blockIdx.x * groups + g;
+  const int hop = gridDim.x * groups;
+  const int rows = first < a.T ? (int)((a.T - first + hop - 1) / hop) : 0;   // of the group
+  // the rows to fetch next, and the rows to write
+  const A* y_in = static_cast<const A*>(a.y) + (has_y ? first * a.ld_y : 0);
+  const A* du_in = static_cast<const A*>(a.du) + (has_du ? first * a.ld_du : 0);
+  const R* x_in = static_cast<const R*>(a.res) + first * a.ld_res;
+  const R* dr_in = static_cast<const R*>(a.dres) + (has_dr ? first * a.ld_dres : 0);
+  R* dr_out = static_cast<R*>(a.out) + first * a.ld_out;
+  A* dy_out = static_cast<A*>(a.u) + (a.u ? first * a.ld_u : 0);
+  auto advance = [&]() {
+    x_in += hop * a.ld_res;
+    if (has_dr) dr_in += hop * a.ld_dres;
+    if (has_y) y_in += hop * a.ld_y;
+    if (has_du) du_in += hop * a.ld_du;
+  };
+  int left = rows;                               // rows not fetched yet
   const uint32_t base = smem_u32(ring);
-  auto fetch = [&](long long row, int stage) {
-    if (in && row < a.T) {
-      const uint32_t at = base + stage * kStage;
-      slot_copy(at, x_in + row * a.ld_res + c0);
-      if (dr_in) slot_copy(at + kR, dr_in + row * a.ld_dres + c0);
-      if (y_in) slot_copy(at + 2 * kR, y_in + row * a.ld_y + c0);
-      if (du_in) slot_copy(at + 2 * kR + kA, du_in + row * a.ld_du + c0);
+  auto fetch = [&](int stage) {
+    if (left > 0) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const int c = col<true>(v, 0, li, tpr);
+        if (c < d) {
+          const uint32_t at = base + stage * kStage + v * kPiece;
+          slot_copy<TH>(at, x_in + c);
+          if (has_dr) slot_copy<TH>(at + kR, dr_in + c);
+          if (has_y) slot_copy<TH>(at + 2 * kR, y_in + c);
+          if (has_du) slot_copy<TH>(at + 2 * kR + kA, du_in + c);
+        }
+      }
+      advance();
+      --left;
     }
     cp_async_commit();
   };
-  float x[8], y[8], dr[8], du[8];
   // the next row as it is in memory: a conversion would wait for the load
   R nx[8], ndr[8];
   A ny[8], ndu[8];
-  auto load = [&](long long row) {
-    if (row >= a.T) return;
+  auto load = [&]() {
+    if (left > 0) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col<false>(0, e, li, tpr);
-      if (c < d) {
-        nx[e] = x_in[row * a.ld_res + c];
-        if (dr_in) ndr[e] = dr_in[row * a.ld_dres + c];
-        if (y_in) ny[e] = y_in[row * a.ld_y + c];
-        if (du_in) ndu[e] = du_in[row * a.ld_du + c];
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<false>(0, e, li, tpr);
+        if (c < d) {
+          nx[e] = x_in[c];
+          if (has_dr) ndr[e] = dr_in[c];
+          if (has_y) ny[e] = y_in[c];
+          if (has_du) ndu[e] = du_in[c];
+        }
       }
+      advance();
+      --left;
     }
   };
-#pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = y[e] = dr[e] = du[e] = 0.f;
   if (VEC) {
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+    // slots that no copy fills (columns past the row, absent tensors) read as zero
+    for (int i = 0; i < kGradStages * kStage / (TH * 16); ++i)
+      *reinterpret_cast<uint4*>(ring + (i * TH + threadIdx.x) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    fetch(0);
   } else {
 #pragma unroll
     for (int e = 0; e < 8; ++e) nx[e] = ndr[e] = 0, ny[e] = ndu[e] = 0;
-    load(first);
+    load();
   }
-  float wp[8], q[8], P[8], S[8];
+  f2 P[V][4], S[V][4];
+  const f2 zero = make_f2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int c = col<VEC>(0, e, li, tpr);
-    wp[e] = P[e] = S[e] = 0.f;
-    q[e] = a.alpha;
-    if (c < d) {
-      if (a.du) wp[e] = param(a.w_pre, a.param_bf16, c);
-      if (a.y && a.w_post) q[e] *= param(a.w_post, a.param_bf16, c);
-      if (a.y && a.gate_kind == MOE_GATE_CHANNEL) q[e] *= param(a.gate, a.param_bf16, c);
-    }
-  }
-  int stage = 0, flip = 0;
-  for (long long row = first; row < a.T; row += hop) {
-    if (VEC) {
-      cp_async_wait<kStages - 2>();
-      const uint8_t* at = ring + stage * kStage;
+  for (int v = 0; v < V; ++v) {
+    float w8[8], q8[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = dr[e] = 0.f;
-      if (in) {
-        slot_read(at, x, x_in);
-        if (dr_in) slot_read(at + kR, dr, x_in);
-        if (y_in) slot_read(at + 2 * kR, y, y_in);
-        if (du_in) slot_read(at + 2 * kR + kA, du, y_in);
+    for (int e = 0; e < 8; ++e) {
+      const int c = col<VEC>(v, e, li, tpr);
+      w8[e] = 0.f;
+      q8[e] = a.alpha;
+      if (c < d) {
+        if (has_du) w8[e] = param(a.w_pre, a.param_bf16, c);
+        if (has_y && a.w_post) q8[e] *= param(a.w_post, a.param_bf16, c);
+        if (has_y && a.gate_kind == MOE_GATE_CHANNEL) q8[e] *= param(a.gate, a.param_bf16, c);
       }
-      fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+    }
+    slot_write<TH>(params + 2 * v * kF, w8);
+    slot_write<TH>(params + (2 * v + 1) * kF, q8);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) P[v][i] = S[v][i] = zero;
+  }
+  const float inv_d = 1.f / (float)d;
+  int stage = 0, flip = 0;
+  long long row = first;
+  for (int n = 0; n < rows; ++n, row += hop) {
+    f2 x[V][4], y[V][4], dr[V][4], du[V][4];
+    float f[8];
+    if (VEC) {
+      cp_async_wait<0>();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint8_t* at = ring + stage * kStage + v * kPiece;
+        slot_read<TH>(at, f, static_cast<const R*>(nullptr));
+        to_f2(f, x[v]);
+        slot_read<TH>(at + kR, f, static_cast<const R*>(nullptr));
+        to_f2(f, dr[v]);
+        slot_read<TH>(at + 2 * kR, f, static_cast<const A*>(nullptr));
+        to_f2(f, y[v]);
+        slot_read<TH>(at + 2 * kR + kA, f, static_cast<const A*>(nullptr));
+        to_f2(f, du[v]);
+      }
+      stage ^= 1;
+      fetch(stage);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        x[e] = to_f(nx[e]), y[e] = to_f(ny[e]), dr[e] = to_f(ndr[e]), du[e] = to_f(ndu[e]);
-      load(row + hop);
+      for (int e = 0; e < 8; ++e) f[e] = to_f(nx[e]);
+      to_f2(f, x[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = to_f(ny[e]);
+      to_f2(f, y[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = to_f(ndr[e]);
+      to_f2(f, dr[0]);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[e] = to_f(ndu[e]);
+      to_f2(f, du[0]);
+      load();
     }
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    row_sums(s, x, y, dr, du, wp, q);
+    float s[6];
+    {
+      f2 z[6] = {zero, zero, zero, zero, zero, zero};
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        f2 wp[4], q[4];
+        slot_read<TH>(params + 2 * v * kF, f, static_cast<const float*>(nullptr));
+        to_f2(f, wp);
+        slot_read<TH>(params + (2 * v + 1) * kF, f, static_cast<const float*>(nullptr));
+        to_f2(f, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const f2 t = mul2(du[v][i], wp[i]), qy = mul2(q[i], y[v][i]);
+          z[0] = fma2(x[v][i], x[v][i], z[0]);
+          z[1] = fma2(t, x[v][i], z[1]);
+          z[2] = fma2(y[v][i], y[v][i], z[2]);
+          z[3] = fma2(qy, dr[v][i], z[3]);
+          z[4] = fma2(qy, t, z[4]);
+          z[5] = fma2(qy, x[v][i], z[5]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < 6; ++i) s[i] = sum_f2(z[i]);
+    }
     group_sum6(s, &red[flip][g * (tpr / 32)], li, tpr, 1 + g);
-    const RowFactors f = row_factors(a, s, row, li == 0);
-    row_grads(f, x, y, dr, du, wp, q, P, S);
-    store8<VEC>(static_cast<R*>(a.out) + row * a.ld_out, 0, li, tpr, d, dr);
-    if (y_in && a.u) store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, 0, li, tpr, d, y);
-    stage = stage + 1 == kStages ? 0 : stage + 1;
     flip ^= 1;
+    const RowFactors k = row_factors<ALL>(a, s, inv_d, row, li == 0);
+    const float gy1 = k.gt * k.ry;
+    const f2 rs = make_f2(k.rs, k.rs), ncx = make_f2(-k.cx, -k.cx), gy = make_f2(gy1, gy1),
+             ncy = make_f2(-k.cy, -k.cy);
+    // dr becomes d_residual, y dy; the column sums take the row's terms
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      f2 wp[4], q[4];
+      slot_read<TH>(params + 2 * v * kF, f, static_cast<const float*>(nullptr));
+      to_f2(f, wp);
+      slot_read<TH>(params + (2 * v + 1) * kF, f, static_cast<const float*>(nullptr));
+      to_f2(f, q);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        P[v][i] = fma2(du[v][i], mul2(x[v][i], rs), P[v][i]);
+        dr[v][i] = fma2(ncx, x[v][i], fma2(rs, mul2(du[v][i], wp[i]), dr[v][i]));
+        S[v][i] = fma2(gy, mul2(dr[v][i], y[v][i]), S[v][i]);
+        y[v][i] = mul2(gy, fma2(ncy, y[v][i], mul2(q[i], dr[v][i])));
+      }
+      from_f2(dr[v], f);
+      store8<VEC>(dr_out, v, li, tpr, d, f);
+      if (has_y && a.u) {
+        from_f2(y[v], f);
+        store8<VEC>(dy_out, v, li, tpr, d, f);
+      }
+    }
+    dr_out += hop * a.ld_out;
+    if (has_y && a.u) dy_out += hop * a.ld_u;
   }
   pdl_trigger();
   if (!wants_column_sums(a)) return;
   cp_async_wait<0>();
+  __syncthreads();
   float* sm = reinterpret_cast<float*>(ring);
   for (int i = 0; i < groups; ++i) {
     __syncthreads();
     if (g == i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<VEC>(0, e, li, tpr);
-        if (c < d) {
-          sm[c] = (i ? sm[c] : 0.f) + P[e];
-          sm[d + c] = (i ? sm[d + c] : 0.f) + S[e];
+      for (int v = 0; v < V; ++v) {
+        float p8[8], s8[8];
+        from_f2(P[v], p8);
+        from_f2(S[v], s8);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int c = col<VEC>(v, e, li, tpr);
+          if (c < d) {
+            sm[c] = (i ? sm[c] : 0.f) + p8[e];
+            sm[d + c] = (i ? sm[d + c] : 0.f) + s8[e];
+          }
         }
       }
   }
@@ -642,7 +807,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
       row_sums(s, x[v], y[v], dr[v], du[v], wp, q);
     }
     group_sum6(s, red[flip], li, tpr, 1);
-    const RowFactors f = row_factors(a, s, row, li == 0);
+    const RowFactors f = row_factors<false>(a, s, 1.f / (float)d, row, li == 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       load8<VEC>(wpre, v, li, tpr, d, wp);
@@ -697,13 +862,22 @@ __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormAr
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-// Gradient: threads of a row and rows at a time of a CTA.
-int grad_pieces(int d) { return d <= kStreamMaxWidth ? 1 : (d <= 2 * kStreamMaxWidth ? 2 : 4); }
-int grad_tpr(int d) { return round32((d + grad_pieces(d) * 8 - 1) / (grad_pieces(d) * 8)); }
-int grad_groups(int d) { return kStreamThreads / grad_tpr(d); }
-int grad_grid(int T, int d) {
-  const int per = grad_groups(d), want = (T + per - 1) / per, sms = num_sms();
-  return want < sms ? want : sms;
+// How the gradient is laid out: pieces of 8 columns a thread, threads of a row, rows
+// at a time of a CTA, CTAs.  Two pieces a thread where that leaves several rows to a
+// CTA (bf16 rows of 1024 to 2048 aligned columns) or one piece would not do.
+struct GradShape {
+  int pieces, tpr, groups, grid;
+};
+GradShape grad_shape(int T, int d, bool vec, bool bf16) {
+  GradShape s;
+  if (d > kStreamMaxWidth) s.pieces = d <= 2 * kStreamMaxWidth ? 2 : 4;
+  else s.pieces = vec && bf16 && d >= 1024 && d <= 2048 ? 2 : 1;
+  s.tpr = round32((d + s.pieces * 8 - 1) / (s.pieces * 8));
+  const int threads = d <= kStreamMaxWidth && s.pieces == 2 ? kGradThreads<2> : kStreamThreads;
+  s.groups = threads / s.tpr;
+  const int want = (T + s.groups - 1) / s.groups, sms = num_sms();
+  s.grid = want < 1 ? 1 : want < sms ? want : sms;
+  return s;
 }
 
 template <typename A, typename R, int V, bool VEC>
@@ -736,42 +910,46 @@ cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
 
 template <typename... KArgs>
 cudaError_t launch_grad(void (*kernel)(KArgs...), std::atomic<unsigned long long>& done,
-                        int max_smem, int smem, const NormArgs& a, int grid, cudaStream_t st) {
+                        int max_smem, int smem, const NormArgs& a, const GradShape& s,
+                        cudaStream_t st) {
   const cudaError_t e = smem_optin_once(kernel, max_smem, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kernel, dim3(grid), dim3(a.tpr * grad_groups(a.d)), smem, st, a);
-}
-
-template <typename A, typename R, bool VEC>
-cudaError_t launch_grad_stream(const NormArgs& a, int grid, cudaStream_t st) {
-  static std::atomic<unsigned long long> done{0};
-  const int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
-  const int ring = kStages * 2 * (slot_bytes<A>() + slot_bytes<R>());
-  const int smem = VEC && ring > sums ? ring : sums;
-  return launch_grad(k_block_norm_grad_stream<A, R, VEC>, done, smem, smem, a, grid, st);
+  return launch_pdl(kernel, dim3(s.grid), dim3(s.tpr * s.groups), smem, st, a);
 }
 
 template <typename A, typename R, int V, bool VEC>
-cudaError_t launch_grad_wide(const NormArgs& a, int grid, cudaStream_t st) {
+cudaError_t launch_grad_stream(const NormArgs& a, const GradShape& s, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0}, done_all{0};
+  // the column sums end up where the ring and the parameters were
+  constexpr int rows = grad_ring_bytes<A, R, V, VEC>() + grad_param_bytes<V>();
+  constexpr int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
+  constexpr int smem = rows > sums ? rows : sums;
+  if (a.y && a.du && a.dres && a.w_post && a.gate_kind != MOE_GATE_TOKEN)
+    return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, true>, done_all, smem, smem, a, s, st);
+  return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, false>, done, smem, smem, a, s, st);
+}
+
+template <typename A, typename R, int V, bool VEC>
+cudaError_t launch_grad_wide(const NormArgs& a, const GradShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   return launch_grad(k_block_norm_grad_wide<A, R, V, VEC>, done,
-                     2 * kNormMaxWidth * (int)sizeof(float), 2 * a.d * (int)sizeof(float), a, grid,
+                     2 * kNormMaxWidth * (int)sizeof(float), 2 * a.d * (int)sizeof(float), a, s,
                      st);
 }
 
 template <typename A, typename R>
-cudaError_t launch_grad_types(const NormArgs& a, bool vec, int grid, cudaStream_t st) {
-  switch (grad_pieces(a.d)) {
-    case 1:
-      return vec ? launch_grad_stream<A, R, true>(a, grid, st)
-                 : launch_grad_stream<A, R, false>(a, grid, st);
-    case 2:
-      return vec ? launch_grad_wide<A, R, 2, true>(a, grid, st)
-                 : launch_grad_wide<A, R, 2, false>(a, grid, st);
-    default:
-      return vec ? launch_grad_wide<A, R, 4, true>(a, grid, st)
-                 : launch_grad_wide<A, R, 4, false>(a, grid, st);
+cudaError_t launch_grad_types(const NormArgs& a, bool vec, const GradShape& s, cudaStream_t st) {
+  if (a.d > kStreamMaxWidth) {
+    if (s.pieces == 2)
+      return vec ? launch_grad_wide<A, R, 2, true>(a, s, st)
+                 : launch_grad_wide<A, R, 2, false>(a, s, st);
+    return vec ? launch_grad_wide<A, R, 4, true>(a, s, st)
+               : launch_grad_wide<A, R, 4, false>(a, s, st);
   }
+  if constexpr (sizeof(A) == 2)
+    if (s.pieces == 2) return launch_grad_stream<A, R, 2, true>(a, s, st);
+  return vec ? launch_grad_stream<A, R, 1, true>(a, s, st)
+             : launch_grad_stream<A, R, 1, false>(a, s, st);
 }
 
 int elem(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
@@ -815,7 +993,10 @@ using namespace moe;
 
 extern "C" size_t moe_block_norm_workspace_bytes(const moe_block_norm_desc* s, int T) {
   if (!desc_ok(s) || T < 0) return 0;
-  return (size_t)grad_grid(T > 0 ? T : 1, s->d) * 2 * s->d * sizeof(float);
+  // the widest layout: whether rows are aligned is known with the call
+  const bool bf16 = s->dtype == MOE_DTYPE_BF16;
+  const int a = grad_shape(T, s->d, true, bf16).grid, b = grad_shape(T, s->d, false, bf16).grid;
+  return (size_t)(a > b ? a : b) * 2 * s->d * sizeof(float);
 }
 
 extern "C" int moe_block_norm_forward(const moe_block_norm_desc* s, int T, const void* residual,
@@ -890,7 +1071,6 @@ extern "C" int moe_block_norm_backward(
     y = d_u = nullptr;              // the column sums below become 0
   }
   NormArgs a = base_args(s, T);
-  a.tpr = grad_tpr(d);
   a.res = residual_out; a.ld_res = ld_out;
   a.y = y; a.ld_y = ld_y;
   a.dres = d_residual_out; a.ld_dres = ld_dout;
@@ -902,29 +1082,30 @@ extern "C" int moe_block_norm_backward(
   a.accumulate = accumulate ? 1 : 0;
   const bool sums = dw_pre || dw_post || (dgate && s->gate == MOE_GATE_CHANNEL);
   if (T == 0 && (!sums || accumulate)) return MOE_OK;
-  // no rows: one CTA, which writes zero sums
-  const int grid = T > 0 ? grad_grid(T, d) : 1;
-  if (sums && grid > 1) {
-    if (!workspace || workspace_bytes < (size_t)grid * 2 * d * sizeof(float))
-      return MOE_ERR_WORKSPACE;
-    if (reinterpret_cast<uintptr_t>(workspace) & 15u) return MOE_ERR_INVALID_ARG;
-    a.partial = static_cast<float*>(workspace);
-  }
-  a.n_partial = grid;
   const bool vec = d % 8 == 0 && rows_vec(residual_out, ld_out, s->residual_dtype) &&
                    rows_vec(y, ld_y, s->dtype) &&
                    rows_vec(d_residual_out, ld_dout, s->residual_dtype) &&
                    rows_vec(d_u, ld_du, s->dtype) &&
                    rows_vec(d_residual, ld_dres, s->residual_dtype) &&
                    rows_vec(dy, ld_dy, s->dtype);
+  // no rows: one CTA, which writes zero sums
+  const GradShape shape = grad_shape(T, d, vec, s->dtype == MOE_DTYPE_BF16);
+  a.tpr = shape.tpr;
+  if (sums && shape.grid > 1) {
+    if (!workspace || workspace_bytes < (size_t)shape.grid * 2 * d * sizeof(float))
+      return MOE_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(workspace) & 15u) return MOE_ERR_INVALID_ARG;
+    a.partial = static_cast<float*>(workspace);
+  }
+  a.n_partial = shape.grid;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (s->dtype == MOE_DTYPE_FP32)
-    e = launch_grad_types<float, float>(a, vec, grid, st);
+    e = launch_grad_types<float, float>(a, vec, shape, st);
   else if (s->residual_dtype == MOE_DTYPE_FP32)
-    e = launch_grad_types<uint16_t, float>(a, vec, grid, st);
+    e = launch_grad_types<uint16_t, float>(a, vec, shape, st);
   else
-    e = launch_grad_types<uint16_t, uint16_t>(a, vec, grid, st);
+    e = launch_grad_types<uint16_t, uint16_t>(a, vec, shape, st);
   if (e == cudaSuccess && a.partial)
     e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32), dim3(kSlices * 32), 0, st, a);
   return cuda_result(e, "moe_block_norm_backward");
