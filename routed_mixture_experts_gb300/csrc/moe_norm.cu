@@ -422,7 +422,7 @@ struct RowFactors {
   float ry, cy, gt;      // 1/rms(y), ry^2 mean(q dr y), token gate
 };
 
-// ALL: w_pre and w_post are given and there is no gate of a value a token.
+// ALL: w_pre and w_post are given.
 template <bool ALL>
 __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float (&s)[6],
                                                   float inv_d, long long row, bool writer) {
@@ -433,7 +433,7 @@ __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float
   f.ry = post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
   const float D = s[3] + f.rs * s[4] - f.cx * s[5];
   f.gt = 1.f;
-  if (!ALL && a.y && a.gate_kind == MOE_GATE_TOKEN) {
+  if ((ALL || a.y) && a.gate_kind == MOE_GATE_TOKEN) {
     f.gt = param(a.gate, a.param_bf16, row);
     if (a.dgate && writer) {
       const float v = f.ry * D;
@@ -530,7 +530,7 @@ __device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
 // its way (VEC: through the ring; else in registers), the sums of a thread's 8 V
 // columns in registers, its parameters in slots of its own.  V = 2 halves what a row
 // costs beside its elements (the reduction, the factors, the addresses).  ALL: every
-// tensor is given and no gate of a value a token.
+// tensor is given.
 template <int V>
 constexpr int kGradThreads = V == 2 ? 384 : kStreamThreads;
 constexpr int kGradStages = 2;
@@ -599,16 +599,17 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
   A ny[8], ndu[8];
   auto load = [&]() {
     if (left > 0) {
+      auto get = [&](const auto* p, auto (&to)[8]) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<false>(0, e, li, tpr);
-        if (c < d) {
-          nx[e] = x_in[c];
-          if (has_dr) ndr[e] = dr_in[c];
-          if (has_y) ny[e] = y_in[c];
-          if (has_du) ndu[e] = du_in[c];
+        for (int e = 0; e < 8; ++e) {
+          const int c = col<false>(0, e, li, tpr);
+          if (c < d) to[e] = p[c];
         }
-      }
+      };
+      get(x_in, nx);
+      if (has_dr) get(dr_in, ndr);
+      if (has_y) get(y_in, ny);
+      if (has_du) get(du_in, ndu);
       advance();
       --left;
     }
@@ -740,27 +741,26 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
   if (!wants_column_sums(a)) return;
   cp_async_wait<0>();
   __syncthreads();
-  float* sm = reinterpret_cast<float*>(ring);
-  for (int i = 0; i < groups; ++i) {
-    __syncthreads();
-    if (g == i)
+  // [group][P, S][d], then the groups in order
+  float* const sm = reinterpret_cast<float*>(ring);
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        float p8[8], s8[8];
-        from_f2(P[v], p8);
-        from_f2(S[v], s8);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int c = col<VEC>(v, e, li, tpr);
-          if (c < d) {
-            sm[c] = (i ? sm[c] : 0.f) + p8[e];
-            sm[d + c] = (i ? sm[d + c] : 0.f) + s8[e];
-          }
-        }
-      }
+  for (int v = 0; v < V; ++v) {
+    float f[8];
+    from_f2(P[v], f);
+    store8<VEC>(sm + (2 * g) * d, v, li, tpr, d, f);
+    from_f2(S[v], f);
+    store8<VEC>(sm + (2 * g + 1) * d, v, li, tpr, d, f);
   }
   __syncthreads();
-  leave_column_sums(a, sm);
+  for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
+    float v = 0.f;
+    for (int i = 0; i < groups; ++i) v += sm[2 * i * d + c];
+    if (a.partial) a.partial[(long long)blockIdx.x * 2 * d + c] = v;
+    else sm[c] = v;                      // only this thread reads group 0's entry
+  }
+  if (a.partial) return;
+  __syncthreads();
+  for (int c = threadIdx.x; c < d; c += blockDim.x) param_grads(a, c, sm[c], sm[d + c]);
 }
 
 // Gradient of wider rows: a group is the CTA, V pieces of 8 columns a thread, the
@@ -829,31 +829,32 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
   leave_column_sums(a, wide_sm);
 }
 
-// Adds the CTAs' column sums in order: 32 columns per CTA, 16 slices of the CTAs.
-constexpr int kSlices = 16;
+// Adds the CTAs' column sums in order: 32 columns per CTA, 32 slices of the CTAs.
+constexpr int kSlices = 32;
 __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormArgs a) {
-  __shared__ float part[2][kSlices][32];
+  __shared__ float part[2][32][kSlices + 1];
   pdl_wait();
   const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
   float P = 0.f, S = 0.f;
   if (c < a.d)
-#pragma unroll 4
+#pragma unroll 5
     for (int i = sl; i < a.n_partial; i += kSlices) {
       P += a.partial[(long long)i * 2 * a.d + c];
       S += a.partial[(long long)i * 2 * a.d + a.d + c];
     }
-  part[0][sl][threadIdx.x & 31] = P;
-  part[1][sl][threadIdx.x & 31] = S;
+  // the slices in order: warp w adds column w's
+  part[0][threadIdx.x & 31][sl] = P;
+  part[1][threadIdx.x & 31][sl] = S;
   __syncthreads();
-  if (sl == 0 && c < a.d) {
-    P = S = 0.f;
+  P = part[0][sl][threadIdx.x & 31];
+  S = part[1][sl][threadIdx.x & 31];
 #pragma unroll
-    for (int i = 0; i < kSlices; ++i) {
-      P += part[0][i][threadIdx.x & 31];
-      S += part[1][i][threadIdx.x & 31];
-    }
-    param_grads(a, c, P, S);
+  for (int o = 16; o > 0; o >>= 1) {
+    P += __shfl_xor_sync(0xffffffffu, P, o);
+    S += __shfl_xor_sync(0xffffffffu, S, o);
   }
+  const int mine = blockIdx.x * 32 + sl;
+  if ((threadIdx.x & 31) == 0 && mine < a.d) param_grads(a, mine, P, S);
   pdl_trigger();
 }
 
@@ -924,7 +925,7 @@ cudaError_t launch_grad_stream(const NormArgs& a, const GradShape& s, cudaStream
   constexpr int rows = grad_ring_bytes<A, R, V, VEC>() + grad_param_bytes<V>();
   constexpr int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
   constexpr int smem = rows > sums ? rows : sums;
-  if (a.y && a.du && a.dres && a.w_post && a.gate_kind != MOE_GATE_TOKEN)
+  if (a.y && a.du && a.dres && a.w_post)
     return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, true>, done_all, smem, smem, a, s, st);
   return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, false>, done, smem, smem, a, s, st);
 }
