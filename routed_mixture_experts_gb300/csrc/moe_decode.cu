@@ -567,7 +567,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_one_w2(const DecodeArgs 
 // joined in shared memory: a unit is over after d / 1024 steps, and one token's eight
 // experts fill the GPU.
 template <bool W13>
-__global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];       // the pairs' list, the tokens' rows
   __shared__ Plan s;
   __shared__ Tokens tok;
@@ -657,15 +657,15 @@ __global__ void __launch_bounds__(kThreads, 3) k_decode_split(const DecodeArgs a
 // ---- many units: a unit a warp ----------------------------------------------------
 //
 // One CTA of 16 warps an SM.  It stages the tokens of two passes of its run at once;
-// its warps then take the run's units one by one and stream them on their own: each
-// lane copies its own pieces of the next steps (and of the next unit's first) into
-// its own slots of a ring with cp.async and reads them back itself, so that nothing
-// in the stream waits for another warp.  Loads of 64 contiguous bytes a row and step
-// reach 5.8 TB/s here with three steps in flight (6.5 with 512).
+// its warps then take the run's units one by one and stream them on their own, each
+// through a ring of its own in shared memory filled with cp.async: a stage is 256
+// elements (128 bytes) of the unit's 32 rows and their scales, copied as whole lines,
+// the next stage (or the next unit's first) on its way while one is read.  Nothing in
+// the stream waits for another warp.
 constexpr int kStreamWarps = 16;
-constexpr int kStages = 3;
-constexpr int kStageBytes = kStreamWarps * 5 * 512;        // five 16-byte pieces a lane
-constexpr int kRingBytes = kStages * kStageBytes;
+constexpr int kStages = 2;
+constexpr int kStageBytes = 32 * 128 + 512;                 // codes, scales
+constexpr int kRingBytes = kStreamWarps * kStages * kStageBytes;
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -692,7 +692,8 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
   const int K = W13 ? a.d : a.I, per = W13 ? a.I / 16 : a.d / 32;
   const int steps = K / kStep, half = (q & 1) * 16;
   const long long gap = 32LL * (K / 2), far = (long long)(W13 ? a.I : 64) * (K / 2);
-  const uint8_t* const slot = smem + warp * (5 * 512) + lane * 16;
+  uint8_t* const ring = smem + warp * (kStages * kStageBytes);
+  const int pairs = steps / 2;          // stages of a unit (K is a multiple of 256)
   if (threadIdx.x < kThreads) s.count[threadIdx.x] = 0;
   __syncthreads();
   if (W13) {
@@ -718,27 +719,39 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
     if (threadIdx.x == 0) taken = kStreamWarps;
     __syncthreads();
     const int n0 = min(n, per - sub0), n1 = min(n - n0, per), here = n0 + n1;
+    // where the lane copies from: row lane / 8 of a unit, piece lane % 8; and the
+    // scales of line lane % 8 in K group lane / 8
     auto rows = [&](int v) {
-      return v < n0 ? rows_of<W13>(a, two[0][0], sub0 + v) : rows_of<W13>(a, two[1][0], v - n0);
+      const int e = v < n0 ? two[0][0] : two[1][0], sub = v < n0 ? sub0 + v : v - n0;
+      const int blk = sub >> 2, at = (sub & 3) * 8;
+      const long long row = (W13 ? (long long)e * 2 * a.I + blk * 64 : (long long)e * a.d + blk * 128) +
+                            at + (lane >> 3);
+      const long long block = W13 ? (long long)e * (a.I / 64) + blk : (long long)e * (a.d / 128) + blk;
+      Rows r;
+      r.code = a.codes + row * (K / 2) + (lane & 7) * 16;
+      r.scale = a.sf + (block * (K / 64) + (lane >> 3)) * 512 + (at + (lane & 7)) * 16;
+      return r;
     };
-    // The copies are kStages - 1 steps ahead: step `to_step` of the rows r comes next,
-    // of the warp's unit or (in_next) of the one it takes after that.
-    int unit = warp, next = here, to_step = 0, to_stage = 0;
+    // The copies are kStages - 1 stages ahead: stage `to` of the rows r comes next, of
+    // the warp's unit or (in_next) of the one it takes after that.
+    int unit = warp, next = here, to = 0, to_slot = 0;
     bool more = unit < here, in_next = false;
     Rows r{nullptr, nullptr};
     if (more) r = rows(unit);
     auto fetch = [&]() {
       if (more) {
-        const uint32_t at = smem_u32(slot) + to_stage * kStageBytes;
-        const uint8_t* p = r.code + to_step * (kStep / 2);
-        cp_async16(at, p);
-        cp_async16(at + 512, p + gap);
-        cp_async16(at + 1024, p + far);
-        cp_async16(at + 1536, p + far + gap);
-        cp_async16(at + 2048, r.scale + to_step * 1024);
-        to_stage = to_stage + 1 == kStages ? 0 : to_stage + 1;
-        if (++to_step == steps) {
-          to_step = 0;
+        // row 4 n + lane / 8; odd rows have their halves exchanged, so that the reads
+        // of two neighbouring rows fall on different banks
+        const uint32_t at = smem_u32(ring) + to_slot * kStageBytes + (lane >> 3) * 128 +
+                            ((lane & 7) ^ ((lane >> 3 & 1) << 2)) * 16;
+        const uint8_t* p = r.code + to * 128;
+#pragma unroll
+        for (int n = 0; n < 8; ++n)
+          cp_async16(at + n * 512, p + (n & 1) * (4 * (K / 2)) + (n >> 1 & 1) * gap + (n >> 2) * far);
+        cp_async16(smem_u32(ring) + to_slot * kStageBytes + 4096 + lane * 16, r.scale + to * 2048);
+        to_slot = to_slot + 1 == kStages ? 0 : to_slot + 1;
+        if (++to == pairs) {
+          to = 0;
           more = !in_next && next < here;
           in_next = true;
           if (more) r = rows(next);
@@ -764,9 +777,9 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
       __syncthreads();
     }
     {
-      const int i = warp >> 3;
+      const int i = (warp >> 3) & 1;     // a third group of warps has nothing to stage
       stage_tokens<W13, W13 ? 8 : 3>(a, tok[i], xs + i * a.cols * row_bytes(K), list + two[i][1],
-                                     i == 0 || n1 > 0 ? two[i][2] : 0);
+                                     warp < 8 || (warp < 16 && n1 > 0) ? two[i][2] : 0);
     }
     __syncthreads();
     int stage = 0;
@@ -776,16 +789,22 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
       const float alpha = a.w_scale[e];
       const uint8_t* lane_xs = xs + (i * a.cols + g) * row_bytes(K) + q * 16;
       float acc[2][2][4] = {};
-      for (int step = 0; step < steps; ++step) {
+      for (int j = 0; j < pairs; ++j) {
         cp_async_wait<kStages - 2>();
-        StepA w;
-        const uint8_t* at = slot + stage * kStageBytes;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) w.c[j] = *reinterpret_cast<const uint4*>(at + j * 512);
-        w.s = *reinterpret_cast<const uint4*>(at + 2048);
+        __syncwarp();                    // the other lanes' copies are there too, and
+        fetch();                         // they have read the stage that this fills
+        const uint8_t* at = ring + stage * kStageBytes;
         stage = stage + 1 == kStages ? 0 : stage + 1;
-        fetch();                         // into the stage read one step ago
-        mma_step(w, half, lane_xs + step * (2 * kStep), g < nt, acc);
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          StepA w;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            w.c[i] = *reinterpret_cast<const uint4*>(
+                at + (8 * i + g) * 128 + ((4 * b + q) ^ ((g & 1) << 2)) * 16);
+          w.s = *reinterpret_cast<const uint4*>(at + 4096 + (2 * b + (q >> 1)) * 128 + g * 16);
+          mma_step(w, half, lane_xs + (2 * j + b) * (2 * kStep), g < nt, acc);
+        }
       }
 #pragma unroll
       for (int c2 = 0; c2 < 2; ++c2) {
@@ -809,7 +828,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
       unit = next;                       // its first steps are on their way
       if (unit < here) {
         next = take();
-        in_next = !more;                 // all of them are (a row of kStages - 1 steps)
+        in_next = !more;                 // all of them are (a row of kStages - 1 stages)
         if (in_next && next < here) {
           more = true;
           r = rows(next);
@@ -817,6 +836,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
       }
     }
     cp_async_wait<0>();
+    __syncwarp();
     n -= here;                           // more to do: both passes are over
     pass += 2;
     sub0 = 0;
@@ -859,7 +879,7 @@ constexpr int kSplitDynamic = 200 * 1024, kStreamDynamic = 216 * 1024;
 // Tokens of a pass: up to 8, fewer where their rows would not fit.
 int split_cols(int K, int pairs, int T) {
   int room = kSplitDynamic - list_bytes(pairs);
-  if (room > 64 * 1024) room = 64 * 1024;              // three CTAs an SM
+  if (room > 88 * 1024) room = 88 * 1024;              // two CTAs an SM
   const int fit = room / row_bytes(K), most = T < kCols ? T : kCols;
   return fit < most ? fit : most;
 }
@@ -912,7 +932,7 @@ cudaError_t launch_product(DecodeArgs a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   a.cols = split_cols(K, pairs, a.T);
   const long long units = units_of<W13>(a);
-  return launch_pdl(k_decode_split<W13>, dim3((unsigned)(units < 3LL * sms ? units : 3LL * sms)),
+  return launch_pdl(k_decode_split<W13>, dim3((unsigned)(units < 2LL * sms ? units : 2LL * sms)),
                     dim3(kThreads), list_bytes(pairs) + a.cols * row_bytes(K), st, a);
 }
 
