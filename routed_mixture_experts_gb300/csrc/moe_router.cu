@@ -62,8 +62,8 @@ __device__ __forceinline__ void store_logit(uint16_t* p, float v) { *p = f2bf(v)
 // number, and 0 stays free for "not there"; -0 = +0.
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t b = __float_as_uint(v + 0.f);
-  if ((b & 0x7FFFFFFFu) > 0x7F800000u) return 1u;
-  return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+  const uint32_t key = b ^ ((uint32_t)((int32_t)b >> 31) | 0x80000000u);
+  return v != v ? 1u : key;
 }
 __device__ __forceinline__ float order_value(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key & 0x7FFFFFFFu : ~key);
@@ -79,13 +79,16 @@ __device__ __forceinline__ float warp_max(float v) {      // NaN only if every l
 }
 
 // A row's weights, before they are divided by their sum: exp(l - top) for the
-// softmax, sigmoid(l) * exp(-top) for the sigmoid, with top the largest logit (the
-// sigmoid: at most 0), so that the sum neither overflows nor underflows.  The
-// hardware exponential errs by a few 2^-23 near the largest logit, where the sum is.
+// softmax, sigmoid(l) * exp(-top) for the sigmoid, with top from shift_of() of the
+// largest logit, so that the sum neither overflows nor underflows.  The hardware
+// exponential errs by a few 2^-23 near the largest logit, where the sum is.
+__device__ __forceinline__ float shift_of(float largest, bool sig) {
+  return !sig ? largest : largest < -40.f ? largest : 0.f;
+}
 __device__ __forceinline__ float weight(float l, float top, bool sig) {
   if (!sig) return __expf(l - top);                       // l = -inf: 0 (top is not)
   const float t = __expf(-fabsf(l));
-  return __fdividef(l > 0.f ? 1.f : __expf(l - top), 1.f + t);
+  return __fdividef(l > 0.f ? 1.f : top == 0.f ? t : __expf(l - top), 1.f + t);
 }
 
 // Sums over the CTA's warps in a fixed order; all threads call it, warp 0 has the sum.
@@ -122,6 +125,9 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
   float ps[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) ps[i] = 0.f;
+  float bias[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) bias[i] = a.bias && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
   float z = 0.f;
   int live_rows = 0;
   for (long long t = (long long)blockIdx.x * nw + warp; t < a.T; t += (long long)gridDim.x * nw) {
@@ -149,7 +155,7 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int e = lane + 32 * i;
-      key[i] = e < E ? order_key(a.bias ? l[i] + a.bias[e] : l[i]) : 0u;
+      key[i] = e < E ? order_key(l[i] + bias[i]) : 0u;
       mine[e] = l[i];
       mx = fmaxf(mx, l[i]);
       nan |= l[i] != l[i];
@@ -190,7 +196,7 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     }
     if (mx == -INFINITY) mx = 0.f;         // NaN and -inf only: any shift gives NaN
     live_rows += 1;
-    const float top = sig ? fminf(mx, 0.f) : mx;
+    const float top = shift_of(mx, sig);
     float total = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -212,8 +218,8 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
         float m = -INFINITY;
         for (int j = lane; j < k; j += 32) m = fmaxf(m, mine[sel_id[warp][j]]);
         ctop = warp_max(m);
-        if (sig) ctop = fminf(ctop, 0.f);
-        if (nan && ctop == -INFINITY) ctop = top;
+        if (ctop != -INFINITY) ctop = shift_of(ctop, sig);
+        else if (nan) ctop = top;
       }
       float sum = 0.f;
       if (ctop != -INFINITY)
@@ -386,7 +392,7 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
           if (e >= 0 && e < E) ctop = fmaxf(ctop, lg[e]);
         }
         ctop = warp_max(ctop);
-        if (sig) ctop = fminf(ctop, 0.f);
+        if (ctop != -INFINITY) ctop = shift_of(ctop, sig);
         float sum = 0.f;
         if (ctop != -INFINITY)
           for (int j = lane; j < k; j += 32) {
@@ -412,18 +418,21 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
       }
       __syncwarp();
     }
-    // p = weight(l, stat): exp(l - lse), or sigmoid(l) / S (for l > 0 divided by S here)
-    const float inv = sig ? __expf(-stat) : 1.f;
+    // p = exp(l - lse), or sigmoid(l) / S with log S = stat
+    const float inv = sig ? __expf(-fmaxf(stat, -40.f)) : 1.f;
+    const float far = sig && stat < -40.f ? stat + 40.f : 0.f;     // S alone would underflow
     float gp = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float p = lane + 32 * i < E ? weight(l[i], stat, sig) : 0.f;
-      float after = 1.f;
+      float p, after = 1.f;
       if (sig) {
-        const float u = __expf(-fabsf(l[i]));
-        after = __fdividef(l[i] > 0.f ? u : 1.f, 1.f + u);       // 1 - sigmoid
-        if (l[i] > 0.f) p *= inv;
+        const float u = __expf(-fabsf(l[i])), v = __fdividef(1.f, 1.f + u);
+        after = l[i] > 0.f ? u * v : v;                            // 1 - sigmoid
+        p = (l[i] > 0.f ? v : (far == 0.f ? u : __expf(l[i] - far)) * v) * inv;
+      } else {
+        p = __expf(l[i] - stat);
       }
+      if (lane + 32 * i >= E) p = 0.f;
       const float x = ex[lane + 32 * i];
       const float g = b[i] + (in_g ? x : 0.f);
       gp += p * g;
