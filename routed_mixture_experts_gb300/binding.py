@@ -240,12 +240,15 @@ class MoePlan:
         xp = _want(x, "x", bf16, (n, self.d))
         if y is None:
             y = torch.empty((n, self.d), dtype=bf16, device=x.device)
+            yp = y.data_ptr()
+        else:
+            yp = _want(y, "y", bf16, (n, self.d))
         w13q, w13s, w13c, w2q, w2s, w2c = prepared
         _check(_lib.moe_decode_nvfp4(
             self.ptr, xp, _want(ids, "ids", torch.int32, (n, k)),
             _want(scores, "scores", torch.float32, (n, k)), n, w13q.data_ptr(), w13s.data_ptr(),
             w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
-            _want(y, "y", bf16, (n, self.d)), _raw_stream(stream)), "decode_nvfp4")
+            yp, _raw_stream(stream)), "decode_nvfp4")
         return y
 
     def backward(self, dy, w13, w2, dw13, dw2, dx=None, dscores=None, stream=None):
@@ -643,33 +646,50 @@ class MoeBlockNorm:
         if T > self.max_tokens:
             raise MoeError(MOE_ERR_INVALID_ARG, "block norm: %d rows, made for %d" % (
                 T, self.max_tokens))
-        shape = (T, self.d)
+        d = self.d
+        shape = (T, d)
         act, res = self.dtype, self.residual_dtype
         rp, ld_r = _rows(residual_out, "residual_out", res, shape)
         wp, gp, wq, gshape = self._params(T, w_post, gate, w_pre)
-        none = (None, 0)
-        yp, ld_y = none if y is None else _rows(y, "y", act, shape)
-        gr, ld_gr = none if d_residual_out is None else _rows(d_residual_out, "d_residual_out",
-                                                              res, shape)
-        gu, ld_gu = none if d_u is None else _rows(d_u, "d_u", act, shape)
+        yp = gr = gu = op = dp = wpp = ggp = wqp = None
+        ld_y = ld_gr = ld_gu = ld_d = 0
+        if y is not None:
+            yp, ld_y = _rows(y, "y", act, shape)
+        if d_residual_out is not None:
+            gr, ld_gr = _rows(d_residual_out, "d_residual_out", res, shape)
+        if d_u is not None:
+            gu, ld_gu = _rows(d_u, "d_u", act, shape)
+        # outputs: the caller's are checked, fresh ones are what they have to be
         new = torch.zeros if accumulate else torch.empty
-        if d_residual is None:
+        if d_residual is not None:
+            op, ld_o = _rows(d_residual, "d_residual", res, shape)
+        else:
             d_residual = torch.empty(shape, dtype=res, device=dev)
-        if dy is None and y is not None:
+            op, ld_o = d_residual.data_ptr(), d
+        if dy is not None:
+            dp, ld_d = _rows(dy, "dy", act, shape)
+        elif y is not None:
             dy = torch.empty(shape, dtype=act, device=dev)
-        if dw_post is None and w_post is not None:
-            dw_post = new(self.d, dtype=f32, device=dev)
-        if dgate is None and gate is not None:
+            dp, ld_d = dy.data_ptr(), d
+        if dw_post is not None:
+            wpp = _want(dw_post, "dw_post", f32, (d,))
+        elif w_post is not None:
+            dw_post = new((d,), dtype=f32, device=dev)
+            wpp = dw_post.data_ptr()
+        if dgate is not None:
+            ggp = _want(dgate, "dgate", f32, gshape)
+        elif gate is not None:
             dgate = new(gshape, dtype=f32, device=dev)
-        if dw_pre is None and w_pre is not None:
-            dw_pre = new(self.d, dtype=f32, device=dev)
+            ggp = dgate.data_ptr()
+        if dw_pre is not None:
+            wqp = _want(dw_pre, "dw_pre", f32, (d,))
+        elif w_pre is not None:
+            dw_pre = new((d,), dtype=f32, device=dev)
+            wqp = dw_pre.data_ptr()
         if self.workspace is None:
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
-        op, ld_o = _rows(d_residual, "d_residual", res, shape)
-        dp, ld_d = none if dy is None else _rows(dy, "dy", act, shape)
         _check(_lib.moe_block_norm_backward(
             self._desc, T, rp, ld_r, yp, ld_y, gr, ld_gr, gu, ld_gu, wp, gp, wq, op, ld_o, dp, ld_d,
-            _maybe(dw_post, "dw_post", f32, (self.d,)), _maybe(dgate, "dgate", f32, gshape),
-            _maybe(dw_pre, "dw_pre", f32, (self.d,)), 1 if accumulate else 0,
-            self.workspace.data_ptr(), self._ws_bytes, _raw_stream(stream)), "block norm backward")
+            wpp, ggp, wqp, 1 if accumulate else 0, self.workspace.data_ptr(), self._ws_bytes,
+            _raw_stream(stream)), "block norm backward")
         return BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre)

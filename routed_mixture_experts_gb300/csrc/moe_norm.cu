@@ -876,8 +876,9 @@ GradShape grad_shape(int T, int d, bool vec, bool bf16) {
   s.tpr = round32((d + s.pieces * 8 - 1) / (s.pieces * 8));
   const int threads = d <= kStreamMaxWidth && s.pieces == 2 ? kGradThreads<2> : kStreamThreads;
   s.groups = threads / s.tpr;
-  const int want = (T + s.groups - 1) / s.groups, sms = num_sms();
-  s.grid = want < 1 ? 1 : want < sms ? want : sms;
+  // a few rows: one CTA, which needs no second launch to add the column sums
+  const int want = T <= 4 * s.groups ? 1 : (T + s.groups - 1) / s.groups, sms = num_sms();
+  s.grid = want < sms ? want : sms;
   return s;
 }
 
