@@ -358,10 +358,14 @@ int moe_forward_nvfp4(moe_plan* plan, const void* x, const int32_t* ids, const f
  *   h = silu(G) * U, (G, U) = w13_scale[e] * W13[e] . x[t] (clipped to the plan's
  *   clamp), e = ids[t,j], in fixed j order.
  * tokens: 0 <= tokens <= min(T, MOE_DECODE_MAX_TOKENS) of the plan's T; x [tokens,
- * d] bf16, ids and scores [tokens, k], y [tokens, d] bf16 (16-byte aligned).  Each
- * chosen expert is read once for every 8 of its tokens; beyond some tens of tokens
- * per expert moe_forward_nvfp4 is the faster call.  Bad ids are dropped and
- * reported as by moe_forward.  Two launches; NVFP4 plans only.
+ * d] bf16, ids and scores [tokens, k], y [tokens, d] bf16 (x, y and the weights
+ * 16-byte aligned).  Each chosen expert is read once for every 8 of its tokens; for
+ * prompts moe_forward_nvfp4 is the faster call.  Bad ids are dropped and reported as
+ * by moe_forward; a token's NaN or infinity stays in its own row of y.  Two launches
+ * for one token of up to 8 experts, else three.  NVFP4 plans only; MOE_ERR_UNSUPPORTED
+ * also where the list of tokens*k pairs (4 bytes each) and one token's row of fp16
+ * do not fit in 200 KB together.  The workspace holds h and the experts' outputs of
+ * the call, apart from what the other calls of the plan use.
  */
 #define MOE_DECODE_MAX_TOKENS 256
 int moe_decode_nvfp4(moe_plan* plan, const void* x, const int32_t* ids, const float* scores,

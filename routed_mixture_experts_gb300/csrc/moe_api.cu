@@ -1446,7 +1446,9 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
     return MOE_ERR_INVALID_ARG;
   if (!p->ws) return MOE_ERR_WORKSPACE;
   if (tokens == 0) return MOE_OK;
-  if (!x || !ids || !scores || !y || !aligned16(x) || !aligned16(y)) return MOE_ERR_INVALID_ARG;
+  if (!x || !ids || !scores || !y || !aligned16(x) || !aligned16(y) ||
+      ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(scores)) & 3u))
+    return MOE_ERR_INVALID_ARG;
   if (!decode_nvfp4_fits(p->d, p->I, tokens * p->k)) return MOE_ERR_UNSUPPORTED;
   DecodeCall c = {};
   c.x = x; c.ids = ids; c.scores = scores;

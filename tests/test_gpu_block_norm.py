@@ -225,6 +225,32 @@ def test_gradient_against_differences(moe):
         assert abs(slope - mine) <= 1e-6 * size + 1e-6, name
 
 
+def test_rows_further_apart_than_32_bits_reach(moe):
+    """Three rows of every tensor 2^30 + 8 elements apart: offsets beyond 2^31."""
+    c = Case(moe, 3, 256, "bf16")
+    want = c.h.forward(c.res, **c.params())
+    g = c.h.backward(c.res, c.d_out, c.d_u, **c.params())
+    apart = 2 ** 30 + 8
+    pool = torch.empty(2 * apart + 4096, dtype=BF, device="cuda")
+    at = 0
+
+    def spread(t=None):
+        nonlocal at
+        v = pool.as_strided((3, 256), (apart, 1), at)
+        at += 256
+        if t is not None:
+            v.copy_(t)
+        return v
+
+    res, y, d_out, d_u = (spread(t) for t in (c.res, c.y, c.d_out, c.d_u))
+    p = dict(y=y, w_post=c.w_post, gate=c.gate, w_pre=c.w_pre)
+    out, u = c.h.forward(res, **p, residual_out=spread(), u=spread())
+    assert torch.equal(out, want[0]) and torch.equal(u, want[1])
+    b = c.h.backward(res, d_out, d_u, **p, d_residual=spread(), dy=spread())
+    for x, z in zip(b, g):
+        assert torch.equal(x, z)
+
+
 def test_another_stream(moe):
     c = Case(moe, 512, 2048)
     want = c.h.forward(c.res, **c.params())

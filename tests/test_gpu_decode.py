@@ -256,6 +256,15 @@ def test_refusals(moe):
     with pytest.raises(moe.MoeError):
         wide.decode_nvfp4(big, torch.zeros(257, 2, dtype=torch.int32, device="cuda"),
                           torch.zeros(257, 2, device="cuda"), prep)
+    # 65536 pairs: their list does not fit in shared memory
+    many = moe.MoePlan(256, 256, 256, 256, 256, precision=moe.MOE_PREC_NVFP4, flags=0)
+    with pytest.raises(moe.MoeError) as e:
+        many.decode_nvfp4(big[:256], torch.arange(256, dtype=torch.int32, device="cuda").expand(
+            256, 256).contiguous(), torch.zeros(256, 256, device="cuda"),
+            moe.prepare_weights_nvfp4(
+                torch.zeros(256, 512, 256, dtype=torch.bfloat16, device="cuda"),
+                torch.zeros(256, 256, 256, dtype=torch.bfloat16, device="cuda")))
+    assert e.value.code == moe.MOE_ERR_UNSUPPORTED
     p16 = moe.MoePlan(4, 256, 256, 4, 2, flags=0)
     with pytest.raises(moe.MoeError) as e:
         p16.decode_nvfp4(*args, prep)
