@@ -91,55 +91,73 @@ __device__ __forceinline__ void store_vec8(uint16_t* p, const float (&f)[8]) {
                                             pack_bf2(f[4], f[5]), pack_bf2(f[6], f[7]));
 }
 
-// A thread's 8 columns of piece v of a row: consecutive ones where every row is
-// 16-byte aligned and d a multiple of 8 (VEC), else one of each tpr columns.
-template <bool VEC>
+// A thread's 8 columns of piece v of a row, W of them next to each other.  Where every
+// row is 16-byte aligned and d a multiple of 8, W is 8 if all tensors are bf16 and 4
+// if one is fp32 (16 bytes of that one, so that a warp's accesses are whole lines:
+// eight fp32 columns a thread touched every sector twice, 56 against 47 us for the
+// fp32 gradient at T=8192, d=1024).  Else W is 1, one of each tpr columns.
+template <int W>
 __device__ __forceinline__ int col(int v, int e, int li, int tpr) {
-  return VEC ? (v * tpr + li) * 8 + e : (v * 8 + e) * tpr + li;
+  return W == 8 ? (v * tpr + li) * 8 + e
+                : W == 4 ? ((2 * v + (e >> 2)) * tpr + li) * 4 + (e & 3) : (v * 8 + e) * tpr + li;
+}
+
+__device__ __forceinline__ void load_vec4(const float* p, float* f) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+}
+__device__ __forceinline__ void load_vec4(const uint16_t* p, float* f) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  f[0] = __uint_as_float(v.x << 16);
+  f[1] = __uint_as_float(v.x & 0xFFFF0000u);
+  f[2] = __uint_as_float(v.y << 16);
+  f[3] = __uint_as_float(v.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void store_vec4(float* p, const float* f) {
+  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+}
+__device__ __forceinline__ void store_vec4(uint16_t* p, const float* f) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]));
 }
 
 // columns past the row's end read as 0
-template <bool VEC, typename T>
+template <int W, typename T>
 __device__ __forceinline__ void load8(const T* p, int v, int li, int tpr, int d, float (&f)[8]) {
-  if (VEC) {
-    const int c = col<true>(v, 0, li, tpr);
+#pragma unroll
+  for (int e = 0; e < 8; e += W) {
+    const int c = col<W>(v, e, li, tpr);
     if (c < d) {
-      load_vec8(p + c, f);
+      if constexpr (W == 8) load_vec8(p + c, f);
+      else if constexpr (W == 4) load_vec4(p + c, f + e);
+      else f[e] = to_f(p[c]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[e] = 0.f;
-    }
-  } else {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col<false>(v, e, li, tpr);
-      f[e] = c < d ? to_f(p[c]) : 0.f;
+      for (int i = 0; i < W; ++i) f[e + i] = 0.f;
     }
   }
 }
 
-template <bool VEC, typename T>
+template <int W, typename T>
 __device__ __forceinline__ void store8(T* p, int v, int li, int tpr, int d, const float (&f)[8]) {
-  if (VEC) {
-    const int c = col<true>(v, 0, li, tpr);
-    if (c < d) store_vec8(p + c, f);
-  } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col<false>(v, e, li, tpr);
-      if (c < d) p[c] = from_f<T>(f[e]);
+  for (int e = 0; e < 8; e += W) {
+    const int c = col<W>(v, e, li, tpr);
+    if (c < d) {
+      if constexpr (W == 8) store_vec8(p + c, f);
+      else if constexpr (W == 4) store_vec4(p + c, f + e);
+      else p[c] = from_f<T>(f[e]);
     }
   }
 }
 
 // parameters (fp32 or bf16), at the same columns
-template <bool VEC>
+template <int W>
 __device__ __forceinline__ void load8_param(const void* p, int bf16, int v, int li, int tpr, int d,
                                             float (&f)[8]) {
   if (bf16)
-    load8<VEC>(static_cast<const uint16_t*>(p), v, li, tpr, d, f);
+    load8<W>(static_cast<const uint16_t*>(p), v, li, tpr, d, f);
   else
-    load8<VEC>(static_cast<const float*>(p), v, li, tpr, d, f);
+    load8<W>(static_cast<const float*>(p), v, li, tpr, d, f);
 }
 
 __device__ __forceinline__ float param(const void* p, int bf16, long long i) {
@@ -171,7 +189,7 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
 
 // Forward, a row per group of tpr threads and no loop: few rows, wide rows and rows
 // without 16-byte alignment.
-template <typename A, typename R, int V, bool VEC>
+template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   __shared__ float red[2][32];
   pdl_wait();
@@ -182,13 +200,13 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   float x[V][8];
 #pragma unroll
   for (int v = 0; v < V; ++v)
-    load8<VEC>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
+    load8<W>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
   if (a.y) {
     float y[V][8];
     float s = 0.f;
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load8<VEC>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
+      load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
     }
@@ -201,19 +219,19 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
     for (int v = 0; v < V; ++v) {
       if (a.w_post) {
         float w[8];
-        load8_param<VEC>(a.w_post, a.param_bf16, v, li, tpr, d, w);
+        load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[v][e] *= w[e];
       }
       if (a.gate_kind == MOE_GATE_CHANNEL) {
         float w[8];
-        load8_param<VEC>(a.gate, a.param_bf16, v, li, tpr, d, w);
+        load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) y[v][e] *= w[e];
       }
 #pragma unroll
       for (int e = 0; e < 8; ++e) x[v][e] += f * y[v][e];
-      store8<VEC>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, x[v]);
+      store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, x[v]);
     }
   }
   if (a.u) {
@@ -226,10 +244,10 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       float w[8];
-      load8_param<VEC>(a.w_pre, a.param_bf16, v, li, tpr, d, w);
+      load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w);
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] = x[v][e] * rs * w[e];
-      store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, w);
+      store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, w);
     }
   }
   pdl_trigger();
@@ -238,19 +256,15 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
 
 // ---- rows streamed through shared memory ---------------------------------------
 //
-// Rows of up to 4096 aligned columns: persistent CTAs of 512 threads, a thread owning
-// 8 columns of every row of its group.  It copies its own 16-byte pieces of the next
-// rows into its own slots of a ring with cp.async and reads them back itself, so a
-// copy in flight costs no register and needs no barrier; the parameters of its
-// columns stay in registers.
+// Many rows: persistent CTAs of 512 threads, a thread owning 8 V columns of every row
+// of its group.  It copies its own pieces of the next rows into its own slots of a
+// ring with cp.async and reads them back itself, so a copy in flight costs no register
+// and needs no barrier; the parameters of its columns stay in registers.
 
 constexpr int kStreamThreads = 512;
 constexpr int kStreamMaxWidth = kStreamThreads * 8;
 constexpr int kStages = 3;
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
@@ -259,109 +273,187 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// A thread's slots of one tensor of one stage (TH threads): sizeof(T) / 2 pieces of
-// 16 bytes, TH pieces apart so that a warp reads and writes consecutive pieces.
+// A thread's slots of one tensor, piece and stage (TH threads): what it copies at a
+// time lies TH of them apart, so that a warp reads and writes whole lines.
 template <typename T, int TH = kStreamThreads>
 __host__ __device__ constexpr int slot_bytes() { return TH * 8 * (int)sizeof(T); }
 
-template <int TH = kStreamThreads, typename T>
-__device__ __forceinline__ void slot_copy(uint32_t slot, const T* src) {
+// Start copying the thread's 8 columns of piece v of the row at `row`.
+template <int W, int TH = kStreamThreads, typename T>
+__device__ __forceinline__ void slot_copy(uint32_t slot, const T* row, int v, int li, int tpr,
+                                          int d) {
+  constexpr int bytes = W * (int)sizeof(T);
 #pragma unroll
-  for (int i = 0; i < (int)sizeof(T) / 2; ++i)
-    cp_async16(slot + (i * TH + threadIdx.x) * 16, src + i * (16 / sizeof(T)));
+  for (int e = 0; e < 8; e += W) {
+    const int c = col<W>(v, e, li, tpr);
+    if (c < d) {
+      const uint32_t at = slot + (e / W * TH + threadIdx.x) * bytes;
+      if constexpr (bytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(row + c) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(at), "l"(row + c) : "memory");
+    }
+  }
 }
-template <int TH = kStreamThreads>
-__device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const uint16_t*) {
-  load_vec8(reinterpret_cast<const uint16_t*>(slot + threadIdx.x * 16), f);
+template <int W, int TH = kStreamThreads, typename T>
+__device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const T*) {
+#pragma unroll
+  for (int e = 0; e < 8; e += W) {
+    const T* p = reinterpret_cast<const T*>(slot) + (e / W * TH + threadIdx.x) * W;
+    if constexpr (W == 8) load_vec8(p, f);
+    else load_vec4(p, f + e);
+  }
 }
-template <int TH = kStreamThreads>
-__device__ __forceinline__ void slot_read(const uint8_t* slot, float (&f)[8], const float*) {
-  const float4 a = *reinterpret_cast<const float4*>(slot + threadIdx.x * 16);
-  const float4 b = *reinterpret_cast<const float4*>(slot + (TH + threadIdx.x) * 16);
-  f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
-  f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+// A thread's 8 values of a parameter.
+template <int TH>
+__device__ __forceinline__ void param_read(const uint8_t* slot, float (&f)[8]) {
+  load_vec4(reinterpret_cast<const float*>(slot) + threadIdx.x * 4, f);
+  load_vec4(reinterpret_cast<const float*>(slot) + (TH + threadIdx.x) * 4, f + 4);
 }
 template <int TH>
-__device__ __forceinline__ void slot_write(uint8_t* slot, const float (&f)[8]) {
+__device__ __forceinline__ void param_write(uint8_t* slot, const float (&f)[8]) {
   *reinterpret_cast<float4*>(slot + threadIdx.x * 16) = make_float4(f[0], f[1], f[2], f[3]);
   *reinterpret_cast<float4*>(slot + (TH + threadIdx.x) * 16) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Forward over streamed rows.
-template <typename A, typename R>
-__global__ void __launch_bounds__(kStreamThreads, 2) k_block_norm_stream(const NormArgs a) {
+// Forward over many rows.  W > 1: the next rows through the ring; else the next row
+// in registers, as it is in memory (a conversion would wait for the load).
+template <typename A, typename R, int V>
+__host__ __device__ constexpr int stream_ring_bytes() {
+  return kStages * V * (slot_bytes<A>() + slot_bytes<R>());
+}
+
+template <typename A, typename R, int V, int W>
+__global__ void __launch_bounds__(kStreamThreads, V == 1 && W > 1 ? 2 : 1) k_block_norm_stream(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][kStreamThreads / 32];
-  constexpr int kStage = slot_bytes<A>() + slot_bytes<R>();
+  constexpr int kPiece = slot_bytes<A>() + slot_bytes<R>(), kStage = V * kPiece;
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
-  const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr;
-  const int d = a.d, c0 = li * 8;
-  const bool in = c0 < d;
+  const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
   const long long first = (long long)blockIdx.x * groups + g, hop = (long long)gridDim.x * groups;
   const uint32_t base = smem_u32(ring);
+  const A* const y_in = static_cast<const A*>(a.y);
+  const R* const x_in = static_cast<const R*>(a.res);
   auto fetch = [&](long long row, int stage) {
-    if (in && row < a.T) {
-      if (a.y) slot_copy(base + stage * kStage, static_cast<const A*>(a.y) + row * a.ld_y + c0);
-      slot_copy(base + stage * kStage + slot_bytes<A>(),
-                static_cast<const R*>(a.res) + row * a.ld_res + c0);
-    }
+    if (row < a.T)
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint32_t at = base + stage * kStage + v * kPiece;
+        if constexpr (W > 1) {
+          if (a.y) slot_copy<W>(at, y_in + row * a.ld_y, v, li, tpr, d);
+          slot_copy<W>(at + slot_bytes<A>(), x_in + row * a.ld_res, v, li, tpr, d);
+        }
+      }
     cp_async_commit();
   };
+  A ny[V][8];
+  R nx[V][8];
+  auto load = [&](long long row) {
+    if (row >= a.T) return;
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
-  float q[8], w[8];          // alpha * w_post * channel gate, w_pre
+    for (int v = 0; v < V; ++v)
 #pragma unroll
-  for (int e = 0; e < 8; ++e) q[e] = a.alpha, w[e] = 0.f;
-  if (in) {
-    float v[8];
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<1>(v, e, li, tpr);
+        if (c < d) nx[v][e] = x_in[row * a.ld_res + c];
+      }
+    if (!a.y) return;
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int c = col<1>(v, e, li, tpr);
+        if (c < d) ny[v][e] = y_in[row * a.ld_y + c];
+      }
+  };
+  if (W > 1) {
+    // slots that no copy fills (columns past the row, no y) read as zero
+    for (int i = threadIdx.x; i < kStages * kStage / 16; i += blockDim.x)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+  } else {
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) nx[v][e] = 0, ny[v][e] = 0;
+    load(first);
+  }
+  float q[V][8], w[V][8];      // alpha * w_post * channel gate, w_pre
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    float f[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) q[v][e] = a.alpha, w[v][e] = 0.f;
     if (a.y && a.w_post) {
-      load8_param<true>(a.w_post, a.param_bf16, 0, li, tpr, d, v);
+      load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] *= v[e];
+      for (int e = 0; e < 8; ++e) q[v][e] *= f[e];
     }
     if (a.y && a.gate_kind == MOE_GATE_CHANNEL) {
-      load8_param<true>(a.gate, a.param_bf16, 0, li, tpr, d, v);
+      load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[e] *= v[e];
+      for (int e = 0; e < 8; ++e) q[v][e] *= f[e];
     }
-    if (a.u) load8_param<true>(a.w_pre, a.param_bf16, 0, li, tpr, d, w);
+    if (a.u) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w[v]);
   }
   int stage = 0, flip = 0;
   for (long long row = first; row < a.T; row += hop) {
-    float x[8], y[8], s;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = y[e] = 0.f;
+    float x[V][8], y[V][8], s;
     float f = 1.f;
     if (a.y && a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
-    cp_async_wait<kStages - 2>();
-    if (in) {
-      if (a.y) slot_read(ring + stage * kStage, y, static_cast<const A*>(nullptr));
-      slot_read(ring + stage * kStage + slot_bytes<A>(), x, static_cast<const R*>(nullptr));
+    if (W > 1) {
+      cp_async_wait<kStages - 2>();
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const uint8_t* at = ring + stage * kStage + v * kPiece;
+        if constexpr (W > 1) {
+          slot_read<W>(at, y[v], y_in);
+          slot_read<W>(at + slot_bytes<A>(), x[v], x_in);
+        }
+      }
+      // into the slots read one row ago
+      fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+      stage = stage + 1 == kStages ? 0 : stage + 1;
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] = to_f(nx[v][e]), y[v][e] = to_f(ny[v][e]);
+      load(row + hop);
     }
-    // into the slots read one row ago
-    fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
     if (a.y) {
       if (a.w_post) {
         s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s += y[e] * y[e];
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
         f *= inv_rms(group_sum(s, &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
       }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += f * (q[e] * y[e]);
-      if (in) store_vec8(static_cast<R*>(a.out) + row * a.ld_out + c0, x);
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] += f * (q[v][e] * y[v][e]);
+        store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, x[v]);
+      }
     }
     if (a.u) {
       s = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += x[e] * x[e];
+      for (int v = 0; v < V; ++v)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s += x[v][e] * x[v][e];
       const float rs = inv_rms(group_sum(s, &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] *= rs * w[e];
-      if (in) store_vec8(static_cast<A*>(a.u) + row * a.ld_u + c0, x);
+      for (int v = 0; v < V; ++v) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[v][e] *= rs * w[v][e];
+        store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, x[v]);
+      }
     }
-    stage = stage + 1 == kStages ? 0 : stage + 1;
     flip ^= 1;
   }
   pdl_trigger();
@@ -527,7 +619,7 @@ __device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
 }
 
 // Gradient of rows of up to 4096 columns: row groups walk the rows, the next row on
-// its way (VEC: through the ring; else in registers), the sums of a thread's 8 V
+// its way (W > 1: through the ring; else in registers), the sums of a thread's 8 V
 // columns in registers, its parameters in slots of its own.  V = 2 halves what a row
 // costs beside its elements (the reduction, the factors, the addresses).  ALL: every
 // tensor is given.
@@ -535,9 +627,9 @@ template <int V>
 constexpr int kGradThreads = V == 2 ? 384 : kStreamThreads;
 constexpr int kGradStages = 2;
 
-template <typename A, typename R, int V, bool VEC>
+template <typename A, typename R, int V, int W>
 __host__ __device__ constexpr int grad_ring_bytes() {
-  return VEC ? kGradStages * V * 2 * (slot_bytes<A, kGradThreads<V>>() + slot_bytes<R, kGradThreads<V>>())
+  return W > 1 ? kGradStages * V * 2 * (slot_bytes<A, kGradThreads<V>>() + slot_bytes<R, kGradThreads<V>>())
              : 0;
 }
 template <int V>
@@ -545,15 +637,15 @@ __host__ __device__ constexpr int grad_param_bytes() {
   return 2 * V * slot_bytes<float, kGradThreads<V>>();
 }
 
-template <typename A, typename R, int V, bool VEC, bool ALL>
+template <typename A, typename R, int V, int W, bool ALL>
 __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];       // ring, then the parameters' slots
   __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
-  static_assert(VEC || V == 1, "rows in registers: one piece a thread");
+  static_assert(W > 1 || V == 1, "rows in registers: one piece a thread");
   constexpr int TH = kGradThreads<V>;
   constexpr int kA = slot_bytes<A, TH>(), kR = slot_bytes<R, TH>(), kF = slot_bytes<float, TH>();
   constexpr int kPiece = 2 * kA + 2 * kR, kStage = V * kPiece;
-  uint8_t* const params = ring + grad_ring_bytes<A, R, V, VEC>();
+  uint8_t* const params = ring + grad_ring_bytes<A, R, V, W>();
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
   const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
@@ -580,14 +672,11 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
     if (left > 0) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        const int c = col<true>(v, 0, li, tpr);
-        if (c < d) {
-          const uint32_t at = base + stage * kStage + v * kPiece;
-          slot_copy<TH>(at, x_in + c);
-          if (has_dr) slot_copy<TH>(at + kR, dr_in + c);
-          if (has_y) slot_copy<TH>(at + 2 * kR, y_in + c);
-          if (has_du) slot_copy<TH>(at + 2 * kR + kA, du_in + c);
-        }
+        const uint32_t at = base + stage * kStage + v * kPiece;
+        slot_copy<W, TH>(at, x_in, v, li, tpr, d);
+        if (has_dr) slot_copy<W, TH>(at + kR, dr_in, v, li, tpr, d);
+        if (has_y) slot_copy<W, TH>(at + 2 * kR, y_in, v, li, tpr, d);
+        if (has_du) slot_copy<W, TH>(at + 2 * kR + kA, du_in, v, li, tpr, d);
       }
       advance();
       --left;
@@ -602,7 +691,7 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
       auto get = [&](const auto* p, auto (&to)[8]) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          const int c = col<false>(0, e, li, tpr);
+          const int c = col<1>(0, e, li, tpr);
           if (c < d) to[e] = p[c];
         }
       };
@@ -614,10 +703,11 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
       --left;
     }
   };
-  if (VEC) {
+  if (W > 1) {
     // slots that no copy fills (columns past the row, absent tensors) read as zero
-    for (int i = 0; i < kGradStages * kStage / (TH * 16); ++i)
-      *reinterpret_cast<uint4*>(ring + (i * TH + threadIdx.x) * 16) = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = threadIdx.x; i < kGradStages * kStage / 16; i += blockDim.x)
+      reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
+    __syncthreads();
     fetch(0);
   } else {
 #pragma unroll
@@ -631,7 +721,7 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
     float w8[8], q8[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int c = col<VEC>(v, e, li, tpr);
+      const int c = col<W>(v, e, li, tpr);
       w8[e] = 0.f;
       q8[e] = a.alpha;
       if (c < d) {
@@ -640,8 +730,8 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
         if (has_y && a.gate_kind == MOE_GATE_CHANNEL) q8[e] *= param(a.gate, a.param_bf16, c);
       }
     }
-    slot_write<TH>(params + 2 * v * kF, w8);
-    slot_write<TH>(params + (2 * v + 1) * kF, q8);
+    param_write<TH>(params + 2 * v * kF, w8);
+    param_write<TH>(params + (2 * v + 1) * kF, q8);
 #pragma unroll
     for (int i = 0; i < 4; ++i) P[v][i] = S[v][i] = zero;
   }
@@ -651,18 +741,18 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
   for (int n = 0; n < rows; ++n, row += hop) {
     f2 x[V][4], y[V][4], dr[V][4], du[V][4];
     float f[8];
-    if (VEC) {
+    if (W > 1) {
       cp_async_wait<0>();
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint8_t* at = ring + stage * kStage + v * kPiece;
-        slot_read<TH>(at, f, static_cast<const R*>(nullptr));
+        if constexpr (W > 1) slot_read<W, TH>(at, f, x_in);
         to_f2(f, x[v]);
-        slot_read<TH>(at + kR, f, static_cast<const R*>(nullptr));
+        if constexpr (W > 1) slot_read<W, TH>(at + kR, f, x_in);
         to_f2(f, dr[v]);
-        slot_read<TH>(at + 2 * kR, f, static_cast<const A*>(nullptr));
+        if constexpr (W > 1) slot_read<W, TH>(at + 2 * kR, f, y_in);
         to_f2(f, y[v]);
-        slot_read<TH>(at + 2 * kR + kA, f, static_cast<const A*>(nullptr));
+        if constexpr (W > 1) slot_read<W, TH>(at + 2 * kR + kA, f, y_in);
         to_f2(f, du[v]);
       }
       stage ^= 1;
@@ -688,9 +778,9 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         f2 wp[4], q[4];
-        slot_read<TH>(params + 2 * v * kF, f, static_cast<const float*>(nullptr));
+        param_read<TH>(params + 2 * v * kF, f);
         to_f2(f, wp);
-        slot_read<TH>(params + (2 * v + 1) * kF, f, static_cast<const float*>(nullptr));
+        param_read<TH>(params + (2 * v + 1) * kF, f);
         to_f2(f, q);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -716,9 +806,9 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       f2 wp[4], q[4];
-      slot_read<TH>(params + 2 * v * kF, f, static_cast<const float*>(nullptr));
+      param_read<TH>(params + 2 * v * kF, f);
       to_f2(f, wp);
-      slot_read<TH>(params + (2 * v + 1) * kF, f, static_cast<const float*>(nullptr));
+      param_read<TH>(params + (2 * v + 1) * kF, f);
       to_f2(f, q);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -728,10 +818,10 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
         y[v][i] = mul2(gy, fma2(ncy, y[v][i], mul2(q[i], dr[v][i])));
       }
       from_f2(dr[v], f);
-      store8<VEC>(dr_out, v, li, tpr, d, f);
+      store8<W>(dr_out, v, li, tpr, d, f);
       if (has_y && a.u) {
         from_f2(y[v], f);
-        store8<VEC>(dy_out, v, li, tpr, d, f);
+        store8<W>(dy_out, v, li, tpr, d, f);
       }
     }
     dr_out += hop * a.ld_out;
@@ -747,9 +837,9 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
   for (int v = 0; v < V; ++v) {
     float f[8];
     from_f2(P[v], f);
-    store8<VEC>(sm + (2 * g) * d, v, li, tpr, d, f);
+    store8<W>(sm + (2 * g) * d, v, li, tpr, d, f);
     from_f2(S[v], f);
-    store8<VEC>(sm + (2 * g + 1) * d, v, li, tpr, d, f);
+    store8<W>(sm + (2 * g + 1) * d, v, li, tpr, d, f);
   }
   __syncthreads();
   for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
@@ -765,7 +855,7 @@ __global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(c
 
 // Gradient of wider rows: a group is the CTA, V pieces of 8 columns a thread, the
 // parameters in shared memory.
-template <typename A, typename R, int V, bool VEC>
+template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
   extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
   __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
@@ -794,27 +884,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
     for (int v = 0; v < V; ++v) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[v][e] = dr[v][e] = du[v][e] = 0.f;
-      load8<VEC>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
-      if (a.y) load8<VEC>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
-      if (a.dres) load8<VEC>(static_cast<const R*>(a.dres) + row * a.ld_dres, v, li, tpr, d, dr[v]);
-      if (a.du) load8<VEC>(static_cast<const A*>(a.du) + row * a.ld_du, v, li, tpr, d, du[v]);
+      load8<W>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
+      if (a.y) load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
+      if (a.dres) load8<W>(static_cast<const R*>(a.dres) + row * a.ld_dres, v, li, tpr, d, dr[v]);
+      if (a.du) load8<W>(static_cast<const A*>(a.du) + row * a.ld_du, v, li, tpr, d, du[v]);
     }
     float wp[8], q[8];
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load8<VEC>(wpre, v, li, tpr, d, wp);
-      load8<VEC>(qs, v, li, tpr, d, q);
+      load8<W>(wpre, v, li, tpr, d, wp);
+      load8<W>(qs, v, li, tpr, d, q);
       row_sums(s, x[v], y[v], dr[v], du[v], wp, q);
     }
     group_sum6(s, red[flip], li, tpr, 1);
     const RowFactors f = row_factors<false>(a, s, 1.f / (float)d, row, li == 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load8<VEC>(wpre, v, li, tpr, d, wp);
-      load8<VEC>(qs, v, li, tpr, d, q);
+      load8<W>(wpre, v, li, tpr, d, wp);
+      load8<W>(qs, v, li, tpr, d, q);
       row_grads(f, x[v], y[v], dr[v], du[v], wp, q, P[v], S[v]);
-      store8<VEC>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, dr[v]);
-      if (a.y && a.u) store8<VEC>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, y[v]);
+      store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, dr[v]);
+      if (a.y && a.u) store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, y[v]);
     }
   }
   pdl_trigger();
@@ -822,8 +912,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
   __syncthreads();
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    store8<VEC>(wpre, v, li, tpr, d, P[v]);
-    store8<VEC>(qs, v, li, tpr, d, S[v]);
+    store8<W>(wpre, v, li, tpr, d, P[v]);
+    store8<W>(qs, v, li, tpr, d, S[v]);
   }
   __syncthreads();
   leave_column_sums(a, wide_sm);
@@ -882,32 +972,44 @@ GradShape grad_shape(int T, int d, bool vec, bool bf16) {
   return s;
 }
 
-template <typename A, typename R, int V, bool VEC>
+// Columns next to each other in a thread's vector accesses (see col()).
+template <typename A, typename R>
+constexpr int kW = sizeof(A) == 2 && sizeof(R) == 2 ? 8 : 4;
+
+template <typename A, typename R, int V, int W>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
   const int rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
-  return launch_pdl(k_block_norm<A, R, V, VEC>, dim3((a.T + rows - 1) / rows), dim3(rows * a.tpr),
+  return launch_pdl(k_block_norm<A, R, V, W>, dim3((a.T + rows - 1) / rows), dim3(rows * a.tpr),
                     0, st, a);
+}
+
+template <typename A, typename R, int V, int W>
+cudaError_t launch_fwd_stream(NormArgs a, cudaStream_t st) {
+  static std::atomic<unsigned long long> done{0};
+  const int smem = W > 1 ? stream_ring_bytes<A, R, V>() : 0;
+  const cudaError_t e = smem_optin_once(k_block_norm_stream<A, R, V, W>, smem, done);
+  if (e != cudaSuccess) return e;
+  a.tpr = round32((a.d + 8 * V - 1) / (8 * V));
+  const int groups = kStreamThreads / a.tpr, want = (a.T + groups - 1) / groups;
+  const int cap = (V == 1 && W > 1 ? 2 : 1) * num_sms();
+  return launch_pdl(k_block_norm_stream<A, R, V, W>, dim3(want < cap ? want : cap),
+                    dim3(groups * a.tpr), smem, st, a);
 }
 
 template <typename A, typename R>
 cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
-  // many aligned rows: the stream
-  if (vec && a.d <= kStreamMaxWidth && a.T >= 4 * num_sms()) {
-    static std::atomic<unsigned long long> done{0};
-    const int smem = kStages * (slot_bytes<A>() + slot_bytes<R>());
-    cudaError_t e = smem_optin_once(k_block_norm_stream<A, R>, smem, done);
-    if (e != cudaSuccess) return e;
-    a.tpr = round32((a.d + 7) / 8);
-    const int groups = kStreamThreads / a.tpr, want = (a.T + groups - 1) / groups;
-    const int cap = 2 * num_sms();
-    return launch_pdl(k_block_norm_stream<A, R>, dim3(want < cap ? want : cap),
-                      dim3(groups * a.tpr), smem, st, a);
-  }
-  // few rows: more threads and fewer columns each; d > 8192 needs two pieces
-  const bool one = a.d <= 8192 && a.T < 4 * num_sms();
+  constexpr int W = kW<A, R>;
+  const bool few = a.T < 4 * num_sms();
+  // many rows: the stream
+  if (!few && a.d <= kStreamMaxWidth)
+    return vec ? launch_fwd_stream<A, R, 1, W>(a, st) : launch_fwd_stream<A, R, 1, 1>(a, st);
+  if (!few && vec && a.d <= 2 * kStreamMaxWidth) return launch_fwd_stream<A, R, 2, W>(a, st);
+  // few rows: a row a group, more threads and fewer columns each; d > 8192 needs two
+  // pieces
+  const bool one = a.d <= 8192;
   a.tpr = round32((a.d + (one ? 7 : 15)) / (one ? 8 : 16));
-  if (one) return vec ? launch_fwd<A, R, 1, true>(a, st) : launch_fwd<A, R, 1, false>(a, st);
-  return vec ? launch_fwd<A, R, 2, true>(a, st) : launch_fwd<A, R, 2, false>(a, st);
+  if (one) return vec ? launch_fwd<A, R, 1, W>(a, st) : launch_fwd<A, R, 1, 1>(a, st);
+  return vec ? launch_fwd<A, R, 2, W>(a, st) : launch_fwd<A, R, 2, 1>(a, st);
 }
 
 template <typename... KArgs>
@@ -919,39 +1021,37 @@ cudaError_t launch_grad(void (*kernel)(KArgs...), std::atomic<unsigned long long
   return launch_pdl(kernel, dim3(s.grid), dim3(s.tpr * s.groups), smem, st, a);
 }
 
-template <typename A, typename R, int V, bool VEC>
+template <typename A, typename R, int V, int W>
 cudaError_t launch_grad_stream(const NormArgs& a, const GradShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0}, done_all{0};
   // the column sums end up where the ring and the parameters were
-  constexpr int rows = grad_ring_bytes<A, R, V, VEC>() + grad_param_bytes<V>();
+  constexpr int rows = grad_ring_bytes<A, R, V, W>() + grad_param_bytes<V>();
   constexpr int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
   constexpr int smem = rows > sums ? rows : sums;
   if (a.y && a.du && a.dres && a.w_post)
-    return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, true>, done_all, smem, smem, a, s, st);
-  return launch_grad(k_block_norm_grad_stream<A, R, V, VEC, false>, done, smem, smem, a, s, st);
+    return launch_grad(k_block_norm_grad_stream<A, R, V, W, true>, done_all, smem, smem, a, s, st);
+  return launch_grad(k_block_norm_grad_stream<A, R, V, W, false>, done, smem, smem, a, s, st);
 }
 
-template <typename A, typename R, int V, bool VEC>
+template <typename A, typename R, int V, int W>
 cudaError_t launch_grad_wide(const NormArgs& a, const GradShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  return launch_grad(k_block_norm_grad_wide<A, R, V, VEC>, done,
+  return launch_grad(k_block_norm_grad_wide<A, R, V, W>, done,
                      2 * kNormMaxWidth * (int)sizeof(float), 2 * a.d * (int)sizeof(float), a, s,
                      st);
 }
 
 template <typename A, typename R>
 cudaError_t launch_grad_types(const NormArgs& a, bool vec, const GradShape& s, cudaStream_t st) {
+  constexpr int W = kW<A, R>;
   if (a.d > kStreamMaxWidth) {
     if (s.pieces == 2)
-      return vec ? launch_grad_wide<A, R, 2, true>(a, s, st)
-                 : launch_grad_wide<A, R, 2, false>(a, s, st);
-    return vec ? launch_grad_wide<A, R, 4, true>(a, s, st)
-               : launch_grad_wide<A, R, 4, false>(a, s, st);
+      return vec ? launch_grad_wide<A, R, 2, W>(a, s, st) : launch_grad_wide<A, R, 2, 1>(a, s, st);
+    return vec ? launch_grad_wide<A, R, 4, W>(a, s, st) : launch_grad_wide<A, R, 4, 1>(a, s, st);
   }
   if constexpr (sizeof(A) == 2)
-    if (s.pieces == 2) return launch_grad_stream<A, R, 2, true>(a, s, st);
-  return vec ? launch_grad_stream<A, R, 1, true>(a, s, st)
-             : launch_grad_stream<A, R, 1, false>(a, s, st);
+    if (s.pieces == 2) return launch_grad_stream<A, R, 2, W>(a, s, st);
+  return vec ? launch_grad_stream<A, R, 1, W>(a, s, st) : launch_grad_stream<A, R, 1, 1>(a, s, st);
 }
 
 int elem(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
