@@ -623,29 +623,24 @@ __device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
 // columns in registers, its parameters in slots of its own.  V = 2 halves what a row
 // costs beside its elements (the reduction, the factors, the addresses).  ALL: every
 // tensor is given.
-template <int V>
-constexpr int kGradThreads = V == 2 ? 384 : kStreamThreads;
+constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
 
-template <typename A, typename R, int V, int W>
+template <typename A, typename R, int V, int W, int TH>
 __host__ __device__ constexpr int grad_ring_bytes() {
-  return W > 1 ? kGradStages * V * 2 * (slot_bytes<A, kGradThreads<V>>() + slot_bytes<R, kGradThreads<V>>())
-             : 0;
+  return W > 1 ? kGradStages * V * 2 * (slot_bytes<A, TH>() + slot_bytes<R, TH>()) : 0;
 }
-template <int V>
-__host__ __device__ constexpr int grad_param_bytes() {
-  return 2 * V * slot_bytes<float, kGradThreads<V>>();
-}
+template <int V, int TH>
+__host__ __device__ constexpr int grad_param_bytes() { return 2 * V * slot_bytes<float, TH>(); }
 
-template <typename A, typename R, int V, int W, bool ALL>
-__global__ void __launch_bounds__(kGradThreads<V>, 1) k_block_norm_grad_stream(const NormArgs a) {
+template <typename A, typename R, int V, int W, int TH, bool ALL>
+__global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];       // ring, then the parameters' slots
   __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
   static_assert(W > 1 || V == 1, "rows in registers: one piece a thread");
-  constexpr int TH = kGradThreads<V>;
   constexpr int kA = slot_bytes<A, TH>(), kR = slot_bytes<R, TH>(), kF = slot_bytes<float, TH>();
   constexpr int kPiece = 2 * kA + 2 * kR, kStage = V * kPiece;
-  uint8_t* const params = ring + grad_ring_bytes<A, R, V, W>();
+  uint8_t* const params = ring + grad_ring_bytes<A, R, V, W, TH>();
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
   const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
@@ -953,19 +948,23 @@ __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormAr
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-// How the gradient is laid out: pieces of 8 columns a thread, threads of a row, rows
-// at a time of a CTA, CTAs.  Two pieces a thread where that leaves several rows to a
-// CTA (bf16 rows of 1024 to 2048 aligned columns) or one piece would not do.
+// How the gradient is laid out: pieces of 8 columns a thread, threads of a CTA and of a
+// row, rows at a time of a CTA, CTAs.  Two pieces a thread for aligned rows of 1024 to
+// 2048 columns with bf16 activations (three rows at a time; T=8192, d=2048: 44 us
+// against 49 with one piece) and where one would not do (d=4096: 57 against 46).
 struct GradShape {
-  int pieces, tpr, groups, grid;
+  int pieces, threads, tpr, groups, grid;
 };
-GradShape grad_shape(int T, int d, bool vec, bool bf16) {
+GradShape grad_shape(int T, int d, bool vec, bool act_bf16) {
   GradShape s;
-  if (d > kStreamMaxWidth) s.pieces = d <= 2 * kStreamMaxWidth ? 2 : 4;
-  else s.pieces = vec && bf16 && d >= 1024 && d <= 2048 ? 2 : 1;
+  s.pieces = d > 2 * kStreamMaxWidth ? 4 : d > kStreamMaxWidth ? 2 : 1;
+  s.threads = kStreamThreads;
+  if (vec && act_bf16 && d >= 1024 && d <= 2048) {
+    s.pieces = 2;
+    s.threads = kGradThreads;
+  }
   s.tpr = round32((d + s.pieces * 8 - 1) / (s.pieces * 8));
-  const int threads = d <= kStreamMaxWidth && s.pieces == 2 ? kGradThreads<2> : kStreamThreads;
-  s.groups = threads / s.tpr;
+  s.groups = s.threads / s.tpr;
   // a few rows: one CTA, which needs no second launch to add the column sums
   const int want = T <= 4 * s.groups ? 1 : (T + s.groups - 1) / s.groups, sms = num_sms();
   s.grid = want < sms ? want : sms;
@@ -1021,16 +1020,17 @@ cudaError_t launch_grad(void (*kernel)(KArgs...), std::atomic<unsigned long long
   return launch_pdl(kernel, dim3(s.grid), dim3(s.tpr * s.groups), smem, st, a);
 }
 
-template <typename A, typename R, int V, int W>
+template <typename A, typename R, int V, int W, int TH>
 cudaError_t launch_grad_stream(const NormArgs& a, const GradShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0}, done_all{0};
-  // the column sums end up where the ring and the parameters were
-  constexpr int rows = grad_ring_bytes<A, R, V, W>() + grad_param_bytes<V>();
-  constexpr int sums = 2 * kStreamMaxWidth * (int)sizeof(float);
+  // the column sums of all groups end up where the ring and the parameters were
+  constexpr int rows = grad_ring_bytes<A, R, V, W, TH>() + grad_param_bytes<V, TH>();
+  constexpr int sums = 2 * 8 * V * TH * (int)sizeof(float);
   constexpr int smem = rows > sums ? rows : sums;
   if (a.y && a.du && a.dres && a.w_post)
-    return launch_grad(k_block_norm_grad_stream<A, R, V, W, true>, done_all, smem, smem, a, s, st);
-  return launch_grad(k_block_norm_grad_stream<A, R, V, W, false>, done, smem, smem, a, s, st);
+    return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, true>, done_all, smem, smem, a, s,
+                       st);
+  return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, false>, done, smem, smem, a, s, st);
 }
 
 template <typename A, typename R, int V, int W>
@@ -1044,14 +1044,18 @@ cudaError_t launch_grad_wide(const NormArgs& a, const GradShape& s, cudaStream_t
 template <typename A, typename R>
 cudaError_t launch_grad_types(const NormArgs& a, bool vec, const GradShape& s, cudaStream_t st) {
   constexpr int W = kW<A, R>;
-  if (a.d > kStreamMaxWidth) {
-    if (s.pieces == 2)
-      return vec ? launch_grad_wide<A, R, 2, W>(a, s, st) : launch_grad_wide<A, R, 2, 1>(a, s, st);
-    return vec ? launch_grad_wide<A, R, 4, W>(a, s, st) : launch_grad_wide<A, R, 4, 1>(a, s, st);
-  }
   if constexpr (sizeof(A) == 2)
-    if (s.pieces == 2) return launch_grad_stream<A, R, 2, W>(a, s, st);
-  return vec ? launch_grad_stream<A, R, 1, W>(a, s, st) : launch_grad_stream<A, R, 1, 1>(a, s, st);
+    if (s.pieces == 2 && s.threads == kGradThreads)
+      return launch_grad_stream<A, R, 2, W, kGradThreads>(a, s, st);
+  if constexpr (sizeof(A) == 2 && sizeof(R) == 2)
+    if (vec && s.pieces == 2)      // d up to 8192; fp32 rows would not fit the ring
+      return launch_grad_stream<A, R, 2, W, kStreamThreads>(a, s, st);
+  if (s.pieces == 4)
+    return vec ? launch_grad_wide<A, R, 4, W>(a, s, st) : launch_grad_wide<A, R, 4, 1>(a, s, st);
+  if (s.pieces == 2)
+    return vec ? launch_grad_wide<A, R, 2, W>(a, s, st) : launch_grad_wide<A, R, 2, 1>(a, s, st);
+  return vec ? launch_grad_stream<A, R, 1, W, kStreamThreads>(a, s, st)
+             : launch_grad_stream<A, R, 1, 1, kStreamThreads>(a, s, st);
 }
 
 int elem(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
