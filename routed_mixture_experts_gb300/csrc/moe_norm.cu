@@ -713,17 +713,19 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   const f2 zero = make_f2(0.f, 0.f);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float w8[8], q8[8];
+    float w8[8], q8[8], f[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int c = col<W>(v, e, li, tpr);
-      w8[e] = 0.f;
-      q8[e] = a.alpha;
-      if (c < d) {
-        if (has_du) w8[e] = param(a.w_pre, a.param_bf16, c);
-        if (has_y && a.w_post) q8[e] *= param(a.w_post, a.param_bf16, c);
-        if (has_y && a.gate_kind == MOE_GATE_CHANNEL) q8[e] *= param(a.gate, a.param_bf16, c);
-      }
+    for (int e = 0; e < 8; ++e) w8[e] = 0.f, q8[e] = a.alpha;
+    if (has_du) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w8);
+    if (has_y && a.w_post) {
+      load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
+    }
+    if (has_y && a.gate_kind == MOE_GATE_CHANNEL) {
+      load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, f);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
     }
     param_write<TH>(params + 2 * v * kF, w8);
     param_write<TH>(params + (2 * v + 1) * kF, q8);
@@ -734,37 +736,46 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   int stage = 0, flip = 0;
   long long row = first;
   for (int n = 0; n < rows; ++n, row += hop) {
-    f2 x[V][4], y[V][4], dr[V][4], du[V][4];
+    f2 x[4], y[4], dr[4], du[4], wp[4], q[4];
     float f[8];
+    // Piece v of the row and of the parameters.  From the ring it is read twice, before
+    // and after the reduction: registers that do not hold the row leave room for more
+    // rows at a time.
+    const uint8_t* const slots = ring + stage * kStage;
+    auto piece = [&](int v) {
+      if constexpr (W > 1) {
+        const uint8_t* at = slots + v * kPiece;
+        slot_read<W, TH>(at, f, x_in);
+        to_f2(f, x);
+        slot_read<W, TH>(at + kR, f, x_in);
+        to_f2(f, dr);
+        slot_read<W, TH>(at + 2 * kR, f, y_in);
+        to_f2(f, y);
+        slot_read<W, TH>(at + 2 * kR + kA, f, y_in);
+        to_f2(f, du);
+      }
+      param_read<TH>(params + 2 * v * kF, f);
+      to_f2(f, wp);
+      param_read<TH>(params + (2 * v + 1) * kF, f);
+      to_f2(f, q);
+    };
     if (W > 1) {
       cp_async_wait<0>();
-#pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint8_t* at = ring + stage * kStage + v * kPiece;
-        if constexpr (W > 1) slot_read<W, TH>(at, f, x_in);
-        to_f2(f, x[v]);
-        if constexpr (W > 1) slot_read<W, TH>(at + kR, f, x_in);
-        to_f2(f, dr[v]);
-        if constexpr (W > 1) slot_read<W, TH>(at + 2 * kR, f, y_in);
-        to_f2(f, y[v]);
-        if constexpr (W > 1) slot_read<W, TH>(at + 2 * kR + kA, f, y_in);
-        to_f2(f, du[v]);
-      }
       stage ^= 1;
       fetch(stage);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = to_f(nx[e]);
-      to_f2(f, x[0]);
+      to_f2(f, x);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = to_f(ny[e]);
-      to_f2(f, y[0]);
+      to_f2(f, y);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = to_f(ndr[e]);
-      to_f2(f, dr[0]);
+      to_f2(f, dr);
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = to_f(ndu[e]);
-      to_f2(f, du[0]);
+      to_f2(f, du);
       load();
     }
     float s[6];
@@ -772,20 +783,16 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
       f2 z[6] = {zero, zero, zero, zero, zero, zero};
 #pragma unroll
       for (int v = 0; v < V; ++v) {
-        f2 wp[4], q[4];
-        param_read<TH>(params + 2 * v * kF, f);
-        to_f2(f, wp);
-        param_read<TH>(params + (2 * v + 1) * kF, f);
-        to_f2(f, q);
+        piece(v);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const f2 t = mul2(du[v][i], wp[i]), qy = mul2(q[i], y[v][i]);
-          z[0] = fma2(x[v][i], x[v][i], z[0]);
-          z[1] = fma2(t, x[v][i], z[1]);
-          z[2] = fma2(y[v][i], y[v][i], z[2]);
-          z[3] = fma2(qy, dr[v][i], z[3]);
+          const f2 t = mul2(du[i], wp[i]), qy = mul2(q[i], y[i]);
+          z[0] = fma2(x[i], x[i], z[0]);
+          z[1] = fma2(t, x[i], z[1]);
+          z[2] = fma2(y[i], y[i], z[2]);
+          z[3] = fma2(qy, dr[i], z[3]);
           z[4] = fma2(qy, t, z[4]);
-          z[5] = fma2(qy, x[v][i], z[5]);
+          z[5] = fma2(qy, x[i], z[5]);
         }
       }
 #pragma unroll
@@ -800,22 +807,18 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
     // dr becomes d_residual, y dy; the column sums take the row's terms
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      f2 wp[4], q[4];
-      param_read<TH>(params + 2 * v * kF, f);
-      to_f2(f, wp);
-      param_read<TH>(params + (2 * v + 1) * kF, f);
-      to_f2(f, q);
+      piece(v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        P[v][i] = fma2(du[v][i], mul2(x[v][i], rs), P[v][i]);
-        dr[v][i] = fma2(ncx, x[v][i], fma2(rs, mul2(du[v][i], wp[i]), dr[v][i]));
-        S[v][i] = fma2(gy, mul2(dr[v][i], y[v][i]), S[v][i]);
-        y[v][i] = mul2(gy, fma2(ncy, y[v][i], mul2(q[i], dr[v][i])));
+        P[v][i] = fma2(du[i], mul2(x[i], rs), P[v][i]);
+        dr[i] = fma2(ncx, x[i], fma2(rs, mul2(du[i], wp[i]), dr[i]));
+        S[v][i] = fma2(gy, mul2(dr[i], y[i]), S[v][i]);
+        y[i] = mul2(gy, fma2(ncy, y[i], mul2(q[i], dr[i])));
       }
-      from_f2(dr[v], f);
+      from_f2(dr, f);
       store8<W>(dr_out, v, li, tpr, d, f);
       if (has_y && a.u) {
-        from_f2(y[v], f);
+        from_f2(y, f);
         store8<W>(dy_out, v, li, tpr, d, f);
       }
     }
@@ -1193,7 +1196,8 @@ extern "C" int moe_block_norm_backward(
                    rows_vec(d_residual_out, ld_dout, s->residual_dtype) &&
                    rows_vec(d_u, ld_du, s->dtype) &&
                    rows_vec(d_residual, ld_dres, s->residual_dtype) &&
-                   rows_vec(dy, ld_dy, s->dtype);
+                   rows_vec(dy, ld_dy, s->dtype) && vec_param(w_post) && vec_param(w_pre) &&
+                   (s->gate != MOE_GATE_CHANNEL || vec_param(gate));
   // no rows: one CTA, which writes zero sums
   const GradShape shape = grad_shape(T, d, vec, s->dtype == MOE_DTYPE_BF16);
   a.tpr = shape.tpr;
