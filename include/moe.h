@@ -352,8 +352,8 @@ int moe_forward_nvfp4(moe_plan* plan, const void* x, const int32_t* ids, const f
  * The routed experts of a few tokens: what moe_forward_nvfp4 is for prompts, for
  * the single tokens of a decoding loop, on the same prepared weights.  The
  * activations are not quantised (no activation scales are needed): x stays bf16,
- * h is rounded to 11 significant bits (relative to the largest of each 128 of its
- * elements), every sum is fp32, and
+ * h is rounded to 11 significant bits (elements below 2^-28 of the largest of their
+ * row: to within 2^-39 of that one), every sum is fp32, and
  *   y[t] = bf16( sum_j scores[t,j] * (w2_scale[e] * W2[e] . h) ),
  *   h = silu(G) * U, (G, U) = w13_scale[e] * W13[e] . x[t] (clipped to the plan's
  *   clamp), e = ids[t,j], in fixed j order.

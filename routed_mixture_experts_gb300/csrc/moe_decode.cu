@@ -1,5 +1,5 @@
-// moe_decode.cu -- the routed experts of a few tokens on NVFP4 weights: two
-// launches of matrix-vector products instead of dispatch and padded GEMM tiles.
+// moe_decode.cu -- the routed experts of a few tokens on NVFP4 weights: matrix-vector
+// products instead of dispatch and padded GEMM tiles.
 //
 //   h[t,j]  = silu(G) * U,  (G, U) = w13_scale[e] * W13[e] x[t],   e = ids[t,j]
 //   y[t]    = sum_j scores[t,j] * w2_scale[e] * W2[e] h[t,j]       (fixed j order)
@@ -8,18 +8,29 @@
 // scales per 16 elements); the activations are not quantised: x stays bf16, h is
 // kept in fp32 and read by the second product as fp16, all sums are fp32.
 //
-// Bound by reading each chosen expert once: 3/2 d I codes and 3/16 d I scales.
-// A CTA takes 32 rows of one expert's matrix for all tokens that chose the expert,
-// its warps splitting K in steps of 128.  The product runs on mma.sync m16n8k16
-// with the weights as the 16-row operand and up to 8 tokens as the columns: one
-// token fills one column of eight, but a weight then costs half a conversion
-// (cvt.e2m1x2), half a multiplication by its block's scale and no accumulation
-// of its own, where per-lane fused multiply-adds cost one and a half instructions
-// a weight and token.  (tcgen05 takes its operands from shared memory and would
-// need the dequantised weights written there.)  E2M1 x E4M3 has at most six
-// significant bits and is exact in fp16, x scaled by a power of two per token and
-// K step is exact down to 2^-32 of the step's largest element; h loses what lies
-// beyond fp16's 11 bits, eight times finer than the bf16 h of the other paths.
+// Bound by reading each chosen expert once: 3/2 d I codes and 3/16 d I scales.  The work
+// is cut into units of 32 rows of one expert's matrix for up to 8 of its tokens:
+//   one token (k <= 8)   a W13 unit a CTA, K split over its warps; W2 with a warp an
+//                        expert, which adds the experts itself: two launches
+//   a few units          a unit a CTA, K split over its warps
+//   many units           a unit a warp, weights streamed through a ring in shared memory
+// and the last two end with a third launch that adds a token's experts.
+// Measured at d=2048, I=768, k=8 (bytes at the rate of a plain copy): 1 token on 128
+// experts 12.2 us (3.1), 7 tokens on 16 experts 20.7 (6.2), 64 tokens on 128 experts
+// 75.7 (49.4).  Up to the last it is bound by the latency of a launch's start (ids, the
+// plan, the tokens' rows, the first weights: some 6 us, twice); the last streams near the
+// memory's rate between its two starts.
+//
+// The product runs on mma.sync m16n8k16 with the weights as the 16-row operand and up to
+// 8 tokens as the columns: one token fills one column of eight, but a weight then costs
+// half a conversion (cvt.e2m1x2), half a multiplication by its block's scale and no
+// accumulation of its own, where per-lane fused multiply-adds cost one and a half
+// instructions a weight and token.  (tcgen05 takes its operands from shared memory and
+// would need the dequantised weights written there.)  Rounding: E2M1 x E4M3 has at most
+// six significant bits and is exact in fp16; a token's x is scaled by a power of two that
+// takes its largest element to the top of fp16's range, which is exact down to 2^-31 of
+// that element and errs below by at most 2^-39 of it; h, scaled the same way, loses what
+// lies beyond fp16's 11 bits, eight times finer than the bf16 h of the other paths.
 //
 // Operand layout.  Any order of K serves as long as both operands share it: lane
 // (g, q) = (lane / 4, lane % 4) loads 16 code bytes (32 elements, two scale blocks)
@@ -564,8 +575,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_one_w2(const DecodeArgs 
 // ---- few units: K split over the warps ------------------------------------------
 //
 // A CTA of eight warps takes one unit at a time, a warp every eighth step, the sums
-// joined in shared memory: a unit is over after d / 1024 steps, and one token's eight
-// experts fill the GPU.
+// joined in shared memory: a unit is over after d / 1024 steps, and two tokens' experts
+// fill the GPU.  Latency bounds it: 7 tokens on 16 experts of d=2048, I=768: 23.4 us.
 template <bool W13>
 __global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];       // the pairs' list, the tokens' rows
@@ -661,7 +672,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a
 // through a ring of its own in shared memory filled with cp.async: a stage is 256
 // elements (128 bytes) of the unit's 32 rows and their scales, copied as whole lines,
 // the next stage (or the next unit's first) on its way while one is read.  Nothing in
-// the stream waits for another warp.
+// the stream waits for another warp.  Whole lines, because lanes that load 64-byte pieces
+// of eight rows stay at 5.1 to 5.8 TB/s where lines reach 6.5.  64 tokens on all of 128
+// experts, d=2048, I=768 (335 MB): 75.7 us with all launches, 4.4 TB/s.
 constexpr int kStreamWarps = 16;
 constexpr int kStages = 2;
 constexpr int kStageBytes = 32 * 128 + 512;                 // codes, scales
@@ -892,8 +905,9 @@ int stream_cols(int K, int pairs, int T) {
 // Units of one launch as far as the host can tell (every pair on an expert of its own
 // while there are experts, full passes after that), and whether it streams: from four
 // units an SM on, where passes of four tokens fit.  Measured with K split against a
-// unit a warp (us): 5 units an SM (7 tokens on 16 experts) 23.4 against 20.8, 10 (4 on
-// 128) 33.4 against 25.2.
+// unit a warp (us; d=2048, I=768): 1.3 to 1.7 units an SM 11.6 against 14.8, 2.5 to 3.4
+// 15.5 against 15.8, 3.8 to 5 19.2 against 18.3, 5 (7 tokens on 16 experts) 23.4 against
+// 20.7, 10 (4 on 128) 33.4 against 25.2.
 template <bool W13>
 long long units_of(const DecodeArgs& a) {
   const int pairs = a.T * a.k, experts = pairs < a.E ? pairs : a.E;

@@ -19,7 +19,9 @@
 // sum_c q dr y splits into sum(q y d_out) + rs sum(q y t) - rs^3 mean(t x) sum(q y x),
 // so one reduction over the row gives everything the row needs.
 //
-// Bound by memory: forward 4, gradient 6 passes over a [T, d] tensor.
+// Bound by memory: forward 4, gradient 6 passes over a [T, d] tensor.  At T=8192, d=2048
+// in bf16 that is 134 and 201 MB, 19.8 and 29.7 us at the rate of a plain copy; measured
+// 24.5 us (5.5 TB/s) and 41.3 us (4.9 TB/s, its second launch included).
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
@@ -94,8 +96,8 @@ __device__ __forceinline__ void store_vec8(uint16_t* p, const float (&f)[8]) {
 // A thread's 8 columns of piece v of a row, W of them next to each other.  Where every
 // row is 16-byte aligned and d a multiple of 8, W is 8 if all tensors are bf16 and 4
 // if one is fp32 (16 bytes of that one, so that a warp's accesses are whole lines:
-// eight fp32 columns a thread touched every sector twice, 56 against 47 us for the
-// fp32 gradient at T=8192, d=1024).  Else W is 1, one of each tpr columns.
+// with eight fp32 columns a thread they touch every sector twice: 56 against 39 us for
+// the fp32 gradient at T=8192, d=1024).  Else W is 1, one of each tpr columns.
 template <int W>
 __device__ __forceinline__ int col(int v, int e, int li, int tpr) {
   return W == 8 ? (v * tpr + li) * 8 + e
@@ -187,8 +189,10 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
   return rsqrtf(sum_sq * (1.f / (float)d) + eps);
 }
 
-// Forward, a row per group of tpr threads and no loop: few rows, wide rows and rows
-// without 16-byte alignment.
+// Forward, a row per group of tpr threads and no loop: few rows, and what the stream
+// below does not take (d > 8192; d > 4096 without 16-byte alignment).  All loads of a
+// row are independent; latency bounds it (one row of d=2048 2.6 us, of which a launch is
+// most).
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   __shared__ float red[2][32];
@@ -259,7 +263,8 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
 // Many rows: persistent CTAs of 512 threads, a thread owning 8 V columns of every row
 // of its group.  It copies its own pieces of the next rows into its own slots of a
 // ring with cp.async and reads them back itself, so a copy in flight costs no register
-// and needs no barrier; the parameters of its columns stay in registers.
+// and needs no barrier; the parameters of its columns stay in registers.  (One row a
+// group without a loop: T=8192, d=2048, bf16: 30.2 us against 24.5.)
 
 constexpr int kStreamThreads = 512;
 constexpr int kStreamMaxWidth = kStreamThreads * 8;
@@ -317,7 +322,8 @@ __device__ __forceinline__ void param_write(uint8_t* slot, const float (&f)[8]) 
 }
 
 // Forward over many rows.  W > 1: the next rows through the ring; else the next row
-// in registers, as it is in memory (a conversion would wait for the load).
+// in registers, as it is in memory (a conversion would wait for the load): accesses of
+// 2 or 4 bytes, which then bound it (bf16, T=8192, d=2047: 55 us against 24.5 at 2048).
 template <typename A, typename R, int V>
 __host__ __device__ constexpr int stream_ring_bytes() {
   return kStages * V * (slot_bytes<A>() + slot_bytes<R>());
@@ -618,11 +624,15 @@ __device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
   for (int i = 0; i < 4; ++i) split_f2(p[i], f[2 * i], f[2 * i + 1]);
 }
 
-// Gradient of rows of up to 4096 columns: row groups walk the rows, the next row on
-// its way (W > 1: through the ring; else in registers), the sums of a thread's 8 V
-// columns in registers, its parameters in slots of its own.  V = 2 halves what a row
-// costs beside its elements (the reduction, the factors, the addresses).  ALL: every
-// tensor is given.
+// Gradient of rows of up to 4096 columns, up to 8192 with V = 2: row groups walk the
+// rows, the next row on its way (W > 1: through the ring; else in registers), the sums of
+// a thread's 8 V columns in registers, its parameters in slots of its own.  V = 2 halves
+// what a row costs beside its elements (the reduction, the factors, the addresses).
+// ALL: every tensor is given.
+// Its row loop runs at nine tenths of a copy's rate; the rest of the time are the start,
+// the CTAs' column sums and the launch that adds them.  Measured with that launch: bf16
+// T=8192, d=2048 41.3 us, T=2048, d=8192 63, fp32 T=8192, d=1024 39; fp32 residual,
+// T=4099, d=1537 (scalar accesses) 34.
 constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
 
@@ -851,8 +861,10 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   for (int c = threadIdx.x; c < d; c += blockDim.x) param_grads(a, c, sm[c], sm[d + c]);
 }
 
-// Gradient of wider rows: a group is the CTA, V pieces of 8 columns a thread, the
-// parameters in shared memory.
+// Gradient of wider rows (d > 8192; d > 4096 with an fp32 tensor or without 16-byte
+// alignment): a group is the CTA, V pieces of 8 columns a thread, the parameters in shared
+// memory.  A row's registers leave no room for the next row, so that its loads are waited
+// for: bf16 T=2048, d=8192 took 77 us here, 63 in the kernel above; T=2047, d=8191 195.
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
   extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
@@ -917,7 +929,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
   leave_column_sums(a, wide_sm);
 }
 
-// Adds the CTAs' column sums in order: 32 columns per CTA, 32 slices of the CTAs.
+// Adds the CTAs' column sums in order: 32 columns per CTA, 32 slices of the CTAs.  2.5 MB
+// at d=2048, from L2: latency (5 us alone, some 3 behind the row kernel's end).
 constexpr int kSlices = 32;
 __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormArgs a) {
   __shared__ float part[2][32][kSlices + 1];
@@ -968,8 +981,9 @@ GradShape grad_shape(int T, int d, bool vec, bool act_bf16) {
   }
   s.tpr = round32((d + s.pieces * 8 - 1) / (s.pieces * 8));
   s.groups = s.threads / s.tpr;
-  // a few rows: one CTA, which needs no second launch to add the column sums
-  const int want = T <= 4 * s.groups ? 1 : (T + s.groups - 1) / s.groups, sms = num_sms();
+  // One CTA needs no second launch to add the column sums, but costs more than that as
+  // soon as it has a second round of rows: 4 rows, d=2048: 10.3 us against 8.9 on two.
+  const int want = T > 0 ? (T + s.groups - 1) / s.groups : 1, sms = num_sms();
   s.grid = want < sms ? want : sms;
   return s;
 }
@@ -1001,8 +1015,9 @@ cudaError_t launch_fwd_stream(NormArgs a, cudaStream_t st) {
 template <typename A, typename R>
 cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
   constexpr int W = kW<A, R>;
-  const bool few = a.T < 4 * num_sms();
-  // many rows: the stream
+  // More than four rows an SM: the stream (bf16, d=2048, stream against a row a group:
+  // 608 rows 3.9 against 3.6 us, 912 rows 5.1 against 6.2).
+  const bool few = a.T <= 4 * num_sms();
   if (!few && a.d <= kStreamMaxWidth)
     return vec ? launch_fwd_stream<A, R, 1, W>(a, st) : launch_fwd_stream<A, R, 1, 1>(a, st);
   if (!few && vec && a.d <= 2 * kStreamMaxWidth) return launch_fwd_stream<A, R, 2, W>(a, st);

@@ -15,7 +15,8 @@
 // (s' the normalised chosen scores).
 //
 // A warp holds a row: expert e = lane + 32 i in slot i, so loads and stores are
-// coalesced and every sum over experts is one warp reduction.
+// coalesced and every sum over experts is one warp reduction.  All arithmetic is fp32;
+// the only rounding to fewer bits is that of a bf16 gradient on its way out.
 
 #include <cmath>
 
@@ -108,6 +109,17 @@ __device__ __forceinline__ void write_losses(const RouterArgs& a, float balance,
 }
 
 // Forward.  L = logits type, NV = slots of 32 experts.
+//
+// One pass over the logits: 4 E bytes a row in, 8 k out, next to nothing for the
+// memory (8192 rows of 128 fp32 logits, 4.75 MB: 0.7 us).  What bounds it is the chain of
+// the selection, k steps of a warp-wide maximum and a ballot each, and the instructions
+// of 32 warps an SM.  A row in one warp keeps that chain free of barriers; integer keys
+// of the same order as the logits need one reduction instruction a step, and a ballot
+// finds the lowest expert that has the maximum.  The per-expert sums stay in the warps'
+// registers over all their rows, so that no atomic adds floating-point values and the
+// results do not depend on the order in which warps run.
+// Measured, both launches: one token 3.5 us, 8192 rows of 128 experts (k = 8) 11.4, 16411
+// rows of 250 bf16 logits (k = 6, sigmoid, bias, 2048 rows masked) 19.6.
 template <typename L, int NV>
 __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
   extern __shared__ float psum[];                 // [warps][NV * 32]
@@ -274,7 +286,8 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
 }
 
 // Adds the CTAs' sums: a cluster of one CTA per 32 experts, warp w of it expert w,
-// the balance loss joined through the cluster's shared memory.
+// the balance loss joined through the cluster's shared memory.  Latency: a few dependent
+// loads and two cluster barriers, some 4 us beside a launch of its own.
 __global__ void __launch_bounds__(1024) k_router_finish(const RouterArgs a) {
   __shared__ float sp[32][33];
   __shared__ int sc[32][33];
@@ -334,6 +347,11 @@ __global__ void __launch_bounds__(1024) k_router_finish(const RouterArgs a) {
 
 // Gradient: a warp per row, as the forward.  A warp's shared memory holds the row's
 // logits and the chosen experts' own terms.
+//
+// Reads the logits again and takes the probabilities from row_stat, so that the forward
+// leaves 4 bytes a row instead of 4 E.  Bound by latency and instructions (two or
+// three exponentials' work a logit): 8192 rows of 128 fp32 logits 5.6 us where the 8.9 MB
+// take 1.3; 16411 rows of 250 bf16 logits, 2048 of them masked, 16.1 where they take 2.4.
 constexpr int kGradWarps = 8;
 
 template <typename L, int NV>
@@ -455,9 +473,10 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
 // ---------------------------------------------------------------------------
 // host side
 
-// Up to this many rows run on one CTA, which also writes the sums (no second
-// launch).
-constexpr int kOneCtaRows = 64;
+// Up to a row per warp one CTA does all, the sums too (32 rows of 128 experts 4.8 us).
+// More rows are spread, and a second launch adds the sums: 64 rows 6.6 us against 7.8
+// on one CTA.
+constexpr int kOneCtaRows = 32;
 
 // warps of a CTA: its chosen experts and per-warp sums take shared memory
 int forward_warps(int T, int grid) { return grid > 1 ? 32 : T > 8 ? 32 : 8; }
