@@ -190,7 +190,7 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
 }
 
 // Forward, a row per group of tpr threads and no loop: few rows, and what the stream
-// below does not take (d > 8192; d > 4096 without 16-byte alignment).  All loads of a
+// below does not take (d > 8192; tensors that are not 16-byte aligned).  All loads of a
 // row are independent; latency bounds it (one row of d=2048 2.6 us, of which a launch is
 // most).
 template <typename A, typename R, int V, int W>
@@ -258,6 +258,41 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
 }
 
 
+// Pairs of fp32 values and the two-wide arithmetic on them: half the instructions of
+// the scalar forms, which is what bounds the row loops.
+typedef unsigned long long f2;
+__device__ __forceinline__ f2 make_f2(float lo, float hi) {
+  f2 r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void split_f2(f2 v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ float sum_f2(f2 v) {
+  float lo, hi;
+  split_f2(v, lo, hi);
+  return lo + hi;
+}
+__device__ __forceinline__ void to_f2(const float (&f)[8], f2 (&p)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) p[i] = make_f2(f[2 * i], f[2 * i + 1]);
+}
+__device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) split_f2(p[i], f[2 * i], f[2 * i + 1]);
+}
+
 // ---- rows streamed through shared memory ---------------------------------------
 //
 // Many rows: persistent CTAs of 512 threads, a thread owning 8 V columns of every row
@@ -321,16 +356,63 @@ __device__ __forceinline__ void param_write(uint8_t* slot, const float (&f)[8]) 
   *reinterpret_cast<float4*>(slot + (TH + threadIdx.x) * 16) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Forward over many rows.  W > 1: the next rows through the ring; else the next row
-// in registers, as it is in memory (a conversion would wait for the load): accesses of
-// 2 or 4 bytes, which then bound it (bf16, T=8192, d=2047: 55 us against 24.5 at 2048).
+// Rows that are not 16-byte aligned (W = 1; the tensors themselves are): a group copies
+// the 16-byte pieces of a row from the one that holds its first element, and reads its
+// elements from there after a barrier of the group.  The pieces begin up to 15 bytes
+// before the row, in the row before or in what lies between (row 0 is aligned, and rows
+// are at least 16 bytes apart: kStagedMinWidth); the last one stops at the row's end.
+// Against loads of single elements into registers, one row ahead (us): forward, T=8192,
+// d=777, bf16 33.2 -> 25.2; T=8191, d=1023, fp32 36.2 -> 32.3; T=2047, d=8191, bf16
+// 85.9 -> 56.2.  What is left is the writing, an element a thread (T=8192, d=2047, bf16
+// 52.9; with one of eight stores 31); pieces written through shared memory too cost as
+// much for their barrier (56.8).  The gradient of up to 4096 columns loses with it (34.0
+// against 39.7 us for an fp32 residual, T=4099, d=1537) and keeps its loads.
+constexpr int kStagedMinWidth = 8;
+
+// A row's slot, and where its first element is in it.
+template <typename T>
+__host__ __device__ constexpr int row_slot(int d) { return (d * (int)sizeof(T) + 31) / 16 * 16; }
+template <typename T>
+__device__ __forceinline__ int row_offset(long long row, long long ld) {
+  return (int)((unsigned)row * (unsigned)ld * (unsigned)sizeof(T) & 15u);
+}
+template <typename T>
+__device__ __forceinline__ void row_copy(uint32_t slot, const T* row, int li, int tpr, int d) {
+  const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15), bytes = off + d * (int)sizeof(T);
+  const uint8_t* const from = reinterpret_cast<const uint8_t*>(row) - off;
+  for (int c = li * 16; c < bytes; c += tpr * 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(slot + c), "l"(from + c),
+                 "r"(min(16, bytes - c)) : "memory");
+}
+template <typename T>
+__device__ __forceinline__ void row_read(const uint8_t* first, int v, int li, int tpr, int d,
+                                         float (&f)[8], const T*) {
+  const T* const p = reinterpret_cast<const T*>(first);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const int c = col<1>(v, e, li, tpr);
+    f[e] = c < d ? to_f(p[c]) : 0.f;
+  }
+}
+// The copies that a thread has waited for are there for all threads of its group.
+__device__ __forceinline__ void group_sees(int bar, int tpr) {
+  if (tpr == 32) __syncwarp();
+  else group_sync(bar, tpr);
+}
+
+// Forward over many rows.
 template <typename A, typename R, int V>
 __host__ __device__ constexpr int stream_ring_bytes() {
   return kStages * V * (slot_bytes<A>() + slot_bytes<R>());
 }
+template <typename A, typename R>
+__host__ __device__ constexpr int staged_ring_bytes(int d, int groups) {
+  return kStages * groups * (row_slot<A>(d) + row_slot<R>(d));
+}
 
 template <typename A, typename R, int V, int W>
-__global__ void __launch_bounds__(kStreamThreads, V == 1 && W > 1 ? 2 : 1) k_block_norm_stream(const NormArgs a) {
+__global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
+    k_block_norm_stream(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];
   __shared__ float red[2][2][kStreamThreads / 32];
   constexpr int kPiece = slot_bytes<A>() + slot_bytes<R>(), kStage = V * kPiece;
@@ -341,123 +423,119 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 && W > 1 ? 2 : 1) k_blo
   const uint32_t base = smem_u32(ring);
   const A* const y_in = static_cast<const A*>(a.y);
   const R* const x_in = static_cast<const R*>(a.res);
+  const int row_bytes = row_slot<A>(d) + row_slot<R>(d);                // W = 1
   auto fetch = [&](long long row, int stage) {
-    if (row < a.T)
+    if (row < a.T) {
+      if constexpr (W > 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint32_t at = base + stage * kStage + v * kPiece;
-        if constexpr (W > 1) {
+        for (int v = 0; v < V; ++v) {
+          const uint32_t at = base + stage * kStage + v * kPiece;
           if (a.y) slot_copy<W>(at, y_in + row * a.ld_y, v, li, tpr, d);
           slot_copy<W>(at + slot_bytes<A>(), x_in + row * a.ld_res, v, li, tpr, d);
         }
+      } else {
+        const uint32_t at = base + (stage * groups + g) * row_bytes;
+        if (a.y) row_copy(at, y_in + row * a.ld_y, li, tpr, d);
+        row_copy(at + row_slot<A>(d), x_in + row * a.ld_res, li, tpr, d);
       }
+    }
     cp_async_commit();
-  };
-  A ny[V][8];
-  R nx[V][8];
-  auto load = [&](long long row) {
-    if (row >= a.T) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<1>(v, e, li, tpr);
-        if (c < d) nx[v][e] = x_in[row * a.ld_res + c];
-      }
-    if (!a.y) return;
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int c = col<1>(v, e, li, tpr);
-        if (c < d) ny[v][e] = y_in[row * a.ld_y + c];
-      }
   };
   if (W > 1) {
     // slots that no copy fills (columns past the row, no y) read as zero
     for (int i = threadIdx.x; i < kStages * kStage / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
-  } else {
-#pragma unroll
-    for (int v = 0; v < V; ++v)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) nx[v][e] = 0, ny[v][e] = 0;
-    load(first);
   }
-  float q[V][8], w[V][8];      // alpha * w_post * channel gate, w_pre
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+  f2 q[V][4], w[V][4];         // alpha * w_post * channel gate, w_pre
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float f[8];
+    float f[8], q8[8], w8[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q[v][e] = a.alpha, w[v][e] = 0.f;
+    for (int e = 0; e < 8; ++e) q8[e] = a.alpha, w8[e] = 0.f;
     if (a.y && a.w_post) {
       load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[v][e] *= f[e];
+      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
     }
     if (a.y && a.gate_kind == MOE_GATE_CHANNEL) {
       load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, f);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) q[v][e] *= f[e];
+      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
     }
-    if (a.u) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w[v]);
+    if (a.u) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w8);
+    to_f2(q8, q[v]);
+    to_f2(w8, w[v]);
   }
+  // the sum of squares of the thread's values
+  auto squares = [&](const f2 (&p)[V][4]) {
+    f2 s = mul2(p[0][0], p[0][0]);
+#pragma unroll
+    for (int v = 0; v < V; ++v)
+#pragma unroll
+      for (int i = v == 0 ? 1 : 0; i < 4; ++i) s = fma2(p[v][i], p[v][i], s);
+    return sum_f2(s);
+  };
   int stage = 0, flip = 0;
   for (long long row = first; row < a.T; row += hop) {
-    float x[V][8], y[V][8], s;
-    float f = 1.f;
+    f2 x[V][4], y[V][4];
+    float f = 1.f, t[8];
     if (a.y && a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
-    if (W > 1) {
-      cp_async_wait<kStages - 2>();
+    cp_async_wait<kStages - 2>();
+    if constexpr (W > 1) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const uint8_t* at = ring + stage * kStage + v * kPiece;
-        if constexpr (W > 1) {
-          slot_read<W>(at, y[v], y_in);
-          slot_read<W>(at + slot_bytes<A>(), x[v], x_in);
-        }
+        slot_read<W>(at, t, y_in);
+        to_f2(t, y[v]);
+        slot_read<W>(at + slot_bytes<A>(), t, x_in);
+        to_f2(t, x[v]);
       }
-      // into the slots read one row ago
-      fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
-      stage = stage + 1 == kStages ? 0 : stage + 1;
     } else {
+      group_sees(1 + g, tpr);
+      const uint8_t* at = ring + (stage * groups + g) * row_bytes;
 #pragma unroll
-      for (int v = 0; v < V; ++v)
+      for (int v = 0; v < V; ++v) {
+        if (a.y) {
+          row_read(at + row_offset<A>(row, a.ld_y), v, li, tpr, d, t, y_in);
+        } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] = to_f(nx[v][e]), y[v][e] = to_f(ny[v][e]);
-      load(row + hop);
-    }
-    if (a.y) {
-      if (a.w_post) {
-        s = 0.f;
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
-        f *= inv_rms(group_sum(s, &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+          for (int e = 0; e < 8; ++e) t[e] = 0.f;
+        }
+        to_f2(t, y[v]);
+        row_read(at + row_slot<A>(d) + row_offset<R>(row, a.ld_res), v, li, tpr, d, t, x_in);
+        to_f2(t, x[v]);
       }
+    }
+    // into the slots read one row ago
+    fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+    if (a.y) {
+      if (a.w_post)
+        f *= inv_rms(group_sum(squares(y), &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d,
+                     a.eps);
+      const f2 f2x = make_f2(f, f);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] += f * (q[v][e] * y[v][e]);
-        store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, x[v]);
+        for (int i = 0; i < 4; ++i) x[v][i] = fma2(f2x, mul2(q[v][i], y[v][i]), x[v][i]);
+        from_f2(x[v], t);
+        store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, t);
       }
     }
     if (a.u) {
-      s = 0.f;
-#pragma unroll
-      for (int v = 0; v < V; ++v)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) s += x[v][e] * x[v][e];
-      const float rs = inv_rms(group_sum(s, &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+      const float rs =
+          inv_rms(group_sum(squares(x), &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+      const f2 rs2 = make_f2(rs, rs);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
+        f2 u[4];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[v][e] *= rs * w[v][e];
-        store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, x[v]);
+        for (int i = 0; i < 4; ++i) u[i] = mul2(x[v][i], mul2(rs2, w[v][i]));
+        from_f2(u, t);
+        store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, t);
       }
     }
     flip ^= 1;
@@ -589,71 +667,40 @@ __device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float
   }
 }
 
-// Pairs of fp32 values and the two-wide arithmetic on them: half the instructions of
-// the scalar forms, which is what bounds the row loop.
-typedef unsigned long long f2;
-__device__ __forceinline__ f2 make_f2(float lo, float hi) {
-  f2 r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void split_f2(f2 v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
-  f2 r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
-  f2 r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ float sum_f2(f2 v) {
-  float lo, hi;
-  split_f2(v, lo, hi);
-  return lo + hi;
-}
-__device__ __forceinline__ void to_f2(const float (&f)[8], f2 (&p)[4]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) p[i] = make_f2(f[2 * i], f[2 * i + 1]);
-}
-__device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) split_f2(p[i], f[2 * i], f[2 * i + 1]);
-}
-
 // Gradient of rows of up to 4096 columns, up to 8192 with V = 2: row groups walk the
-// rows, the next row on its way (W > 1: through the ring; else in registers), the sums of
+// rows, the next row on its way (through the ring; one piece of unaligned rows in
+// registers), the sums of
 // a thread's 8 V columns in registers, its parameters in slots of its own.  V = 2 halves
 // what a row costs beside its elements (the reduction, the factors, the addresses).
 // ALL: every tensor is given.
 // Its row loop runs at nine tenths of a copy's rate; the rest of the time are the start,
 // the CTAs' column sums and the launch that adds them.  Measured with that launch: bf16
-// T=8192, d=2048 41.3 us, T=2048, d=8192 63, fp32 T=8192, d=1024 39; fp32 residual,
-// T=4099, d=1537 (scalar accesses) 34.
+// T=8192, d=2048 41.3 us, T=2048, d=8192 63, T=2047, d=8191 98, fp32 T=8192, d=1024
+// 37; fp32 residual, T=4099, d=1537 (one piece of single elements) 34.
 constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
 
-template <typename A, typename R, int V, int W, int TH>
-__host__ __device__ constexpr int grad_ring_bytes() {
-  return W > 1 ? kGradStages * V * 2 * (slot_bytes<A, TH>() + slot_bytes<R, TH>()) : 0;
-}
 template <int V, int TH>
 __host__ __device__ constexpr int grad_param_bytes() { return 2 * V * slot_bytes<float, TH>(); }
+template <typename A, typename R, int V, int W, int TH>
+__host__ __device__ constexpr int grad_ring_bytes(int d, int groups) {
+  return W == 1 && V == 1 ? 0
+         : kGradStages * 2 * (W > 1 ? V * (slot_bytes<A, TH>() + slot_bytes<R, TH>())
+                                    : groups * (row_slot<A>(d) + row_slot<R>(d)));
+}
 
 template <typename A, typename R, int V, int W, int TH, bool ALL>
 __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs a) {
   extern __shared__ __align__(16) uint8_t ring[];       // ring, then the parameters' slots
   __shared__ __align__(16) float red[2][kStreamThreads / 32][8];
-  static_assert(W > 1 || V == 1, "rows in registers: one piece a thread");
   constexpr int kA = slot_bytes<A, TH>(), kR = slot_bytes<R, TH>(), kF = slot_bytes<float, TH>();
   constexpr int kPiece = 2 * kA + 2 * kR, kStage = V * kPiece;
-  uint8_t* const params = ring + grad_ring_bytes<A, R, V, W, TH>();
+  constexpr bool kKept = W == 1 && V == 1;       // the next row in registers, not in the ring
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
   const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
+  uint8_t* const params = kKept ? ring : ring + grad_ring_bytes<A, R, V, W, TH>(d, groups);
+  const int slot_a = row_slot<A>(d), slot_r = row_slot<R>(d);            // W = 1
   const bool has_y = ALL || a.y, has_du = ALL || a.du, has_dr = ALL || a.dres;
   const long long first = (long long)blockIdx.x * groups + g;
   const int hop = gridDim.x * groups;
@@ -675,13 +722,21 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   const uint32_t base = smem_u32(ring);
   auto fetch = [&](int stage) {
     if (left > 0) {
+      if constexpr (W > 1) {
 #pragma unroll
-      for (int v = 0; v < V; ++v) {
-        const uint32_t at = base + stage * kStage + v * kPiece;
-        slot_copy<W, TH>(at, x_in, v, li, tpr, d);
-        if (has_dr) slot_copy<W, TH>(at + kR, dr_in, v, li, tpr, d);
-        if (has_y) slot_copy<W, TH>(at + 2 * kR, y_in, v, li, tpr, d);
-        if (has_du) slot_copy<W, TH>(at + 2 * kR + kA, du_in, v, li, tpr, d);
+        for (int v = 0; v < V; ++v) {
+          const uint32_t at = base + stage * kStage + v * kPiece;
+          slot_copy<W, TH>(at, x_in, v, li, tpr, d);
+          if (has_dr) slot_copy<W, TH>(at + kR, dr_in, v, li, tpr, d);
+          if (has_y) slot_copy<W, TH>(at + 2 * kR, y_in, v, li, tpr, d);
+          if (has_du) slot_copy<W, TH>(at + 2 * kR + kA, du_in, v, li, tpr, d);
+        }
+      } else if constexpr (!kKept) {
+        const uint32_t at = base + (stage * groups + g) * 2 * (slot_a + slot_r);
+        row_copy(at, x_in, li, tpr, d);
+        if (has_dr) row_copy(at + slot_r, dr_in, li, tpr, d);
+        if (has_y) row_copy(at + 2 * slot_r, y_in, li, tpr, d);
+        if (has_du) row_copy(at + 2 * slot_r + slot_a, du_in, li, tpr, d);
       }
       advance();
       --left;
@@ -713,11 +768,13 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
     for (int i = threadIdx.x; i < kGradStages * kStage / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
-    fetch(0);
-  } else {
+  }
+  if constexpr (kKept) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) nx[e] = ndr[e] = 0, ny[e] = ndu[e] = 0;
     load();
+  } else {
+    fetch(0);
   }
   f2 P[V][4], S[V][4];
   const f2 zero = make_f2(0.f, 0.f);
@@ -751,7 +808,15 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
     // Piece v of the row and of the parameters.  From the ring it is read twice, before
     // and after the reduction: registers that do not hold the row leave room for more
     // rows at a time.
-    const uint8_t* const slots = ring + stage * kStage;
+    const uint8_t* const slots =
+        ring + (W > 1 ? stage * kStage : (stage * groups + g) * 2 * (slot_a + slot_r));
+    int off[4] = {0, 0, 0, 0};
+    if constexpr (W == 1 && !kKept) {
+      off[0] = row_offset<R>(row, a.ld_res);
+      off[1] = slot_r + row_offset<R>(row, a.ld_dres);
+      off[2] = 2 * slot_r + row_offset<A>(row, a.ld_y);
+      off[3] = 2 * slot_r + slot_a + row_offset<A>(row, a.ld_du);
+    }
     auto piece = [&](int v) {
       if constexpr (W > 1) {
         const uint8_t* at = slots + v * kPiece;
@@ -763,17 +828,25 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
         to_f2(f, y);
         slot_read<W, TH>(at + 2 * kR + kA, f, y_in);
         to_f2(f, du);
+      } else if constexpr (!kKept) {
+        auto get = [&](bool has, int at, const auto* type, f2 (&to)[4]) {
+          if (has) row_read(slots + at, v, li, tpr, d, f, type);
+          else
+#pragma unroll
+            for (int e = 0; e < 8; ++e) f[e] = 0.f;
+          to_f2(f, to);
+        };
+        get(true, off[0], x_in, x);
+        get(has_dr, off[1], x_in, dr);
+        get(has_y, off[2], y_in, y);
+        get(has_du, off[3], y_in, du);
       }
       param_read<TH>(params + 2 * v * kF, f);
       to_f2(f, wp);
       param_read<TH>(params + (2 * v + 1) * kF, f);
       to_f2(f, q);
     };
-    if (W > 1) {
-      cp_async_wait<0>();
-      stage ^= 1;
-      fetch(stage);
-    } else {
+    if constexpr (kKept) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) f[e] = to_f(nx[e]);
       to_f2(f, x);
@@ -787,6 +860,11 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
       for (int e = 0; e < 8; ++e) f[e] = to_f(ndu[e]);
       to_f2(f, du);
       load();
+    } else {
+      cp_async_wait<0>();
+      if (W == 1) group_sees(1 + g, tpr);
+      stage ^= 1;
+      fetch(stage);                      // into the slots read one row ago
     }
     float s[6];
     {
@@ -861,10 +939,11 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   for (int c = threadIdx.x; c < d; c += blockDim.x) param_grads(a, c, sm[c], sm[d + c]);
 }
 
-// Gradient of wider rows (d > 8192; d > 4096 with an fp32 tensor or without 16-byte
-// alignment): a group is the CTA, V pieces of 8 columns a thread, the parameters in shared
-// memory.  A row's registers leave no room for the next row, so that its loads are waited
-// for: bf16 T=2048, d=8192 took 77 us here, 63 in the kernel above; T=2047, d=8191 195.
+// Gradient of wider rows (d > 8192; d > 4096 with an fp32 tensor or tensors that are not
+// 16-byte aligned): a group is the CTA, V pieces of 8 columns a thread, the parameters in
+// shared memory.  A row's registers leave no room for the next row, so that its loads are
+// waited for: bf16 T=2048, d=8192 took 77 us here, 63 in the kernel above; T=2047, d=8191
+// 219 against 98.
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
   extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
@@ -962,6 +1041,10 @@ __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormAr
 // ---------------------------------------------------------------------------
 // host side
 
+// How the rows can be accessed: any rows, rows of aligned tensors (staged), aligned rows
+// and parameters.
+enum class Access { kAny, kStaged, kVector };
+
 int round32(int n) { return (n + 31) / 32 * 32; }
 
 // How the gradient is laid out: pieces of 8 columns a thread, threads of a CTA and of a
@@ -1002,25 +1085,32 @@ cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
 template <typename A, typename R, int V, int W>
 cudaError_t launch_fwd_stream(NormArgs a, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
-  const int smem = W > 1 ? stream_ring_bytes<A, R, V>() : 0;
-  const cudaError_t e = smem_optin_once(k_block_norm_stream<A, R, V, W>, smem, done);
-  if (e != cudaSuccess) return e;
   a.tpr = round32((a.d + 8 * V - 1) / (8 * V));
   const int groups = kStreamThreads / a.tpr, want = (a.T + groups - 1) / groups;
-  const int cap = (V == 1 && W > 1 ? 2 : 1) * num_sms();
+  // the most that a width can take: rows of 4096 V columns' bytes, and 32 more for each row
+  constexpr int most =
+      W > 1 ? stream_ring_bytes<A, R, V>()
+            : kStages * (V * (slot_bytes<A>() + slot_bytes<R>()) + 2 * 16 * 32);
+  const int smem = W > 1 ? most : staged_ring_bytes<A, R>(a.d, groups);
+  const cudaError_t e = smem_optin_once(k_block_norm_stream<A, R, V, W>, most, done);
+  if (e != cudaSuccess) return e;
+  const int cap = (V == 1 ? 2 : 1) * num_sms();
   return launch_pdl(k_block_norm_stream<A, R, V, W>, dim3(want < cap ? want : cap),
                     dim3(groups * a.tpr), smem, st, a);
 }
 
 template <typename A, typename R>
-cudaError_t launch_fwd_types(NormArgs a, bool vec, cudaStream_t st) {
+cudaError_t launch_fwd_types(NormArgs a, Access access, cudaStream_t st) {
   constexpr int W = kW<A, R>;
+  const bool vec = access == Access::kVector;
   // More than four rows an SM: the stream (bf16, d=2048, stream against a row a group:
   // 608 rows 3.9 against 3.6 us, 912 rows 5.1 against 6.2).
-  const bool few = a.T <= 4 * num_sms();
-  if (!few && a.d <= kStreamMaxWidth)
-    return vec ? launch_fwd_stream<A, R, 1, W>(a, st) : launch_fwd_stream<A, R, 1, 1>(a, st);
-  if (!few && vec && a.d <= 2 * kStreamMaxWidth) return launch_fwd_stream<A, R, 2, W>(a, st);
+  if (a.T > 4 * num_sms() && access != Access::kAny) {
+    if (a.d <= kStreamMaxWidth)
+      return vec ? launch_fwd_stream<A, R, 1, W>(a, st) : launch_fwd_stream<A, R, 1, 1>(a, st);
+    if (a.d <= 2 * kStreamMaxWidth)
+      return vec ? launch_fwd_stream<A, R, 2, W>(a, st) : launch_fwd_stream<A, R, 2, 1>(a, st);
+  }
   // few rows: a row a group, more threads and fewer columns each; d > 8192 needs two
   // pieces
   const bool one = a.d <= 8192;
@@ -1042,13 +1132,17 @@ template <typename A, typename R, int V, int W, int TH>
 cudaError_t launch_grad_stream(const NormArgs& a, const GradShape& s, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0}, done_all{0};
   // the column sums of all groups end up where the ring and the parameters were
-  constexpr int rows = grad_ring_bytes<A, R, V, W, TH>() + grad_param_bytes<V, TH>();
   constexpr int sums = 2 * 8 * V * TH * (int)sizeof(float);
-  constexpr int smem = rows > sums ? rows : sums;
+  const int rows = grad_ring_bytes<A, R, V, W, TH>(a.d, s.groups) + grad_param_bytes<V, TH>();
+  const int smem = rows > sums ? rows : sums;
+  // the most that a width can take
+  constexpr int stage = 2 * V * (slot_bytes<A, TH>() + slot_bytes<R, TH>()) + 4 * 16 * 32;
+  constexpr int most = (W == 1 && V == 1 ? 0 : kGradStages * stage) + grad_param_bytes<V, TH>();
+  static_assert(most >= sums, "the column sums fit");
   if (a.y && a.du && a.dres && a.w_post)
-    return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, true>, done_all, smem, smem, a, s,
+    return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, true>, done_all, most, smem, a, s,
                        st);
-  return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, false>, done, smem, smem, a, s, st);
+  return launch_grad(k_block_norm_grad_stream<A, R, V, W, TH, false>, done, most, smem, a, s, st);
 }
 
 template <typename A, typename R, int V, int W>
@@ -1060,20 +1154,23 @@ cudaError_t launch_grad_wide(const NormArgs& a, const GradShape& s, cudaStream_t
 }
 
 template <typename A, typename R>
-cudaError_t launch_grad_types(const NormArgs& a, bool vec, const GradShape& s, cudaStream_t st) {
+cudaError_t launch_grad_types(const NormArgs& a, Access access, const GradShape& s,
+                              cudaStream_t st) {
   constexpr int W = kW<A, R>;
+  const bool vec = access == Access::kVector;
+  if (s.pieces == 1)
+    return vec ? launch_grad_stream<A, R, 1, W, kStreamThreads>(a, s, st)
+               : launch_grad_stream<A, R, 1, 1, kStreamThreads>(a, s, st);
   if constexpr (sizeof(A) == 2)
-    if (s.pieces == 2 && s.threads == kGradThreads)
+    if (s.threads == kGradThreads)
       return launch_grad_stream<A, R, 2, W, kGradThreads>(a, s, st);
   if constexpr (sizeof(A) == 2 && sizeof(R) == 2)
-    if (vec && s.pieces == 2)      // d up to 8192; fp32 rows would not fit the ring
-      return launch_grad_stream<A, R, 2, W, kStreamThreads>(a, s, st);
+    if (s.pieces == 2 && access != Access::kAny)       // fp32 rows would not fit the ring
+      return vec ? launch_grad_stream<A, R, 2, W, kStreamThreads>(a, s, st)
+                 : launch_grad_stream<A, R, 2, 1, kStreamThreads>(a, s, st);
   if (s.pieces == 4)
     return vec ? launch_grad_wide<A, R, 4, W>(a, s, st) : launch_grad_wide<A, R, 4, 1>(a, s, st);
-  if (s.pieces == 2)
-    return vec ? launch_grad_wide<A, R, 2, W>(a, s, st) : launch_grad_wide<A, R, 2, 1>(a, s, st);
-  return vec ? launch_grad_stream<A, R, 1, W, kStreamThreads>(a, s, st)
-             : launch_grad_stream<A, R, 1, 1, kStreamThreads>(a, s, st);
+  return vec ? launch_grad_wide<A, R, 2, W>(a, s, st) : launch_grad_wide<A, R, 2, 1>(a, s, st);
 }
 
 int elem(int dtype) { return dtype == MOE_DTYPE_FP32 ? 4 : 2; }
@@ -1093,7 +1190,7 @@ bool rows_ok(const void* p, long long ld, int d, int dtype) {
 bool rows_vec(const void* p, long long ld, int dtype) {
   return !p || ((reinterpret_cast<uintptr_t>(p) & 15u) == 0 && ld * elem(dtype) % 16 == 0);
 }
-bool vec_param(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool base_aligned(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool elem_aligned(const void* p, int dtype) {
   return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(elem(dtype) - 1)) == 0;
 }
@@ -1151,16 +1248,19 @@ extern "C" int moe_block_norm_forward(const moe_block_norm_desc* s, int T, const
   const bool vec = d % 8 == 0 && rows_vec(residual, ld_residual, s->residual_dtype) &&
                    rows_vec(y, ld_y, s->dtype) && rows_vec(u, ld_u, s->dtype) &&
                    (!y || rows_vec(residual_out, ld_out, s->residual_dtype)) &&
-                   vec_param(w_post) && vec_param(w_pre) &&
-                   (s->gate != MOE_GATE_CHANNEL || vec_param(gate));
+                   base_aligned(w_post) && base_aligned(w_pre) &&
+                   (s->gate != MOE_GATE_CHANNEL || base_aligned(gate));
+  const Access access = vec ? Access::kVector
+                        : d >= kStagedMinWidth && base_aligned(residual) && base_aligned(y)
+                            ? Access::kStaged : Access::kAny;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (s->dtype == MOE_DTYPE_FP32)
-    e = launch_fwd_types<float, float>(a, vec, st);
+    e = launch_fwd_types<float, float>(a, access, st);
   else if (s->residual_dtype == MOE_DTYPE_FP32)
-    e = launch_fwd_types<uint16_t, float>(a, vec, st);
+    e = launch_fwd_types<uint16_t, float>(a, access, st);
   else
-    e = launch_fwd_types<uint16_t, uint16_t>(a, vec, st);
+    e = launch_fwd_types<uint16_t, uint16_t>(a, access, st);
   return cuda_result(e, "moe_block_norm_forward");
 }
 
@@ -1211,9 +1311,13 @@ extern "C" int moe_block_norm_backward(
                    rows_vec(d_residual_out, ld_dout, s->residual_dtype) &&
                    rows_vec(d_u, ld_du, s->dtype) &&
                    rows_vec(d_residual, ld_dres, s->residual_dtype) &&
-                   rows_vec(dy, ld_dy, s->dtype) && vec_param(w_post) && vec_param(w_pre) &&
-                   (s->gate != MOE_GATE_CHANNEL || vec_param(gate));
+                   rows_vec(dy, ld_dy, s->dtype) && base_aligned(w_post) && base_aligned(w_pre) &&
+                   (s->gate != MOE_GATE_CHANNEL || base_aligned(gate));
   // no rows: one CTA, which writes zero sums
+  const Access access = vec ? Access::kVector
+                        : d >= kStagedMinWidth && base_aligned(residual_out) && base_aligned(y) &&
+                                  base_aligned(d_residual_out) && base_aligned(d_u)
+                            ? Access::kStaged : Access::kAny;
   const GradShape shape = grad_shape(T, d, vec, s->dtype == MOE_DTYPE_BF16);
   a.tpr = shape.tpr;
   if (sums && shape.grid > 1) {
@@ -1226,11 +1330,11 @@ extern "C" int moe_block_norm_backward(
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (s->dtype == MOE_DTYPE_FP32)
-    e = launch_grad_types<float, float>(a, vec, shape, st);
+    e = launch_grad_types<float, float>(a, access, shape, st);
   else if (s->residual_dtype == MOE_DTYPE_FP32)
-    e = launch_grad_types<uint16_t, float>(a, vec, shape, st);
+    e = launch_grad_types<uint16_t, float>(a, access, shape, st);
   else
-    e = launch_grad_types<uint16_t, uint16_t>(a, vec, shape, st);
+    e = launch_grad_types<uint16_t, uint16_t>(a, access, shape, st);
   if (e == cudaSuccess && a.partial)
     e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32), dim3(kSlices * 32), 0, st, a);
   return cuda_result(e, "moe_block_norm_backward");

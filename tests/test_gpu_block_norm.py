@@ -114,6 +114,36 @@ def test_forward_and_gradient(moe, T, d, types):
     c.check_backward()
 
 
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("T,d,extra", [(700, 1537, 0), (1300, 77, 0), (5000, 9, 2), (650, 4095, 0),
+                                       (700, 2048, 3), (620, 5001, 1), (700, 250, 0)])
+def test_many_unaligned_rows(moe, T, d, extra, types):
+    c = Case(moe, T, d, types, gate="token" if d % 2 else "channel", extra=extra)
+    c.check_forward()
+    c.check_backward()
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("T,d", [(700, 1537), (700, 2048), (3, 513), (640, 4097), (620, 8191)])
+def test_tensors_that_begin_between_16_byte_boundaries(moe, T, d, types):
+    c = Case(moe, T, d, types)
+
+    def moved(t):
+        wide = torch.full((t.numel() + 1,), float("nan"), dtype=t.dtype, device=t.device)
+        wide[1:] = t.reshape(-1)
+        return wide[1:].view(t.shape)
+
+    for name in ("res", "y", "d_out", "d_u", "w_post", "w_pre", "gate"):
+        whole = getattr(c, name)
+        setattr(c, name, moved(whole))
+        c.check_forward()
+        c.check_backward()
+        setattr(c, name, whole)
+    c.res, c.y, c.d_out, c.d_u = moved(c.res), moved(c.y), moved(c.d_out), moved(c.d_u)
+    c.check_forward()
+    c.check_backward()
+
+
 @pytest.mark.parametrize("parts", [
     dict(y=False, gate="none"), dict(pre=False), dict(post=False), dict(post=False, pre=False),
     dict(gate="none"), dict(gate="token"), dict(post=False, gate="token"),

@@ -73,6 +73,18 @@ def test_sizes(moe, T, E, k, scoring, dtype):
 
 
 @pytest.mark.parametrize("scoring", SCORINGS)
+def test_several_rows_to_a_warp(moe, scoring):
+    """More rows than warps on the GPU, live and masked ones in turn."""
+    T, E, k = 15001, 40, 3
+    g = torch.Generator().manual_seed(11)
+    logits = (torch.randn(T, E, generator=g) * 2).cuda()
+    mask = (torch.rand(T, generator=g) < 0.7).to(torch.uint8).cuda()
+    r = make_router(moe, T, E, k, scoring)
+    f = check_forward(r, logits, k, scoring, mask=mask)
+    check_backward(r, logits, f, k, scoring)
+
+
+@pytest.mark.parametrize("scoring", SCORINGS)
 @pytest.mark.parametrize("dtype", list(TYPES))
 def test_bias_mask_strides_and_switched_off_experts(moe, scoring, dtype):
     T, E, k = 517, 90, 7
