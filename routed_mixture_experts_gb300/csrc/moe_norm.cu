@@ -152,18 +152,33 @@ __device__ __forceinline__ void store8(T* p, int v, int li, int tpr, int d, cons
   }
 }
 
-// parameters (fp32 or bf16), at the same columns
-template <int W>
-__device__ __forceinline__ void load8_param(const void* p, int bf16, int v, int li, int tpr, int d,
-                                            float (&f)[8]) {
-  if (bf16)
-    load8<W>(static_cast<const uint16_t*>(p), v, li, tpr, d, f);
-  else
-    load8<W>(static_cast<const float*>(p), v, li, tpr, d, f);
-}
-
 __device__ __forceinline__ float param(const void* p, int bf16, long long i) {
   return bf16 ? bf2f(static_cast<const uint16_t*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+template <int W, typename P>
+__device__ __forceinline__ void load_factors_as(const NormArgs& a, bool y, bool u, int v, int li,
+                                                int tpr, float (&q)[8], float (&g)[8],
+                                                float (&w)[8]) {
+  if (y && a.w_post) load8<W>(static_cast<const P*>(a.w_post), v, li, tpr, a.d, q);
+  if (y && a.gate_kind == MOE_GATE_CHANNEL)
+    load8<W>(static_cast<const P*>(a.gate), v, li, tpr, a.d, g);
+  if (u) load8<W>(static_cast<const P*>(a.w_pre), v, li, tpr, a.d, w);
+}
+// The row-independent factors of a thread's columns: q = alpha * w_post * channel gate
+// (of y) and w_pre (of u; 0 without).  All loads first: one wait instead of three.
+template <int W>
+__device__ __forceinline__ void load_factors(const NormArgs& a, bool y, bool u, int v, int li,
+                                             int tpr, float (&q)[8], float (&w)[8]) {
+  float g[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = g[e] = 1.f, w[e] = 0.f;
+  if (a.param_bf16)
+    load_factors_as<W, uint16_t>(a, y, u, v, li, tpr, q, g, w);
+  else
+    load_factors_as<W, float>(a, y, u, v, li, tpr, q, g, w);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) q[e] = a.alpha * q[e] * g[e];
 }
 
 __device__ __forceinline__ void group_sync(int id, int threads) {
@@ -201,40 +216,26 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
   const long long row = (long long)blockIdx.x * (blockDim.x / tpr) + g;
   if (row >= a.T) return;                      // whole groups: their barriers are their own
   const int d = a.d;
-  float x[V][8];
+  float x[V][8], y[V][8], q[V][8], w[V][8];
 #pragma unroll
-  for (int v = 0; v < V; ++v)
+  for (int v = 0; v < V; ++v) {
     load8<W>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
+    if (a.y) load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
+    if (V == 1) load_factors<W>(a, a.y, a.u, v, li, tpr, q[v], w[v]);   // else no registers
+  }
   if (a.y) {
-    float y[V][8];
-    float s = 0.f;
+    float s = 0.f, f = 1.f;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
+    for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
-    }
-    float f = a.alpha;
-    if (a.gate_kind == MOE_GATE_TOKEN) f *= param(a.gate, a.param_bf16, row);
-    if (a.w_post) {
-      f *= inv_rms(group_sum(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
-    }
+    if (a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
+    if (a.w_post) f *= inv_rms(group_sum(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      if (a.w_post) {
-        float w[8];
-        load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, w);
+      if (V > 1) load_factors<W>(a, true, false, v, li, tpr, q[v], w[v]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[v][e] *= w[e];
-      }
-      if (a.gate_kind == MOE_GATE_CHANNEL) {
-        float w[8];
-        load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) y[v][e] *= w[e];
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[v][e] += f * y[v][e];
+      for (int e = 0; e < 8; ++e) x[v][e] += f * (q[v][e] * y[v][e]);
       store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, x[v]);
     }
   }
@@ -247,11 +248,10 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
     const float rs = inv_rms(group_sum(s, &red[1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      float w[8];
-      load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w);
+      if (V > 1) load_factors<W>(a, false, true, v, li, tpr, q[v], w[v]);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) w[e] = x[v][e] * rs * w[e];
-      store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, w);
+      for (int e = 0; e < 8; ++e) x[v][e] *= rs * w[v][e];
+      store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, x[v]);
     }
   }
   pdl_trigger();
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
     }
     cp_async_commit();
   };
-  if (W > 1) {
+  if (W > 1 && (d < 8 * V * tpr || !a.y)) {
     // slots that no copy fills (columns past the row, no y) read as zero
     for (int i = threadIdx.x; i < kStages * kStage / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -452,20 +452,8 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
   f2 q[V][4], w[V][4];         // alpha * w_post * channel gate, w_pre
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float f[8], q8[8], w8[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) q8[e] = a.alpha, w8[e] = 0.f;
-    if (a.y && a.w_post) {
-      load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
-    }
-    if (a.y && a.gate_kind == MOE_GATE_CHANNEL) {
-      load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
-    }
-    if (a.u) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w8);
+    float q8[8], w8[8];
+    load_factors<W>(a, a.y, a.u, v, li, tpr, q8, w8);
     to_f2(q8, q[v]);
     to_f2(w8, w[v]);
   }
@@ -763,7 +751,7 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
       --left;
     }
   };
-  if (W > 1) {
+  if (W > 1 && (!ALL || d < 8 * V * tpr)) {
     // slots that no copy fills (columns past the row, absent tensors) read as zero
     for (int i = threadIdx.x; i < kGradStages * kStage / 16; i += blockDim.x)
       reinterpret_cast<uint4*>(ring)[i] = make_uint4(0u, 0u, 0u, 0u);
@@ -780,20 +768,8 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
   const f2 zero = make_f2(0.f, 0.f);
 #pragma unroll
   for (int v = 0; v < V; ++v) {
-    float w8[8], q8[8], f[8];
-#pragma unroll
-    for (int e = 0; e < 8; ++e) w8[e] = 0.f, q8[e] = a.alpha;
-    if (has_du) load8_param<W>(a.w_pre, a.param_bf16, v, li, tpr, d, w8);
-    if (has_y && a.w_post) {
-      load8_param<W>(a.w_post, a.param_bf16, v, li, tpr, d, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
-    }
-    if (has_y && a.gate_kind == MOE_GATE_CHANNEL) {
-      load8_param<W>(a.gate, a.param_bf16, v, li, tpr, d, f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) q8[e] *= f[e];
-    }
+    float q8[8], w8[8];
+    load_factors<W>(a, has_y, has_du, v, li, tpr, q8, w8);
     param_write<TH>(params + 2 * v * kF, w8);
     param_write<TH>(params + (2 * v + 1) * kF, q8);
 #pragma unroll
