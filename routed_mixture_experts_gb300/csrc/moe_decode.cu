@@ -17,7 +17,7 @@
 // and the last two end with a third launch that adds a token's experts.
 // Measured at d=2048, I=768, k=8 (bytes at the rate of a plain copy): 1 token on 128
 // experts 12.2 us (3.1), 7 tokens on 16 experts 20.7 (6.2), 64 tokens on 128 experts
-// 75.7 (49.4).  Up to the last it is bound by the latency of a launch's start (ids, the
+// 73.6 (49.4).  Up to the last it is bound by the latency of a launch's start (ids, the
 // plan, the tokens' rows, the first weights: some 6 us, twice); the last streams near the
 // memory's rate between its two starts.
 //
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a
 // the next stage (or the next unit's first) on its way while one is read.  Nothing in
 // the stream waits for another warp.  Whole lines, because lanes that load 64-byte pieces
 // of eight rows stay at 5.1 to 5.8 TB/s where lines reach 6.5.  64 tokens on all of 128
-// experts, d=2048, I=768 (335 MB): 75.7 us with all launches, 4.4 TB/s.
+// experts, d=2048, I=768 (335 MB): 73.6 us with all launches, 4.6 TB/s.
 constexpr int kStreamWarps = 16;
 constexpr int kStages = 2;
 constexpr int kStageBytes = 32 * 128 + 512;                 // codes, scales
@@ -729,9 +729,13 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
         two[i][2] = min(a.cols, m.tokens - k * a.cols);
       }
     }
-    if (threadIdx.x == 0) taken = kStreamWarps;
-    __syncthreads();
     const int n0 = min(n, per - sub0), n1 = min(n - n0, per), here = n0 + n1;
+    // as many warps as bring whole rounds of units: a last round of a few leaves the
+    // memory idle (64 tokens on 128 experts 75.4 us with all warps, 73.6 so; 32: 67.2, 63.2)
+    const int rounds = (here + kStreamWarps - 1) / kStreamWarps;
+    const int active = (here + rounds - 1) / rounds;
+    if (threadIdx.x == 0) taken = active;
+    __syncthreads();
     // where the lane copies from: row lane / 8 of a unit, piece lane % 8; and the
     // scales of line lane % 8 in K group lane / 8
     auto rows = [&](int v) {
@@ -747,7 +751,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) k_decode_stream(const De
     };
     // The copies are kStages - 1 stages ahead: stage `to` of the rows r comes next, of
     // the warp's unit or (in_next) of the one it takes after that.
-    int unit = warp, next = here, to = 0, to_slot = 0;
+    int unit = warp < active ? warp : here, next = here, to = 0, to_slot = 0;
     bool more = unit < here, in_next = false;
     Rows r{nullptr, nullptr};
     if (more) r = rows(unit);
