@@ -97,11 +97,13 @@ __device__ __forceinline__ void store_vec8(uint16_t* p, const float (&f)[8]) {
 // row is 16-byte aligned and d a multiple of 8, W is 8 if all tensors are bf16 and 4
 // if one is fp32 (16 bytes of that one, so that a warp's accesses are whole lines:
 // with eight fp32 columns a thread they touch every sector twice: 56 against 39 us for
-// the fp32 gradient at T=8192, d=1024).  Else W is 1, one of each tpr columns.
+// the fp32 gradient at T=8192, d=1024).  Else W is 1: a warp's 256
+// columns, each 32nd to a lane, so that they lie at constant distances.
 template <int W>
 __device__ __forceinline__ int col(int v, int e, int li, int tpr) {
   return W == 8 ? (v * tpr + li) * 8 + e
-                : W == 4 ? ((2 * v + (e >> 2)) * tpr + li) * 4 + (e & 3) : (v * 8 + e) * tpr + li;
+                : W == 4 ? ((2 * v + (e >> 2)) * tpr + li) * 4 + (e & 3)
+                         : (v * tpr + (li & ~31)) * 8 + e * 32 + (li & 31);
 }
 
 __device__ __forceinline__ void load_vec4(const float* p, float* f) {
@@ -185,19 +187,21 @@ __device__ __forceinline__ void group_sync(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
 
-// Sum a value over the tpr threads of a row group: the warps' sums in `buf` (one per
-// warp), then every warp adds them in the same order, so all threads get the same
-// bits.
+// Sum a value over the tpr threads of a row group of up to WARPS warps (16 or 32): the
+// warps' sums in `buf` (one per warp), then every warp adds them in the same order, so
+// all threads get the same bits.
+template <int WARPS>
 __device__ __forceinline__ float group_sum(float s, float* buf, int li, int tpr, int bar) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   if (tpr == 32) return s;
-  const int lane = li & 31, warps = tpr / 32;
-  if (lane == 0) buf[li >> 5] = s;
+  const int at = li & (WARPS - 1);
+  if ((li & 31) == 0) buf[li >> 5] = s;
   group_sync(bar, tpr);
-  s = lane < warps ? buf[lane] : 0.f;
-  for (int o = 1; o < warps; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return __shfl_sync(0xffffffffu, s, 0);
+  s = at < tpr / 32 ? buf[at] : 0.f;
+#pragma unroll
+  for (int o = 1; o < WARPS; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+  return s;
 }
 
 __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
@@ -230,7 +234,7 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += y[v][e] * y[v][e];
     if (a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
-    if (a.w_post) f *= inv_rms(group_sum(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+    if (a.w_post) f *= inv_rms(group_sum<32>(s, &red[0][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (V > 1) load_factors<W>(a, true, false, v, li, tpr, q[v], w[v]);
@@ -245,7 +249,7 @@ __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s += x[v][e] * x[v][e];
-    const float rs = inv_rms(group_sum(s, &red[1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+    const float rs = inv_rms(group_sum<32>(s, &red[1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       if (V > 1) load_factors<W>(a, false, true, v, li, tpr, q[v], w[v]);
@@ -419,25 +423,34 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
   pdl_wait();
   const int tpr = a.tpr, groups = blockDim.x / tpr;
   const int g = threadIdx.x / tpr, li = threadIdx.x - g * tpr, d = a.d;
-  const long long first = (long long)blockIdx.x * groups + g, hop = (long long)gridDim.x * groups;
+  const long long first = (long long)blockIdx.x * groups + g;
+  const int hop = gridDim.x * groups;
   const uint32_t base = smem_u32(ring);
-  const A* const y_in = static_cast<const A*>(a.y);
-  const R* const x_in = static_cast<const R*>(a.res);
+  const int rows = first < a.T ? (int)((a.T - first + hop - 1) / hop) : 0;   // of the group
+  // the rows to fetch next, and the rows to write
+  const A* y_in = static_cast<const A*>(a.y) + (a.y ? first * a.ld_y : 0);
+  const R* x_in = static_cast<const R*>(a.res) + first * a.ld_res;
+  R* out = static_cast<R*>(a.out) + (a.y ? first * a.ld_out : 0);
+  A* u_out = static_cast<A*>(a.u) + (a.u ? first * a.ld_u : 0);
+  int left = rows;                               // rows not fetched yet
   const int row_bytes = row_slot<A>(d) + row_slot<R>(d);                // W = 1
-  auto fetch = [&](long long row, int stage) {
-    if (row < a.T) {
+  auto fetch = [&](int stage) {
+    if (left > 0) {
       if constexpr (W > 1) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
           const uint32_t at = base + stage * kStage + v * kPiece;
-          if (a.y) slot_copy<W>(at, y_in + row * a.ld_y, v, li, tpr, d);
-          slot_copy<W>(at + slot_bytes<A>(), x_in + row * a.ld_res, v, li, tpr, d);
+          if (a.y) slot_copy<W>(at, y_in, v, li, tpr, d);
+          slot_copy<W>(at + slot_bytes<A>(), x_in, v, li, tpr, d);
         }
       } else {
         const uint32_t at = base + (stage * groups + g) * row_bytes;
-        if (a.y) row_copy(at, y_in + row * a.ld_y, li, tpr, d);
-        row_copy(at + row_slot<A>(d), x_in + row * a.ld_res, li, tpr, d);
+        if (a.y) row_copy(at, y_in, li, tpr, d);
+        row_copy(at + row_slot<A>(d), x_in, li, tpr, d);
       }
+      if (a.y) y_in += hop * a.ld_y;
+      x_in += hop * a.ld_res;
+      --left;
     }
     cp_async_commit();
   };
@@ -448,7 +461,7 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < kStages - 1; ++i) fetch(first + i * hop, i);
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
   f2 q[V][4], w[V][4];         // alpha * w_post * channel gate, w_pre
 #pragma unroll
   for (int v = 0; v < V; ++v) {
@@ -467,7 +480,8 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
     return sum_f2(s);
   };
   int stage = 0, flip = 0;
-  for (long long row = first; row < a.T; row += hop) {
+  long long row = first;
+  for (int n = 0; n < rows; ++n, row += hop) {
     f2 x[V][4], y[V][4];
     float f = 1.f, t[8];
     if (a.y && a.gate_kind == MOE_GATE_TOKEN) f = param(a.gate, a.param_bf16, row);
@@ -498,11 +512,11 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
       }
     }
     // into the slots read one row ago
-    fetch(row + (kStages - 1) * hop, stage == 0 ? kStages - 1 : stage - 1);
+    fetch(stage == 0 ? kStages - 1 : stage - 1);
     stage = stage + 1 == kStages ? 0 : stage + 1;
     if (a.y) {
       if (a.w_post)
-        f *= inv_rms(group_sum(squares(y), &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d,
+        f *= inv_rms(group_sum<16>(squares(y), &red[flip][0][g * (tpr / 32)], li, tpr, 1 + g), d,
                      a.eps);
       const f2 f2x = make_f2(f, f);
 #pragma unroll
@@ -510,12 +524,12 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[v][i] = fma2(f2x, mul2(q[v][i], y[v][i]), x[v][i]);
         from_f2(x[v], t);
-        store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, t);
+        store8<W>(out, v, li, tpr, d, t);
       }
     }
     if (a.u) {
       const float rs =
-          inv_rms(group_sum(squares(x), &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
+          inv_rms(group_sum<16>(squares(x), &red[flip][1][g * (tpr / 32)], li, tpr, 1 + g), d, a.eps);
       const f2 rs2 = make_f2(rs, rs);
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -523,9 +537,11 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
 #pragma unroll
         for (int i = 0; i < 4; ++i) u[i] = mul2(x[v][i], mul2(rs2, w[v][i]));
         from_f2(u, t);
-        store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, t);
+        store8<W>(u_out, v, li, tpr, d, t);
       }
     }
+    if (a.y) out += hop * a.ld_out;
+    if (a.u) u_out += hop * a.ld_u;
     flip ^= 1;
   }
   pdl_trigger();
