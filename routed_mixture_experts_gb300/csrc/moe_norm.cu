@@ -21,7 +21,7 @@
 //
 // Bound by memory: forward 4, gradient 6 passes over a [T, d] tensor.  At T=8192, d=2048
 // in bf16 that is 134 and 201 MB, 19.8 and 29.7 us at the rate of a plain copy; measured
-// 24.5 us (5.5 TB/s) and 41.3 us (4.9 TB/s, its second launch included).
+// 22.5 us (6.0 TB/s) and 40.3 us (5.0 TB/s, its second launch included).
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
@@ -210,7 +210,7 @@ __device__ __forceinline__ float inv_rms(float sum_sq, int d, float eps) {
 
 // Forward, a row per group of tpr threads and no loop: few rows, and what the stream
 // below does not take (d > 8192; tensors that are not 16-byte aligned).  All loads of a
-// row are independent; latency bounds it (one row of d=2048 2.6 us, of which a launch is
+// row are independent; latency bounds it (one row of d=2048 2.3 us, of which a launch is
 // most).
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(1024) k_block_norm(const NormArgs a) {
@@ -303,7 +303,7 @@ __device__ __forceinline__ void from_f2(const f2 (&p)[4], float (&f)[8]) {
 // of its group.  It copies its own pieces of the next rows into its own slots of a
 // ring with cp.async and reads them back itself, so a copy in flight costs no register
 // and needs no barrier; the parameters of its columns stay in registers.  (One row a
-// group without a loop: T=8192, d=2048, bf16: 30.2 us against 24.5.)
+// group without a loop: T=8192, d=2048, bf16: 30.2 us against 22.5.)
 
 constexpr int kStreamThreads = 512;
 constexpr int kStreamMaxWidth = kStreamThreads * 8;
@@ -367,10 +367,11 @@ __device__ __forceinline__ void param_write(uint8_t* slot, const float (&f)[8]) 
 // are at least 16 bytes apart: kStagedMinWidth); the last one stops at the row's end.
 // Against loads of single elements into registers, one row ahead (us): forward, T=8192,
 // d=777, bf16 33.2 -> 25.2; T=8191, d=1023, fp32 36.2 -> 32.3; T=2047, d=8191, bf16
-// 85.9 -> 56.2.  What is left is the writing, an element a thread (T=8192, d=2047, bf16
-// 52.9; with one of eight stores 31); pieces written through shared memory too cost as
-// much for their barrier (56.8).  The gradient of up to 4096 columns loses with it (34.0
-// against 39.7 us for an fp32 residual, T=4099, d=1537) and keeps its loads.
+// 85.9 -> 56.2; with the columns of a lane at constant distances 19.9, 26.5 and 43.6.
+// Bound by the instructions of single elements (T=8192, d=2047, bf16 39.8); writing whole
+// pieces through shared memory too costs more for its barrier than it saves.  The
+// gradient of up to 4096 columns keeps its loads (an fp32 residual, T=4099, d=1537: 34.7
+// against 39.3 us with copied rows; bf16, T=8192, d=2047: 62.5 against 59.5).
 constexpr int kStagedMinWidth = 8;
 
 // A row's slot, and where its first element is in it.
@@ -679,8 +680,8 @@ __device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float
 // ALL: every tensor is given.
 // Its row loop runs at nine tenths of a copy's rate; the rest of the time are the start,
 // the CTAs' column sums and the launch that adds them.  Measured with that launch: bf16
-// T=8192, d=2048 41.3 us, T=2048, d=8192 63, T=2047, d=8191 98, fp32 T=8192, d=1024
-// 37; fp32 residual, T=4099, d=1537 (one piece of single elements) 34.
+// T=8192, d=2048 40.3 us, T=2048, d=8192 63, T=2047, d=8191 72, fp32 T=8192, d=1024
+// 37; fp32 residual, T=4099, d=1537 (one piece of single elements) 34.5.
 constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
 
@@ -935,7 +936,7 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
 // 16-byte aligned): a group is the CTA, V pieces of 8 columns a thread, the parameters in
 // shared memory.  A row's registers leave no room for the next row, so that its loads are
 // waited for: bf16 T=2048, d=8192 took 77 us here, 63 in the kernel above; T=2047, d=8191
-// 219 against 98.
+// 219 against 72.  Slowest where four pieces of single elements spill (T=1000, d=9001: 241).
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
   extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
@@ -959,33 +960,46 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
     for (int e = 0; e < 8; ++e) P[v][e] = S[v][e] = 0.f;
   int flip = 0;
   for (long long row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
-    float x[V][8], y[V][8], dr[V][8], du[V][8];
-    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int v = 0; v < V; ++v) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[v][e] = dr[v][e] = du[v][e] = 0.f;
-      load8<W>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[v]);
-      if (a.y) load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[v]);
-      if (a.dres) load8<W>(static_cast<const R*>(a.dres) + row * a.ld_dres, v, li, tpr, d, dr[v]);
-      if (a.du) load8<W>(static_cast<const A*>(a.du) + row * a.ld_du, v, li, tpr, d, du[v]);
-    }
+    // Two pieces of a row are kept over the reduction; four would spill and are read
+    // again (T=1000, d=16384: bf16 142 -> 90 us, fp32 196 -> 116; with two pieces, d=8192,
+    // 95 -> 103).
+    constexpr bool kKept = V <= 2;
+    float x[kKept ? V : 1][8], y[kKept ? V : 1][8], dr[kKept ? V : 1][8], du[kKept ? V : 1][8];
     float wp[8], q[8];
+    auto piece = [&](int v) {
+      const int i = kKept ? v : 0;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
+      for (int e = 0; e < 8; ++e) y[i][e] = dr[i][e] = du[i][e] = 0.f;
+      load8<W>(static_cast<const R*>(a.res) + row * a.ld_res, v, li, tpr, d, x[i]);
+      if (a.y) load8<W>(static_cast<const A*>(a.y) + row * a.ld_y, v, li, tpr, d, y[i]);
+      if (a.dres) load8<W>(static_cast<const R*>(a.dres) + row * a.ld_dres, v, li, tpr, d, dr[i]);
+      if (a.du) load8<W>(static_cast<const A*>(a.du) + row * a.ld_du, v, li, tpr, d, du[i]);
+    };
+    auto factors = [&](int v) {
       load8<W>(wpre, v, li, tpr, d, wp);
       load8<W>(qs, v, li, tpr, d, q);
-      row_sums(s, x[v], y[v], dr[v], du[v], wp, q);
+    };
+    float s[6] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (kKept)
+#pragma unroll
+      for (int v = 0; v < V; ++v) piece(v);
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const int i = kKept ? v : 0;
+      if (!kKept) piece(v);
+      factors(v);
+      row_sums(s, x[i], y[i], dr[i], du[i], wp, q);
     }
     group_sum6(s, red[flip], li, tpr, 1);
     const RowFactors f = row_factors<false>(a, s, 1.f / (float)d, row, li == 0);
 #pragma unroll
     for (int v = 0; v < V; ++v) {
-      load8<W>(wpre, v, li, tpr, d, wp);
-      load8<W>(qs, v, li, tpr, d, q);
-      row_grads(f, x[v], y[v], dr[v], du[v], wp, q, P[v], S[v]);
-      store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, dr[v]);
-      if (a.y && a.u) store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, y[v]);
+      const int i = kKept ? v : 0;
+      if (!kKept) piece(v);
+      factors(v);
+      row_grads(f, x[i], y[i], dr[i], du[i], wp, q, P[v], S[v]);
+      store8<W>(static_cast<R*>(a.out) + row * a.ld_out, v, li, tpr, d, dr[i]);
+      if (a.y && a.u) store8<W>(static_cast<A*>(a.u) + row * a.ld_u, v, li, tpr, d, y[i]);
     }
   }
   pdl_trigger();
