@@ -16,8 +16,8 @@
 //   many units           a unit a warp, weights streamed through a ring in shared memory
 // and the last two end with a third launch that adds a token's experts.
 // Measured at d=2048, I=768, k=8 (bytes at the rate of a plain copy): 1 token on 128
-// experts 12.2 us (3.1), 7 tokens on 16 experts 20.7 (6.2), 64 tokens on 128 experts
-// 73.6 (49.4).  Up to the last it is bound by the latency of a launch's start (ids, the
+// experts 12.2 us (3.1), 7 tokens on 16 experts 21.0 (6.2), 64 tokens on 128 experts
+// 72.2 (49.4).  Up to the last it is bound by the latency of a launch's start (ids, the
 // plan, the tokens' rows, the first weights: some 6 us, twice); the last streams near the
 // memory's rate between its two starts.
 //
@@ -674,7 +674,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a
 // the next stage (or the next unit's first) on its way while one is read.  Nothing in
 // the stream waits for another warp.  Whole lines, because lanes that load 64-byte pieces
 // of eight rows stay at 5.1 to 5.8 TB/s where lines reach 6.5.  64 tokens on all of 128
-// experts, d=2048, I=768 (335 MB): 73.6 us with all launches, 4.6 TB/s.
+// experts, d=2048, I=768 (335 MB): 72.2 us with all launches, 4.6 TB/s.
 constexpr int kStreamWarps = 16;
 constexpr int kStages = 2;
 constexpr int kStageBytes = 32 * 128 + 512;                 // codes, scales
