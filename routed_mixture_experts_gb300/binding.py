@@ -178,6 +178,9 @@ class MoePlan:
         _check(L.moe_plan_set_swiglu_clamp(self.ptr, float(clamp)), "clamp")
         if cta_pairs:
             _check(L.moe_plan_set_cta_pairs(self.ptr, 1), "cta_pairs")
+        if precision == MOE_PREC_NVFP4:       # of codes, scales and fp32 scales of W13 and W2
+            size = [L.moe_nvfp4_weight_bytes(d, I, E, which) for which in range(4)]
+            self._prepared_bytes = [size[0], size[1], 4 * E, size[2], size[3], 4 * E]
         nbytes = L.moe_plan_workspace_bytes(self.ptr, flags)
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         _check(L.moe_plan_set_workspace(self.ptr, _p(self.workspace), nbytes, flags), "workspace")
@@ -235,6 +238,9 @@ class MoePlan:
         prepared = prepare_weights_nvfp4(w13, w2) (see moe_decode_nvfp4 in moe.h)."""
         import torch
 
+        if stream is not None:               # y then belongs to that stream too
+            with torch.cuda.stream(stream):
+                return self.decode_nvfp4(x, ids, scores, prepared, y)
         n, k = x.shape[0], self.k
         bf16 = torch.bfloat16
         xp = _want(x, "x", bf16, (n, self.d))
@@ -243,12 +249,16 @@ class MoePlan:
             yp = y.data_ptr()
         else:
             yp = _want(y, "y", bf16, (n, self.d))
+        if (self.precision == MOE_PREC_NVFP4 and
+                [t.nbytes if t.is_cuda else 0 for t in prepared] != self._prepared_bytes):
+            raise MoeError(MOE_ERR_INVALID_ARG, "decode_nvfp4: the weights are not those of "
+                           "prepare_weights_nvfp4 for this plan's d, I and E")
         w13q, w13s, w13c, w2q, w2s, w2c = prepared
         _check(_lib.moe_decode_nvfp4(
             self.ptr, xp, _want(ids, "ids", torch.int32, (n, k)),
             _want(scores, "scores", torch.float32, (n, k)), n, w13q.data_ptr(), w13s.data_ptr(),
             w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
-            yp, _raw_stream(stream)), "decode_nvfp4")
+            yp, _raw_stream()), "decode_nvfp4")
         return y
 
     def backward(self, dy, w13, w2, dw13, dw2, dx=None, dscores=None, stream=None):
@@ -438,14 +448,12 @@ def gemm_bf16(mode, A, B, C, M, N, K, stream=None):
 # ---- the operators around the experts -----------------------------------------
 
 
-def _raw_stream(stream):
-    """The handle of `stream`, or of the current device's current stream.  (The public
+def _raw_stream():
+    """The handle of the current device's current stream.  (The public
     torch.cuda.current_stream() builds a Stream object for it, a third of the host
     time of a small call.)"""
     import torch
 
-    if stream is not None:
-        return stream.cuda_stream
     return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
@@ -528,6 +536,9 @@ class MoeRouter:
         `out`: an earlier result (or outputs(T)) to overwrite."""
         import torch
 
+        if stream is not None:               # the outputs then belong to that stream too
+            with torch.cuda.stream(stream):
+                return self.forward(logits, bias, token_mask, out)
         f32, i32 = torch.float32, torch.int32
         T, E, k = logits.shape[0], self.E, self.k
         if T > self.max_tokens:
@@ -545,8 +556,8 @@ class MoeRouter:
                   _want(out.prob_sum, "prob_sum", f32, (E,)),
                   _want(out.losses, "losses", f32, (2,)),
                   _want(out.row_stat, "row_stat", f32, (T,)))
-        _check(_lib.moe_router_forward(self._desc, T, lp, ld, bp, mp, *at, *self._ws, _raw_stream(stream)),
-               "router forward")
+        _check(_lib.moe_router_forward(self._desc, T, lp, ld, bp, mp, *at, *self._ws,
+                                       _raw_stream()), "router forward")
         return out
 
     def backward(self, logits, ids, counts, row_stat, d_scores=None, d_losses=None,
@@ -554,6 +565,9 @@ class MoeRouter:
         """Gradient at the logits of sum(d_scores * scores) + sum(d_losses * losses)."""
         import torch
 
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(logits, ids, counts, row_stat, d_scores, d_losses, d_logits)
         T, E, k = logits.shape[0], self.E, self.k
         f32 = torch.float32
         lp, ld = _rows(logits, "logits", self.dtype, (T, E))
@@ -566,7 +580,7 @@ class MoeRouter:
             self._desc, T, lp, ld, _maybe(ids, "ids", torch.int32, (T, k)),
             _want(counts, "counts", torch.int32, (E + 1,)),
             _want(row_stat, "row_stat", f32, (T,)), _maybe(d_scores, "d_scores", f32, (T, k)),
-            _maybe(d_losses, "d_losses", f32, (2,)), dp, ld_d, _raw_stream(stream)),
+            _maybe(d_losses, "d_losses", f32, (2,)), dp, ld_d, _raw_stream()),
             "router backward")
         return d_logits
 
@@ -611,6 +625,9 @@ class MoeBlockNorm:
         """-> (residual_out, u); without y the first is residual, without w_pre u is None."""
         import torch
 
+        if stream is not None:               # the outputs then belong to that stream too
+            with torch.cuda.stream(stream):
+                return self.forward(residual, y, w_post, gate, w_pre, residual_out, u)
         T = residual.shape[0]
         shape = (T, self.d)
         rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape)
@@ -632,7 +649,7 @@ class MoeBlockNorm:
             else:
                 up, ld_u = _rows(u, "u", self.dtype, shape)
         _check(_lib.moe_block_norm_forward(self._desc, T, rp, ld_r, yp, ld_y, wp, gp, wq, op, ld_o,
-                                            up, ld_u, _raw_stream(stream)), "block norm forward")
+                                            up, ld_u, _raw_stream()), "block norm forward")
         return (residual if y is None else residual_out), (None if w_pre is None else u)
 
     def backward(self, residual_out, d_residual_out=None, d_u=None, y=None, w_post=None, gate=None,
@@ -642,6 +659,10 @@ class MoeBlockNorm:
         inputs are None.  accumulate adds to the given dw_post, dgate and dw_pre."""
         import torch
 
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.backward(residual_out, d_residual_out, d_u, y, w_post, gate, w_pre,
+                                     d_residual, dy, dw_post, dgate, dw_pre, accumulate)
         T, dev, f32 = residual_out.shape[0], residual_out.device, torch.float32
         if T > self.max_tokens:
             raise MoeError(MOE_ERR_INVALID_ARG, "block norm: %d rows, made for %d" % (
@@ -691,5 +712,5 @@ class MoeBlockNorm:
         _check(_lib.moe_block_norm_backward(
             self._desc, T, rp, ld_r, yp, ld_y, gr, ld_gr, gu, ld_gu, wp, gp, wq, op, ld_o, dp, ld_d,
             wpp, ggp, wqp, 1 if accumulate else 0, self.workspace.data_ptr(), self._ws_bytes,
-            _raw_stream(stream)), "block norm backward")
+            _raw_stream()), "block norm backward")
         return BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre)

@@ -293,6 +293,23 @@ def test_another_stream(moe):
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
 
 
+def test_outputs_belong_to_the_given_stream(moe):
+    """Memory that the current stream has yet to write is not handed to another one."""
+    c = Case(moe, 64, 2048)
+    want = c.h.forward(c.res, **c.params())
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    busy = [torch.empty_like(t) for t in want for _ in range(2)]
+    torch.cuda._sleep(100_000_000)                      # some 50 ms
+    for t in busy:
+        t.fill_(77)
+    del t, busy
+    got = c.h.forward(c.res, stream=s, **c.params())
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_refusals(moe):
     with pytest.raises(moe.MoeError):
         moe.MoeBlockNorm(4, 16385)

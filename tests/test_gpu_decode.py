@@ -237,6 +237,26 @@ def test_beside_the_prompt_path_on_one_plan(moe):
     assert rel < 0.3, rel
 
 
+def test_outputs_belong_to_the_given_stream(moe):
+    """Memory that the current stream has yet to write is not handed to another one."""
+    inp = make(T=5, d=256, I=256, E=8, k=2)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, 8, 256, 256)
+    plan = moe.MoePlan(5, 256, 256, 8, 2, precision=moe.MOE_PREC_NVFP4, flags=0)
+    want = [plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)]
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    busy = [torch.empty_like(t) for t in want for _ in range(2)]
+    torch.cuda._sleep(100_000_000)                      # some 50 ms
+    for t in busy:
+        t.fill_(77)
+    del t, busy
+    got = [plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep, stream=s)]
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_refusals(moe):
     L = moe.lib()
     inp = make(T=4, d=256, I=256, E=4, k=2)
@@ -279,3 +299,19 @@ def test_refusals(moe):
     assert call(vp(args[0].data_ptr() + 2), p(y)) == moe.MOE_ERR_INVALID_ARG
     assert call(p(args[0]), p(y), -1) == moe.MOE_ERR_INVALID_ARG
     assert call(None, None, 0) == moe.MOE_OK
+
+
+def test_weights_of_another_plan_are_refused(moe):
+    inp = make(T=5, d=256, I=256, E=8, k=2)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, 8, 256, 256)
+    plan = moe.MoePlan(5, 256, 256, 16, 2, precision=moe.MOE_PREC_NVFP4, flags=0)
+    with pytest.raises(moe.MoeError):
+        plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
+    plan = moe.MoePlan(5, 256, 256, 8, 2, precision=moe.MOE_PREC_NVFP4, flags=0)
+    for i in range(6):
+        wrong = list(w.prep)
+        wrong[i] = wrong[i].reshape(-1)[:-1]
+        with pytest.raises(moe.MoeError):
+            plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], wrong)
+    plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)

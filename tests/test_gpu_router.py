@@ -259,6 +259,24 @@ def test_ids_and_scores_feed_the_experts(moe):
     assert (y[170:] == 0).all() and not (y[:170] == 0).all()
 
 
+def test_outputs_belong_to_the_given_stream(moe):
+    """Memory that the current stream has yet to write is not handed to another one."""
+    logits = torch.randn(500, 60, generator=torch.Generator().manual_seed(3)).cuda()
+    r = make_router(moe, 500, 60, 4, "softmax_topk")
+    want = r.forward(logits)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    busy = [torch.empty_like(t) for t in want for _ in range(2)]
+    torch.cuda._sleep(100_000_000)                      # some 50 ms
+    for t in busy:
+        t.fill_(77)
+    del t, busy
+    got = r.forward(logits, stream=s)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
 def test_refusals(moe):
     for bad in (dict(E=257), dict(E=0), dict(k=0), dict(k=17), dict(scoring=9),
                 dict(dtype=torch.float16), dict(scale=float("nan"))):
