@@ -921,11 +921,22 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
     store8<W>(sm + (2 * g + 1) * d, v, li, tpr, d, f);
   }
   __syncthreads();
-  for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
-    float v = 0.f;
-    for (int i = 0; i < groups; ++i) v += sm[2 * i * d + c];
-    if (a.partial) a.partial[(long long)blockIdx.x * 2 * d + c] = v;
-    else sm[c] = v;                      // only this thread reads group 0's entry
+  float* const to = a.partial ? a.partial + (long long)blockIdx.x * 2 * d : sm;
+  if (d % 2 == 0) {
+    for (int c = 4 * threadIdx.x; c < 2 * d; c += 4 * blockDim.x) {
+      float4 v = *reinterpret_cast<const float4*>(sm + c);
+      for (int i = 1; i < groups; ++i) {
+        const float4 w = *reinterpret_cast<const float4*>(sm + 2 * i * d + c);
+        v.x += w.x, v.y += w.y, v.z += w.z, v.w += w.w;
+      }
+      *reinterpret_cast<float4*>(to + c) = v;      // in sm only this thread reads it
+    }
+  } else {
+    for (int c = threadIdx.x; c < 2 * d; c += blockDim.x) {
+      float v = sm[c];
+      for (int i = 1; i < groups; ++i) v += sm[2 * i * d + c];
+      to[c] = v;
+    }
   }
   if (a.partial) return;
   __syncthreads();
