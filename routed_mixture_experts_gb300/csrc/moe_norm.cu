@@ -21,7 +21,7 @@
 //
 // Bound by memory: forward 4, gradient 6 passes over a [T, d] tensor.  At T=8192, d=2048
 // in bf16 that is 134 and 201 MB, 19.8 and 29.7 us at the rate of a plain copy; measured
-// 22.5 us (6.0 TB/s) and 40.3 us (5.0 TB/s, its second launch included).
+// 22.5 us (6.0 TB/s) and 37.6 us (5.4 TB/s, its second launch included).
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
@@ -550,14 +550,22 @@ __global__ void __launch_bounds__(kStreamThreads, V == 1 ? 2 : 1)
 
 // The column sums' last step: the parameter gradients of column c from
 // P = sum_t du x rs and S = sum_t g_t dr y ry.
+__device__ __forceinline__ void put_grad(const NormArgs& a, float* p, int c, float v) {
+  p[c] = a.accumulate ? p[c] + v : v;
+}
+// The factors of S in dw_post and in the channel gate's gradient.
+__device__ __forceinline__ float2 gate_factors(const NormArgs& a, int c) {
+  const bool channel = a.gate_kind == MOE_GATE_CHANNEL;
+  return make_float2(a.dw_post && channel ? param(a.gate, a.param_bf16, c) : 1.f,
+                     a.dgate && channel && a.w_post ? param(a.w_post, a.param_bf16, c) : 1.f);
+}
+__device__ __forceinline__ void gate_grads(const NormArgs& a, int c, float S, float2 f) {
+  if (a.dw_post) put_grad(a, a.dw_post, c, a.alpha * S * f.x);
+  if (a.dgate && a.gate_kind == MOE_GATE_CHANNEL) put_grad(a, a.dgate, c, a.alpha * S * f.y);
+}
 __device__ __forceinline__ void param_grads(const NormArgs& a, int c, float P, float S) {
-  auto put = [&](float* p, float v) { p[c] = a.accumulate ? p[c] + v : v; };
-  if (a.dw_pre) put(a.dw_pre, P);
-  if (a.dw_post)
-    put(a.dw_post, a.alpha * S *
-                       (a.gate_kind == MOE_GATE_CHANNEL ? param(a.gate, a.param_bf16, c) : 1.f));
-  if (a.dgate && a.gate_kind == MOE_GATE_CHANNEL)
-    put(a.dgate, a.alpha * S * (a.w_post ? param(a.w_post, a.param_bf16, c) : 1.f));
+  if (a.dw_pre) put_grad(a, a.dw_pre, c, P);
+  gate_grads(a, c, S, gate_factors(a, c));
 }
 
 // ---- gradient --------------------------------------------------------------------
@@ -674,13 +682,13 @@ __device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float
 
 // Gradient of rows of up to 4096 columns, up to 8192 with V = 2: row groups walk the
 // rows, the next row on its way (through the ring; one piece of unaligned rows in
-// registers), the sums of
-// a thread's 8 V columns in registers, its parameters in slots of its own.  V = 2 halves
-// what a row costs beside its elements (the reduction, the factors, the addresses).
+// registers), the sums of a thread's 8 V columns in registers, its parameters in slots of
+// its own.  V = 2 halves what a row costs beside its elements (the reduction, the factors,
+// the addresses).
 // ALL: every tensor is given.
 // Its row loop runs at nine tenths of a copy's rate; the rest of the time are the start,
 // the CTAs' column sums and the launch that adds them.  Measured with that launch: bf16
-// T=8192, d=2048 40.3 us, T=2048, d=8192 63, T=2047, d=8191 72, fp32 T=8192, d=1024
+// T=8192, d=2048 37.6 us, T=2048, d=8192 63, T=2047, d=8191 72, fp32 T=8192, d=1024
 // 37; fp32 residual, T=4099, d=1537 (one piece of single elements) 34.5.
 constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
@@ -1029,29 +1037,29 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
 // at d=2048, from L2: latency (5 us alone, some 3 behind the row kernel's end).
 constexpr int kSlices = 32;
 __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormArgs a) {
-  __shared__ float part[2][32][kSlices + 1];
+  __shared__ float part[32][kSlices + 1];
+  const int lane = threadIdx.x & 31, sl = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
+  const float* const mine = a.partial + (blockIdx.y ? a.d : 0) + c;     // P or S
+  const int to = blockIdx.x * 32 + sl;             // the column that this warp's sum is of
+  const bool writes = lane == 0 && to < a.d;
   pdl_wait();
-  const int c = blockIdx.x * 32 + (threadIdx.x & 31), sl = threadIdx.x >> 5;
-  float P = 0.f, S = 0.f;
+  float v = 0.f;
+  float2 f = make_float2(0.f, 0.f);
+  if (writes && blockIdx.y) f = gate_factors(a, to);
   if (c < a.d)
 #pragma unroll 5
-    for (int i = sl; i < a.n_partial; i += kSlices) {
-      P += a.partial[(long long)i * 2 * a.d + c];
-      S += a.partial[(long long)i * 2 * a.d + a.d + c];
-    }
+    for (int i = sl; i < a.n_partial; i += kSlices) v += mine[(long long)i * 2 * a.d];
   // the slices in order: warp w adds column w's
-  part[0][threadIdx.x & 31][sl] = P;
-  part[1][threadIdx.x & 31][sl] = S;
+  part[lane][sl] = v;
   __syncthreads();
-  P = part[0][sl][threadIdx.x & 31];
-  S = part[1][sl][threadIdx.x & 31];
+  v = part[sl][lane];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    P += __shfl_xor_sync(0xffffffffu, P, o);
-    S += __shfl_xor_sync(0xffffffffu, S, o);
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  if (writes) {
+    if (blockIdx.y) gate_grads(a, to, v, f);
+    else if (a.dw_pre) put_grad(a, a.dw_pre, to, v);
   }
-  const int mine = blockIdx.x * 32 + sl;
-  if ((threadIdx.x & 31) == 0 && mine < a.d) param_grads(a, mine, P, S);
   pdl_trigger();
 }
 
@@ -1353,6 +1361,6 @@ extern "C" int moe_block_norm_backward(
   else
     e = launch_grad_types<uint16_t, uint16_t>(a, access, shape, st);
   if (e == cudaSuccess && a.partial)
-    e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32), dim3(kSlices * 32), 0, st, a);
+    e = launch_pdl(k_block_norm_finish, dim3((d + 31) / 32, 2), dim3(kSlices * 32), 0, st, a);
   return cuda_result(e, "moe_block_norm_backward");
 }
