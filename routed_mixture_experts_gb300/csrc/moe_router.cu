@@ -350,8 +350,8 @@ __global__ void __launch_bounds__(1024) k_router_finish(const RouterArgs a) {
 //
 // Reads the logits again and takes the probabilities from row_stat, so that the forward
 // leaves 4 bytes a row instead of 4 E.  Bound by latency and instructions (two or
-// three exponentials' work a logit): 8192 rows of 128 fp32 logits 5.6 us where the 8.9 MB
-// take 1.3; 16411 rows of 250 bf16 logits, 2048 of them masked, 16.1 where they take 2.4.
+// three exponentials' work a logit): 8192 rows of 128 fp32 logits 5.7 us where the 8.9 MB
+// take 1.3; 16411 rows of 250 bf16 logits, 2048 of them masked, 16.3 where they take 2.4.
 constexpr int kGradWarps = 8;
 
 template <typename L, int NV>
@@ -437,19 +437,27 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
       __syncwarp();
     }
     // p = exp(l - lse), or sigmoid(l) / S with log S = stat
-    const float inv = sig ? __expf(-fmaxf(stat, -40.f)) : 1.f;
+    float inv = sig ? __expf(-fmaxf(stat, -40.f)) : 1.f;
     const float far = sig && stat < -40.f ? stat + 40.f : 0.f;     // S alone would underflow
+    auto probability = [&](float v, float& after) {                // after: 1 - sigmoid
+      if (!sig) return __expf(v - stat) * inv;
+      const float u = __expf(-fabsf(v)), s = __fdividef(1.f, 1.f + u);
+      after = v > 0.f ? u * s : s;
+      return (v > 0.f ? s : (far == 0.f ? u : __expf(v - far)) * s) * inv;
+    };
+    // The rounding of stat, 2^-24 |stat|, is a factor of all of them: divided out, except
+    // where it is less than what the exponential errs by (dividing always, with the sum
+    // taken beside gp's, 7.1 us against 5.7 at 8192 rows of 128 experts).
+    if (fabsf(stat) > 8.f) {
+      float sum = 0.f, unused;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) sum += lane + 32 * i < E ? probability(l[i], unused) : 0.f;
+      inv *= __fdividef(1.f, warp_sum(sum));
+    }
     float gp = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      float p, after = 1.f;
-      if (sig) {
-        const float u = __expf(-fabsf(l[i])), v = __fdividef(1.f, 1.f + u);
-        after = l[i] > 0.f ? u * v : v;                            // 1 - sigmoid
-        p = (l[i] > 0.f ? v : (far == 0.f ? u : __expf(l[i] - far)) * v) * inv;
-      } else {
-        p = __expf(l[i] - stat);
-      }
+      float after = 1.f, p = probability(l[i], after);
       if (lane + 32 * i >= E) p = 0.f;
       const float x = ex[lane + 32 * i];
       const float g = b[i] + (in_g ? x : 0.f);

@@ -293,3 +293,39 @@ def test_refusals(moe):
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("scoring", SCORINGS)
+def test_gradient_of_rows_far_from_zero(moe, scoring):
+    """The gradient where row_stat is large, so that its rounding to fp32 is not small
+    beside 1.  A logit d below the logarithm of the row's sum has a weight that errs by
+    2^-24 d for each of: d itself, its product with log2(e), and half of that for the
+    constant; 4 d 2^-24 holds them all, on top of the other roundings.  A weight below
+    2^-126, fp32's smallest normal number, may be lost whole, times factors below 2^10."""
+    low = torch.finfo(torch.float32).min
+    T, E, k = 10, 40, 6
+    rows = torch.randn(T, E, generator=torch.Generator().manual_seed(2))
+    rows[0, :30] = low
+    rows[1] *= 1e4
+    rows[2] -= 88.0
+    rows[3] *= 1e-30
+    rows[4, 7] = 80.0
+    rows[5, 1:] = low
+    rows[6] += 1e4
+    rows[7] -= 600.0
+    rows[8] += 300.0
+    logits = rows.cuda()
+    r = make_router(moe, T, E, k, scoring)
+    f = r.forward(logits)
+    ds = torch.randn(T, k, generator=torch.Generator().manual_seed(3)).cuda()
+    dl = torch.tensor([0.3 * T, 0.0 if scoring == "sigmoid" else 0.01 * T], device="cuda")
+    l = npy(logits).astype(np.float64)
+    exact = ref.router_forward(l, k, scoring, ids=npy(f.ids))["row_stat"]
+    below = np.abs(l - exact[:, None])
+    for a, b in ((ds, dl), (None, dl), (ds, None)):
+        got = r.backward(logits, f.ids, f.counts, f.row_stat, d_scores=a, d_losses=b)
+        want, mag = ref.router_backward(l, npy(f.ids), npy(f.counts),
+                                        npy(f.row_stat).astype(np.float64), k, scoring, 1.0,
+                                        npy(a), npy(b))
+        ref.check(npy(got), want, "d_logits",
+                  mag * (1.0 + below / 16.0) + 2.0 ** -116 / ref.FP32)
