@@ -94,7 +94,9 @@ void moe_plan_destroy(moe_plan* plan);
  * Clamped SwiGLU ("What it is selling": plain or clamped SwiGLU).  limit = 0
  * selects plain silu(gate)*up; limit > 0 clips gate and up to [-limit, limit]
  * before the activation, and the backward passes gradient only where the
- * pre-activation lies inside the closed interval.
+ * pre-activation lies inside the closed interval.  A NaN gate or up value of a
+ * plan with a limit counts as -limit, except in moe_decode_nvfp4, where it stays
+ * NaN.
  */
 int moe_plan_set_swiglu_clamp(moe_plan* plan, float limit);
 

@@ -435,9 +435,9 @@ __device__ __forceinline__ int out_col(int sub, int i) {
 }
 
 __device__ __forceinline__ float swiglu(const DecodeArgs& a, float G, float U) {
-  if (a.clamp > 0.f) {
-    G = fminf(fmaxf(G, -a.clamp), a.clamp);
-    U = fminf(fmaxf(U, -a.clamp), a.clamp);
+  if (a.clamp > 0.f) {                   // by comparisons: fminf and fmaxf drop a NaN
+    G = G > a.clamp ? a.clamp : G < -a.clamp ? -a.clamp : G;
+    U = U > a.clamp ? a.clamp : U < -a.clamp ? -a.clamp : U;
   }
   return __fdividef(G, 1.f + __expf(-G)) * U;
 }

@@ -315,3 +315,22 @@ def test_weights_of_another_plan_are_refused(moe):
         with pytest.raises(moe.MoeError):
             plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], wrong)
     plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
+
+
+@pytest.mark.parametrize("clamp", [0.0, 0.5])
+@pytest.mark.parametrize("T,E,I", [(1, 4, 256), (9, 4, 256), (40, 64, 256)],
+                         ids=["one token", "split", "stream"])
+def test_nan_stays_in_its_row_with_a_clamp(moe, T, E, I, clamp):
+    """Clipping a NaN gives a NaN."""
+    inp = make(T=T, d=256, I=I, E=E, k=2)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, E, I, 256)
+    plan = moe.MoePlan(T, 256, I, E, 2, precision=moe.MOE_PREC_NVFP4, flags=0, clamp=clamp)
+    clean = plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
+    x = dev["x"].clone()
+    at = T // 2
+    x[at, 17] = float("nan")
+    y = plan.decode_nvfp4(x, dev["ids"], dev["scores"], w.prep)
+    assert y[at].isnan().all()
+    keep = [t for t in range(T) if t != at]
+    assert torch.equal(y[keep], clean[keep])
