@@ -618,7 +618,7 @@ __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float
   const bool post = ALL || a.w_post;
   RowFactors f;
   f.rs = ALL || a.du ? rsqrtf(s[0] * inv_d + a.eps) : 0.f;
-  f.cx = f.rs * f.rs * f.rs * (s[1] * inv_d);
+  f.cx = f.rs * (f.rs * (f.rs * (s[1] * inv_d)));      // rs^3 alone leaves fp32's range
   f.ry = post ? rsqrtf(s[2] * inv_d + a.eps) : 1.f;
   const float D = s[3] + f.rs * s[4] - f.cx * s[5];
   f.gt = 1.f;
@@ -629,7 +629,7 @@ __device__ __forceinline__ RowFactors row_factors(const NormArgs& a, const float
       a.dgate[row] = a.accumulate ? a.dgate[row] + v : v;
     }
   }
-  f.cy = post ? f.ry * f.ry * D * inv_d : 0.f;
+  f.cy = post ? f.ry * (f.ry * (D * inv_d)) : 0.f;
   return f;
 }
 

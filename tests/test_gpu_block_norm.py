@@ -327,3 +327,29 @@ def test_refusals(moe):
     with pytest.raises(moe.MoeError):
         c.h.backward(torch.cat([c.res, c.res]), None, None, y=torch.cat([c.y, c.y]),
                      gate=c.gate)                       # more rows than it was made for
+
+
+@pytest.mark.parametrize("d", [512, 777, 5120, 9216])
+def test_gradient_of_very_large_rows(moe, d):
+    """rms(x)^-3 is below fp32's range, the gradient is not."""
+    c = Case(moe, 6, d, "fp32")
+    c.res[2:4] *= 1e15
+    c.d_out[2:4] *= 1e-15                # else it hides what comes through the norm
+    c.y[3:5] *= 1e15
+    c.check_forward()
+    c.check_backward()
+
+
+@pytest.mark.parametrize("d", [512, 777, 5120, 9216])
+def test_gradient_of_rows_of_zeros_with_a_tiny_eps(moe, d):
+    """rms^-3 of a row of zeros is above fp32's range, the gradient is not."""
+    c = Case(moe, 5, d, "fp32")
+    c.res[1] = 0
+    c.y[1:3] = 0
+    h = moe.MoeBlockNorm(5, d, dtype=F, gate=moe.MOE_GATE_CHANNEL, alpha=c.alpha, eps=1e-30)
+    got = h.backward(c.res, c.d_out, c.d_u, **c.params())
+    want, mag = ref.block_norm_backward(np64(c.res), d_out=np64(c.d_out), d_u=np64(c.d_u),
+                                        eps=1e-30, **c.np_params())
+    for name in ("d_residual", "dy", "dw_post", "dw_pre"):
+        check(getattr(got, name), want[name], name, mag[name])
+    check(got.dgate, want["dgate_full"].sum(0), "dgate", mag["dgate_full"].sum(0))
