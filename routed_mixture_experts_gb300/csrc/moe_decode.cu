@@ -893,11 +893,12 @@ __global__ void __launch_bounds__(kThreads) k_decode_combine(const DecodeArgs a)
 // Dynamic shared memory the kernels may take beside their static.
 constexpr int kSplitDynamic = 200 * 1024, kStreamDynamic = 216 * 1024;
 
-// Tokens of a pass: up to 8, fewer where their rows would not fit.
+// Tokens of a pass: up to 8, fewer where their rows would not fit; two CTAs an SM where
+// that leaves room for a row.
 int split_cols(int K, int pairs, int T) {
-  int room = kSplitDynamic - list_bytes(pairs);
-  if (room > 88 * 1024) room = 88 * 1024;              // two CTAs an SM
-  const int fit = room / row_bytes(K), most = T < kCols ? T : kCols;
+  const int room = kSplitDynamic - list_bytes(pairs), half = room < 88 * 1024 ? room : 88 * 1024;
+  const int fit = (half >= row_bytes(K) ? half : room) / row_bytes(K);
+  const int most = T < kCols ? T : kCols;
   return fit < most ? fit : most;
 }
 int stream_cols(int K, int pairs, int T) {

@@ -334,3 +334,16 @@ def test_nan_stays_in_its_row_with_a_clamp(moe, T, E, I, clamp):
     assert y[at].isnan().all()
     keep = [t for t in range(T) if t != at]
     assert torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("T", [1, 2])
+@pytest.mark.parametrize("d,I", [(46080, 256), (256, 46080)])
+def test_rows_that_leave_room_for_one_cta_an_sm(moe, d, I, T):
+    """A row of fp16 that fits in 200 KB, but not twice."""
+    inp = make(T=T, d=d, I=I, E=1, k=1)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, 1, I, d)
+    plan = moe.MoePlan(T, d, I, 1, 1, precision=moe.MOE_PREC_NVFP4, flags=0)
+    y = plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
+    assert plan.check()[0] == moe.MOE_OK
+    check(y, inp["x"], inp["ids"], inp["scores"], w)
