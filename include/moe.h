@@ -113,7 +113,10 @@ size_t moe_plan_workspace_bytes(const moe_plan* plan, int flags);
  * moe_plan_workspace_bytes(plan, flags) bytes.  The plan owns its contents from
  * now on ("MoE layer": the workspace is overwritten by the next call).  Clears
  * the device error word (a synchronous cudaMemset on the legacy stream).
- * Returns MOE_ERR_WORKSPACE if `bytes` is too small.
+ * Returns MOE_ERR_WORKSPACE if `bytes` is too small.  An NVFP4 plan also takes a
+ * workspace without the scratch of moe_decode_nvfp4 at its end, which is, with n =
+ * min(T, MOE_DECODE_MAX_TOKENS) * k, 4*n*I, 4*n*d and n bytes, each rounded up to 256;
+ * decoding then returns MOE_ERR_WORKSPACE.
  */
 int moe_plan_set_workspace(moe_plan* plan, void* workspace, size_t bytes, int flags);
 

@@ -78,8 +78,8 @@ struct moe_plan {
   float nv_x_scale, nv_h_scale;
   CUtensorMap tm_w13nv, tm_w2nv;
   const void *w13nv_cached, *w2nv_cached;
-  // moe_decode_nvfp4: h and ys of up to dec_tokens tokens, and which pairs count
-  int dec_tokens;
+  // moe_decode_nvfp4: h and ys of its tokens, and which pairs count (NULL in a workspace
+  // without them)
   float *dec_h, *dec_ys;
   uint8_t* dec_keep;
   int ngr_d, ngr_I;                 // 128-element scale groups along d and along I
@@ -238,7 +238,8 @@ size_t align_up(size_t v) { return (v + kAlign - 1) / kAlign * kAlign; }
 int pick_bn_n(int n) { return n % 256 == 0 ? 256 : (n % 128 == 0 ? 128 : 64); }
 
 // Lays the workspace out (bases relative to `base`; base may be nullptr to size it).
-size_t layout(moe_plan* p, char* base, int flags) {
+// decode = false leaves out what only moe_decode_nvfp4 uses, the workspace's end.
+size_t layout(moe_plan* p, char* base, int flags, bool decode) {
   size_t off = 0;
   auto take = [&](size_t bytes) -> char* {
     char* r = base ? base + off : nullptr;
@@ -277,11 +278,6 @@ size_t layout(moe_plan* p, char* base, int flags) {
     p->xsf = reinterpret_cast<uint8_t*>(take((size_t)nv_sf_bytes(RP, (int)d)));
     p->hq = reinterpret_cast<uint8_t*>(take(RP * I / 2));
     p->hsf = reinterpret_cast<uint8_t*>(take((size_t)nv_sf_bytes(RP, (int)I)));
-    p->dec_tokens = p->T < kDecodeMaxTokens ? p->T : kDecodeMaxTokens;
-    const size_t pairs = (size_t)p->dec_tokens * k;
-    p->dec_h = reinterpret_cast<float*>(take(4 * pairs * I));
-    p->dec_ys = reinterpret_cast<float*>(take(4 * pairs * d));
-    p->dec_keep = reinterpret_cast<uint8_t*>(take(pairs));
   }
   if (mx) {
     p->xq = reinterpret_cast<uint8_t*>(take(RP * d));
@@ -333,6 +329,14 @@ size_t layout(moe_plan* p, char* base, int flags) {
       p->st_dx = reinterpret_cast<uint16_t*>(take(2 * T * d));
       p->st_dscores = reinterpret_cast<float*>(take(4 * T * k));
     }
+  }
+  p->dec_h = p->dec_ys = nullptr;
+  p->dec_keep = nullptr;
+  if (nv && decode) {
+    const size_t pairs = (T < (size_t)kDecodeMaxTokens ? T : (size_t)kDecodeMaxTokens) * k;
+    p->dec_h = reinterpret_cast<float*>(take(4 * pairs * I));
+    p->dec_ys = reinterpret_cast<float*>(take(4 * pairs * d));
+    p->dec_keep = reinterpret_cast<uint8_t*>(take(pairs));
   }
   return off;
 }
@@ -659,14 +663,16 @@ int moe_plan_set_swiglu_clamp(moe_plan* p, float limit) {
 size_t moe_plan_workspace_bytes(const moe_plan* p, int flags) {
   if (!p) return 0;
   moe_plan tmp = *p;
-  return layout(&tmp, nullptr, flags);
+  return layout(&tmp, nullptr, flags, true);
 }
 
 int moe_plan_set_workspace(moe_plan* p, void* ws, size_t bytes, int flags) {
   if (!p || !ws || (reinterpret_cast<uintptr_t>(ws) & (kAlign - 1))) return MOE_ERR_INVALID_ARG;
   // NVFP4 is inference-only: it refuses a training workspace
   if (p->precision == MOE_PREC_NVFP4 && (flags & MOE_WS_TRAINING)) return MOE_ERR_UNSUPPORTED;
-  if (bytes < moe_plan_workspace_bytes(p, flags)) return MOE_ERR_WORKSPACE;
+  moe_plan tmp = *p;
+  const bool decode = bytes >= layout(&tmp, nullptr, flags, true);
+  if (!decode && bytes < layout(&tmp, nullptr, flags, false)) return MOE_ERR_WORKSPACE;
   if ((flags & MOE_WS_HOST_STAGING) && !p->side) {
     const unsigned ef = cudaEventDisableTiming;
     if (cudaStreamCreateWithFlags(&p->side, cudaStreamNonBlocking) != cudaSuccess ||
@@ -682,7 +688,7 @@ int moe_plan_set_workspace(moe_plan* p, void* ws, size_t bytes, int flags) {
   p->ws = static_cast<char*>(ws);
   p->ws_bytes = bytes;
   p->ws_flags = flags;
-  layout(p, p->ws, flags);
+  layout(p, p->ws, flags, decode);
   p->saved = 0;
   p->prev_step_train = 0;
   p->w13_cached = p->w2_cached = nullptr;
@@ -1444,7 +1450,7 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
   if (!w13q || !w13_sf || !w13_scale || !w2q || !w2_sf || !w2_scale || !aligned16(w13q) ||
       !aligned16(w2q) || !aligned16(w13_sf) || !aligned16(w2_sf))
     return MOE_ERR_INVALID_ARG;
-  if (!p->ws) return MOE_ERR_WORKSPACE;
+  if (!p->ws || !p->dec_h) return MOE_ERR_WORKSPACE;
   if (tokens == 0) return MOE_OK;
   if (!x || !ids || !scores || !y || !aligned16(x) || !aligned16(y) ||
       ((reinterpret_cast<uintptr_t>(ids) | reinterpret_cast<uintptr_t>(scores)) & 3u))

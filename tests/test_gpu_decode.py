@@ -347,3 +347,32 @@ def test_rows_that_leave_room_for_one_cta_an_sm(moe, d, I, T):
     y = plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
     assert plan.check()[0] == moe.MOE_OK
     check(y, inp["x"], inp["ids"], inp["scores"], w)
+
+
+def test_a_workspace_without_the_decode_scratch(moe):
+    """Its size before there was decoding: the plan takes it and runs prompts, and only
+    decoding is refused."""
+    T, d, I, E, k = 40, 256, 512, 8, 2
+    inp = make(T=T, d=d, I=I, E=E, k=k)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, E, I, d)
+    plan = moe.MoePlan(T, d, I, E, k, precision=moe.MOE_PREC_NVFP4, flags=0)
+    plan.set_activation_scales(0.002, 0.002)
+    args = dev["x"], dev["ids"], dev["scores"], w.prep
+    want = plan.forward_nvfp4(*args)
+    L = moe.lib()
+    up = lambda n: (n + 255) // 256 * 256
+    scratch = up(4 * T * k * I) + up(4 * T * k * d) + up(T * k)
+    small = plan.workspace.numel() - scratch
+    p = ctypes.c_void_p(plan.workspace.data_ptr())
+    assert L.moe_plan_set_workspace(plan.ptr, p, small - 1, 0) == moe.MOE_ERR_WORKSPACE
+    assert L.moe_plan_set_workspace(plan.ptr, p, small, 0) == moe.MOE_OK
+    plan.workspace[small:] = 7
+    assert torch.equal(plan.forward_nvfp4(*args), want)
+    assert plan.check()[0] == moe.MOE_OK
+    assert (plan.workspace[small:] == 7).all()
+    with pytest.raises(moe.MoeError) as e:
+        plan.decode_nvfp4(*args)
+    assert e.value.code == moe.MOE_ERR_WORKSPACE
+    assert L.moe_plan_set_workspace(plan.ptr, p, plan.workspace.numel(), 0) == moe.MOE_OK
+    check(plan.decode_nvfp4(*args), inp["x"], inp["ids"], inp["scores"], w)
