@@ -1071,6 +1071,8 @@ __global__ void __launch_bounds__(kSlices * 32) k_block_norm_finish(const NormAr
 enum class Access { kAny, kStaged, kVector };
 
 int round32(int n) { return (n + 31) / 32 * 32; }
+// ceil(T / n) for T > 0 up to INT_MAX.
+int groups_of(int T, int n) { return (T - 1) / n + 1; }
 
 // How the gradient is laid out: pieces of 8 columns a thread, threads of a CTA and of a
 // row, rows at a time of a CTA, CTAs.  Two pieces a thread for aligned rows of 1024 to
@@ -1091,7 +1093,7 @@ GradShape grad_shape(int T, int d, bool vec, bool act_bf16) {
   s.groups = s.threads / s.tpr;
   // One CTA needs no second launch to add the column sums, but costs more than that as
   // soon as it has a second round of rows: 4 rows, d=2048: 10.3 us against 8.9 on two.
-  const int want = T > 0 ? (T + s.groups - 1) / s.groups : 1, sms = num_sms();
+  const int want = T > 0 ? groups_of(T, s.groups) : 1, sms = num_sms();
   s.grid = want < sms ? want : sms;
   return s;
 }
@@ -1103,7 +1105,7 @@ constexpr int kW = sizeof(A) == 2 && sizeof(R) == 2 ? 8 : 4;
 template <typename A, typename R, int V, int W>
 cudaError_t launch_fwd(const NormArgs& a, cudaStream_t st) {
   const int rows = a.tpr >= 256 ? 1 : 256 / a.tpr;
-  return launch_pdl(k_block_norm<A, R, V, W>, dim3((a.T + rows - 1) / rows), dim3(rows * a.tpr),
+  return launch_pdl(k_block_norm<A, R, V, W>, dim3(groups_of(a.T, rows)), dim3(rows * a.tpr),
                     0, st, a);
 }
 
@@ -1111,7 +1113,7 @@ template <typename A, typename R, int V, int W>
 cudaError_t launch_fwd_stream(NormArgs a, cudaStream_t st) {
   static std::atomic<unsigned long long> done{0};
   a.tpr = round32((a.d + 8 * V - 1) / (8 * V));
-  const int groups = kStreamThreads / a.tpr, want = (a.T + groups - 1) / groups;
+  const int groups = kStreamThreads / a.tpr, want = groups_of(a.T, groups);
   // the most that a width can take: rows of 4096 V columns' bytes, and 32 more for each row
   constexpr int most =
       W > 1 ? stream_ring_bytes<A, R, V>()

@@ -491,7 +491,7 @@ int forward_warps(int T, int grid) { return grid > 1 ? 32 : T > 8 ? 32 : 8; }
 
 int forward_grid(int T) {
   if (T <= kOneCtaRows) return 1;
-  const int want = (T + 31) / 32, cap = num_sms();
+  const int want = (T - 1) / 32 + 1, cap = num_sms();      // T + 31 may pass INT_MAX
   return want < cap ? want : cap;
 }
 
@@ -534,7 +534,7 @@ cudaError_t launch_finish(const RouterArgs& a, cudaStream_t st) {
 
 template <typename L>
 cudaError_t launch_backward(const RouterArgs& a, cudaStream_t st) {
-  const int want = (a.T + kGradWarps - 1) / kGradWarps, cap = num_sms() * 6;
+  const int want = (a.T - 1) / kGradWarps + 1, cap = num_sms() * 6;
   const dim3 g(want < cap ? want : cap), b(kGradWarps * 32);
   switch ((a.E + 31) / 32) {
     case 1: return launch_pdl(k_router_grad<L, 1>, g, b, 0, st, a);

@@ -329,3 +329,21 @@ def test_gradient_of_rows_far_from_zero(moe, scoring):
                                         npy(a), npy(b))
         ref.check(npy(got), want, "d_logits",
                   mag * (1.0 + below / 16.0) + 2.0 ** -116 / ref.FP32)
+
+
+def test_as_many_rows_as_an_int_counts(moe):
+    T = 2 ** 31 - 1
+    logits = torch.zeros(T, 1, dtype=torch.bfloat16, device="cuda")
+    r = make_router(moe, T, 1, 1, "softmax_topk", dtype="bf16")
+    f = r.forward(logits)
+    assert f.counts.tolist() == [T, T]
+    for part in (slice(0, 1 << 20), slice(T - (1 << 20), T)):
+        assert (f.scores[part] == 1).all() and (f.ids[part] == 0).all()
+        assert (f.row_stat[part] == 0).all()
+    del f
+    logits[-3:] = 5.0
+    n = moe.MoeBlockNorm(T, 1, eps=0.0)
+    u = n.forward(logits, w_pre=torch.full((1,), 2.0, device="cuda"))[1]
+    assert (u[-3:] == 2).all()
+    del logits, u, r
+    torch.cuda.empty_cache()

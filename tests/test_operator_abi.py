@@ -93,3 +93,20 @@ def test_block_norm_checks(B):
     assert backward(ws=None) == WORKSPACE
     assert backward(nbytes=64) == WORKSPACE
     assert backward(T=0, acc=1) == OK
+
+
+def test_row_counts_near_the_limit_of_an_int(B):
+    """The largest accepted T: a full grid's scratch, as from a few thousand rows on."""
+    L = B.lib()
+    most = 2 ** 31 - 1
+    r = B.RouterDesc(16, 1, 1, 0, 1.0)
+    p = ctypes.addressof(r)
+    full = L.moe_router_workspace_bytes(p, 1 << 20)
+    for T in (most, most - 30, most - 31):
+        assert L.moe_router_workspace_bytes(p, T) == full, T
+    for d in (1, 2048, 16384):
+        s = B.BlockNormDesc(d, 0, 0, 1, 1, 1.0, 1e-6)
+        p = ctypes.addressof(s)
+        full = L.moe_block_norm_workspace_bytes(p, 1 << 20)
+        for T in (most, most - 15):
+            assert L.moe_block_norm_workspace_bytes(p, T) == full, (d, T)
