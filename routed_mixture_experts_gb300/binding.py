@@ -243,22 +243,25 @@ class MoePlan:
                 return self.decode_nvfp4(x, ids, scores, prepared, y)
         n, k = x.shape[0], self.k
         bf16 = torch.bfloat16
-        xp = _want(x, "x", bf16, (n, self.d))
+        dev = _device()
+        _scratch_on(self.workspace, dev)
+        xp = _want(x, "x", bf16, (n, self.d), dev)
         if y is None:
             y = torch.empty((n, self.d), dtype=bf16, device=x.device)
             yp = y.data_ptr()
         else:
-            yp = _want(y, "y", bf16, (n, self.d))
+            yp = _want(y, "y", bf16, (n, self.d), dev)
         if (self.precision == MOE_PREC_NVFP4 and
-                [t.nbytes if t.is_cuda else 0 for t in prepared] != self._prepared_bytes):
+                [t.nbytes if t.get_device() == dev else 0 for t in prepared]
+                != self._prepared_bytes):
             raise MoeError(MOE_ERR_INVALID_ARG, "decode_nvfp4: the weights are not those of "
                            "prepare_weights_nvfp4 for this plan's d, I and E")
         w13q, w13s, w13c, w2q, w2s, w2c = prepared
         _check(_lib.moe_decode_nvfp4(
-            self.ptr, xp, _want(ids, "ids", torch.int32, (n, k)),
-            _want(scores, "scores", torch.float32, (n, k)), n, w13q.data_ptr(), w13s.data_ptr(),
+            self.ptr, xp, _want(ids, "ids", torch.int32, (n, k), dev),
+            _want(scores, "scores", torch.float32, (n, k), dev), n, w13q.data_ptr(), w13s.data_ptr(),
             w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
-            yp, _raw_stream()), "decode_nvfp4")
+            yp, _raw_stream(dev)), "decode_nvfp4")
         return y
 
     def backward(self, dy, w13, w2, dw13, dw2, dx=None, dscores=None, stream=None):
@@ -448,13 +451,20 @@ def gemm_bf16(mode, A, B, C, M, N, K, stream=None):
 # ---- the operators around the experts -----------------------------------------
 
 
-def _raw_stream():
-    """The handle of the current device's current stream.  (The public
+def _device():
+    """The index of the current device, whose stream a call takes."""
+    import torch
+
+    return torch._C._cuda_getDevice()
+
+
+def _raw_stream(dev):
+    """The handle of device dev's current stream.  (The public
     torch.cuda.current_stream() builds a Stream object for it, a third of the host
     time of a small call.)"""
     import torch
 
-    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _dtype_code(dtype, what):
@@ -467,21 +477,23 @@ def _dtype_code(dtype, what):
     raise MoeError(MOE_ERR_INVALID_ARG, "%s: dtype %s (bfloat16 or float32)" % (what, dtype))
 
 
-def _want(t, what, dtype, shape):
-    """t: a contiguous CUDA tensor of this dtype and shape (its address)."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda and t.is_contiguous():
+def _want(t, what, dtype, shape, dev):
+    """t: a contiguous tensor of this dtype and shape on CUDA device dev (its address)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
         return t.data_ptr()
-    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want contiguous %s %s on the GPU, got %s %s" % (
-        what, dtype, tuple(shape), t.dtype, tuple(t.shape)))
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want contiguous %s %s on the current GPU (%d), got "
+                   "%s %s on %s" % (what, dtype, tuple(shape), dev, t.dtype, tuple(t.shape),
+                                    t.device))
 
 
-def _maybe(t, what, dtype, shape):
-    return None if t is None else _want(t, what, dtype, shape)
+def _maybe(t, what, dtype, shape, dev):
+    return None if t is None else _want(t, what, dtype, shape, dev)
 
 
-def _rows(t, what, dtype, shape):
-    """t: a CUDA [T, n] tensor whose rows may lie further apart (address, row distance)."""
-    if t.dtype is dtype and t.shape == shape and t.is_cuda:
+def _rows(t, what, dtype, shape, dev):
+    """t: a [T, n] tensor on CUDA device dev whose rows may lie further apart (address, row
+    distance)."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == dev:
         if t.is_contiguous():
             return t.data_ptr(), shape[1]
         apart, inner = t.stride()
@@ -489,9 +501,15 @@ def _rows(t, what, dtype, shape):
             apart = shape[1]
         if (inner == 1 or shape[1] == 1) and apart >= shape[1]:
             return t.data_ptr(), apart
-    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %s %s on the GPU, rows dense and apart; got %s "
-                   "%s, strides %s" % (what, dtype, tuple(shape), t.dtype, tuple(t.shape),
-                                       t.stride()))
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %s %s on the current GPU (%d), rows dense and "
+                   "apart; got %s %s on %s, strides %s" % (what, dtype, tuple(shape), dev, t.dtype,
+                                                           tuple(t.shape), t.device, t.stride()))
+
+
+def _scratch_on(workspace, dev):
+    if workspace.get_device() != dev:
+        raise MoeError(MOE_ERR_INVALID_ARG, "the handle's scratch is on %s, the current GPU is %d"
+                       % (workspace.device, dev))
 
 
 RouterResult = collections.namedtuple(
@@ -544,20 +562,23 @@ class MoeRouter:
         if T > self.max_tokens:
             raise MoeError(MOE_ERR_INVALID_ARG, "router: %d tokens, made for %d" % (
                 T, self.max_tokens))
-        lp, ld = _rows(logits, "logits", self.dtype, (T, E))
-        bp = _maybe(bias, "bias", f32, (E,))
-        mp = _maybe(token_mask, "token_mask", torch.uint8, (T,))
+        dev = _device()
+        _scratch_on(self.workspace, dev)
+        lp, ld = _rows(logits, "logits", self.dtype, (T, E), dev)
+        bp = _maybe(bias, "bias", f32, (E,), dev)
+        mp = _maybe(token_mask, "token_mask", torch.uint8, (T,), dev)
         if out is None:
             out = self.outputs(T)
             at = [t.data_ptr() for t in out]
         else:
-            at = (_want(out.ids, "ids", i32, (T, k)), _want(out.scores, "scores", f32, (T, k)),
-                  _want(out.counts, "counts", i32, (E + 1,)),
-                  _want(out.prob_sum, "prob_sum", f32, (E,)),
-                  _want(out.losses, "losses", f32, (2,)),
-                  _want(out.row_stat, "row_stat", f32, (T,)))
+            at = (_want(out.ids, "ids", i32, (T, k), dev),
+                  _want(out.scores, "scores", f32, (T, k), dev),
+                  _want(out.counts, "counts", i32, (E + 1,), dev),
+                  _want(out.prob_sum, "prob_sum", f32, (E,), dev),
+                  _want(out.losses, "losses", f32, (2,), dev),
+                  _want(out.row_stat, "row_stat", f32, (T,), dev))
         _check(_lib.moe_router_forward(self._desc, T, lp, ld, bp, mp, *at, *self._ws,
-                                       _raw_stream()), "router forward")
+                                       _raw_stream(dev)), "router forward")
         return out
 
     def backward(self, logits, ids, counts, row_stat, d_scores=None, d_losses=None,
@@ -570,17 +591,19 @@ class MoeRouter:
                 return self.backward(logits, ids, counts, row_stat, d_scores, d_losses, d_logits)
         T, E, k = logits.shape[0], self.E, self.k
         f32 = torch.float32
-        lp, ld = _rows(logits, "logits", self.dtype, (T, E))
+        dev = _device()
+        lp, ld = _rows(logits, "logits", self.dtype, (T, E), dev)
         if d_logits is None:
             d_logits = torch.empty((T, E), dtype=self.dtype, device=logits.device)
             dp, ld_d = d_logits.data_ptr(), E
         else:
-            dp, ld_d = _rows(d_logits, "d_logits", self.dtype, (T, E))
+            dp, ld_d = _rows(d_logits, "d_logits", self.dtype, (T, E), dev)
         _check(_lib.moe_router_backward(
-            self._desc, T, lp, ld, _maybe(ids, "ids", torch.int32, (T, k)),
-            _want(counts, "counts", torch.int32, (E + 1,)),
-            _want(row_stat, "row_stat", f32, (T,)), _maybe(d_scores, "d_scores", f32, (T, k)),
-            _maybe(d_losses, "d_losses", f32, (2,)), dp, ld_d, _raw_stream()),
+            self._desc, T, lp, ld, _maybe(ids, "ids", torch.int32, (T, k), dev),
+            _want(counts, "counts", torch.int32, (E + 1,), dev),
+            _want(row_stat, "row_stat", f32, (T,), dev),
+            _maybe(d_scores, "d_scores", f32, (T, k), dev),
+            _maybe(d_losses, "d_losses", f32, (2,), dev), dp, ld_d, _raw_stream(dev)),
             "router backward")
         return d_logits
 
@@ -613,12 +636,12 @@ class MoeBlockNorm:
             raise MoeError(MOE_ERR_INVALID_ARG, "MoeBlockNorm(%d,%d)" % (max_tokens, d))
         self.device, self.workspace = device, None     # scratch: from the first backward on
 
-    def _params(self, T, w_post, gate, w_pre):
+    def _params(self, T, w_post, gate, w_pre, dev):
         """Addresses of w_post, gate and w_pre, and the gate's shape."""
         pt, d = self.param_dtype, (self.d,)
         shape = (T,) if self.gate == MOE_GATE_TOKEN else d
-        return (_maybe(w_post, "w_post", pt, d), _maybe(gate, "gate", pt, shape),
-                _maybe(w_pre, "w_pre", pt, d), shape)
+        return (_maybe(w_post, "w_post", pt, d, dev), _maybe(gate, "gate", pt, shape, dev),
+                _maybe(w_pre, "w_pre", pt, d, dev), shape)
 
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, residual_out=None,
                 u=None, stream=None):
@@ -629,27 +652,27 @@ class MoeBlockNorm:
             with torch.cuda.stream(stream):
                 return self.forward(residual, y, w_post, gate, w_pre, residual_out, u)
         T = residual.shape[0]
-        shape = (T, self.d)
-        rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape)
-        wp, gp, wq, _ = self._params(T, w_post, gate, w_pre)
+        shape, dev = (T, self.d), _device()
+        rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape, dev)
+        wp, gp, wq, _ = self._params(T, w_post, gate, w_pre, dev)
         yp = op = up = None
         ld_y = ld_o = ld_u = 0
         if y is not None:
-            yp, ld_y = _rows(y, "y", self.dtype, shape)
+            yp, ld_y = _rows(y, "y", self.dtype, shape, dev)
             if residual_out is None:
                 residual_out = torch.empty(shape, dtype=self.residual_dtype,
                                            device=residual.device)
                 op, ld_o = residual_out.data_ptr(), self.d
             else:
-                op, ld_o = _rows(residual_out, "residual_out", self.residual_dtype, shape)
+                op, ld_o = _rows(residual_out, "residual_out", self.residual_dtype, shape, dev)
         if w_pre is not None:
             if u is None:
                 u = torch.empty(shape, dtype=self.dtype, device=residual.device)
                 up, ld_u = u.data_ptr(), self.d
             else:
-                up, ld_u = _rows(u, "u", self.dtype, shape)
+                up, ld_u = _rows(u, "u", self.dtype, shape, dev)
         _check(_lib.moe_block_norm_forward(self._desc, T, rp, ld_r, yp, ld_y, wp, gp, wq, op, ld_o,
-                                            up, ld_u, _raw_stream()), "block norm forward")
+                                            up, ld_u, _raw_stream(dev)), "block norm forward")
         return (residual if y is None else residual_out), (None if w_pre is None else u)
 
     def backward(self, residual_out, d_residual_out=None, d_u=None, y=None, w_post=None, gate=None,
@@ -663,54 +686,55 @@ class MoeBlockNorm:
             with torch.cuda.stream(stream):
                 return self.backward(residual_out, d_residual_out, d_u, y, w_post, gate, w_pre,
                                      d_residual, dy, dw_post, dgate, dw_pre, accumulate)
-        T, dev, f32 = residual_out.shape[0], residual_out.device, torch.float32
+        T, at, f32 = residual_out.shape[0], residual_out.device, torch.float32
         if T > self.max_tokens:
             raise MoeError(MOE_ERR_INVALID_ARG, "block norm: %d rows, made for %d" % (
                 T, self.max_tokens))
-        d = self.d
+        d, dev = self.d, _device()
         shape = (T, d)
         act, res = self.dtype, self.residual_dtype
-        rp, ld_r = _rows(residual_out, "residual_out", res, shape)
-        wp, gp, wq, gshape = self._params(T, w_post, gate, w_pre)
+        rp, ld_r = _rows(residual_out, "residual_out", res, shape, dev)
+        wp, gp, wq, gshape = self._params(T, w_post, gate, w_pre, dev)
         yp = gr = gu = op = dp = wpp = ggp = wqp = None
         ld_y = ld_gr = ld_gu = ld_d = 0
         if y is not None:
-            yp, ld_y = _rows(y, "y", act, shape)
+            yp, ld_y = _rows(y, "y", act, shape, dev)
         if d_residual_out is not None:
-            gr, ld_gr = _rows(d_residual_out, "d_residual_out", res, shape)
+            gr, ld_gr = _rows(d_residual_out, "d_residual_out", res, shape, dev)
         if d_u is not None:
-            gu, ld_gu = _rows(d_u, "d_u", act, shape)
+            gu, ld_gu = _rows(d_u, "d_u", act, shape, dev)
         # outputs: the caller's are checked, fresh ones are what they have to be
         new = torch.zeros if accumulate else torch.empty
         if d_residual is not None:
-            op, ld_o = _rows(d_residual, "d_residual", res, shape)
+            op, ld_o = _rows(d_residual, "d_residual", res, shape, dev)
         else:
-            d_residual = torch.empty(shape, dtype=res, device=dev)
+            d_residual = torch.empty(shape, dtype=res, device=at)
             op, ld_o = d_residual.data_ptr(), d
         if dy is not None:
-            dp, ld_d = _rows(dy, "dy", act, shape)
+            dp, ld_d = _rows(dy, "dy", act, shape, dev)
         elif y is not None:
-            dy = torch.empty(shape, dtype=act, device=dev)
+            dy = torch.empty(shape, dtype=act, device=at)
             dp, ld_d = dy.data_ptr(), d
         if dw_post is not None:
-            wpp = _want(dw_post, "dw_post", f32, (d,))
+            wpp = _want(dw_post, "dw_post", f32, (d,), dev)
         elif w_post is not None:
-            dw_post = new((d,), dtype=f32, device=dev)
+            dw_post = new((d,), dtype=f32, device=at)
             wpp = dw_post.data_ptr()
         if dgate is not None:
-            ggp = _want(dgate, "dgate", f32, gshape)
+            ggp = _want(dgate, "dgate", f32, gshape, dev)
         elif gate is not None:
-            dgate = new(gshape, dtype=f32, device=dev)
+            dgate = new(gshape, dtype=f32, device=at)
             ggp = dgate.data_ptr()
         if dw_pre is not None:
-            wqp = _want(dw_pre, "dw_pre", f32, (d,))
+            wqp = _want(dw_pre, "dw_pre", f32, (d,), dev)
         elif w_pre is not None:
-            dw_pre = new((d,), dtype=f32, device=dev)
+            dw_pre = new((d,), dtype=f32, device=at)
             wqp = dw_pre.data_ptr()
         if self.workspace is None:
             self.workspace = torch.empty(self._ws_bytes, dtype=torch.uint8, device=self.device)
+        _scratch_on(self.workspace, dev)
         _check(_lib.moe_block_norm_backward(
             self._desc, T, rp, ld_r, yp, ld_y, gr, ld_gr, gu, ld_gu, wp, gp, wq, op, ld_o, dp, ld_d,
             wpp, ggp, wqp, 1 if accumulate else 0, self.workspace.data_ptr(), self._ws_bytes,
-            _raw_stream()), "block norm backward")
+            _raw_stream(dev)), "block norm backward")
         return BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre)

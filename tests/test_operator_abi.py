@@ -110,3 +110,134 @@ def test_row_counts_near_the_limit_of_an_int(B):
         full = L.moe_block_norm_workspace_bytes(p, 1 << 20)
         for T in (most, most - 15):
             assert L.moe_block_norm_workspace_bytes(p, T) == full, (d, T)
+
+
+class OnGpu:
+    """What the binding looks at of a tensor on GPU `dev` (no GPU needed)."""
+
+    is_cuda = True
+
+    def __init__(self, dtype, shape, dev=0):
+        self.dtype, self.shape, self.dev = dtype, shape, dev
+        self.device = "cuda:%d" % dev
+
+    def get_device(self):
+        return self.dev
+
+    def is_contiguous(self):
+        return True
+
+    def stride(self):
+        return (self.shape[-1], 1)
+
+    def data_ptr(self):
+        return 1 << 20
+
+    @property
+    def nbytes(self):
+        n = self.dtype.itemsize
+        for s in self.shape:
+            n *= s
+        return n
+
+
+@pytest.fixture
+def on_gpu_0(B, monkeypatch):
+    """The binding with GPU 0 current and a library that only counts its calls."""
+    import torch
+
+    class Library:
+        calls = 0
+
+        def moe_status_string(self, code):
+            return b"status"
+
+        def __getattr__(self, name):
+            def call(*args):
+                self.calls += 1
+                return OK
+
+            return call
+
+    library = Library()
+    monkeypatch.setattr(B, "_lib", library)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: 0, raising=False)
+    return library
+
+
+def only_one_elsewhere(B, library, call, tensors):
+    """`call` is made with all tensors on GPU 0, and refused with any of them on GPU 1."""
+    made = {n: OnGpu(*t) for n, t in tensors.items()}
+    call(made)
+    before = library.calls
+    assert before > 0
+    for n, t in tensors.items():
+        with pytest.raises(B.MoeError) as e:
+            call({**made, n: OnGpu(*t, dev=1)})
+        assert e.value.code == INVALID, n
+    assert library.calls == before
+
+
+def test_tensors_on_another_gpu_are_refused_by_the_router(B, on_gpu_0):
+    import torch
+
+    T, E, k = 40, 16, 2
+    r = object.__new__(B.MoeRouter)
+    r.max_tokens, r.E, r.k, r.dtype, r._desc, r._ws = T, E, k, torch.float32, 0, (0, 0)
+    f32, i32 = torch.float32, torch.int32
+    out = dict(ids=(i32, (T, k)), scores=(f32, (T, k)), counts=(i32, (E + 1,)),
+               prob_sum=(f32, (E,)), losses=(f32, (2,)), row_stat=(f32, (T,)))
+
+    def forward(t):
+        r.workspace = t["workspace"]
+        r.forward(t["logits"], t["bias"], t["mask"], out=B.RouterResult(*(t[n] for n in out)))
+
+    only_one_elsewhere(B, on_gpu_0, forward, dict(
+        out, workspace=(torch.uint8, (64,)), logits=(f32, (T, E)), bias=(f32, (E,)),
+        mask=(torch.uint8, (T,))))
+    only_one_elsewhere(B, on_gpu_0, lambda t: r.backward(
+        t["logits"], t["ids"], t["counts"], t["row_stat"], t["d_scores"], t["d_losses"],
+        t["d_logits"]), dict(
+            logits=(f32, (T, E)), ids=out["ids"], counts=out["counts"], row_stat=out["row_stat"],
+            d_scores=(f32, (T, k)), d_losses=(f32, (2,)), d_logits=(f32, (T, E))))
+
+
+def test_tensors_on_another_gpu_are_refused_by_the_block_norm(B, on_gpu_0):
+    import torch
+
+    T, d, f32 = 10, 64, torch.float32
+    h = object.__new__(B.MoeBlockNorm)
+    h.max_tokens, h.d, h.gate, h._desc, h._ws_bytes = T, d, B.MOE_GATE_CHANNEL, 0, 0
+    h.dtype = h.residual_dtype = h.param_dtype = f32
+    rows, column = (f32, (T, d)), (f32, (d,))
+    params = dict(w_post=column, gate=column, w_pre=column)
+    only_one_elsewhere(B, on_gpu_0, lambda t: h.forward(
+        t["residual"], **{n: v for n, v in t.items() if n != "residual"}), dict(
+            params, residual=rows, y=rows, residual_out=rows, u=rows))
+
+    def backward(t):
+        h.workspace = t["workspace"]
+        h.backward(t["x"], **{n: v for n, v in t.items() if n not in ("x", "workspace")})
+
+    only_one_elsewhere(B, on_gpu_0, backward, dict(
+        params, workspace=(torch.uint8, (64,)), x=rows, d_residual_out=rows, d_u=rows, y=rows,
+        d_residual=rows, dy=rows, dw_post=column, dgate=column, dw_pre=column))
+
+
+def test_tensors_on_another_gpu_are_refused_by_the_decode(B, on_gpu_0):
+    import torch
+
+    n, d, E, k = 3, 256, 4, 2
+    p = object.__new__(B.MoePlan)
+    p.ptr, p.d, p.k, p.precision, p._prepared_bytes = None, d, k, B.MOE_PREC_NVFP4, [64] * 6
+    bf16 = torch.bfloat16
+    weights = {"w%d" % i: (torch.uint8, (64,)) for i in range(6)}
+
+    def call(t):
+        p.workspace = t["workspace"]
+        p.decode_nvfp4(t["x"], t["ids"], t["scores"], [t[n] for n in weights], t["y"])
+
+    only_one_elsewhere(B, on_gpu_0, call, dict(
+        weights, workspace=(torch.uint8, (64,)), x=(bf16, (n, d)), y=(bf16, (n, d)),
+        ids=(torch.int32, (n, k)), scores=(torch.float32, (n, k))))
