@@ -252,16 +252,16 @@ class MoePlan:
         else:
             yp = _want(y, "y", bf16, (n, self.d), dev)
         if (self.precision == MOE_PREC_NVFP4 and
-                [t.nbytes if t.get_device() == dev else 0 for t in prepared]
+                [t.nbytes if t.get_device() == dev and t.is_contiguous() else 0 for t in prepared]
                 != self._prepared_bytes):
             raise MoeError(MOE_ERR_INVALID_ARG, "decode_nvfp4: the weights are not those of "
                            "prepare_weights_nvfp4 for this plan's d, I and E")
         w13q, w13s, w13c, w2q, w2s, w2c = prepared
         _check(_lib.moe_decode_nvfp4(
             self.ptr, xp, _want(ids, "ids", torch.int32, (n, k), dev),
-            _want(scores, "scores", torch.float32, (n, k), dev), n, w13q.data_ptr(), w13s.data_ptr(),
-            w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(), w2c.data_ptr(),
-            yp, _raw_stream(dev)), "decode_nvfp4")
+            _want(scores, "scores", torch.float32, (n, k), dev), n,
+            w13q.data_ptr(), w13s.data_ptr(), w13c.data_ptr(), w2q.data_ptr(), w2s.data_ptr(),
+            w2c.data_ptr(), yp, _raw_stream(dev)), "decode_nvfp4")
         return y
 
     def backward(self, dy, w13, w2, dw13, dw2, dx=None, dscores=None, stream=None):

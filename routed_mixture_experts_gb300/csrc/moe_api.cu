@@ -1448,7 +1448,8 @@ int moe_decode_nvfp4(moe_plan* p, const void* x, const int32_t* ids, const float
   if (p->precision != MOE_PREC_NVFP4) return MOE_ERR_UNSUPPORTED;
   if (tokens > (p->T < kDecodeMaxTokens ? p->T : kDecodeMaxTokens)) return MOE_ERR_INVALID_ARG;
   if (!w13q || !w13_sf || !w13_scale || !w2q || !w2_sf || !w2_scale || !aligned16(w13q) ||
-      !aligned16(w2q) || !aligned16(w13_sf) || !aligned16(w2_sf))
+      !aligned16(w2q) || !aligned16(w13_sf) || !aligned16(w2_sf) ||
+      ((reinterpret_cast<uintptr_t>(w13_scale) | reinterpret_cast<uintptr_t>(w2_scale)) & 3u))
     return MOE_ERR_INVALID_ARG;
   if (!p->ws || !p->dec_h) return MOE_ERR_WORKSPACE;
   if (tokens == 0) return MOE_OK;

@@ -241,3 +241,44 @@ def test_tensors_on_another_gpu_are_refused_by_the_decode(B, on_gpu_0):
     only_one_elsewhere(B, on_gpu_0, call, dict(
         weights, workspace=(torch.uint8, (64,)), x=(bf16, (n, d)), y=(bf16, (n, d)),
         ids=(torch.int32, (n, k)), scores=(torch.float32, (n, k))))
+
+
+def test_decode_checks_without_a_workspace(B):
+    """Argument checks come first: a plan without a workspace refuses a good call for that."""
+    L = B.lib()
+    plan = L.moe_plan_create(8, 256, 256, 4, 2, 2)
+    assert plan
+    names = ("x", "ids", "scores", "w13", "w13_sf", "w13_scale", "w2", "w2_sf", "w2_scale", "y")
+
+    def call(n=8, **change):
+        a = [change.get(name, A) for name in names]
+        return L.moe_decode_nvfp4(plan, *a[:3], n, *a[3:], None)
+
+    assert call() == WORKSPACE
+    for name in ("w13", "w13_sf", "w13_scale", "w2", "w2_sf", "w2_scale"):
+        assert call(**{name: ODD}) == INVALID, name
+        assert call(**{name: None}) == INVALID, name
+    assert call(n=9) == INVALID and call(n=-1) == INVALID
+    L.moe_plan_destroy(plan)
+
+
+def test_decode_refuses_weights_that_are_not_whole(B, on_gpu_0):
+    """An expanded tensor counts bytes that it does not have."""
+    import torch
+
+    n, d, E, k = 3, 256, 4, 2
+    p = object.__new__(B.MoePlan)
+    p.ptr, p.d, p.k, p.precision, p._prepared_bytes = None, d, k, B.MOE_PREC_NVFP4, [64] * 6
+    p.workspace = OnGpu(torch.uint8, (64,))
+    x = OnGpu(torch.bfloat16, (n, d))
+    args = x, OnGpu(torch.int32, (n, k)), OnGpu(torch.float32, (n, k))
+    good = [OnGpu(torch.uint8, (64,)) for _ in range(6)]
+    p.decode_nvfp4(*args, good, x)
+    assert on_gpu_0.calls == 1
+    for i in range(6):
+        bad = list(good)
+        bad[i] = OnGpu(torch.uint8, (64,))
+        bad[i].is_contiguous = lambda: False
+        with pytest.raises(B.MoeError):
+            p.decode_nvfp4(*args, bad, x)
+    assert on_gpu_0.calls == 1
