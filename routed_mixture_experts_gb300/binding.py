@@ -645,7 +645,8 @@ class MoeBlockNorm:
 
     def forward(self, residual, y=None, w_post=None, gate=None, w_pre=None, residual_out=None,
                 u=None, stream=None):
-        """-> (residual_out, u); without y the first is residual, without w_pre u is None."""
+        """-> (residual_out, u); without y the first is residual, without w_pre u is None
+        (and a tensor given for it is refused)."""
         import torch
 
         if stream is not None:               # the outputs then belong to that stream too
@@ -655,6 +656,8 @@ class MoeBlockNorm:
         shape, dev = (T, self.d), _device()
         rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape, dev)
         wp, gp, wq, _ = self._params(T, w_post, gate, w_pre, dev)
+        if (y is None and residual_out is not None) or (w_pre is None and u is not None):
+            raise MoeError(MOE_ERR_INVALID_ARG, "block norm: residual_out goes with y, u with w_pre")
         yp = op = up = None
         ld_y = ld_o = ld_u = 0
         if y is not None:

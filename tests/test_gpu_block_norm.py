@@ -353,3 +353,14 @@ def test_gradient_of_rows_of_zeros_with_a_tiny_eps(moe, d):
     for name in ("d_residual", "dy", "dw_post", "dw_pre"):
         check(getattr(got, name), want[name], name, mag[name])
     check(got.dgate, want["dgate_full"].sum(0), "dgate", mag["dgate_full"].sum(0))
+
+
+def test_outputs_without_their_inputs_are_refused(moe):
+    """A tensor that the call would leave unwritten."""
+    c = Case(moe, 8, 64)
+    buf = torch.empty_like(c.res)
+    for call in (lambda: c.h.forward(c.res, w_pre=c.w_pre, residual_out=buf),
+                 lambda: c.h.forward(c.res, y=c.y, gate=c.gate, w_post=c.w_post, u=buf)):
+        with pytest.raises(moe.MoeError) as e:
+            call()
+        assert e.value.code == moe.MOE_ERR_INVALID_ARG
