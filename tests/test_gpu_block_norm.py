@@ -364,3 +364,24 @@ def test_outputs_without_their_inputs_are_refused(moe):
         with pytest.raises(moe.MoeError) as e:
             call()
         assert e.value.code == moe.MOE_ERR_INVALID_ARG
+
+
+@pytest.mark.parametrize("types", list(TYPES))
+@pytest.mark.parametrize("T,d,extra", [(700, 2048, 0), (700, 1537, 0), (640, 4095, 0),
+                                       (620, 5001, 1), (300, 8192, 0), (200, 9216, 0),
+                                       (200, 9001, 0), (200, 16384, 0), (700, 250, 3)])
+def test_in_place_at_every_layout(moe, T, d, extra, types):
+    """Aligned and unaligned rows of every kernel, each read before it is overwritten."""
+    c = Case(moe, T, d, types, gate="token" if d % 2 else "channel", extra=extra)
+    p = c.params()
+    out, u = c.h.forward(c.res, **p)
+    g = c.h.backward(c.res, c.d_out, c.d_u, **p)
+    copy = lambda t: strided(t.clone(), extra)
+    for _ in range(3):
+        res, y = copy(c.res), copy(c.y)
+        c.h.forward(res, **{**p, "y": y}, residual_out=res, u=y)
+        assert torch.equal(res, out) and torch.equal(y, u)
+        d_out, d_u = copy(c.d_out), copy(c.d_u)
+        b = c.h.backward(c.res, d_out, d_u, **p, d_residual=d_out, dy=d_u)
+        for got, want in zip(b, g):
+            assert torch.equal(got, want)
