@@ -376,3 +376,39 @@ def test_a_workspace_without_the_decode_scratch(moe):
     assert e.value.code == moe.MOE_ERR_WORKSPACE
     assert L.moe_plan_set_workspace(plan.ptr, p, plan.workspace.numel(), 0) == moe.MOE_OK
     check(plan.decode_nvfp4(*args), inp["x"], inp["ids"], inp["scores"], w)
+
+
+# Rows wider than 2048: eight tokens' rows no longer fit beside the stream's ring (4096:
+# four do, in several passes of one expert) or in half an SM's shared memory (7168: six
+# do); and one token that leaves the two-launch path: more than eight experts, or eight
+# rows of h that do not fit together.
+WIDE = [dict(T=20, d=4096, I=1280, E=8, k=2), dict(T=19, d=256, I=4096, E=3, k=2),
+        dict(T=11, d=7168, I=256, E=2, k=1), dict(T=13, d=256, I=7168, E=2, k=1),
+        dict(T=9, d=2560, I=2560, E=2, k=2), dict(T=1, d=256, I=256, E=12, k=9),
+        dict(T=1, d=512, I=256, E=40, k=33), dict(T=1, d=256, I=12800, E=8, k=8),
+        dict(T=1, d=7168, I=2048, E=3, k=2)]
+
+
+@pytest.mark.parametrize("sizes", WIDE, ids=lambda s: ",".join("%s%s" % kv for kv in s.items()))
+def test_wide_rows_and_many_experts_of_one_token(moe, sizes):
+    inp = make(**sizes)
+    c, dev = inp["cfg"], to_dev(inp)
+    w = Weights(moe, dev, c["E"], c["I"], c["d"])
+    plan = moe.MoePlan(c["T"], c["d"], c["I"], c["E"], c["k"], precision=moe.MOE_PREC_NVFP4,
+                       flags=0)
+    y = plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep)
+    assert plan.check()[0] == moe.MOE_OK
+    check(y, inp["x"], inp["ids"], inp["scores"], w)
+    assert torch.equal(y, plan.decode_nvfp4(dev["x"], dev["ids"], dev["scores"], w.prep))
+
+
+def test_a_token_alone_and_among_others(moe):
+    """Different kernels add K in different orders: both are within the bound."""
+    T, d, I, E, k = 50, 2048, 768, 16, 4
+    inp = make(T=T, d=d, I=I, E=E, k=k)
+    dev = to_dev(inp)
+    w = Weights(moe, dev, E, I, d)
+    plan = moe.MoePlan(T, d, I, E, k, precision=moe.MOE_PREC_NVFP4, flags=0)
+    for n in (1, 3, T):
+        y = plan.decode_nvfp4(dev["x"][:n], dev["ids"][:n], dev["scores"][:n], w.prep)
+        check(y, inp["x"][:n], inp["ids"][:n], inp["scores"][:n], w)
