@@ -242,6 +242,7 @@ class MoePlan:
             with torch.cuda.stream(stream):
                 return self.decode_nvfp4(x, ids, scores, prepared, y)
         n, k = x.shape[0], self.k
+        _rows_fit(n, "decode_nvfp4")
         bf16 = torch.bfloat16
         dev = _device()
         _scratch_on(self.workspace, dev)
@@ -477,6 +478,12 @@ def _dtype_code(dtype, what):
     raise MoeError(MOE_ERR_INVALID_ARG, "%s: dtype %s (bfloat16 or float32)" % (what, dtype))
 
 
+def _rows_fit(T, what):
+    """ctypes would cut a row count to 32 bits without a word."""
+    if T > 0x7FFFFFFF:
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: %d rows (2^31 - 1 at most)" % (what, T))
+
+
 def _want(t, what, dtype, shape, dev):
     """t: a contiguous tensor of this dtype and shape on CUDA device dev (its address)."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
@@ -527,6 +534,7 @@ class MoeRouter:
         import torch
 
         L = lib()
+        _rows_fit(max_tokens, "MoeRouter")
         self.max_tokens, self.E, self.k = max_tokens, E, k
         self.dtype = dtype if dtype is not None else torch.float32
         self.desc = RouterDesc(E, k, _dtype_code(self.dtype, "MoeRouter"), scoring, scale)
@@ -590,6 +598,7 @@ class MoeRouter:
             with torch.cuda.stream(stream):
                 return self.backward(logits, ids, counts, row_stat, d_scores, d_losses, d_logits)
         T, E, k = logits.shape[0], self.E, self.k
+        _rows_fit(T, "router backward")
         f32 = torch.float32
         dev = _device()
         lp, ld = _rows(logits, "logits", self.dtype, (T, E), dev)
@@ -623,6 +632,7 @@ class MoeBlockNorm:
                  gate=MOE_GATE_NONE, alpha=1.0, eps=1e-6, device="cuda"):
         import torch
 
+        _rows_fit(max_tokens, "MoeBlockNorm")
         self.max_tokens, self.d, self.gate = max_tokens, d, gate
         self.dtype = dtype if dtype is not None else torch.bfloat16
         self.residual_dtype = residual_dtype if residual_dtype is not None else self.dtype
@@ -653,6 +663,7 @@ class MoeBlockNorm:
             with torch.cuda.stream(stream):
                 return self.forward(residual, y, w_post, gate, w_pre, residual_out, u)
         T = residual.shape[0]
+        _rows_fit(T, "block norm forward")
         shape, dev = (T, self.d), _device()
         rp, ld_r = _rows(residual, "residual", self.residual_dtype, shape, dev)
         wp, gp, wq, _ = self._params(T, w_post, gate, w_pre, dev)

@@ -282,3 +282,36 @@ def test_decode_refuses_weights_that_are_not_whole(B, on_gpu_0):
         with pytest.raises(B.MoeError):
             p.decode_nvfp4(*args, bad, x)
     assert on_gpu_0.calls == 1
+
+
+def test_more_rows_than_an_int_counts_are_refused(B, on_gpu_0):
+    """2^32 + 5 rows are not five rows."""
+    import torch
+
+    many, f32, bf16 = 2 ** 32 + 5, torch.float32, torch.bfloat16
+    r = object.__new__(B.MoeRouter)
+    r.max_tokens, r.E, r.k, r.dtype, r._desc = 8, 1, 1, f32, 0
+    n = object.__new__(B.MoeBlockNorm)
+    n.max_tokens, n.d, n.gate, n._desc = 8, 1, B.MOE_GATE_NONE, 0
+    n.dtype = n.residual_dtype = n.param_dtype = f32
+    p = object.__new__(B.MoePlan)
+    p.ptr, p.d, p.k, p.precision, p._prepared_bytes = None, 256, 1, B.MOE_PREC_NVFP4, [64] * 6
+    p.workspace = OnGpu(torch.uint8, (64,))
+    rows, one = OnGpu(f32, (many, 1)), OnGpu(f32, (1,))
+    x = OnGpu(bf16, (many, 256))
+    for call in (lambda: r.backward(rows, OnGpu(torch.int32, (many, 1)), OnGpu(torch.int32, (2,)),
+                                    OnGpu(f32, (many,)), d_logits=rows),
+                 lambda: n.forward(rows, w_pre=one, u=rows),
+                 lambda: p.decode_nvfp4(x, OnGpu(torch.int32, (many, 1)), rows,
+                                        [OnGpu(torch.uint8, (64,))] * 6, x)):
+        with pytest.raises(B.MoeError) as e:
+            call()
+        assert e.value.code == INVALID
+    assert on_gpu_0.calls == 0
+
+
+def test_handles_for_more_rows_than_an_int_counts_are_refused(B):
+    for make in (lambda: B.MoeRouter(2 ** 32 + 5, 1, 1), lambda: B.MoeBlockNorm(2 ** 32 + 5, 1)):
+        with pytest.raises(B.MoeError) as e:
+            make()
+        assert e.value.code == INVALID
