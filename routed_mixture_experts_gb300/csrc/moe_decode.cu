@@ -459,8 +459,8 @@ __device__ __forceinline__ void check_ids(const DecodeArgs& a) {
 //
 // No list is needed: a pair is an expert of its own.  W13: a unit of one pair a CTA,
 // K split over its eight warps as in k_decode_split.  W2: 32 rows a CTA, a warp a pair
-// (k <= 8), its whole row of weights on its way before h is there, and the pairs
-// added in the CTA: no third launch.
+// (k <= 8), the first two of its I / 128 steps of weights on their way before h is there,
+// and the pairs added in the CTA: no third launch.
 
 // The expert of pair j of the one token; -1 for a bad id or a repeated one.
 __device__ __forceinline__ int expert_of(const DecodeArgs& a, int j) {
@@ -576,7 +576,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_decode_one_w2(const DecodeArgs 
 //
 // A CTA of eight warps takes one unit at a time, a warp every eighth step, the sums
 // joined in shared memory: a unit is over after d / 1024 steps, and two tokens' experts
-// fill the GPU.  Latency bounds it: 7 tokens on 16 experts of d=2048, I=768: 23.4 us.
+// fill the GPU.  Latency bounds it: 8 tokens with all of 8 experts of d=2048, I=768 17.5 us
+// with all launches, 1.2 TB/s.
 template <bool W13>
 __global__ void __launch_bounds__(kThreads, 2) k_decode_split(const DecodeArgs a) {
   extern __shared__ __align__(16) uint8_t smem[];       // the pairs' list, the tokens' rows
@@ -908,7 +909,8 @@ int stream_cols(int K, int pairs, int T) {
 }
 
 // Units of one launch as far as the host can tell (every pair on an expert of its own
-// while there are experts, full passes after that), and whether it streams: from four
+// while there are experts, passes of eight tokens after that; wide rows take fewer at a
+// time, and then there are more units than these), and whether it streams: from four
 // units an SM on, where passes of four tokens fit.  Measured with K split against a
 // unit a warp (us; d=2048, I=768): 1.3 to 1.7 units an SM 11.6 against 14.8, 2.5 to 3.4
 // 15.5 against 15.8, 3.8 to 5 19.2 against 18.3, 5 (7 tokens on 16 experts) 23.4 against

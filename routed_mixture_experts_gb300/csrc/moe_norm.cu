@@ -368,8 +368,10 @@ __device__ __forceinline__ void param_write(uint8_t* slot, const float (&f)[8]) 
 // Against loads of single elements into registers, one row ahead (us): forward, T=8192,
 // d=777, bf16 33.2 -> 25.2; T=8191, d=1023, fp32 36.2 -> 32.3; T=2047, d=8191, bf16
 // 85.9 -> 56.2; with the columns of a lane at constant distances 19.9, 26.5 and 43.6.
-// Bound by the instructions of single elements (T=8192, d=2047, bf16 39.8); writing whole
-// pieces through shared memory too costs more for its barrier than it saves.  The
+// Bound by the instructions of single elements (T=8192, d=2047, bf16 39.9); writing whole
+// pieces through shared memory too costs more for its barrier than it saves.  (Where the
+// rows of a group lie a multiple of 16 bytes apart they all begin at the same offset, and
+// columns shifted by it would keep 16-byte accesses: not built.)  The
 // gradient of up to 4096 columns keeps its loads (an fp32 residual, T=4099, d=1537: 34.7
 // against 39.3 us with copied rows; bf16, T=8192, d=2047: 62.5 against 59.5).
 constexpr int kStagedMinWidth = 8;
@@ -687,9 +689,10 @@ __device__ __forceinline__ void leave_column_sums(const NormArgs& a, const float
 // the addresses).
 // ALL: every tensor is given.
 // Its row loop runs at nine tenths of a copy's rate; the rest of the time are the start,
-// the CTAs' column sums and the launch that adds them.  Measured with that launch: bf16
-// T=8192, d=2048 37.6 us, T=2048, d=8192 63, T=2047, d=8191 72, fp32 T=8192, d=1024
-// 37; fp32 residual, T=4099, d=1537 (one piece of single elements) 34.5.
+// the CTAs' column sums and the launch that adds them.  Measured with that launch and a
+// channel gate: bf16 T=8192, d=2048 37.7 us, T=4096, d=4096 43, T=2048, d=8192 53 (one row
+// at a time: the wait for its sums is not covered), T=2047, d=8191 70, fp32 T=8192, d=1024
+// 35; token gate, fp32 residual, T=4099, d=1537 (one piece of single elements) 34.6.
 constexpr int kGradThreads = 384;      // with V = 2 and several rows to a CTA
 constexpr int kGradStages = 2;
 
@@ -954,8 +957,9 @@ __global__ void __launch_bounds__(TH, 1) k_block_norm_grad_stream(const NormArgs
 // Gradient of wider rows (d > 8192; d > 4096 with an fp32 tensor or tensors that are not
 // 16-byte aligned): a group is the CTA, V pieces of 8 columns a thread, the parameters in
 // shared memory.  A row's registers leave no room for the next row, so that its loads are
-// waited for: bf16 T=2048, d=8192 took 77 us here, 63 in the kernel above; T=2047, d=8191
-// 219 against 72.  Slowest where four pieces of single elements spill (T=1000, d=9001: 241).
+// waited for: bf16 T=2048, d=8192 took 77 us here when the kernel above took 63; T=2047,
+// d=8191 219 against 72.  With a channel gate bf16 T=1000, d=9216 takes 86 us, d=16384 105
+// (fp32 131); slowest where four pieces of single elements spill (T=1000, d=9001: 255).
 template <typename A, typename R, int V, int W>
 __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(const NormArgs a) {
   extern __shared__ __align__(16) float wide_sm[];                  // [2][d]: w_pre and q; later P and S
@@ -980,8 +984,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) k_block_norm_grad_wide(cons
   int flip = 0;
   for (long long row = blockIdx.x; row < a.T; row += gridDim.x, flip ^= 1) {
     // Two pieces of a row are kept over the reduction; four would spill and are read
-    // again (T=1000, d=16384: bf16 142 -> 90 us, fp32 196 -> 116; with two pieces, d=8192,
-    // 95 -> 103).
+    // again (without a gate, T=1000, d=16384: bf16 142 -> 90 us, fp32 196 -> 116; with two
+    // pieces, d=8192, 95 -> 103).
     constexpr bool kKept = V <= 2;
     float x[kKept ? V : 1][8], y[kKept ? V : 1][8], dr[kKept ? V : 1][8], du[kKept ? V : 1][8];
     float wp[8], q[8];
