@@ -666,6 +666,45 @@ int moe_router_backward(const moe_router_desc* desc, int T, const void* logits, 
                         long long ld_d, void* stream);
 
 /*
+ * Router with groups: the experts stand in `groups` groups of E / groups neighbours, and a
+ * token's k experts come from its top_groups best groups.  With s = sigmoid(l)
+ * (MOE_ROUTER_SIGMOID) or the softmax over all experts, and key = s + bias:
+ *   group_score  a group's value: MOE_GROUP_MAX its largest key, MOE_GROUP_TOP2 the sum of
+ *                its two largest (of those whose logit is above -inf; a NaN does not count)
+ *   ids          the k largest keys among the top_groups groups of the largest values,
+ *                largest first; ties, of groups too, to the lowest index
+ * Here the bias is added to the scores, not to the logits as in moe_router_forward.  The
+ * order is that of the exact keys: keys closer than fp32 tells are compared in 64 bits, so
+ * that ids do not depend on rounding.  Without a bias the logits order the experts.  A
+ * logit of -inf has the key -inf; with a NaN logit every softmax key of the row is NaN
+ * (below every number), a sigmoid key only its own.
+ * Scores, counts, prob_sum, losses, row_stat, padding, the workspace and everything else
+ * are as in moe_router_forward, and the gradient is moe_router_backward's with
+ * desc->router (the choice is a constant there).
+ * groups divides E; k <= top_groups * E / groups.
+ */
+#define MOE_GROUP_MAX  0
+#define MOE_GROUP_TOP2 1
+typedef struct moe_group_router_desc {
+  moe_router_desc router;
+  int groups, top_groups;
+  int group_score;
+} moe_group_router_desc;
+
+size_t moe_group_router_workspace_bytes(const moe_group_router_desc* desc, int T);
+int moe_group_router_forward(const moe_group_router_desc* desc, int T, const void* logits,
+                             long long ld, const float* bias, const uint8_t* token_mask,
+                             int32_t* ids, float* scores, int32_t* counts, float* prob_sum,
+                             float* losses, float* row_stat, void* workspace,
+                             size_t workspace_bytes, void* stream);
+
+/*
+ * Balance without a loss: bias[e] += rate where counts[e] is below the mean of counts[0..E),
+ * -= rate where it is above (bias [E] fp32, counts as a router's forward leaves them).
+ */
+int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate, void* stream);
+
+/*
  * The norms around a block with its gate and residual scale.  On rows of d
  * elements, with rms(v) = sqrt(mean(v^2) + eps):
  *   n   = y / rms(y) * w_post             (n = y where w_post is NULL)
@@ -734,6 +773,116 @@ int moe_block_norm_backward(const moe_block_norm_desc* desc, int T, const void* 
                             long long ld_dy, float* dw_post, float* dgate, float* dw_pre,
                             int accumulate, void* workspace, size_t workspace_bytes,
                             void* stream);
+
+/*
+ * 8-bit block products: E4M3 codes (uint8) with one fp32 scale per 128 elements along the
+ * summed dimension, value = code * scale.  Unlike the MXFP8 path's, the scales are any
+ * fp32 numbers, and weights have one per 128 x 128 tile: the format of checkpoints stored
+ * with 128 x 128 weight blocks and activations quantised per token and 128 channels.
+ *
+ * Block rule (fp32, every step rounded to nearest): top = max(max |v|, 2^-100), scale =
+ * top / 448, code = E4M3(v * (448 / top)).  With MOE_FP8_POW2 the scale is the power of two
+ * at or above top / 448 (and the factor its exact inverse).  A NaN or infinity makes
+ * every value of its block NaN.
+ *
+ * Rows may belong to experts: offsets [E+1] int32 (device), expert e's rows are
+ * [offsets[e], offsets[e+1]), as m_indptr or off_pad of a dispatch are.  NULL (E = 1 only)
+ * is one segment of all rows.  Offsets that decrease or leave the rows make a call write
+ * nothing; the products record MOE_ERR_INVALID_ARG then.
+ *
+ * Two layouts of a matrix's codes:
+ *   by rows     codes [M, width], rows ld_codes bytes apart; scales [ceil(width/128),
+ *               M], rows ld_scales apart: blocks along a row, for sums over columns
+ *   by columns  codes_t [width, R], rows ld_codes_t bytes apart; scales_t [R/128, width]:
+ *               blocks along 128 rows of a segment, for sums over rows.  Segment e takes
+ *               columns from 128 * sum_{i<e} ceil(rows_i / 128) on, the codes of the rest
+ *               of its last block are 0, and blocks beyond the last segment's are
+ *               neither written nor read.  R is a multiple of 128; with offsets M + 127 E,
+ *               rounded down to such, always holds all of it.
+ * Codes start at 16-byte boundaries with row distances that are multiples of 16; the
+ * codes' own rows may have any width.
+ */
+#define MOE_FP8_POW2 1             /* flags: scales are powers of two                */
+#define MOE_FP8_MAX_WIDTH (1 << 20)
+#define MOE_FP8_ROWS        0      /* v = x, rows of C                               */
+#define MOE_FP8_SWIGLU      1      /* v = silu(g) u of x = [g | u], rows of 2C       */
+#define MOE_FP8_SWIGLU_GRAD 2      /* v = the gradient at [g | u] from dh, rows of C */
+typedef struct moe_fp8_quant_desc {
+  int source;                      /* MOE_FP8_*                                      */
+  int C;                           /* columns; v has C, of the gradient 2C           */
+  int dtype;                       /* MOE_DTYPE_* of x and dh                        */
+  int E;                           /* segments, 1..256                               */
+  float clamp;                     /* SwiGLU limit as in moe_plan_set_swiglu_clamp;
+                                      a NaN stays NaN                                */
+  int flags;                       /* MOE_FP8_POW2                                   */
+} moe_fp8_quant_desc;
+
+/*
+ * Quantise M rows by rows (codes, scales), by columns (codes_t, scales_t) or both, from
+ * one reading of x and without a rounding in between.
+ *   x     [., C or 2C], rows ld_x elements apart
+ *   rows  [M] int32 or NULL (MOE_FP8_ROWS only): v's row r is x's row rows[r]; zeros where
+ *         it is negative or not below x_rows (token_of of a dispatch gathers)
+ *   dh    [M, C] gradient at h, with MOE_FP8_SWIGLU_GRAD
+ * With offsets only the segments' rows are read and written.  codes or codes_t may be
+ * NULL.  Columns that do not fit below cols_t = R are left out, of both layouts.
+ */
+int moe_fp8_quantize(const moe_fp8_quant_desc* desc, int M, const void* x, long long ld_x,
+                     int x_rows, const void* dh, long long ld_dh, const int32_t* rows,
+                     const int32_t* offsets, uint8_t* codes, long long ld_codes, float* scales,
+                     long long ld_scales, uint8_t* codes_t, long long ld_codes_t,
+                     long long cols_t, float* scales_t, long long ld_scales_t, void* stream);
+
+/*
+ * Weights w [E, N, K] (dtype, dense) in 128 x 128 tiles:
+ *   codes   [E, N, K]  rows ld_codes bytes apart, scales [E, ceil(N/128), ceil(K/128)]
+ *   codes_t [E, K, N]  transposed, for the gradient at the inputs, rows ld_codes_t bytes
+ *                      apart, scales_t [E, ceil(K/128), ceil(N/128)]
+ * Either pair may be NULL.
+ */
+int moe_fp8_quantize_weights(const void* w, int dtype, int E, int N, int K, int flags,
+                             uint8_t* codes, long long ld_codes, float* scales, uint8_t* codes_t,
+                             long long ld_codes_t, float* scales_t, void* stream);
+
+/*
+ * Products.  status: 16 bytes of device memory, 16-byte aligned, zero before the first
+ * call, which calls on any stream may share: a wait that gave up or bad offsets are
+ * recorded there (moe_fp8_check).
+ */
+typedef struct moe_fp8_gemm_desc {
+  int N, K, E;                     /* weights [E, N, K]                              */
+  int out_dtype;                   /* MOE_DTYPE_* of c                               */
+} moe_fp8_gemm_desc;
+
+/*
+ * c[r, n] = sum_k a[r, k] * b[e, n, k], e the expert of row r: a by rows [M, K], b weights;
+ * products and sums fp32 (each block of 128 summed by the tensor core, then scaled and
+ * added in order), rounded once.  c [M, N], rows ld_c elements apart; rows of no segment
+ * are left as they are.  With b the transposed weights and N, K exchanged this is the
+ * gradient at the inputs.
+ */
+int moe_fp8_gemm(const moe_fp8_gemm_desc* desc, int M, const uint8_t* a, long long ld_a,
+                 const float* a_scales, long long ld_as, const uint8_t* b, long long ld_b,
+                 const float* b_scales, const int32_t* offsets, void* c, long long ld_c,
+                 void* status, void* stream);
+
+/*
+ * dw[e, n, k] = sum over expert e's rows of dy[r, n] * x[r, k], added to dw with
+ * accumulate = 1: dy and x by columns (dyt [N, R], xt [K, R]), with the offsets that
+ * they were quantised with.  dw [E, N, K] fp32, dense.  Without accumulate the dw of an
+ * expert without rows is 0.  desc->out_dtype is not looked at beyond its range.
+ */
+int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* desc, long long R, const uint8_t* dyt,
+                       long long ld_dyt, const float* dyt_scales, long long ld_dys,
+                       const uint8_t* xt, long long ld_xt, const float* xt_scales,
+                       long long ld_xs, const int32_t* offsets, float* dw, int accumulate,
+                       void* status, void* stream);
+
+/*
+ * Synchronise the device, read and clear a status: MOE_OK, MOE_ERR_INVALID_ARG (bad
+ * offsets) or MOE_ERR_TIMEOUT (*where, which may be NULL: the wait's site).
+ */
+int moe_fp8_check(void* status, int* where);
 
 #ifdef __cplusplus
 }

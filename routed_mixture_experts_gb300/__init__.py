@@ -21,9 +21,16 @@ from .binding import (  # noqa: F401
     MOE_ERR_TIMEOUT,
     MOE_ERR_UNSUPPORTED,
     MOE_ERR_WORKSPACE,
+    MOE_FP8_MAX_WIDTH,
+    MOE_FP8_POW2,
+    MOE_FP8_ROWS,
+    MOE_FP8_SWIGLU,
+    MOE_FP8_SWIGLU_GRAD,
     MOE_GATE_CHANNEL,
     MOE_GATE_NONE,
     MOE_GATE_TOKEN,
+    MOE_GROUP_MAX,
+    MOE_GROUP_TOP2,
     MOE_OK,
     MOE_PREC_BF16,
     MOE_PREC_MXFP8,
@@ -34,16 +41,24 @@ from .binding import (  # noqa: F401
     MOE_WS_HOST_STAGING,
     MOE_WS_TRAINING,
     BlockNormGrads,
+    Fp8Matrix,
     MoeBlockNorm,
     MoeError,
+    MoeFp8Linear,
+    MoeGroupRouter,
     MoePlan,
     MoeRouter,
     RouterResult,
     amax_bf16,
+    fp8_columns,
     gemm_bf16,
     lib,
     prepare_weights_mxfp8,
     prepare_weights_mxfp8_backward,
     prepare_weights_nvfp4,
+    quantize_fp8,
+    quantize_fp8_weights,
     quantize_mxfp8,
+    swiglu_fp8,
+    swiglu_grad_fp8,
 )

@@ -34,6 +34,13 @@ MOE_GATE_NONE = 0
 MOE_GATE_CHANNEL = 1
 MOE_GATE_TOKEN = 2
 MOE_DECODE_MAX_TOKENS = 256
+MOE_GROUP_MAX = 0
+MOE_GROUP_TOP2 = 1
+MOE_FP8_POW2 = 1
+MOE_FP8_ROWS = 0
+MOE_FP8_SWIGLU = 1
+MOE_FP8_SWIGLU_GRAD = 2
+MOE_FP8_MAX_WIDTH = 1 << 20
 
 _lock = threading.Lock()
 _lib = None
@@ -43,6 +50,24 @@ class RouterDesc(ctypes.Structure):
     """moe_router_desc"""
     _fields_ = [("E", ctypes.c_int), ("k", ctypes.c_int), ("dtype", ctypes.c_int),
                 ("scoring", ctypes.c_int), ("scale", ctypes.c_float)]
+
+
+class GroupRouterDesc(ctypes.Structure):
+    """moe_group_router_desc"""
+    _fields_ = [("router", RouterDesc), ("groups", ctypes.c_int), ("top_groups", ctypes.c_int),
+                ("group_score", ctypes.c_int)]
+
+
+class Fp8QuantDesc(ctypes.Structure):
+    """moe_fp8_quant_desc"""
+    _fields_ = [("source", ctypes.c_int), ("C", ctypes.c_int), ("dtype", ctypes.c_int),
+                ("E", ctypes.c_int), ("clamp", ctypes.c_float), ("flags", ctypes.c_int)]
+
+
+class Fp8GemmDesc(ctypes.Structure):
+    """moe_fp8_gemm_desc"""
+    _fields_ = [("N", ctypes.c_int), ("K", ctypes.c_int), ("E", ctypes.c_int),
+                ("out_dtype", ctypes.c_int)]
 
 
 class BlockNormDesc(ctypes.Structure):
@@ -116,8 +141,20 @@ def _declare(L):
     L.moe_block_norm_forward.argtypes = [vp, i32] + [vp, i64x] * 2 + [vp] * 3 + [vp, i64x] * 2 + [vp]
     L.moe_block_norm_backward.argtypes = ([vp, i32] + [vp, i64x] * 4 + [vp] * 3 + [vp, i64x] * 2 +
                                           [vp] * 3 + [i32, vp, sz, vp])
+    L.moe_group_router_workspace_bytes.argtypes = [vp, i32]
+    L.moe_group_router_workspace_bytes.restype = sz
+    L.moe_group_router_forward.argtypes = [vp, i32, vp, i64x] + [vp] * 9 + [sz, vp]
+    L.moe_router_update_bias.argtypes = [vp, vp, i32, f32, vp]
+    L.moe_fp8_quantize.argtypes = ([vp, i32, vp, i64x, i32, vp, i64x, vp, vp] + [vp, i64x] * 3 +
+                                   [i64x, vp, i64x, vp])
+    L.moe_fp8_quantize_weights.argtypes = [vp, i32, i32, i32, i32, i32] + [vp, i64x, vp] * 2 + [vp]
+    L.moe_fp8_gemm.argtypes = [vp, i32] + [vp, i64x] * 3 + [vp, vp, vp, i64x, vp, vp]
+    L.moe_fp8_gemm_wgrad.argtypes = [vp, i64x] + [vp, i64x] * 4 + [vp, vp, i32, vp, vp]
+    L.moe_fp8_check.argtypes = [vp, ctypes.POINTER(ctypes.c_int)]
     for name in ("moe_router_forward", "moe_router_backward", "moe_block_norm_forward",
-                 "moe_block_norm_backward"):
+                 "moe_block_norm_backward", "moe_group_router_forward", "moe_router_update_bias",
+                 "moe_fp8_quantize", "moe_fp8_quantize_weights", "moe_fp8_gemm",
+                 "moe_fp8_gemm_wgrad", "moe_fp8_check"):
         getattr(L, name).restype = i32
     for name in ("moe_plan_set_swiglu_clamp", "moe_plan_set_workspace", "moe_forward",
                  "moe_forward_routed",
@@ -539,11 +576,18 @@ class MoeRouter:
         self.dtype = dtype if dtype is not None else torch.float32
         self.desc = RouterDesc(E, k, _dtype_code(self.dtype, "MoeRouter"), scoring, scale)
         self._desc = ctypes.addressof(self.desc)
-        nbytes = L.moe_router_workspace_bytes(self._desc, max_tokens)
+        nbytes = self._scratch_bytes(L, max_tokens)
         if not nbytes:
-            raise MoeError(MOE_ERR_INVALID_ARG, "MoeRouter(%d,%d,%d)" % (max_tokens, E, k))
+            raise MoeError(MOE_ERR_INVALID_ARG, "%s(%d,%d,%d)" % (type(self).__name__, max_tokens,
+                                                                  E, k))
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=device)
         self._ws = (self.workspace.data_ptr(), nbytes)
+
+    def _scratch_bytes(self, L, max_tokens):
+        return L.moe_router_workspace_bytes(self._desc, max_tokens)
+
+    def _forward(self, *args):
+        return _lib.moe_router_forward(self._desc, *args)
 
     def outputs(self, T):
         """Fresh output tensors of a forward over T tokens."""
@@ -585,8 +629,8 @@ class MoeRouter:
                   _want(out.prob_sum, "prob_sum", f32, (E,), dev),
                   _want(out.losses, "losses", f32, (2,), dev),
                   _want(out.row_stat, "row_stat", f32, (T,), dev))
-        _check(_lib.moe_router_forward(self._desc, T, lp, ld, bp, mp, *at, *self._ws,
-                                       _raw_stream(dev)), "router forward")
+        _check(self._forward(T, lp, ld, bp, mp, *at, *self._ws, _raw_stream(dev)),
+               "router forward")
         return out
 
     def backward(self, logits, ids, counts, row_stat, d_scores=None, d_losses=None,
@@ -615,6 +659,43 @@ class MoeRouter:
             _maybe(d_losses, "d_losses", f32, (2,), dev), dp, ld_d, _raw_stream(dev)),
             "router backward")
         return d_logits
+
+
+class MoeGroupRouter(MoeRouter):
+    """Top-k routing within the best groups of experts, by scores plus a bias
+    (moe_group_router_forward in moe.h); backward is MoeRouter's.
+
+    groups: of E / groups neighbouring experts each; top_groups of them compete;
+    group_score: MOE_GROUP_TOP2 or MOE_GROUP_MAX."""
+
+    def __init__(self, max_tokens, E, k, groups, top_groups, scoring=MOE_ROUTER_SIGMOID,
+                 group_score=MOE_GROUP_TOP2, scale=1.0, dtype=None, device="cuda"):
+        self.groups, self.top_groups, self.group_score = groups, top_groups, group_score
+        super().__init__(max_tokens, E, k, scoring, scale, dtype, device)
+
+    def _scratch_bytes(self, L, max_tokens):
+        self.group_desc = GroupRouterDesc(self.desc, self.groups, self.top_groups,
+                                          self.group_score)
+        self._group_desc = ctypes.addressof(self.group_desc)
+        return L.moe_group_router_workspace_bytes(self._group_desc, max_tokens)
+
+    def _forward(self, *args):
+        return _lib.moe_group_router_forward(self._group_desc, *args)
+
+    def update_bias(self, bias, counts, rate, stream=None):
+        """bias[e] += rate for experts chosen less than the mean, -= rate for those chosen
+        more; counts: a forward's."""
+        import torch
+
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.update_bias(bias, counts, rate)
+        dev = _device()
+        _check(_lib.moe_router_update_bias(
+            _want(bias, "bias", torch.float32, (self.E,), dev),
+            _want(counts, "counts", torch.int32, (self.E + 1,), dev), self.E, rate,
+            _raw_stream(dev)), "update_bias")
+        return bias
 
 
 BlockNormGrads = collections.namedtuple("BlockNormGrads", "d_residual dy dw_post dgate dw_pre")
@@ -752,3 +833,259 @@ class MoeBlockNorm:
             wpp, ggp, wqp, 1 if accumulate else 0, self.workspace.data_ptr(), self._ws_bytes,
             _raw_stream(dev)), "block norm backward")
         return BlockNormGrads(d_residual, dy, dw_post, dgate, dw_pre)
+
+
+# ---- 8-bit block products -----------------------------------------------------------
+
+Fp8Matrix = collections.namedtuple("Fp8Matrix", "codes scales")
+
+
+def _codes(t, what, shape, dev):
+    """t: E4M3 codes [..., width] whose rows lie a multiple of 16 bytes apart (address, row
+    distance); a batch's matrices follow one another."""
+    import torch
+
+    if t.dtype is torch.float8_e4m3fn and t.shape == shape and t.get_device() == dev:
+        if t.is_contiguous() and shape[-1] % 16 == 0:
+            return t.data_ptr(), shape[-1]
+        st = t.stride()
+        ld = st[-2] if shape[-2] > 1 else (st[-3] if len(shape) == 3 and shape[0] > 1
+                                           else (shape[-1] + 15) // 16 * 16)
+        if ((st[-1] == 1 or shape[-1] == 1) and ld % 16 == 0 and ld >= shape[-1] and
+                (len(shape) == 2 or shape[0] == 1 or st[0] == shape[1] * ld)):
+            return t.data_ptr(), ld
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want float8_e4m3fn %s on the current GPU (%d), rows a "
+                   "multiple of 16 bytes apart; got %s %s on %s, strides %s" % (
+                       what, tuple(shape), dev, t.dtype, tuple(t.shape), t.device, t.stride()))
+
+
+def _new_codes(lead, width, device):
+    """Codes [*lead, width] with rows a multiple of 16 bytes apart."""
+    import torch
+
+    ld = (width + 15) // 16 * 16
+    return torch.empty((*lead, ld), dtype=torch.float8_e4m3fn, device=device)[..., :width]
+
+
+def _offsets(offsets, E, dev):
+    """Address of the offsets and the number of segments."""
+    import torch
+
+    if offsets is None:
+        if E not in (None, 1):
+            raise MoeError(MOE_ERR_INVALID_ARG, "%d experts need offsets" % E)
+        return None, 1
+    if E is None:
+        E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+    return _want(offsets, "offsets", torch.int32, (E + 1,), dev), E
+
+
+def fp8_columns(M, E=1, offsets=True):
+    """Columns R of codes along the columns that hold M rows of E experts whatever the
+    offsets (one segment without)."""
+    return (M + 127 * E) // 128 * 128 if offsets else (M + 127) // 128 * 128
+
+
+def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_column, out, out_t,
+                  what):
+    import torch
+
+    _rows_fit(max(M, x.shape[0]), what)
+    if not (by_row or by_column) or (out is not None and not by_row) or (
+            out_t is not None and not by_column):
+        raise MoeError(MOE_ERR_INVALID_ARG, "%s: out goes with by_row, out_t with by_column, and "
+                       "one of them is needed" % what)
+    dev, at, f32 = _device(), x.device, torch.float32
+    dtype = _dtype_code(x.dtype, what)
+    width = 2 * C if source == MOE_FP8_SWIGLU_GRAD else C
+    xp, ld_x = _rows(x, "x", x.dtype, (x.shape[0], C if source == MOE_FP8_ROWS else 2 * C), dev)
+    dp, ld_d = (None, 0) if dh is None else _rows(dh, "dh", x.dtype, (M, C), dev)
+    rp = _maybe(rows, "rows", torch.int32, (M,), dev)
+    fp, E = _offsets(offsets, None, dev)
+    cp = sp = tp = up = None
+    ld_c = ld_s = ld_t = ld_u = R = 0
+    if by_row:
+        if out is None:
+            out = Fp8Matrix(_new_codes((M,), width, at),
+                            torch.empty(((width + 127) // 128, M), dtype=f32, device=at))
+        cp, ld_c = _codes(out[0], "codes", (M, width), dev)
+        sp, ld_s = _rows(out[1], "scales", f32, ((width + 127) // 128, M), dev)
+    if by_column:
+        if out_t is None:
+            R = fp8_columns(M, E, offsets is not None)
+            out_t = Fp8Matrix(torch.empty((width, R), dtype=torch.float8_e4m3fn, device=at),
+                              torch.empty((R // 128, width), dtype=f32, device=at))
+        R = out_t[0].shape[-1]
+        tp, ld_t = _codes(out_t[0], "codes_t", (width, R), dev)
+        up, ld_u = _rows(out_t[1], "scales_t", f32, (R // 128, width), dev)
+    desc = Fp8QuantDesc(source, C, dtype, E, clamp, MOE_FP8_POW2 if pow2 else 0)
+    _check(_lib.moe_fp8_quantize(ctypes.addressof(desc), M, xp, ld_x, x.shape[0], dp, ld_d, rp, fp,
+                                 cp, ld_c, sp, ld_s, tp, ld_t, R, up, ld_u, _raw_stream(dev)), what)
+    return (Fp8Matrix(*out) if by_row else None), (Fp8Matrix(*out_t) if by_column else None)
+
+
+def quantize_fp8(x, rows=None, offsets=None, pow2=False, by_row=True, by_column=False, out=None,
+                 out_t=None, stream=None):
+    """E4M3 codes of x [., C] with a scale per 128 (moe_fp8_quantize in moe.h).
+
+    rows [M] int32 gathers (zeros where it is out of range); offsets [E+1] int32 are the
+    experts' rows.  -> (by row: Fp8Matrix(codes [M, C], scales [ceil(C/128), M]) or None,
+    by column: Fp8Matrix(codes [C, R], scales [R/128, C]) or None)."""
+    import torch
+
+    if stream is not None:               # the outputs then belong to that stream too
+        with torch.cuda.stream(stream):
+            return quantize_fp8(x, rows, offsets, pow2, by_row, by_column, out, out_t)
+    lib()
+    M = x.shape[0] if rows is None else rows.shape[0]
+    return _quantize_fp8(MOE_FP8_ROWS, x, x.shape[1], M, None, rows, offsets, 0.0, pow2, by_row,
+                         by_column, out, out_t, "quantize_fp8")
+
+
+def swiglu_fp8(a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=False, out=None,
+               out_t=None, stream=None):
+    """Codes of silu(g) * u for a = [g | u] [M, 2C], as quantize_fp8."""
+    import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu_fp8(a, clamp, offsets, pow2, by_row, by_column, out, out_t)
+    lib()
+    return _quantize_fp8(MOE_FP8_SWIGLU, a, a.shape[1] // 2, a.shape[0], None, None, offsets,
+                         clamp, pow2, by_row, by_column, out, out_t, "swiglu_fp8")
+
+
+def swiglu_grad_fp8(dh, a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=False,
+                    out=None, out_t=None, stream=None):
+    """Codes of the gradient [M, 2C] at a = [g | u] from dh [M, C], as quantize_fp8."""
+    import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return swiglu_grad_fp8(dh, a, clamp, offsets, pow2, by_row, by_column, out, out_t)
+    lib()
+    return _quantize_fp8(MOE_FP8_SWIGLU_GRAD, a, a.shape[1] // 2, a.shape[0], dh, None, offsets,
+                         clamp, pow2, by_row, by_column, out, out_t, "swiglu_grad_fp8")
+
+
+def quantize_fp8_weights(w, transposed=False, pow2=False, stream=None):
+    """Weights [E, N, K] or [N, K] in 128 x 128 tiles (moe_fp8_quantize_weights in moe.h)
+    -> Fp8Matrix(codes [E, N, K], scales [E, ceil(N/128), ceil(K/128)]); with transposed the
+    pair of it and the transposed weights' (codes [E, K, N]), which grad_input reads."""
+    import torch
+
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return quantize_fp8_weights(w, transposed, pow2)
+    L, dev, at = lib(), _device(), w.device
+    if w.dim() == 2:
+        w = w[None]
+    E, N, K = w.shape
+    nb, kb = (N + 127) // 128, (K + 127) // 128
+    wp = _want(w, "w", w.dtype, (E, N, K), dev)
+    make = lambda rows, width, a, b: Fp8Matrix(
+        _new_codes((E, rows), width, at), torch.empty((E, a, b), dtype=torch.float32, device=at))
+    q = make(N, K, nb, kb)
+    t = make(K, N, kb, nb) if transposed else None
+    _check(L.moe_fp8_quantize_weights(
+        wp, _dtype_code(w.dtype, "w"), E, N, K, MOE_FP8_POW2 if pow2 else 0, q.codes.data_ptr(),
+        (K + 15) // 16 * 16, q.scales.data_ptr(), None if t is None else t.codes.data_ptr(),
+        (N + 15) // 16 * 16, None if t is None else t.scales.data_ptr(), _raw_stream(dev)),
+        "quantize_fp8_weights")
+    return (q, t) if transposed else q
+
+
+class MoeFp8Linear:
+    """Products with weights [E, N, K] on 8-bit codes (moe_fp8_gemm, moe_fp8_gemm_wgrad in
+    moe.h): y = x w[e]^T, its gradient at x, and the weights' gradient.  E = 1 without
+    offsets is a dense layer.  dtype: of y and of the gradient at x.
+
+    Matrices are Fp8Matrix (or pairs) as quantize_fp8 and quantize_fp8_weights make them."""
+
+    def __init__(self, N, K, E=1, dtype=None, device="cuda"):
+        import torch
+
+        lib()
+        self.N, self.K, self.E = N, K, E
+        self.dtype = dtype if dtype is not None else torch.bfloat16
+        code = _dtype_code(self.dtype, "MoeFp8Linear")
+        if not (0 < N <= MOE_FP8_MAX_WIDTH and 0 < K <= MOE_FP8_MAX_WIDTH and 0 < E <= 256):
+            raise MoeError(MOE_ERR_INVALID_ARG, "MoeFp8Linear(%d,%d,%d)" % (N, K, E))
+        self.desc = Fp8GemmDesc(N, K, E, code)
+        self._desc_t = Fp8GemmDesc(K, N, E, code)
+        self.status = torch.zeros(4, dtype=torch.int32, device=device)
+
+    def _product(self, desc, x, w, offsets, out, what):
+        import torch
+
+        N, K, E = desc.N, desc.K, desc.E
+        dev, f32 = _device(), torch.float32
+        _scratch_on(self.status, dev)
+        M = x[0].shape[0]
+        _rows_fit(M, what)
+        ap, ld_a = _codes(x[0], "codes", (M, K), dev)
+        sp, ld_s = _rows(x[1], "scales", f32, ((K + 127) // 128, M), dev)
+        wc = w[0] if w[0].dim() == 3 else w[0][None]
+        bp, ld_b = _codes(wc, "weights' codes", (E, N, K), dev)
+        ws = w[1] if w[1].dim() == 3 else w[1][None]
+        wp = _want(ws, "weights' scales", f32, (E, (N + 127) // 128, (K + 127) // 128), dev)
+        fp, _ = _offsets(offsets, E, dev)
+        if out is None:
+            out = torch.empty((M, N), dtype=self.dtype, device=x[0].device)
+            op, ld_o = out.data_ptr(), N
+        else:
+            op, ld_o = _rows(out, "out", self.dtype, (M, N), dev)
+        _check(_lib.moe_fp8_gemm(ctypes.addressof(desc), M, ap, ld_a, sp, ld_s, bp, ld_b, wp, fp,
+                                 op, ld_o, self.status.data_ptr(), _raw_stream(dev)), what)
+        return out
+
+    def forward(self, x, w, offsets=None, out=None, stream=None):
+        """y [M, N] = x w[e]^T of x by rows [M, K] and weights w; rows of no segment are not
+        written."""
+        import torch
+
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.forward(x, w, offsets, out)
+        return self._product(self.desc, x, w, offsets, out, "fp8 forward")
+
+    def grad_input(self, dy, w_t, offsets=None, out=None, stream=None):
+        """dx [M, K] = dy w[e] of dy by rows [M, N] and the transposed weights w_t."""
+        import torch
+
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.grad_input(dy, w_t, offsets, out)
+        return self._product(self._desc_t, dy, w_t, offsets, out, "fp8 grad_input")
+
+    def grad_weight(self, dy_t, x_t, offsets=None, dw=None, accumulate=False, stream=None):
+        """dw [E, N, K] fp32 = dy^T x of each expert's rows, of dy and x by columns [N, R],
+        [K, R]; accumulate adds to the given dw."""
+        import torch
+
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                return self.grad_weight(dy_t, x_t, offsets, dw, accumulate)
+        N, K, E = self.N, self.K, self.E
+        dev, f32 = _device(), torch.float32
+        _scratch_on(self.status, dev)
+        R = x_t[0].shape[-1]
+        yp, ld_y = _codes(dy_t[0], "dy's codes", (N, R), dev)
+        xp, ld_x = _codes(x_t[0], "x's codes", (K, R), dev)
+        sp, ld_sy = _rows(dy_t[1], "dy's scales", f32, (R // 128, N), dev)
+        tp, ld_sx = _rows(x_t[1], "x's scales", f32, (R // 128, K), dev)
+        fp, _ = _offsets(offsets, E, dev)
+        if dw is None:
+            new = torch.zeros if accumulate else torch.empty
+            dw = new((E, N, K), dtype=f32, device=x_t[0].device)
+        _check(_lib.moe_fp8_gemm_wgrad(
+            ctypes.addressof(self.desc), R, yp, ld_y, sp, ld_sy, xp, ld_x, tp, ld_sx, fp,
+            _want(dw, "dw", f32, (E, N, K), dev), 1 if accumulate else 0, self.status.data_ptr(),
+            _raw_stream(dev)), "fp8 grad_weight")
+        return dw
+
+    def check(self):
+        """Synchronise; (status, detail) of what the device recorded, which is cleared."""
+        where = ctypes.c_int(0)
+        rc = _lib.moe_fp8_check(self.status.data_ptr(), ctypes.byref(where))
+        return rc, where.value

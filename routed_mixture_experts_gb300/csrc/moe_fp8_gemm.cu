@@ -1,0 +1,574 @@
+// moe_fp8_gemm.cu -- products of E4M3 codes with one fp32 scale per 128 elements.
+//
+//   rows      C[r, n] = sum_b sa[b, r] sb[e, n / 128, b] (A[r, b] . B[e, n, b])
+//             e the expert of row r, b the blocks of 128 along K
+//   weights   dW[e, n, k] (+)= sum_b sy[b, n] sx[b, k] (dYt[n, b] . Xt[k, b])
+//             b the blocks of expert e's rows; operands with codes along the rows
+//
+// The scales change with every block of 128, so the tensor core's sum ends there: the
+// 128 products of a block go to tensor memory in fp32 (four K = 32 instructions), are read
+// back, and join the running sum in registers with one fused multiply-add an element, all
+// fp32.  tcgen05.mma writes one part of tensor memory while eight warps read the other.
+
+#include "../../include/moe.h"
+#include "moe_device.cuh"
+#include "moe_fp8.cuh"
+#include "moe_gemm_common.cuh"
+#include "moe_internal.h"
+
+namespace moe {
+
+namespace {
+
+// warp 0 copies, warp 1 MMA (2, 3 idle), warps 4..11 sums.  A third of the launch's 168
+// registers a thread goes from the first four warps to the others, which hold 128 sums.
+constexpr int kThreads = 384;
+constexpr int kEpiWarps = 8;
+constexpr int kLaunchRegs = 168, kCopyRegs = 56, kSumRegs = 224;
+static_assert(kCopyRegs + 2 * kSumRegs <= 3 * kLaunchRegs, "registers of three warpgroups");
+
+struct Fp8GemmArgs {
+  int M, N, K, E;                    // rows, columns, depth (weights: dW is [E, N, K])
+  const float* sa;  long long ld_sa; // [blocks][rows of A]
+  const float* sb;  long long ld_sb; // rows: [E][N blocks][K blocks]; weights: [blocks][K]
+  const int32_t* offsets;            // [E+1] or NULL: one segment
+  void* c;  long long ld_c;
+  int row_blocks;                    // weights: blocks of 128 that the codes have
+  int f32, accumulate, wide;         // wide: 32-byte stores
+  DevError* err;
+};
+
+// D[tmem] (+)= A B^T, kind::f8f6f4: E4M3 operands, fp32 sums.
+__device__ __forceinline__ void umma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                        uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Instruction descriptor, kind::f8f6f4: fp32 D (bits 4-5 = 1), E4M3 A and B (format 0 in
+// bits 7-9 and 10-12), both K-major, N >> 3 in bits 17-22, M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {
+  return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t pair_u(uint32_t a, uint32_t b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+
+__device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
+template <int BN>
+struct Shape {
+  static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int TURN = kEpiWarps * 32 * 17 * 4;       // narrow stores, a warp 32 x 16
+  static constexpr int SCALES = kEpiWarps * 2 * (BN / 2) * 4;   // weights: scales of columns
+  static constexpr int REST = TURN + SCALES + 512;
+  static constexpr int FIT = (226 * 1024 - 3584 - REST) / STAGE;
+  static constexpr int STAGES = FIT > 8 ? 8 : FIT;
+  static constexpr int SMEM = STAGES * STAGE + REST + 1024;
+  static constexpr int NBUF = 512 / BN;                      // parts of tensor memory
+};
+
+struct Tile {
+  int e, m0, m1;       // expert, rows [m0, m1) of C (weights: of dW)
+  int n0;
+  int b0, b1;          // blocks along the depth
+};
+
+// Persistent: tiles in turn over the CTAs, every role walking the same sequence.
+template <int BN, bool WGRAD>
+__device__ __forceinline__ Tile tile_of(const Fp8GemmArgs& a, const Segments& seg, int t,
+                                        int n_tiles) {
+  Tile r;
+  if (WGRAD) {
+    const int m_tiles = (a.N + 127) >> 7, per = m_tiles * n_tiles;
+    r.e = t / per;
+    const int q = t - r.e * per;
+    r.m0 = (q / n_tiles) << 7;
+    r.m1 = min(r.m0 + 128, a.N);
+    r.n0 = (q % n_tiles) * BN;
+    r.b0 = a.offsets ? min(seg.first[r.e], a.row_blocks) : 0;
+    r.b1 = a.offsets ? min(seg.first[r.e + 1], a.row_blocks) : a.row_blocks;
+  } else {
+    const int b = t / n_tiles;
+    r.n0 = (t - b * n_tiles) * BN;
+    r.b0 = 0;
+    r.b1 = (a.K + 127) >> 7;
+    if (a.offsets) {
+      r.e = seg.find(b, a.E);
+      r.m0 = seg.begin[r.e] + ((b - seg.first[r.e]) << 7);
+      r.m1 = min(seg.end[r.e], r.m0 + 128);
+    } else {
+      r.e = 0;
+      r.m0 = b << 7;
+      r.m1 = min(a.M, r.m0 + 128);
+    }
+  }
+  return r;
+}
+
+template <int BN, bool WGRAD>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_fp8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const Fp8GemmArgs args) {
+  using S = Shape<BN>;
+  constexpr int STAGES = S::STAGES, NBUF = S::NBUF, HALF = BN / 2;
+  static_assert(S::SMEM + 3584 <= 232448, "shared memory");
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ Segments seg;
+  __shared__ uint32_t tmem_holder;
+  __shared__ volatile int abort_s;
+
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  float* const turn_all = reinterpret_cast<float*>(smem + STAGES * S::STAGE);
+  float* const scales_all = turn_all + S::TURN / 4;
+  const uint32_t bar0 = smem_u32(scales_all + S::SCALES / 4);
+  auto full_bar = [&](int s) { return bar0 + 8u * s; };
+  auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
+  auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
+  auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + NBUF + b); };
+  const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
+  static_assert(8 * (2 * STAGES + 2 * NBUF + 1) <= 512, "barriers");
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    abort_s = 0;
+    for (int s = 0; s < STAGES; ++s) {
+      mbar_init(full_bar(s), 1);
+      mbar_init(empty_bar(s), 1);
+    }
+    for (int b = 0; b < NBUF; ++b) {
+      mbar_init(tfull_bar(b), 1);
+      mbar_init(tempty_bar(b), kEpiWarps);
+    }
+    mbar_init(drain_bar, 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmA);
+    tma_prefetch_desc(&tmB);
+  }
+  pdl_wait();                        // the previous kernel of the stream has completed
+  if (args.offsets) {
+    seg.init<kThreads>(args.offsets, args.E, WGRAD ? 0x7FFFFFFF : args.M);
+    if (seg.bad && blockIdx.x == 0 && threadIdx.x == 0)
+      record_error(args.err, MOE_ERR_INVALID_ARG, 0);
+  }
+  const int n_tiles = ((WGRAD ? args.K : args.N) + BN - 1) / BN;
+  const int num_tiles =
+      WGRAD ? args.E * ((args.N + 127) >> 7) * n_tiles
+            : (args.offsets ? seg.first[args.E] : (args.M + 127) >> 7) * n_tiles;
+  if ((int)blockIdx.x >= num_tiles || (WGRAD && args.offsets && seg.bad)) return;
+
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_holder), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = tmem_holder;
+  const uint32_t stage0 = smem_u32(smem);
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kCopyRegs));
+  if (warp == 0) {
+    // ---------------- copies ----------------
+    if (lane == 0) {
+      int stage = 0;
+      uint32_t phase = 0;
+      int issued_parity[STAGES];
+#pragma unroll
+      for (int s = 0; s < STAGES; ++s) issued_parity[s] = -1;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+        for (int b = ti.b0; b < ti.b1; ++b) {
+          ok = mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 1);
+          if (!ok) break;
+          const uint32_t fb = full_bar(stage), sa = stage0 + stage * S::STAGE;
+          mbar_arrive_expect_tx(fb, S::STAGE);
+          tma_load_2d(sa, &tmA, b << 7, ti.m0, fb);
+          if (WGRAD)
+            tma_load_2d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, fb);
+          else
+            tma_load_3d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, ti.e, fb);
+          issued_parity[stage] = (int)phase;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (!abort_s) {
+        for (int s = 0; s < STAGES; ++s) {       // every stage has been released
+          if (!mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 2)) break;
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      if (abort_s) {                             // let the copies in flight land
+        for (int s = 0; s < STAGES; ++s)
+          if (issued_parity[s] >= 0) gemm::mbar_wait_drain(full_bar(s), (uint32_t)issued_parity[s]);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMA: a block of 128 a time ----------------
+    if (lane == 0) {
+      const uint64_t a0 = smem_desc_sw128(stage0, 16, 1024);
+      const uint64_t b0 = smem_desc_sw128(stage0 + S::A_BYTES, 16, 1024);
+      constexpr uint32_t IDESC = idesc_f8(128, BN);
+      int stage = 0, buf = 0;
+      uint32_t phase = 0, buf_phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+        const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+        for (int b = ti.b0; b < ti.b1; ++b) {
+          ok = mbar_wait(tempty_bar(buf), buf_phase ^ 1u, &abort_s, args.err, 3) &&
+               mbar_wait(full_bar(stage), phase, &abort_s, args.err, 4);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t off = (uint64_t)((uint32_t)(stage * S::STAGE) >> 4);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            umma_f8(tmem_base + (uint32_t)(buf * BN), a0 + off + 2 * k, b0 + off + 2 * k, IDESC,
+                    k != 0);
+          umma_commit(empty_bar(stage));
+          umma_commit(tfull_bar(buf));
+          if (++stage == STAGES) {
+            stage = 0;
+            phase ^= 1u;
+          }
+          if (++buf == NBUF) {
+            buf = 0;
+            buf_phase ^= 1u;
+          }
+        }
+      }
+      if (abort_s) {
+        umma_commit(drain_bar);                  // every MMA issued so far has completed
+        gemm::mbar_wait_drain(drain_bar, 0);
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
+    // ---------------- sums: a warp 32 rows x HALF columns ----------------
+    const int quarter = warp & 3, half = (warp - 4) >> 2;
+    const int row = quarter * 32 + lane;
+    float* const turn = turn_all + (warp - 4) * 32 * 17;
+    float* const col_scale = scales_all + (warp - 4) * 2 * HALF;
+    const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
+    const int k_blocks = (args.K + 127) >> 7, nb_all = (args.N + 127) >> 7;
+    int buf = 0;
+    uint32_t buf_phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+      const int r = ti.m0 + row, c0 = ti.n0 + half * HALF;
+      const int n_all = WGRAD ? args.K : args.N;
+      const bool row_in = r < ti.m1;
+      uint64_t acc[HALF / 2];
+#pragma unroll
+      for (int i = 0; i < HALF / 2; ++i) acc[i] = 0;
+      // scales of the next block: of this thread's row, and of the weights' block or of
+      // this warp's columns
+      const float* pa = args.sa + r;
+      const float* pb =
+          WGRAD ? args.sb + c0
+                : args.sb + ((long long)ti.e * nb_all + min(c0 >> 7, nb_all - 1)) * k_blocks;
+      float sa = 0.f, sb[WGRAD ? HALF / 32 : 1];
+      auto fetch = [&](int b) {
+        sa = row_in && b < ti.b1 ? __ldg(pa + b * args.ld_sa) : 0.f;
+        if (WGRAD) {
+#pragma unroll
+          for (int i = 0; i < HALF / 32; ++i)
+            sb[i] = b < ti.b1 && c0 + lane + 32 * i < n_all
+                        ? __ldg(pb + b * args.ld_sb + lane + 32 * i) : 0.f;
+        } else {
+          sb[0] = b < ti.b1 ? __ldg(pb + b) : 0.f;
+        }
+      };
+      fetch(ti.b0);
+      for (int b = ti.b0; b < ti.b1; ++b) {
+        float s = sa;
+        const float* cs = col_scale + (b & 1) * HALF;
+        if (WGRAD) {
+#pragma unroll
+          for (int i = 0; i < HALF / 32; ++i) col_scale[(b & 1) * HALF + lane + 32 * i] = sb[i];
+          __syncwarp();
+        } else {
+          s *= sb[0];
+        }
+        fetch(b + 1);
+        const uint64_t s2 = pair(s, s);
+        ok = mbar_wait(tfull_bar(buf), buf_phase, &abort_s, args.err, 5);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const uint32_t tb = lane_base + (uint32_t)(buf * BN);
+        uint32_t d[2][16];
+        tmem_ld16(tb, d[0]);
+#pragma unroll
+        for (int i = 0; i < HALF / 16; ++i) {
+          tmem_ld_wait();
+          if (i + 1 < HALF / 16) {
+            tmem_ld16(tb + 16u * (i + 1), d[(i + 1) & 1]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(tempty_bar(buf));
+          }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint64_t v = pair_u(d[i & 1][2 * j], d[i & 1][2 * j + 1]);
+            if (WGRAD) {
+              const float2 q = *reinterpret_cast<const float2*>(cs + 16 * i + 2 * j);
+              v = mul2(v, pair(q.x, q.y));
+            }
+            acc[8 * i + j] = fma2(v, s2, acc[8 * i + j]);
+          }
+        }
+        if (++buf == NBUF) {
+          buf = 0;
+          buf_phase ^= 1u;
+        }
+      }
+      if (!ok) break;
+      // ---- out ----
+      const int n_here = min(HALF, n_all - c0);            // columns of this warp
+      if (n_here <= 0 || (WGRAD && args.accumulate && ti.b0 == ti.b1)) continue;
+      const long long row_at = (WGRAD ? (long long)ti.e * args.N : 0LL) + r;
+      if (args.wide && n_here == HALF) {
+        if (row_in) {
+          if (args.f32) {
+            float* p = static_cast<float*>(args.c) + row_at * args.ld_c + c0;
+#pragma unroll
+            for (int i = 0; i < HALF / 8; ++i) {
+              float v[8];
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 4; ++j) unpair(acc[4 * i + j], v[2 * j], v[2 * j + 1]);
+              if (WGRAD && args.accumulate) {
+                const float4 x = *reinterpret_cast<const float4*>(p + 8 * i);
+                const float4 y = *reinterpret_cast<const float4*>(p + 8 * i + 4);
+                v[0] += x.x; v[1] += x.y; v[2] += x.z; v[3] += x.w;
+                v[4] += y.x; v[5] += y.y; v[6] += y.z; v[7] += y.w;
+              }
+#pragma unroll
+              for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[j]);
+              st_global_32B(p + 8 * i, w);
+            }
+          } else if (!WGRAD) {
+            uint16_t* p = static_cast<uint16_t*>(args.c) + row_at * args.ld_c + c0;
+#pragma unroll
+            for (int i = 0; i < HALF / 16; ++i) {
+              uint32_t w[8];
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                float x, y;
+                unpair(acc[8 * i + j], x, y);
+                w[j] = pack_bf2(x, y);
+              }
+              st_global_32B(p + 16 * i, w);
+            }
+          }
+        }
+      } else {
+        // rows of any width: 16 columns at a time turned, so that half a warp writes a
+        // row's neighbours
+        const int rows_here = min(32, ti.m1 - ti.m0 - quarter * 32);
+        const int q0 = lane >> 4, c = lane & 15;
+#pragma unroll
+        for (int i = 0; i < HALF / 16; ++i) {
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            float x, y;
+            unpair(acc[8 * i + j], x, y);
+            turn[lane * 17 + 2 * j] = x;
+            turn[lane * 17 + 2 * j + 1] = y;
+          }
+          __syncwarp();
+          if (16 * i + c < n_here) {
+            const long long at0 = (row_at - lane) * args.ld_c + c0 + 16 * i + c;
+            for (int q = q0; q < rows_here; q += 2) {
+              float v = turn[q * 17 + c];
+              const long long at = at0 + q * args.ld_c;
+              if (args.f32) {
+                float* p = static_cast<float*>(args.c) + at;
+                if (WGRAD && args.accumulate) v += *p;
+                *p = v;
+              } else {
+                static_cast<uint16_t*>(args.c)[at] = f2bf(v);
+              }
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+  pdl_trigger();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+template <int BN, bool WGRAD>
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmArgs& a, int grid,
+                   cudaStream_t st) {
+  static std::atomic<unsigned long long> configured{0};
+  const cudaError_t e = smem_optin_once(k_fp8_gemm<BN, WGRAD>, Shape<BN>::SMEM, configured);
+  if (e != cudaSuccess) return e;
+  // the shares above are of what a thread is launched with
+  static std::atomic<int> regs{0};
+  if (!regs.load(std::memory_order_relaxed)) {
+    cudaFuncAttributes at;
+    const cudaError_t q = cudaFuncGetAttributes(&at, k_fp8_gemm<BN, WGRAD>);
+    if (q != cudaSuccess) return q;
+    regs.store(at.numRegs, std::memory_order_relaxed);
+  }
+  if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
+  return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(kThreads), Shape<BN>::SMEM, st, ta, tb,
+                    a);
+}
+
+bool aligned(const void* p, int bytes) {
+  return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(bytes - 1)) == 0;
+}
+
+bool desc_ok(const moe_fp8_gemm_desc* s) {
+  return s && s->N >= 1 && s->N <= MOE_FP8_MAX_WIDTH && s->K >= 1 && s->K <= MOE_FP8_MAX_WIDTH &&
+         s->E >= 1 && s->E <= kMaxSegments &&
+         (s->out_dtype == MOE_DTYPE_BF16 || s->out_dtype == MOE_DTYPE_FP32);
+}
+
+bool codes_ok(const void* p, long long ld, long long width) {
+  return p && aligned(p, 16) && ld >= width && ld % 16 == 0 && ld < (1LL << 39);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+using namespace moe;
+
+extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a, long long ld_a,
+                            const float* a_scales, long long ld_as, const uint8_t* b,
+                            long long ld_b, const float* b_scales, const int32_t* offsets, void* c,
+                            long long ld_c, void* status, void* stream) {
+  if (!desc_ok(s) || M < 0 || (s->E > 1 && !offsets) || !status || !aligned(status, 16))
+    return MOE_ERR_INVALID_ARG;
+  if (M == 0) return MOE_OK;
+  const int es = s->out_dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (!codes_ok(a, ld_a, s->K) || !codes_ok(b, ld_b, s->K) || !a_scales || !b_scales || !c ||
+      ld_as < M || ld_c < s->N || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
+      !aligned(c, es) || !aligned(offsets, 4) || ld_b >= (1LL << 39) / s->N)
+    return MOE_ERR_INVALID_ARG;
+  Fp8GemmArgs g = {};
+  g.M = M; g.N = s->N; g.K = s->K; g.E = s->E;
+  g.sa = a_scales; g.ld_sa = ld_as; g.sb = b_scales;
+  g.offsets = offsets; g.c = c; g.ld_c = ld_c;
+  g.f32 = es == 4;
+  g.wide = aligned(c, 32) && ld_c * es % 32 == 0;
+  g.err = static_cast<DevError*>(status);
+  const bool narrow = s->N <= 128;
+  const long long n_tiles = (s->N + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
+  const long long most = ((M + 127LL * (offsets ? s->E : 1)) / 128) * n_tiles;
+  if (most > (1LL << 30)) return MOE_ERR_INVALID_ARG;
+  CUtensorMap ta, tb;
+  if (encode_tmap_codes(&ta, a, 0, M, s->K, ld_a, 128) != MOE_OK ||
+      encode_tmap_codes(&tb, b, s->E, s->N, s->K, ld_b, narrow ? 128 : 256) != MOE_OK)
+    return MOE_ERR_CUDA;
+  const int grid = (int)(most < num_sms() ? most : num_sms());
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return cuda_result(narrow ? launch<128, false>(ta, tb, g, grid, st)
+                            : launch<256, false>(ta, tb, g, grid, st), "moe_fp8_gemm");
+}
+
+extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const uint8_t* dyt,
+                                  long long ld_dyt, const float* dyt_scales, long long ld_dys,
+                                  const uint8_t* xt, long long ld_xt, const float* xt_scales,
+                                  long long ld_xs, const int32_t* offsets, float* dw,
+                                  int accumulate, void* status, void* stream) {
+  if (!desc_ok(s) || R < 0 || R % 128 || R > 0x7FFFFF80LL || (s->E > 1 && !offsets) || !dw ||
+      !aligned(dw, 4) || !status || !aligned(status, 16))
+    return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (R == 0) {
+    if (accumulate) return MOE_OK;
+    return cuda_result(cudaMemsetAsync(dw, 0, 4ull * s->E * s->N * s->K, st),
+                       "moe_fp8_gemm_wgrad");
+  }
+  if (!codes_ok(dyt, ld_dyt, R) || !codes_ok(xt, ld_xt, R) || !dyt_scales || !xt_scales ||
+      ld_dys < s->N || ld_xs < s->K || !aligned(dyt_scales, 4) || !aligned(xt_scales, 4) ||
+      !aligned(offsets, 4))
+    return MOE_ERR_INVALID_ARG;
+  Fp8GemmArgs g = {};
+  g.N = s->N; g.K = s->K; g.E = s->E;
+  g.sa = dyt_scales; g.ld_sa = ld_dys; g.sb = xt_scales; g.ld_sb = ld_xs;
+  g.offsets = offsets; g.c = dw; g.ld_c = s->K;
+  g.row_blocks = (int)(R / 128);
+  g.f32 = 1;
+  g.accumulate = accumulate != 0;
+  g.wide = aligned(dw, 32) && s->K % 8 == 0;
+  g.err = static_cast<DevError*>(status);
+  const bool narrow = s->K <= 128;
+  const long long tiles = (long long)s->E * ((s->N + 127) / 128) *
+                          ((s->K + (narrow ? 127 : 255)) / (narrow ? 128 : 256));
+  if (tiles > (1LL << 30)) return MOE_ERR_INVALID_ARG;
+  CUtensorMap ta, tb;
+  if (encode_tmap_codes(&ta, dyt, 0, s->N, R, ld_dyt, 128) != MOE_OK ||
+      encode_tmap_codes(&tb, xt, 0, s->K, R, ld_xt, narrow ? 128 : 256) != MOE_OK)
+    return MOE_ERR_CUDA;
+  const int grid = (int)(tiles < num_sms() ? tiles : num_sms());
+  return cuda_result(narrow ? launch<128, true>(ta, tb, g, grid, st)
+                            : launch<256, true>(ta, tb, g, grid, st), "moe_fp8_gemm_wgrad");
+}
+
+extern "C" int moe_fp8_check(void* status, int* where) {
+  if (!status) return MOE_ERR_INVALID_ARG;
+  DevError e;
+  cudaError_t rc = cudaDeviceSynchronize();
+  if (rc == cudaSuccess) rc = cudaMemcpy(&e, status, sizeof e, cudaMemcpyDeviceToHost);
+  if (rc == cudaSuccess && e.code) rc = cudaMemset(status, 0, sizeof e);
+  if (rc != cudaSuccess) return cuda_result(rc, "moe_fp8_check");
+  if (where) *where = e.where;
+  return e.code;
+}

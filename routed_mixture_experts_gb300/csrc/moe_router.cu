@@ -52,6 +52,8 @@ struct RouterArgs {
   const float* d_scores;
   const float* d_losses;
   void* d_logits;  long long ld_d;
+  // choice within groups of neighbouring experts
+  int groups, top_groups, group_size, pair;
 };
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -108,7 +110,220 @@ __device__ __forceinline__ void write_losses(const RouterArgs& a, float balance,
   a.losses[1] = z / n;
 }
 
-// Forward.  L = logits type, NV = slots of 32 experts.
+// ---- the choice within groups ---------------------------------------------------
+//
+// key = s + bias, s = sigmoid(l) or softmax(l); a group's value is the sum of its two
+// largest keys (or the largest); the experts of the top_groups best groups compete.  The
+// order is that of the exact keys: keys are computed in fp32 with an error below
+// key_error(), and where two that the choice separates, or orders, lie closer, the row is
+// chosen again on 64-bit keys (choose_slowly).  Without a bias the logits themselves order
+// the experts, and the groups too where a group's value is its largest key.
+
+struct GroupRow {
+  float* key;                        // [NV * 32] keys by expert, NaN as -inf
+  float* value;                      // [256] of the groups
+  uint32_t* kept;                    // [8] bit g: group g competes
+};
+
+// How close two fp32 keys, or sums of two, may come without their order being known.  The
+// error of s: sigmoid, expf's 2^-23 of e^-l is at most 2^-25, the sum's and the quotient's
+// roundings less than 2^-23; softmax, the same relative to s, plus the rounding of l - max
+// (D 2^-24 of a weight e^-D) and the total's, together below 2^-20 of the largest s.  Adding
+// biases up to `wide` and two keys: 2^-24 of at most twice (1 + wide) each.  Four keys are
+// compared.
+__device__ __forceinline__ float key_error(bool sig, float largest, float wide) {
+  return (sig ? 0x1p-19f : 0x1p-18f * largest) + 0x1p-20f * wide;
+}
+
+__device__ __forceinline__ uint64_t order_key64(double v) {
+  const uint64_t b = (uint64_t)__double_as_longlong(v + 0.0);
+  const uint64_t key = b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
+  return v != v ? 1ull : key;
+}
+__device__ __forceinline__ double order_value64(uint64_t key) {
+  return __longlong_as_double(
+      (long long)((key >> 63) ? key & 0x7FFFFFFFFFFFFFFFull : ~key));
+}
+__device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
+  const uint32_t hi = __reduce_max_sync(kAll, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(kAll, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((uint64_t)hi << 32) | lo;
+}
+
+// The choice of one row on 64-bit keys, by one warp (logits by expert in shared memory).
+template <int NV>
+__device__ __noinline__ void choose_slowly(const RouterArgs& a, const float* logits,
+                                           uint32_t* kept, uint8_t* chosen) {
+  const int lane = threadIdx.x & 31, E = a.E;
+  const bool sig = a.scoring == MOE_ROUTER_SIGMOID;
+  float mx = -INFINITY;
+  for (int e = lane; e < E; e += 32) mx = fmaxf(mx, logits[e]);
+  mx = warp_max(mx);
+  double w[NV], total = 0.0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    w[i] = 0.0;
+    if (e < E) w[i] = sig ? 1.0 / (1.0 + exp(-(double)logits[e])) : exp((double)logits[e] - mx);
+    total += w[i];
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  uint64_t key[NV];
+  int group[NV];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i;
+    key[i] = 0;
+    group[i] = e < E ? e / a.group_size : -1;
+    if (e < E) {
+      const double s = sig ? w[i] : w[i] / total;
+      const double v = logits[e] == -INFINITY ? -INFINITY : a.bias ? s + (double)a.bias[e] : s;
+      key[i] = order_key64(v);
+    }
+  }
+  const uint64_t none = order_key64(-INFINITY);
+  if (a.top_groups < a.groups) {
+    uint64_t value[8];                       // of group lane + 32 i
+#pragma unroll
+    for (int i = 0; i < 8; ++i) value[i] = 0;
+    for (int g = 0; g < a.groups; ++g) {
+      uint64_t best = 0;
+      int at = -1;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (group[i] == g && key[i] > best) {
+          best = key[i];
+          at = i;
+        }
+      const uint64_t first = warp_max64(best);
+      uint64_t v = first < none ? none : first;       // NaN counts as -inf
+      if (a.pair) {
+        const unsigned has = __ballot_sync(kAll, at >= 0 && best == first);
+        const bool mine = has && lane == __ffs(has) - 1;
+        best = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (group[i] == g && !(mine && i == at)) best = max(best, key[i]);
+        const uint64_t second = warp_max64(best);
+        if (second > none && v > none)
+          v = order_key64(order_value64(v) + order_value64(second));
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (g == lane + 32 * i) value[i] = v;
+    }
+    __syncwarp();
+    if (lane < 8) kept[lane] = 0;
+    __syncwarp();
+    for (int j = 0; j < a.top_groups; ++j) {
+      uint64_t best = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) best = max(best, value[i]);
+      const uint64_t top = warp_max64(best);
+      bool open = true;
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        if (open) {
+          const unsigned has = __ballot_sync(kAll, value[i] == top);
+          if (has) {
+            if (lane == __ffs(has) - 1) {
+              value[i] = 0;
+              kept[i] |= 1u << lane;
+            }
+            open = false;
+          }
+        }
+      __syncwarp();
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (group[i] >= 0 && !((kept[group[i] >> 5] >> (group[i] & 31)) & 1u)) key[i] = 0;
+  }
+  if (!a.bias)           // the logits have the order, and ties, that their scores round away
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (key[i]) key[i] = order_key(logits[lane + 32 * i]);
+  for (int j = 0; j < a.k; ++j) {
+    uint64_t best = 0;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) best = max(best, key[i]);
+    const uint64_t top = warp_max64(best);
+    bool open = true;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (open) {
+        const unsigned has = __ballot_sync(kAll, key[i] == top);
+        if (has) {
+          if (lane == __ffs(has) - 1) {
+            key[i] = 0;
+            chosen[j] = (uint8_t)(32 * i + lane);
+          }
+          open = false;
+        }
+      }
+  }
+  __syncwarp();
+}
+
+// Which groups compete (row.kept), from the keys in shared memory.  Several lanes share a
+// group, from places that differ by group so that they do not meet in a bank.  Returns
+// whether the last group in and the first one out are too close to tell.
+__device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRow& row, bool exact,
+                                              float error) {
+  const int lane = threadIdx.x & 31, G = a.groups, size = a.group_size;
+  int share = 1;                             // lanes a group
+  while (2 * share * G <= 32 && 2 * share <= size) share *= 2;
+  const int per = (size + share - 1) / share, at_once = 32 / share;
+  for (int g0 = 0; g0 < G; g0 += at_once) {
+    const int g = g0 + lane / share, q = lane % share;
+    float first = -INFINITY, second = -INFINITY;
+    if (g < G) {
+      int j = g % per;
+      for (int n = 0; n < per; ++n) {
+        const int i = q + share * j;
+        const float v = i < size ? row.key[g * size + i] : -INFINITY;
+        second = fmaxf(second, fminf(first, v));
+        first = fmaxf(first, v);
+        if (++j == per) j = 0;
+      }
+    }
+    for (int o = share >> 1; o > 0; o >>= 1) {
+      const float f = __shfl_xor_sync(kAll, first, o), s = __shfl_xor_sync(kAll, second, o);
+      second = fmaxf(fminf(first, f), fmaxf(second, s));
+      first = fmaxf(first, f);
+    }
+    if (g < G && q == 0)
+      row.value[g] = a.pair && second > -INFINITY ? first + second : first;
+  }
+  __syncwarp();
+  uint32_t low = 0xFFFFFFFFu, high = 0u;     // of those that stay, of those that do not
+  for (int g0 = 0; g0 < G; g0 += 32) {
+    const int g = g0 + lane;
+    bool stays = false;
+    if (g < G) {
+      const float v = row.value[g];
+      int ahead = 0;
+      for (int h = 0; h < G; ++h) {
+        const float w = row.value[h];
+        ahead += (w > v || (w == v && h < g)) ? 1 : 0;
+      }
+      stays = ahead < a.top_groups;
+      const uint32_t k = order_key(v);
+      if (stays) low = min(low, k); else high = max(high, k);
+    }
+    const unsigned word = __ballot_sync(kAll, stays);
+    if (lane == 0) row.kept[g0 >> 5] = word;
+  }
+  low = __reduce_min_sync(kAll, low);
+  high = __reduce_max_sync(kAll, high);
+  __syncwarp();
+  if (exact) return false;
+  const float in = order_value(low), out = order_value(high);
+  return in - out <= error;                             // infinities: NaN, not close
+}
+
+// Forward.  L = logits type, NV = slots of 32 experts, GROUPS: the choice within groups.
 //
 // One pass over the logits: 4 E bytes a row in, 8 k out, next to nothing for the
 // memory (8192 rows of 128 fp32 logits, 4.75 MB: 0.7 us).  What bounds it is the chain of
@@ -120,16 +335,19 @@ __device__ __forceinline__ void write_losses(const RouterArgs& a, float balance,
 // results do not depend on the order in which warps run.
 // Measured, both launches: one token 3.5 us, 8192 rows of 128 experts (k = 8) 11.4, 16411
 // rows of 250 bf16 logits (k = 6, sigmoid, bias, 2048 rows masked) 19.6.
-template <typename L, int NV>
+template <typename L, int NV, bool GROUPS>
 __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
-  extern __shared__ float psum[];                 // [warps][NV * 32]
+  extern __shared__ float psum[];                 // [warps][NV * 32], GROUPS: and the keys
   __shared__ int cnt[kMaxE];
   __shared__ uint8_t sel_id[32][kMaxE];           // a warp's chosen experts, in order
   __shared__ float wz[32];
   __shared__ int wlive[32];
+  __shared__ uint32_t kept[GROUPS ? 32 : 1][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int E = a.E, k = a.k;
   float* const mine = psum + warp * (NV * 32);    // first the row's logits, by expert
+  float* const keys = GROUPS ? psum + (nw + warp) * (NV * 32) : nullptr;
+  float* const values = GROUPS ? psum + 2 * nw * (NV * 32) + warp * a.groups : nullptr;
   for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   pdl_wait();
@@ -140,6 +358,12 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
   float bias[NV];
 #pragma unroll
   for (int i = 0; i < NV; ++i) bias[i] = a.bias && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
+  float wide = 0.f;                               // the largest bias
+  if (GROUPS) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) wide = fmaxf(wide, fabsf(bias[i]));
+    wide = warp_max(wide);
+  }
   float z = 0.f;
   int live_rows = 0;
   for (long long t = (long long)blockIdx.x * nw + warp; t < a.T; t += (long long)gridDim.x * nw) {
@@ -172,9 +396,55 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
       mx = fmaxf(mx, l[i]);
       nan |= l[i] != l[i];
     }
+    int count = k;
+    bool close = false;
+    float error = 0.f;
+    if (GROUPS) {
+      mx = warp_max(mx);
+      float largest = 0.f;
+      const bool keyed = a.bias != nullptr;
+      if (keyed || a.pair) {
+        // fp32 keys of scores
+        float s[NV], sum = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const float x = expf(sig ? -l[i] : l[i] - mx);
+          s[i] = sig ? __fdiv_rn(1.f, 1.f + x) : lane + 32 * i < E ? x : 0.f;
+          sum += s[i];
+        }
+        if (!sig) {
+          sum = warp_sum(sum);
+          largest = 1.f / sum;
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int e = lane + 32 * i;
+          if (!sig) s[i] = __fdiv_rn(s[i], sum);
+          const float v = l[i] == -INFINITY ? -INFINITY : s[i] + bias[i];
+          if (keyed) key[i] = e < E ? order_key(v) : 0u;
+          keys[e] = v == v ? v : -INFINITY;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) keys[lane + 32 * i] = l[i] == l[i] ? l[i] : -INFINITY;
+      }
+      __syncwarp();
+      error = key_error(sig, largest, wide);
+      if (a.top_groups < a.groups) {
+        const GroupRow row = {keys, values, kept[warp]};
+        close = choose_groups(a, row, !keyed && !a.pair, error);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int g = (lane + 32 * i) / a.group_size;
+          if (lane + 32 * i < E && !((kept[warp][g >> 5] >> (g & 31)) & 1u)) key[i] = 0u;
+        }
+      }
+      // the next one too, to see how close it comes
+      if (keyed && k < a.top_groups * a.group_size) count = k + 1;
+    }
     // the largest key k times; slots are searched in order and lanes within a slot,
     // so equal keys go to the lowest expert.  A chosen key becomes 0.
-    for (int j = 0; j < k; ++j) {
+    for (int j = 0; j < count; ++j) {
       uint32_t best = key[0];
 #pragma unroll
       for (int i = 1; i < NV; ++i) best = max(best, key[i]);
@@ -193,6 +463,21 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
             open = false;
           }
         }
+    }
+    if (GROUPS && !close && a.bias) {
+      __syncwarp();
+      for (int j = lane; j + 1 < count; j += 32) {
+        const int e = sel_id[warp][j], f = sel_id[warp][j + 1];
+        // equal logits and biases are a tie in any arithmetic
+        if (keys[e] - keys[f] <= error &&
+            !(mine[e] == mine[f] && a.bias[e] == a.bias[f]))
+          close = true;
+      }
+      close = __any_sync(kAll, close);
+    }
+    if (GROUPS && close) {
+      __syncwarp();
+      choose_slowly<NV>(a, mine, kept[warp], sel_id[warp]);
     }
     mx = warp_max(mx);
     nan = __any_sync(kAll, nan);
@@ -226,7 +511,7 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     // them, and its shift serves.
     float ctop = top, cinv = inv;
     if (a.scoring != MOE_ROUTER_SOFTMAX) {
-      if (a.bias) {
+      if (GROUPS || a.bias) {
         float m = -INFINITY;
         for (int j = lane; j < k; j += 32) m = fmaxf(m, mine[sel_id[warp][j]]);
         ctop = warp_max(m);
@@ -495,23 +780,27 @@ int forward_grid(int T) {
   return want < cap ? want : cap;
 }
 
-template <typename L, int NV>
+template <typename L, int NV, bool GROUPS>
 cudaError_t launch_forward_nv(const RouterArgs& a, int grid, cudaStream_t st) {
-  const int warps = forward_warps(a.T, grid), smem = warps * NV * 32 * (int)sizeof(float);
+  const int warps = forward_warps(a.T, grid);
+  // with groups: the keys too, and the groups' values (256 at most)
+  const int a_warp = GROUPS ? 2 * NV * 32 + a.groups : NV * 32;
+  constexpr int most = 32 * (GROUPS ? 2 * NV * 32 + kMaxE : NV * 32) * (int)sizeof(float);
   static std::atomic<unsigned long long> done{0};
-  const cudaError_t e = smem_optin_once(k_router<L, NV>, 32 * NV * 32 * (int)sizeof(float), done);
+  const cudaError_t e = smem_optin_once(k_router<L, NV, GROUPS>, most, done);
   if (e != cudaSuccess) return e;
-  return launch_pdl(k_router<L, NV>, dim3(grid), dim3(warps * 32), smem, st, a);
+  return launch_pdl(k_router<L, NV, GROUPS>, dim3(grid), dim3(warps * 32),
+                    warps * a_warp * (int)sizeof(float), st, a);
 }
 
-template <typename L>
+template <typename L, bool GROUPS>
 cudaError_t launch_forward(const RouterArgs& a, int grid, cudaStream_t st) {
   switch ((a.E + 31) / 32) {
-    case 1: return launch_forward_nv<L, 1>(a, grid, st);
-    case 2: return launch_forward_nv<L, 2>(a, grid, st);
-    case 3: return launch_forward_nv<L, 3>(a, grid, st);
-    case 4: return launch_forward_nv<L, 4>(a, grid, st);
-    default: return launch_forward_nv<L, 8>(a, grid, st);
+    case 1: return launch_forward_nv<L, 1, GROUPS>(a, grid, st);
+    case 2: return launch_forward_nv<L, 2, GROUPS>(a, grid, st);
+    case 3: return launch_forward_nv<L, 3, GROUPS>(a, grid, st);
+    case 4: return launch_forward_nv<L, 4, GROUPS>(a, grid, st);
+    default: return launch_forward_nv<L, 8, GROUPS>(a, grid, st);
   }
 }
 
@@ -571,11 +860,15 @@ extern "C" size_t moe_router_workspace_bytes(const moe_router_desc* s, int T) {
   return (size_t)forward_grid(T) * (2 * s->E + 2) * 4;
 }
 
-extern "C" int moe_router_forward(const moe_router_desc* s, int T, const void* logits,
-                                  long long ld, const float* bias, const uint8_t* token_mask,
-                                  int32_t* ids, float* scores, int32_t* counts, float* prob_sum,
-                                  float* losses, float* row_stat, void* workspace,
-                                  size_t workspace_bytes, void* stream) {
+namespace moe {
+
+namespace {
+
+// Both forwards; g: the choice within groups (NULL: among all experts).
+int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, const void* logits, long long ld, const float* bias,
+            const uint8_t* token_mask, int32_t* ids, float* scores, int32_t* counts,
+            float* prob_sum, float* losses, float* row_stat, void* workspace,
+            size_t workspace_bytes, void* stream) {
   if (!sizes_ok(s, T) || !counts || !prob_sum || !losses) return MOE_ERR_INVALID_ARG;
   const int es = s->dtype == MOE_DTYPE_FP32 ? 4 : 2;
   if (T > 0 && (!logits || ld < s->E || !ids || !scores || !row_stat || !aligned(logits, es)))
@@ -598,10 +891,79 @@ extern "C" int moe_router_forward(const moe_router_desc* s, int T, const void* l
     a.n_part = grid;
   }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  cudaError_t e = s->dtype == MOE_DTYPE_FP32 ? launch_forward<float>(a, grid, st)
-                                             : launch_forward<uint16_t>(a, grid, st);
+  const bool f32 = s->dtype == MOE_DTYPE_FP32;
+  cudaError_t e;
+  if (g) {
+    a.groups = g->groups; a.top_groups = g->top_groups; a.group_size = s->E / g->groups;
+    a.pair = g->group_score == MOE_GROUP_TOP2 && a.group_size > 1;
+    e = f32 ? launch_forward<float, true>(a, grid, st) : launch_forward<uint16_t, true>(a, grid, st);
+  } else {
+    e = f32 ? launch_forward<float, false>(a, grid, st)
+            : launch_forward<uint16_t, false>(a, grid, st);
+  }
   if (e == cudaSuccess && a.part_prob) e = launch_finish(a, st);
-  return cuda_result(e, "moe_router_forward");
+  return cuda_result(e, g ? "moe_group_router_forward" : "moe_router_forward");
+}
+
+// Adds `rate` to the biases of experts chosen less than the mean, subtracts it from those
+// chosen more.  One warp; counts are whole numbers, so the comparison is exact.
+__global__ void k_router_bias(float* bias, const int32_t* counts, int E, float rate) {
+  pdl_wait();
+  const int lane = threadIdx.x;
+  long long total = 0;
+  for (int e = lane; e < E; e += 32) total += counts[e];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(kAll, total, o);
+  for (int e = lane; e < E; e += 32) {
+    const long long mine = (long long)counts[e] * E;
+    if (mine != total) bias[e] += mine < total ? rate : -rate;
+  }
+  pdl_trigger();
+}
+
+bool group_desc_ok(const moe_group_router_desc* g) {
+  return g && desc_ok(&g->router) && g->groups >= 1 && g->router.E % g->groups == 0 &&
+         g->top_groups >= 1 && g->top_groups <= g->groups &&
+         g->router.k <= g->top_groups * (g->router.E / g->groups) &&
+         (g->group_score == MOE_GROUP_MAX || g->group_score == MOE_GROUP_TOP2);
+}
+
+}  // namespace
+
+}  // namespace moe
+
+extern "C" int moe_router_forward(const moe_router_desc* s, int T, const void* logits,
+                                  long long ld, const float* bias, const uint8_t* token_mask,
+                                  int32_t* ids, float* scores, int32_t* counts, float* prob_sum,
+                                  float* losses, float* row_stat, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+  return forward(s, nullptr, T, logits, ld, bias, token_mask, ids, scores, counts, prob_sum,
+                 losses, row_stat, workspace, workspace_bytes, stream);
+}
+
+extern "C" size_t moe_group_router_workspace_bytes(const moe_group_router_desc* g, int T) {
+  return group_desc_ok(g) ? moe_router_workspace_bytes(&g->router, T) : 0;
+}
+
+extern "C" int moe_group_router_forward(const moe_group_router_desc* g, int T, const void* logits,
+                                        long long ld, const float* bias,
+                                        const uint8_t* token_mask, int32_t* ids, float* scores,
+                                        int32_t* counts, float* prob_sum, float* losses,
+                                        float* row_stat, void* workspace, size_t workspace_bytes,
+                                        void* stream) {
+  if (!group_desc_ok(g)) return MOE_ERR_INVALID_ARG;
+  return forward(&g->router, g, T, logits, ld, bias, token_mask, ids, scores, counts, prob_sum,
+                 losses, row_stat, workspace, workspace_bytes, stream);
+}
+
+extern "C" int moe_router_update_bias(float* bias, const int32_t* counts, int E, float rate,
+                                      void* stream) {
+  if (!bias || !counts || E < 1 || E > kMaxE || !std::isfinite(rate) || !aligned(bias, 4) ||
+      !aligned(counts, 4))
+    return MOE_ERR_INVALID_ARG;
+  return cuda_result(launch_pdl(k_router_bias, dim3(1), dim3(32), 0,
+                                static_cast<cudaStream_t>(stream), bias, counts, E, rate),
+                     "moe_router_update_bias");
 }
 
 extern "C" int moe_router_backward(const moe_router_desc* s, int T, const void* logits,
