@@ -20,7 +20,7 @@ namespace moe {
 
 namespace {
 
-// warp 0 copies, warp 1 MMA (2, 3 idle), warps 4..11 sums.  A third of the launch's 168
+// warp 0 copies codes, warp 1 MMA, warp 2 copies scales (3 idle), warps 4..11 sums.  A third of the launch's 168
 // registers a thread goes from the first four warps to the others, which hold 128 sums.
 constexpr int kThreads = 384;
 constexpr int kEpiWarps = 8;
@@ -85,13 +85,21 @@ __device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
-template <int BN>
+// Asynchronous copy of 4 bytes into shared memory, zero where `there` is false.
+__device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
+  const int n = there ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n)
+               : "memory");
+}
+
+template <int BN, bool WGRAD>
 struct Shape {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TURN = kEpiWarps * 32 * 17 * 4;       // narrow stores, a warp 32 x 16
-  static constexpr int SCALES = kEpiWarps * 2 * (BN / 2) * 4;   // weights: scales of columns
-  static constexpr int REST = TURN + SCALES + 512;
+  // scales of a block: 128 rows', then (weights) BN columns' or the two weight blocks'
+  static constexpr int SLOTS = 8, SLOT = 512 + (WGRAD ? BN * 4 : 16);
+  static constexpr int REST = TURN + SLOTS * SLOT + 512;
   static constexpr int FIT = (226 * 1024 - 3584 - REST) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
   static constexpr int SMEM = STAGES * STAGE + REST + 1024;
@@ -140,8 +148,8 @@ template <int BN, bool WGRAD>
 __global__ void __launch_bounds__(kThreads, 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                const Fp8GemmArgs args) {
-  using S = Shape<BN>;
-  constexpr int STAGES = S::STAGES, NBUF = S::NBUF, HALF = BN / 2;
+  using S = Shape<BN, WGRAD>;
+  constexpr int STAGES = S::STAGES, NBUF = S::NBUF, SLOTS = S::SLOTS, HALF = BN / 2;
   static_assert(S::SMEM + 3584 <= 232448, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Segments seg;
@@ -151,14 +159,16 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   float* const turn_all = reinterpret_cast<float*>(smem + STAGES * S::STAGE);
-  float* const scales_all = turn_all + S::TURN / 4;
-  const uint32_t bar0 = smem_u32(scales_all + S::SCALES / 4);
+  float* const slots = turn_all + S::TURN / 4;
+  const uint32_t bar0 = smem_u32(slots + SLOTS * S::SLOT / 4);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
   auto tfull_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + b); };
   auto tempty_bar = [&](int b) { return bar0 + 8u * (2 * STAGES + NBUF + b); };
   const uint32_t drain_bar = bar0 + 8u * (2 * STAGES + 2 * NBUF);
-  static_assert(8 * (2 * STAGES + 2 * NBUF + 1) <= 512, "barriers");
+  auto sfull_bar = [&](int s) { return drain_bar + 8u * (1 + s); };
+  auto sempty_bar = [&](int s) { return drain_bar + 8u * (1 + SLOTS + s); };
+  static_assert(8 * (2 * STAGES + 2 * NBUF + 1 + 2 * SLOTS) <= 512, "barriers");
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
@@ -172,6 +182,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(tempty_bar(b), kEpiWarps);
     }
     mbar_init(drain_bar, 1);
+    for (int s = 0; s < SLOTS; ++s) {
+      mbar_init(sfull_bar(s), 32);
+      mbar_init(sempty_bar(s), kEpiWarps);
+    }
     fence_mbar_init();
     tma_prefetch_desc(&tmA);
     tma_prefetch_desc(&tmB);
@@ -282,6 +296,48 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- scales of a block, as far ahead as there are slots ----------------
+    const int nb_all = (args.N + 127) >> 7, k_blocks = (args.K + 127) >> 7;
+    int slot = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
+      const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+      const float* const pb = WGRAD ? args.sb + ti.n0
+                                    : args.sb + ((long long)ti.e * nb_all + (ti.n0 >> 7)) * k_blocks;
+      for (int b = ti.b0; b < ti.b1; ++b) {
+        ok = mbar_wait(sempty_bar(slot), phase ^ 1u, &abort_s, args.err, 6);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint32_t to = smem_u32(slots) + slot * S::SLOT;
+        const float* const pa = args.sa + b * args.ld_sa + ti.m0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 32 * i + lane;
+          const bool there = ti.m0 + r < ti.m1;
+          copy4(to + 4 * r, pa + (there ? r : 0), there);
+        }
+        if (WGRAD) {
+#pragma unroll
+          for (int i = 0; i < BN / 32; ++i) {
+            const int c = 32 * i + lane;
+            const bool there = ti.n0 + c < args.K;
+            copy4(to + 512 + 4 * c, pb + b * args.ld_sb + (there ? c : 0), there);
+          }
+        } else if (lane < BN / 128) {
+          const bool there = (ti.n0 >> 7) + lane < nb_all;
+          copy4(to + 512 + 4 * lane, pb + b + (there ? lane * k_blocks : 0), there);
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull_bar(slot))
+                     : "memory");
+        if (++slot == SLOTS) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      }
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSumRegs));
@@ -289,11 +345,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int quarter = warp & 3, half = (warp - 4) >> 2;
     const int row = quarter * 32 + lane;
     float* const turn = turn_all + (warp - 4) * 32 * 17;
-    float* const col_scale = scales_all + (warp - 4) * 2 * HALF;
     const uint32_t lane_base = tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(half * HALF);
-    const int k_blocks = (args.K + 127) >> 7, nb_all = (args.N + 127) >> 7;
-    int buf = 0;
-    uint32_t buf_phase = 0;
+    int buf = 0, slot = 0;
+    uint32_t buf_phase = 0, slot_phase = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
       const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
@@ -303,38 +357,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[HALF / 2];
 #pragma unroll
       for (int i = 0; i < HALF / 2; ++i) acc[i] = 0;
-      // scales of the next block: of this thread's row, and of the weights' block or of
-      // this warp's columns
-      const float* pa = args.sa + r;
-      const float* pb =
-          WGRAD ? args.sb + c0
-                : args.sb + ((long long)ti.e * nb_all + min(c0 >> 7, nb_all - 1)) * k_blocks;
-      float sa = 0.f, sb[WGRAD ? HALF / 32 : 1];
-      auto fetch = [&](int b) {
-        sa = row_in && b < ti.b1 ? __ldg(pa + b * args.ld_sa) : 0.f;
-        if (WGRAD) {
-#pragma unroll
-          for (int i = 0; i < HALF / 32; ++i)
-            sb[i] = b < ti.b1 && c0 + lane + 32 * i < n_all
-                        ? __ldg(pb + b * args.ld_sb + lane + 32 * i) : 0.f;
-        } else {
-          sb[0] = b < ti.b1 ? __ldg(pb + b) : 0.f;
-        }
-      };
-      fetch(ti.b0);
       for (int b = ti.b0; b < ti.b1; ++b) {
-        float s = sa;
-        const float* cs = col_scale + (b & 1) * HALF;
-        if (WGRAD) {
-#pragma unroll
-          for (int i = 0; i < HALF / 32; ++i) col_scale[(b & 1) * HALF + lane + 32 * i] = sb[i];
+        ok = mbar_wait(sfull_bar(slot), slot_phase, &abort_s, args.err, 7);
+        const float* const sc = slots + slot * (S::SLOT / 4);
+        float s = sc[row];
+        const float* const cs = sc + 128 + half * HALF;          // weights: of the columns
+        if (!WGRAD) {
+          s *= sc[128 + (half * HALF >> 7)];
           __syncwarp();
-        } else {
-          s *= sb[0];
+          if (lane == 0) mbar_arrive(sempty_bar(slot));
         }
-        fetch(b + 1);
         const uint64_t s2 = pair(s, s);
-        ok = mbar_wait(tfull_bar(buf), buf_phase, &abort_s, args.err, 5);
+        ok = mbar_wait(tfull_bar(buf), buf_phase, &abort_s, args.err, 5) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -351,15 +385,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(tempty_bar(buf));
           }
+          uint64_t cq[WGRAD ? 8 : 1];
+          if (WGRAD) {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float4 q = *reinterpret_cast<const float4*>(cs + 16 * i + 4 * j);
+              cq[2 * j] = pair(q.x, q.y);
+              cq[2 * j + 1] = pair(q.z, q.w);
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint64_t v = pair_u(d[i & 1][2 * j], d[i & 1][2 * j + 1]);
-            if (WGRAD) {
-              const float2 q = *reinterpret_cast<const float2*>(cs + 16 * i + 2 * j);
-              v = mul2(v, pair(q.x, q.y));
-            }
+            if (WGRAD) v = mul2(v, cq[j]);
             acc[8 * i + j] = fma2(v, s2, acc[8 * i + j]);
           }
+        }
+        if (WGRAD) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sempty_bar(slot));
+        }
+        if (++slot == SLOTS) {
+          slot = 0;
+          slot_phase ^= 1u;
         }
         if (++buf == NBUF) {
           buf = 0;
@@ -454,7 +502,7 @@ template <int BN, bool WGRAD>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmArgs& a, int grid,
                    cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};
-  const cudaError_t e = smem_optin_once(k_fp8_gemm<BN, WGRAD>, Shape<BN>::SMEM, configured);
+  const cudaError_t e = smem_optin_once(k_fp8_gemm<BN, WGRAD>, (Shape<BN, WGRAD>::SMEM), configured);
   if (e != cudaSuccess) return e;
   // the shares above are of what a thread is launched with
   static std::atomic<int> regs{0};
@@ -465,7 +513,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmAr
     regs.store(at.numRegs, std::memory_order_relaxed);
   }
   if (regs.load(std::memory_order_relaxed) != kLaunchRegs) return cudaErrorInvalidConfiguration;
-  return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(kThreads), Shape<BN>::SMEM, st, ta, tb,
+  return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(kThreads), (Shape<BN, WGRAD>::SMEM), st, ta, tb,
                     a);
 }
 

@@ -17,6 +17,7 @@
 // the column group, so that neither the writes nor the 16-byte reads meet in a bank.
 
 #include <cmath>
+#include <type_traits>
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
@@ -30,22 +31,24 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr unsigned kAll = 0xffffffffu;
+constexpr long long kMaxApart = 0x7FFFFFF0;      // elements between rows
 
 struct QuantArgs {
   int M, C, width;             // rows, columns of the source's operand, columns of v
   int E;
   float clamp;
   int pow2;
-  const void* x;  long long ld_x;  int x_rows;
-  const void* dh;  long long ld_dh;
+  const void* x;  int ld_x;  int x_rows;
+  const void* dh;  int ld_dh;
   const int32_t* rows;         // source row of each row, or NULL
   const int32_t* offsets;      // [E+1] or NULL
-  uint8_t* codes;  long long ld_codes;
+  uint8_t* codes;  int ld_codes;
   float* scales;  long long ld_scales;
-  uint8_t* codes_t;  long long ld_codes_t;
+  uint8_t* codes_t;  int ld_codes_t;
   float* scales_t;  long long ld_scales_t;
   int row_blocks;              // blocks of 128 rows (with offsets: at most)
   int col_blocks;
+  int run, runs, run_blocks;   // column blocks of a unit, units and column blocks a row block
 };
 
 template <typename T> __device__ __forceinline__ float to_f32(T v);
@@ -143,22 +146,45 @@ __device__ __forceinline__ void source4(const QuantArgs& a, long long row, int c
   }
 }
 
-// scale and factor of a block from the bits of its largest magnitude
+// scale = top / 448 and factor = 448 / top of a block from the bits of its largest
+// magnitude.  On the significand x in [1, 2): a quotient from an approximate reciprocal,
+// corrected by its remainder (Markstein's method), which for all 2^23 significands, and a
+// reciprocal off by up to two units in the last place before its Newton step, is the
+// quotient rounded to nearest.  (Two fp32 divisions took 120 issue slots a warp.)
 __device__ __forceinline__ void block_scale(uint32_t bits, int pow2, float& scale, float& factor) {
-  const float top = __uint_as_float(max(bits, 0x0D800000u));           // 2^-100
-  scale = __fdiv_rn(top, 448.f);
-  if (pow2 && top <= 3.402823466e38f) {
-    const uint32_t b = __float_as_uint(scale);
-    const uint32_t up = ((b + 0x7FFFFFu) & 0x7F800000u);               // the power at or above
-    scale = __uint_as_float(up);
-    factor = __uint_as_float(0x7F000000u - up);                        // 2^-e
-  } else {
-    factor = __fdiv_rn(448.f, top);
+  const uint32_t b = max(bits, 0x0D800000u), e = b & 0x7F800000u;      // 2^-100 at least
+  const float x = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
+  float q = x * (1.f / 448.f);
+  q = __fmaf_rn(__fmaf_rn(-q, 448.f, x), 1.f / 448.f, q);
+  float y = __fdividef(1.f, x);
+  y = __fmaf_rn(__fmaf_rn(-x, y, 1.f), y, y);
+  float p = 448.f * y;
+  p = __fmaf_rn(__fmaf_rn(-p, x, 448.f), y, p);
+  uint32_t s = __float_as_uint(q) + (e - 0x3F800000u);
+  uint32_t f = __float_as_uint(p) - (e - 0x3F800000u);
+  if (pow2) {
+    s = (s + 0x7FFFFFu) & 0x7F800000u;                                 // the power at or above
+    f = 0x7F000000u - s;                                               // its inverse
   }
+  if (e == 0x7F800000u) {                                              // infinity or NaN
+    s = b;
+    f = b == e ? 0u : b;
+  }
+  scale = __uint_as_float(s);
+  factor = __uint_as_float(f);
 }
 
+// Four codes, a in the lowest byte.  (Packed inside the statement: through 16-bit values the
+// compiler clears and shifts each half.)
 __device__ __forceinline__ uint32_t codes4(float a, float b, float c, float d) {
-  return (uint32_t)cvt_e4m3x2(a, b) | ((uint32_t)cvt_e4m3x2(c, d) << 16);
+  uint32_t r;
+  asm("{\n\t.reg .b16 lo, hi;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 lo, %2, %1;\n\t"
+      "cvt.rn.satfinite.e4m3x2.f32 hi, %4, %3;\n\t"
+      "mov.b32 %0, {lo, hi};\n\t}"
+      : "=r"(r)
+      : "f"(a), "f"(b), "f"(c), "f"(d));
+  return r;
 }
 
 __device__ __forceinline__ uint32_t magnitude(float v) { return __float_as_uint(v) & 0x7FFFFFFFu; }
@@ -175,12 +201,114 @@ __device__ __forceinline__ void store_codes16(uint8_t* p, const uint4& v, int n)
   }
 }
 
-// SRC: what v is.  BLOCKS: one scale a tile (weights, E matrices of M rows); else one a
+// ---- a thread's share of a tile: rows 8 warp .. 8 warp + 7, columns col .. col + 3 ----
+
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& a, float& b) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// Asynchronous copy of BYTES (8 or 16) into shared memory, zeros where `there` is false.
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES)
+               : "memory");
+}
+template <int BYTES>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+  const int n = there ? BYTES : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES),
+               "r"(n)
+               : "memory");
+}
+
+// A run of column blocks of one row block, the unit that CTAs take in turn, and the block
+// of it that is at hand.
+struct Place {
+  int unit;
+  int cb, cb_end;      // column block, end of the run
+  int rb, e;           // row block, matrix or segment
+  int row0, rows;      // first row of this warp's eight, how many of them are there
+  int source;          // source row of row `lane` of them (-1: none)
+};
+
+template <bool BLOCKS>
+__device__ __forceinline__ void decode(const QuantArgs& a, const Segments& seg, Place& p) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  p.rb = p.unit / a.runs;
+  p.cb = (p.unit - p.rb * a.runs) * a.run;
+  p.cb_end = min(p.cb + a.run, a.run_blocks);
+  p.e = 0;
+  int n;
+  if (BLOCKS) {
+    const int per = (a.M + 127) >> 7;
+    p.e = p.rb / per;
+    p.row0 = (p.rb - p.e * per) << 7;
+    n = a.M - p.row0;
+  } else if (a.offsets) {
+    p.e = seg.find(p.rb, a.E);
+    p.row0 = seg.begin[p.e] + ((p.rb - seg.first[p.e]) << 7);
+    n = seg.end[p.e] - p.row0;
+  } else {
+    p.row0 = p.rb << 7;
+    n = a.M - p.row0;
+  }
+  p.row0 += 8 * warp;
+  p.rows = min(max(n - 8 * warp, 0), 8);
+  p.source = -1;
+  if (lane < p.rows) {
+    p.source = p.row0 + lane;
+    if (!BLOCKS && a.rows) {
+      p.source = __ldg(a.rows + p.source);
+      if (p.source >= a.x_rows) p.source = -1;
+    }
+  }
+}
+
+// The next block: of the run, or of this CTA's next unit.
+template <bool BLOCKS>
+__device__ __forceinline__ void advance(const QuantArgs& a, const Segments& seg, int units,
+                                        Place& p) {
+  if (++p.cb < p.cb_end) return;
+  p.unit += gridDim.x;
+  if (p.unit < units) decode<BLOCKS>(a, seg, p);
+}
+
+// Operands that v is made of, and whether a thread's share of them is copied ahead into
+// shared memory (64 KB a CTA at most, so that two fit an SM).
+template <int SRC, typename T, bool VEC>
+struct Share {
+  static constexpr int OPS = SRC == MOE_FP8_ROWS ? 1 : SRC + 1;
+  static constexpr int PIECE = 4 * (int)sizeof(T);
+  static constexpr bool AHEAD = VEC && OPS * sizeof(T) <= 4;
+  static constexpr int BYTES = AHEAD ? OPS * 8 * PIECE * kThreads : 0;
+};
+
+// SRC: what v is.  COLS: codes along the columns are wanted.  BLOCKS: one scale a tile (weights, E matrices of M rows); else one a
 // row and one a column of the tile.
-template <int SRC, typename T, bool VEC, bool BLOCKS>
+template <int SRC, typename T, bool VEC, bool BLOCKS, bool COLS>
 __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
+  using S = Share<SRC, T, VEC>;
+  constexpr bool AHEAD = S::AHEAD;
+  constexpr bool PACKED = SRC == MOE_FP8_ROWS && VEC && sizeof(T) == 2;   // v are bf16 words
+  constexpr int OPS = S::OPS, PIECE = S::PIECE;
+  // the gradient's two halves from one reading, where a block lies on one side
+  const int passes = a.run_blocks < a.col_blocks ? 2 : 1;
+  extern __shared__ uint4 ring[];                // [row of the warp][operand][thread]
   __shared__ Segments seg;
-  __shared__ uint4 colmax[kWarps][32];           // [warp][four columns]
+  // the warps' largest magnitudes of the columns; a row 32 (16) bytes longer than it is
+  // wide, so that the eight columns of four rows lie in 32 banks
+  constexpr int COLMAX_ROW = PACKED ? 272 : 544;
+  __shared__ uint4 colmax[kWarps * COLMAX_ROW / 16];
   __shared__ float4 factors[32];                 // of the columns
   __shared__ uint4 turned[128][8];               // codes of a column, 16 rows a piece
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -188,164 +316,312 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
   if (!BLOCKS && a.offsets) seg.init<kThreads>(a.offsets, a.E, a.M);
   const int row_blocks =
       !BLOCKS && a.offsets ? min(seg.first[a.E], a.row_blocks) : a.row_blocks;
-  const int tiles = row_blocks * a.col_blocks;   // fits: checked on the host
-  const int half = a.C >> 7;
-  for (int t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int rb = t / a.col_blocks;
-    int cb = t - rb * a.col_blocks;
-    // the two tiles that read the same gate, up and dh one after the other
-    if (SRC == MOE_FP8_SWIGLU_GRAD && (a.C & 127) == 0) cb = (cb >> 1) + ((cb & 1) ? half : 0);
-    int e = 0, row0, n_rows;
-    if (BLOCKS) {
-      const int per = (a.M + 127) >> 7;
-      e = rb / per;
-      row0 = (rb - e * per) << 7;
-      n_rows = a.M - row0;
-    } else if (a.offsets) {
-      e = seg.find(rb, a.E);
-      row0 = seg.begin[e] + ((rb - seg.first[e]) << 7);
-      n_rows = seg.end[e] - row0;
+  const int units = row_blocks * a.runs;         // fits: checked on the host
+  const uint32_t my_ring = smem_u32(ring) + threadIdx.x * PIECE;
+  auto copy = [&](const Place& p) {
+    const int col = (p.cb << 7) + 4 * lane;
+    const bool in = col < a.width;
+    const T* x = static_cast<const T*>(a.x) + (BLOCKS ? (long long)p.e * a.M * a.ld_x : 0LL) +
+                 (in ? col : 0);
+    // (all there in all but the last blocks: no tests then)
+    if (__all_sync(kAll, in && (lane >= 8 || p.source >= 0))) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const T* q = x + (long long)__shfl_sync(kAll, p.source, i) * a.ld_x;
+        copy_async<PIECE>(my_ring + (i * OPS) * (kThreads * PIECE), q);
+        if (SRC != MOE_FP8_ROWS)
+          copy_async<PIECE>(my_ring + (i * OPS + 1) * (kThreads * PIECE), q + a.C);
+      }
     } else {
-      row0 = rb << 7;
-      n_rows = a.M - row0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int src = __shfl_sync(kAll, p.source, i);
+        const bool there = in && src >= 0;
+        const T* q = x + (long long)max(src, 0) * a.ld_x;
+        copy_async<PIECE>(my_ring + (i * OPS) * (kThreads * PIECE), q, there);
+        if (SRC != MOE_FP8_ROWS)
+          copy_async<PIECE>(my_ring + (i * OPS + 1) * (kThreads * PIECE), q + a.C, there);
+      }
     }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+
+  Place next;
+  next.unit = blockIdx.x;
+  if (next.unit < units) {
+    decode<BLOCKS>(a, seg, next);
+    if (AHEAD) copy(next);
+  }
+  while (next.unit < units) {
+    const Place t = next;
+    advance<BLOCKS>(a, seg, units, next);
+    for (int pass = 0; pass < passes; ++pass) {
+    const int cb = t.cb + pass * a.run_blocks;
     const int col = (cb << 7) + 4 * lane;
     const int n = a.width - col;                 // columns of this lane that are there
-    float v[8][4];
-    const bool direct = BLOCKS || !a.rows;
+    uint64_t v[8][2];                            // two neighbours a word
+    uint2 raw[PACKED ? 8 : 1];                   // four bf16
+    if (AHEAD) {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int r = warp * 8 + i;
-      long long src = -1;
-      if (r < n_rows) {
-        src = BLOCKS ? (long long)e * a.M + row0 + r
-                     : direct ? row0 + r : (long long)__ldg(a.rows + row0 + r);
-        if (!direct && src >= a.x_rows) src = -1;
+      for (int i = 0; i < 8; ++i) {
+        const uint8_t* p = reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
+                           (size_t)(i * OPS) * (kThreads * PIECE);
+        if (PACKED) {
+          raw[i] = *reinterpret_cast<const uint2*>(p);
+          v[i][0] = pair(__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xFFFF0000u));
+          v[i][1] = pair(__uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xFFFF0000u));
+        } else {
+          float f[4];
+          if (SRC == MOE_FP8_ROWS) {
+            const float4 q = *reinterpret_cast<const float4*>(p);
+            f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
+          } else {
+            const uint2 g = *reinterpret_cast<const uint2*>(p);
+            const uint2 u = *reinterpret_cast<const uint2*>(p + kThreads * PIECE);
+            const float gf[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xFFFF0000u),
+                                 __uint_as_float(g.y << 16), __uint_as_float(g.y & 0xFFFF0000u)};
+            const float uf[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float c = clip(gf[j], a.clamp);
+              f[j] = c * sigmoid(c) * clip(uf[j], a.clamp);
+            }
+          }
+          v[i][0] = pair(f[0], f[1]);
+          v[i][1] = pair(f[2], f[3]);
+        }
       }
-      if (src >= 0 && n > 0) {
-        source4<SRC, VEC, T>(a, src, col, n, v[i]);
-      } else {
+      // the next block's share arrives while this one is worked on
+      if (next.unit < units) copy(next);
+    } else {
+      const long long base = BLOCKS ? (long long)t.e * a.M : 0LL;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = 0.f;
+      for (int i = 0; i < 8; ++i) {
+        const int src = __shfl_sync(kAll, t.source, i);
+        float f[4] = {0.f, 0.f, 0.f, 0.f};
+        if (src >= 0 && n > 0) source4<SRC, VEC, T>(a, base + src, col, n, f);
+        v[i][0] = pair(f[0], f[1]);
+        v[i][1] = pair(f[2], f[3]);
       }
     }
-    // ---- along the rows ----
+    auto four = [&](int i, float (&f)[4]) {
+      unpair(v[i][0], f[0], f[1]);
+      unpair(v[i][1], f[2], f[3]);
+    };
+    // ---- largest magnitudes: of the columns, over this warp's rows; of the rows ----
+    uint4 m = make_uint4(0u, 0u, 0u, 0u);         // (PACKED: two 16-bit magnitudes a word)
+    uint32_t top;                                 // of row lane / 4
+    if (PACKED) {
+      uint32_t w[4];                              // two rows a word
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        uint32_t r[2];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t p = raw[i + j].x & 0x7FFF7FFFu, q = raw[i + j].y & 0x7FFF7FFFu;
+          if (COLS) {
+            m.x = __vmaxu2(m.x, p);
+            m.y = __vmaxu2(m.y, q);
+          }
+          r[j] = __vmaxu2(p, q);
+        }
+        w[i >> 1] = __vmaxu2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[0], r[1], 0x7632));
+      }
+      // lanes exchange rows: half of them each time, until a lane has two
+      const bool a16 = lane & 16, a8 = lane & 8;
+      const uint32_t k0 = __vmaxu2(a16 ? w[2] : w[0], __shfl_xor_sync(kAll, a16 ? w[0] : w[2], 16));
+      const uint32_t k1 = __vmaxu2(a16 ? w[3] : w[1], __shfl_xor_sync(kAll, a16 ? w[1] : w[3], 16));
+      uint32_t k = __vmaxu2(a8 ? k1 : k0, __shfl_xor_sync(kAll, a8 ? k0 : k1, 8));
+#pragma unroll
+      for (int o = 4; o > 0; o >>= 1) k = __vmaxu2(k, __shfl_xor_sync(kAll, k, o));
+      top = (lane & 4) ? k & 0xFFFF0000u : k << 16;
+    } else {
+      uint32_t w[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float f[4];
+        four(i, f);
+        const uint32_t b[4] = {magnitude(f[0]), magnitude(f[1]), magnitude(f[2]),
+                               magnitude(f[3])};
+        if (COLS) {
+          m.x = max(m.x, b[0]);
+          m.y = max(m.y, b[1]);
+          m.z = max(m.z, b[2]);
+          m.w = max(m.w, b[3]);
+        }
+        w[i] = max(max(b[0], b[1]), max(b[2], b[3]));
+      }
+      // lanes exchange rows: half of them each time, until a lane has one
+#pragma unroll
+      for (int n = 4; n > 0; n >>= 1) {
+        const bool hi = lane & (4 * n);
+#pragma unroll
+        for (int i = 0; i < n; ++i) {
+          const uint32_t send = hi ? w[i] : w[i + n], keep = hi ? w[i + n] : w[i];
+          w[i] = max(keep, __shfl_xor_sync(kAll, send, 4 * n));
+        }
+      }
+      top = w[0];
+      top = max(top, __shfl_xor_sync(kAll, top, 2));
+      top = max(top, __shfl_xor_sync(kAll, top, 1));
+    }
     float scale = 0.f, factor = 0.f;
     if (BLOCKS) {
-      uint32_t m = 0;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) m = max(m, magnitude(v[i][j]));
-      m = __reduce_max_sync(kAll, m);
-      if (lane == 0) colmax[warp][0].x = m;
+      top = __reduce_max_sync(kAll, top);
+      if (lane == 0) colmax[warp].x = top;
       __syncthreads();
-      m = __reduce_max_sync(kAll, lane < kWarps ? colmax[lane][0].x : 0u);
-      block_scale(m, a.pow2, scale, factor);
+      top = __reduce_max_sync(kAll, lane < kWarps ? colmax[lane].x : 0u);
+      block_scale(top, a.pow2, scale, factor);
       if (threadIdx.x == 0) {
-        const int nb = (a.M + 127) >> 7, b = row0 >> 7;
-        if (a.scales) a.scales[((long long)e * nb + b) * a.col_blocks + cb] = scale;
-        if (a.scales_t) a.scales_t[((long long)e * a.col_blocks + cb) * nb + b] = scale;
+        const int nb = (a.M + 127) >> 7, b = t.rb - t.e * nb;
+        if (a.scales) a.scales[((long long)t.e * nb + b) * a.col_blocks + cb] = scale;
+        if (a.scales_t) a.scales_t[((long long)t.e * a.col_blocks + cb) * nb + b] = scale;
       }
-    } else if (a.codes) {
-      uint32_t mine = 0;                          // lane i: of row i
+    } else {
+      // one reckoning for both: lanes 4 i take row i, lanes 4 i + 1 this warp's column i
+      if (COLS) {
+        uint8_t* const at = reinterpret_cast<uint8_t*>(colmax) + warp * COLMAX_ROW;
+        if (PACKED)
+          reinterpret_cast<uint2*>(at)[lane] = make_uint2(m.x, m.y);
+        else
+          reinterpret_cast<uint4*>(at)[lane] = m;
+        __syncthreads();
+        uint32_t c = 0;                           // column 8 warp + lane % 8
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        uint32_t m = max(max(magnitude(v[i][0]), magnitude(v[i][1])),
-                         max(magnitude(v[i][2]), magnitude(v[i][3])));
-        m = __reduce_max_sync(kAll, m);
-        if (lane == i) mine = m;
+        for (int j = 0; j < kWarps; j += 4) {
+          const uint8_t* const q =
+              reinterpret_cast<const uint8_t*>(colmax) + ((lane >> 3) + j) * COLMAX_ROW;
+          const int i = 8 * warp + (lane & 7);
+          c = max(c, PACKED ? (uint32_t)reinterpret_cast<const uint16_t*>(q)[i] << 16
+                            : reinterpret_cast<const uint32_t*>(q)[i]);
+        }
+        c = max(c, __shfl_xor_sync(kAll, c, 8));
+        c = max(c, __shfl_xor_sync(kAll, c, 16));
+        c = __shfl_sync(kAll, c, lane >> 2);
+        if (lane & 1) top = c;
       }
-      block_scale(mine, a.pow2, scale, factor);
-      const int r = warp * 8 + lane;
-      if (lane < 8 && r < n_rows) a.scales[(long long)cb * a.ld_scales + row0 + r] = scale;
+      block_scale(top, a.pow2, scale, factor);
+      const int i = lane >> 2;
+      if (a.codes && (lane & 3) == 0 && i < t.rows)
+        a.scales[(long long)cb * a.ld_scales + t.row0 + i] = scale;
+      if (COLS && (lane & 3) == 1) {
+        const int c = (cb << 7) + 8 * warp + i;
+        reinterpret_cast<float*>(factors)[8 * warp + i] = factor;
+        if (c < a.width) a.scales_t[(long long)t.rb * a.ld_scales_t + c] = scale;
+      }
     }
+    // ---- codes along the rows ----
     if (a.codes) {
+      uint8_t* const p =
+          a.codes + ((BLOCKS ? (long long)t.e * a.M : 0LL) + t.row0) * a.ld_codes + col;
+      const int rows = n > 0 ? t.rows : 0;
+      auto code_rows = [&](auto full) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float f = BLOCKS ? factor : __shfl_sync(kAll, factor, i);
-        const int r = warp * 8 + i;
-        if (r < n_rows && n > 0) {
-        const uint32_t w = codes4(v[i][0] * f, v[i][1] * f, v[i][2] * f, v[i][3] * f);
-        const long long at = (BLOCKS ? (long long)e * a.M : 0LL) + row0 + r;
-        uint8_t* p = a.codes + at * a.ld_codes + col;
-        if (VEC || n >= 4) {
-          *reinterpret_cast<uint32_t*>(p) = w;
-        } else {
+        for (int i = 0; i < 8; ++i) {
+          const float s = BLOCKS ? factor : __shfl_sync(kAll, factor, 4 * i);
+          const uint64_t s2 = pair(s, s);
+          float f[4];
+          unpair(mul2(v[i][0], s2), f[0], f[1]);
+          unpair(mul2(v[i][1], s2), f[2], f[3]);
+          const uint32_t w = codes4(f[0], f[1], f[2], f[3]);
+          if (decltype(full)::value || i < rows) {
+            uint8_t* const q = p + (long long)i * a.ld_codes;
+            if (VEC || n >= 4) {
+              *reinterpret_cast<uint32_t*>(q) = w;
+            } else {
 #pragma unroll
-          for (int j = 0; j < 3; ++j)
-            if (j < n) p[j] = (uint8_t)(w >> (8 * j));
+              for (int j = 0; j < 3; ++j)
+                if (j < n) q[j] = (uint8_t)(w >> (8 * j));
+            }
+          }
         }
-        }
-      }
+      };
+      if (VEC && __all_sync(kAll, rows == 8))
+        code_rows(std::true_type{});
+      else
+        code_rows(std::false_type{});
     }
-    if (!a.codes_t) {
+    if (!COLS) {
       if (BLOCKS) __syncthreads();                // colmax has been read
       continue;
     }
-    // ---- along the columns ----
+    // ---- codes along the columns ----
     float4 f = make_float4(factor, factor, factor, factor);
     if (!BLOCKS) {
-      uint4 m = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        m.x = max(m.x, magnitude(v[i][0]));
-        m.y = max(m.y, magnitude(v[i][1]));
-        m.z = max(m.z, magnitude(v[i][2]));
-        m.w = max(m.w, magnitude(v[i][3]));
-      }
-      colmax[warp][lane] = m;
-      __syncthreads();
-      if (threadIdx.x < 128) {
-        const uint32_t* all = reinterpret_cast<const uint32_t*>(colmax);
-        uint32_t top = 0;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = max(top, all[w * 128 + threadIdx.x]);
-        float s, g;
-        block_scale(top, a.pow2, s, g);
-        reinterpret_cast<float*>(factors)[threadIdx.x] = g;
-        const int c = (cb << 7) + threadIdx.x;
-        if (c < a.width) a.scales_t[(long long)rb * a.ld_scales_t + c] = s;
-      }
       __syncthreads();
       f = factors[lane];
     }
     {
-      const float fj[4] = {f.x, f.y, f.z, f.w};
+      const uint64_t f2[2] = {pair(f.x, f.y), pair(f.z, f.w)};
       // rows 8 warp.. of a column: half `warp & 1` of piece warp / 2
       const int piece = (warp >> 1) ^ (lane & 7), side = (warp & 1) ^ ((lane >> 3) & 1);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t lo = codes4(v[0][j] * fj[j], v[1][j] * fj[j], v[2][j] * fj[j],
-                                   v[3][j] * fj[j]);
-        const uint32_t hi = codes4(v[4][j] * fj[j], v[5][j] * fj[j], v[6][j] * fj[j],
-                                   v[7][j] * fj[j]);
-        reinterpret_cast<uint2*>(&turned[4 * lane + j][piece])[side] = make_uint2(lo, hi);
+      for (int h = 0; h < 2; ++h) {
+        float x[8], y[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) unpair(mul2(v[i][h], f2[h]), x[i], y[i]);
+        reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h][piece])[side] =
+            make_uint2(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]));
+        reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h + 1][piece])[side] =
+            make_uint2(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
       }
     }
     __syncthreads();
-    const long long at_t = BLOCKS ? row0 : (long long)rb << 7;     // column of codes_t
-    const int n_t = BLOCKS ? a.M - row0 : 128;                     // of them there
+    // first column of codes_t, and how many there are
+    const int at_t = BLOCKS ? (t.rb - t.e * ((a.M + 127) >> 7)) << 7 : t.rb << 7;
+    const int n_t = BLOCKS ? a.M - at_t : 128;
+#pragma unroll
     for (int q = threadIdx.x; q < 1024; q += kThreads) {
       const int c = q >> 3, piece = q & 7, group = c >> 2;
       if ((cb << 7) + c >= a.width || 16 * piece >= n_t) continue;
       uint4 w = turned[c][piece ^ (group & 7)];
       if ((group >> 3) & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-      const long long row = (BLOCKS ? (long long)e * a.width : 0LL) + (cb << 7) + c;
-      store_codes16(a.codes_t + row * a.ld_codes_t + at_t + 16 * piece, w, n_t - 16 * piece);
+      const long long row = (BLOCKS ? (long long)t.e * a.width : 0LL) + (cb << 7) + c;
+      uint8_t* p = a.codes_t + row * a.ld_codes_t + at_t + 16 * piece;
+      if (BLOCKS)
+        store_codes16(p, w, n_t - 16 * piece);
+      else
+        *reinterpret_cast<uint4*>(p) = w;
     }
-    __syncthreads();                              // before the next tile
+    // (between two barriers only: the next block writes colmax before its first, when this
+    // one's has been read, factors before its second, turned after that)
+    if (BLOCKS) __syncthreads();
+    }
   }
   pdl_trigger();
 }
 
+template <int SRC, typename T, bool VEC, bool BLOCKS, bool COLS>
+cudaError_t launch_one(const QuantArgs& a, dim3 g, dim3 b, cudaStream_t st) {
+  constexpr int ring = Share<SRC, T, VEC>::BYTES;
+  static std::atomic<unsigned long long> done{0};
+  if (ring) {
+    const cudaError_t e = smem_optin_once(k_fp8_quant<SRC, T, VEC, BLOCKS, COLS>, ring, done);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_pdl(k_fp8_quant<SRC, T, VEC, BLOCKS, COLS>, g, b, ring, st, a);
+}
+
+template <int SRC, typename T, bool VEC, bool BLOCKS>
+cudaError_t launch_with(const QuantArgs& a, dim3 g, dim3 b, cudaStream_t st) {
+  return a.codes_t ? launch_one<SRC, T, VEC, BLOCKS, true>(a, g, b, st)
+                   : launch_one<SRC, T, VEC, BLOCKS, false>(a, g, b, st);
+}
+
 template <int SRC, typename T, bool BLOCKS>
-cudaError_t launch(const QuantArgs& a, bool vec, cudaStream_t st) {
-  const long long tiles = (long long)a.row_blocks * a.col_blocks;
-  const long long cap = 2LL * num_sms();
-  const dim3 g((unsigned)(tiles < cap ? tiles : cap)), b(kThreads);
-  return vec ? launch_pdl(k_fp8_quant<SRC, T, true, BLOCKS>, g, b, 0, st, a)
-             : launch_pdl(k_fp8_quant<SRC, T, false, BLOCKS>, g, b, 0, st, a);
+cudaError_t launch(QuantArgs a, bool vec, cudaStream_t st) {
+  const int most = 2 * num_sms();
+  a.run_blocks = SRC == MOE_FP8_SWIGLU_GRAD && vec && a.C % 128 == 0 ? a.C / 128 : a.col_blocks;
+  // runs as long as leave every CTA some six of them
+  const long long each = (long long)a.row_blocks * a.run_blocks / (6LL * most);
+  a.run = (int)(each < 1 ? 1 : each < a.run_blocks ? each : a.run_blocks);
+  a.runs = (a.run_blocks + a.run - 1) / a.run;
+  const long long units = (long long)a.row_blocks * a.runs;
+  const dim3 g((unsigned)(units < most ? units : most)), b(kThreads);
+  return vec ? launch_with<SRC, T, true, BLOCKS>(a, g, b, st)
+             : launch_with<SRC, T, false, BLOCKS>(a, g, b, st);
 }
 
 bool aligned(const void* p, int bytes) {
@@ -376,6 +652,8 @@ extern "C" int moe_fp8_quantize(const moe_fp8_quant_desc* s, int M, const void* 
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   const int es = s->dtype == MOE_DTYPE_FP32 ? 4 : 2;
+  if (ld_x > kMaxApart || ld_dh > kMaxApart || ld_codes > kMaxApart || ld_codes_t > kMaxApart)
+    return MOE_ERR_INVALID_ARG;
   if (!x || !aligned(x, es) || ld_x < in_width || (grad && (ld_dh < s->C || !aligned(dh, es))) ||
       !aligned(rows, 4) || !aligned(offsets, 4))
     return MOE_ERR_INVALID_ARG;
@@ -399,10 +677,10 @@ extern "C" int moe_fp8_quantize(const moe_fp8_quant_desc* s, int M, const void* 
   QuantArgs a = {};
   a.M = M; a.C = s->C; a.width = width; a.E = s->E; a.clamp = s->clamp;
   a.pow2 = s->flags & MOE_FP8_POW2;
-  a.x = x; a.ld_x = ld_x; a.x_rows = x_rows; a.dh = dh; a.ld_dh = ld_dh; a.rows = rows;
+  a.x = x; a.ld_x = (int)ld_x; a.x_rows = x_rows; a.dh = dh; a.ld_dh = (int)ld_dh; a.rows = rows;
   a.offsets = offsets;
-  a.codes = codes; a.ld_codes = ld_codes; a.scales = scales; a.ld_scales = ld_scales;
-  a.codes_t = codes_t; a.ld_codes_t = ld_codes_t; a.scales_t = scales_t;
+  a.codes = codes; a.ld_codes = (int)ld_codes; a.scales = scales; a.ld_scales = ld_scales;
+  a.codes_t = codes_t; a.ld_codes_t = (int)ld_codes_t; a.scales_t = scales_t;
   a.ld_scales_t = ld_scales_t;
   a.col_blocks = (width + 127) / 128;
   if (blocks * a.col_blocks > (1LL << 30)) return MOE_ERR_INVALID_ARG;
@@ -438,7 +716,8 @@ extern "C" int moe_fp8_quantize_weights(const void* w, int dtype, int E, int N, 
       (!codes && !codes_t))
     return MOE_ERR_INVALID_ARG;
   const int es = dtype == MOE_DTYPE_FP32 ? 4 : 2;
-  if (!w || !aligned(w, es)) return MOE_ERR_INVALID_ARG;
+  if (!w || !aligned(w, es) || ld_codes > kMaxApart || ld_codes_t > kMaxApart)
+    return MOE_ERR_INVALID_ARG;
   if (codes && (!scales || !aligned(codes, 16) || ld_codes < K || ld_codes % 16 ||
                 !aligned(scales, 4)))
     return MOE_ERR_INVALID_ARG;
@@ -448,8 +727,8 @@ extern "C" int moe_fp8_quantize_weights(const void* w, int dtype, int E, int N, 
   QuantArgs a = {};
   a.M = N; a.C = a.width = K; a.E = E; a.pow2 = flags & MOE_FP8_POW2;
   a.x = w; a.ld_x = K; a.x_rows = 0;
-  a.codes = codes; a.ld_codes = ld_codes; a.scales = codes ? scales : nullptr;
-  a.codes_t = codes_t; a.ld_codes_t = ld_codes_t; a.scales_t = codes_t ? scales_t : nullptr;
+  a.codes = codes; a.ld_codes = (int)ld_codes; a.scales = codes ? scales : nullptr;
+  a.codes_t = codes_t; a.ld_codes_t = (int)ld_codes_t; a.scales_t = codes_t ? scales_t : nullptr;
   a.col_blocks = (K + 127) / 128;
   const long long blocks = (long long)E * ((N + 127) / 128);
   if (blocks * a.col_blocks > (1LL << 30)) return MOE_ERR_INVALID_ARG;
