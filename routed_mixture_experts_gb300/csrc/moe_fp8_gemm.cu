@@ -75,8 +75,47 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
 }
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  asm volatile("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
   return r;
+}
+
+// 32 lanes x 32 consecutive 32-bit columns of TMEM into 32 registers per thread.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]),
+        "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
+        "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+
+// Waits for this thread's loads; their registers pass through it, so that nothing that uses
+// them is scheduled before.
+__device__ __forceinline__ void tmem_wait32(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                 "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                 "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]),
+                 "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+
+// Arrival of lane 0 for its warp, without a branch.  Relaxed: what the warp has read is in
+// its registers, and it has written nothing that others wait for.  (An arrival that
+// releases took 150 cycles a block.)
+__device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.eq.s32 p, %1, 0;\n\t"
+      "@p mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar), "r"(lane)
+      : "memory");
 }
 
 __device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
@@ -97,8 +136,10 @@ struct Shape {
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int TURN = kEpiWarps * 32 * 17 * 4;       // narrow stores, a warp 32 x 16
-  // scales of a block: 128 rows', then (weights) BN columns' or the two weight blocks'
-  static constexpr int SLOTS = 8, SLOT = 512 + (WGRAD ? BN * 4 : 16);
+  // scales of GROUP blocks: of each its 128 rows', then (weights) BN columns' or the two
+  // weight blocks'
+  static constexpr int GROUP = 4, SLOTS = 2, BLOCK = 512 + (WGRAD ? BN * 4 : 16);
+  static constexpr int SLOT = GROUP * BLOCK;
   static constexpr int REST = TURN + SLOTS * SLOT + 512;
   static constexpr int FIT = (226 * 1024 - 3584 - REST) / STAGE;
   static constexpr int STAGES = FIT > 8 ? 8 : FIT;
@@ -306,28 +347,31 @@ __global__ void __launch_bounds__(kThreads, 1)
       const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
       const float* const pb = WGRAD ? args.sb + ti.n0
                                     : args.sb + ((long long)ti.e * nb_all + (ti.n0 >> 7)) * k_blocks;
-      for (int b = ti.b0; b < ti.b1; ++b) {
-        ok = mbar_wait(sempty_bar(slot), phase ^ 1u, &abort_s, args.err, 6);
-        ok = __all_sync(0xffffffffu, ok);
+      for (int g = ti.b0; g < ti.b1; g += S::GROUP) {
+        if (lane == 0) ok = mbar_wait(sempty_bar(slot), phase ^ 1u, &abort_s, args.err, 6);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const uint32_t to = smem_u32(slots) + slot * S::SLOT;
-        const float* const pa = args.sa + b * args.ld_sa + ti.m0;
+        const int end = min(g + S::GROUP, ti.b1);
+        for (int b = g; b < end; ++b) {
+          const uint32_t to = smem_u32(slots) + slot * S::SLOT + (b - g) * S::BLOCK;
+          const float* const pa = args.sa + b * args.ld_sa + ti.m0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 32 * i + lane;
-          const bool there = ti.m0 + r < ti.m1;
-          copy4(to + 4 * r, pa + (there ? r : 0), there);
-        }
-        if (WGRAD) {
-#pragma unroll
-          for (int i = 0; i < BN / 32; ++i) {
-            const int c = 32 * i + lane;
-            const bool there = ti.n0 + c < args.K;
-            copy4(to + 512 + 4 * c, pb + b * args.ld_sb + (there ? c : 0), there);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 32 * i + lane;
+            const bool there = ti.m0 + r < ti.m1;
+            copy4(to + 4 * r, pa + (there ? r : 0), there);
           }
-        } else if (lane < BN / 128) {
-          const bool there = (ti.n0 >> 7) + lane < nb_all;
-          copy4(to + 512 + 4 * lane, pb + b + (there ? lane * k_blocks : 0), there);
+          if (WGRAD) {
+#pragma unroll
+            for (int i = 0; i < BN / 32; ++i) {
+              const int c = 32 * i + lane;
+              const bool there = ti.n0 + c < args.K;
+              copy4(to + 512 + 4 * c, pb + b * args.ld_sb + (there ? c : 0), there);
+            }
+          } else if (lane < BN / 128) {
+            const bool there = (ti.n0 >> 7) + lane < nb_all;
+            copy4(to + 512 + 4 * lane, pb + b + (there ? lane * k_blocks : 0), there);
+          }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull_bar(slot))
                      : "memory");
@@ -357,63 +401,78 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint64_t acc[HALF / 2];
 #pragma unroll
       for (int i = 0; i < HALF / 2; ++i) acc[i] = 0;
-      for (int b = ti.b0; b < ti.b1; ++b) {
-        ok = mbar_wait(sfull_bar(slot), slot_phase, &abort_s, args.err, 7);
-        const float* const sc = slots + slot * (S::SLOT / 4);
-        float s = sc[row];
-        const float* const cs = sc + 128 + half * HALF;          // weights: of the columns
-        if (!WGRAD) {
-          s *= sc[128 + (half * HALF >> 7)];
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sempty_bar(slot));
-        }
-        const uint64_t s2 = pair(s, s);
-        ok = mbar_wait(tfull_bar(buf), buf_phase, &abort_s, args.err, 5) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+      // 32 columns a load, the next one on its way while one is added: of the same block,
+      // or the first of the next, whose barrier is looked at before this one's last
+      // addition.  After a wait that gave up nothing waits any more, and the tile's end
+      // leaves.
+      uint32_t d[2][32];
+      float s = 0.f;
+      const float* sc = slots;                   // this block's scales
+      auto start = [&](int b) {
+        const int i = (b - ti.b0) % S::GROUP;
+        if (i == 0) ok = ok && mbar_wait(sfull_bar(slot), slot_phase, &abort_s, args.err, 7);
+        sc = slots + (slot * S::SLOT + i * S::BLOCK) / 4;
+        s = sc[row];
+        if (!WGRAD) s *= sc[128 + (half * HALF >> 7)];
+        ok = ok && mbar_wait(tfull_bar(buf), buf_phase, &abort_s, args.err, 5);
+        __syncwarp();
         tc_fence_after();
+        tmem_ld32(lane_base + (uint32_t)(buf * BN), d[0]);
+      };
+      if (ti.b0 < ti.b1) start(ti.b0);
+      for (int b = ti.b0; b < ti.b1; ++b) {
         const uint32_t tb = lane_base + (uint32_t)(buf * BN);
-        uint32_t d[2][16];
-        tmem_ld16(tb, d[0]);
+        const float* const cs = sc + 128 + half * HALF;
+        const uint64_t s2 = pair(s, s);
+        // the group's last block: its slot is free once the scales have been read
+        const bool last = (b - ti.b0) % S::GROUP == S::GROUP - 1 || b + 1 == ti.b1;
+        const uint32_t used = sempty_bar(slot);
 #pragma unroll
-        for (int i = 0; i < HALF / 16; ++i) {
-          tmem_ld_wait();
-          if (i + 1 < HALF / 16) {
-            tmem_ld16(tb + 16u * (i + 1), d[(i + 1) & 1]);
+        for (int i = 0; i < HALF / 32; ++i) {
+          tmem_wait32(d[i & 1]);
+          if (i + 1 < HALF / 32) {
+            tmem_ld32(tb + 32u * (i + 1), d[(i + 1) & 1]);
           } else {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(tempty_bar(buf));
+            arrive_lane0(tempty_bar(buf), lane);
+            if (!WGRAD && last) arrive_lane0(used, lane);
+            if (++buf == NBUF) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+            if (last && ++slot == SLOTS) {
+              slot = 0;
+              slot_phase ^= 1u;
+            }
+            static_assert((HALF / 32) % 2 == 0, "the next block starts with d[0]");
+            if (b + 1 < ti.b1) start(b + 1);
           }
-          uint64_t cq[WGRAD ? 8 : 1];
-          if (WGRAD) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float4 q = *reinterpret_cast<const float4*>(cs + 16 * i + 4 * j);
-              cq[2 * j] = pair(q.x, q.y);
-              cq[2 * j + 1] = pair(q.z, q.w);
+          for (int q = 0; q < 2; ++q) {
+            uint64_t cq[WGRAD ? 8 : 1];
+            if (WGRAD) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const float4 x = *reinterpret_cast<const float4*>(cs + 32 * i + 16 * q + 4 * j);
+                cq[2 * j] = pair(x.x, x.y);
+                cq[2 * j + 1] = pair(x.z, x.w);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              uint64_t v = pair_u(d[i & 1][16 * q + 2 * j], d[i & 1][16 * q + 2 * j + 1]);
+              if (WGRAD) v = mul2(v, cq[j]);
+              acc[16 * i + 8 * q + j] = fma2(v, s2, acc[16 * i + 8 * q + j]);
             }
           }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint64_t v = pair_u(d[i & 1][2 * j], d[i & 1][2 * j + 1]);
-            if (WGRAD) v = mul2(v, cq[j]);
-            acc[8 * i + j] = fma2(v, s2, acc[8 * i + j]);
-          }
         }
-        if (WGRAD) {
+        if (WGRAD && last) {
           __syncwarp();
-          if (lane == 0) mbar_arrive(sempty_bar(slot));
-        }
-        if (++slot == SLOTS) {
-          slot = 0;
-          slot_phase ^= 1u;
-        }
-        if (++buf == NBUF) {
-          buf = 0;
-          buf_phase ^= 1u;
+          arrive_lane0(used, lane);
         }
       }
+      ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       // ---- out ----
       const int n_here = min(HALF, n_all - c0);            // columns of this warp
