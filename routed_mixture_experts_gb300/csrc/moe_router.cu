@@ -54,6 +54,7 @@ struct RouterArgs {
   void* d_logits;  long long ld_d;
   // choice within groups of neighbouring experts
   int groups, top_groups, group_size, pair;
+  int share_log2;        // lanes a group in the search for its largest keys
 };
 
 __device__ __forceinline__ float load_logit(const float* p) { return *p; }
@@ -121,16 +122,16 @@ __device__ __forceinline__ void write_losses(const RouterArgs& a, float balance,
 
 struct GroupRow {
   float* key;                        // [NV * 32] keys by expert, NaN as -inf
-  float* value;                      // [256] of the groups
+  float *value, *second;             // [groups] values, second keys
   uint32_t* kept;                    // [8] bit g: group g competes
 };
 
 // How close two fp32 keys, or sums of two, may come without their order being known.  The
-// error of s: sigmoid, expf's 2^-23 of e^-l is at most 2^-25, the sum's and the quotient's
-// roundings less than 2^-23; softmax, the same relative to s, plus the rounding of l - max
-// (D 2^-24 of a weight e^-D) and the total's, together below 2^-20 of the largest s.  Adding
-// biases up to `wide` and two keys: 2^-24 of at most twice (1 + wide) each.  Four keys are
-// compared.
+// error of s: sigmoid, the exponential's (2 + 1.5 |l|) 2^-23 of e^-l is s (1 - s) times that
+// of s, below 2^-23, the sum's rounding and the quotient's 2^-24 + 2^-23; softmax, the same
+// relative to s, plus the rounding of l - max (D 2^-24 of a weight e^-D) and the total's,
+// together below 2^-20 of the largest s.  Adding biases up to `wide` and two keys: 2^-24 of
+// at most twice (1 + wide) each.  Four keys are compared.
 __device__ __forceinline__ float key_error(bool sig, float largest, float wide) {
   return (sig ? 0x1p-19f : 0x1p-18f * largest) + 0x1p-20f * wide;
 }
@@ -266,23 +267,129 @@ __device__ __noinline__ void choose_slowly(const RouterArgs& a, const float* log
   __syncwarp();
 }
 
+// The choice of one row of sigmoid keys whose groups are known, on the 64-bit keys of the
+// experts that come within `error` of the last one chosen, a lane each: an exponential in 64
+// bits costs a warp some 1000 cycles, and choose_slowly eight of them.  False where there
+// are more of them than lanes.
+template <int NV>
+__device__ __noinline__ bool choose_among(const RouterArgs& a, const float* logits,
+                                          const float* keys, const uint32_t* kept,
+                                          uint8_t* chosen, float error) {
+  const int lane = threadIdx.x & 31;
+  if (a.k >= 32) return false;
+  const float low = keys[chosen[a.k - 1]] - 2.f * error;
+  if (!(low > -INFINITY)) return false;
+  __syncwarp();
+  int n = 0;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int e = lane + 32 * i, g = e / a.group_size;
+    const bool in = e < a.E && keys[e] >= low &&
+                    (a.top_groups == a.groups || ((kept[g >> 5] >> (g & 31)) & 1u));
+    const unsigned has = __ballot_sync(kAll, in);
+    const int at = n + __popc(has & ((1u << lane) - 1u));
+    if (in && at < 32) chosen[64 + at] = (uint8_t)e;
+    n += __popc(has);
+  }
+  if (n > 32) return false;
+  __syncwarp();
+  const int e = lane < n ? chosen[64 + lane] : 0;
+  const double key = lane < n ? 1.0 / (1.0 + exp(-(double)logits[e])) + (double)a.bias[e] : 0.0;
+  int ahead = 0;                               // the list is in the experts' order
+  for (int j = 0; j < n; ++j) {
+    const double other = __shfl_sync(kAll, key, j);
+    ahead += (other > key || (other == key && j < lane)) ? 1 : 0;
+  }
+  if (lane < n && ahead < a.k) chosen[ahead] = (uint8_t)e;
+  __syncwarp();
+  return true;
+}
+
+// The values of the groups that fp32 does not tell apart, on the 64-bit keys of the experts
+// that make them: those within `error` of a group's second (or largest) key, a lane each.
+// Chooses among them so that top_groups compete.  False where there are more than lanes.
+// (Sigmoid keys: a softmax key needs the whole row in 64 bits.)
+__device__ __noinline__ bool choose_close_groups(const RouterArgs& a, const GroupRow& row,
+                                                 const float* logits, float in, float out,
+                                                 float error) {
+  const int lane = threadIdx.x & 31, G = a.groups;
+  int n = 0, expert = 0, mine = -1;              // list of experts; this lane's and its group
+  int open = a.top_groups, close = 0, held = -1; // places left; close groups; this lane's
+  for (int g = 0; g < G; ++g) {
+    const float v = row.value[g];
+    if (v > out + error) open -= 1;
+    if (v > out + error || v < in - error) continue;
+    if (lane == close) held = g;
+    close += 1;
+    const float least = (a.pair ? row.second[g] : v) - error;
+    for (int i0 = 0; i0 < a.group_size; i0 += 32) {
+      const int i = i0 + lane;
+      const bool takes = i < a.group_size && row.key[g * a.group_size + i] >= least;
+      unsigned has = __ballot_sync(kAll, takes);
+      const int m = __popc(has);
+      if (n + m > 32) return false;
+      if (lane >= n && lane < n + m) {           // the (lane - n)-th of them
+        for (int k = lane - n; k > 0; --k) has &= has - 1;
+        expert = g * a.group_size + i0 + __ffs(has) - 1;
+        mine = g;
+      }
+      n += m;
+    }
+  }
+  if (close > 32) return false;
+  double key = -INFINITY;
+  if (mine >= 0 && row.key[expert] > -INFINITY)
+    key = 1.0 / (1.0 + exp(-(double)logits[expert])) + (a.bias ? (double)a.bias[expert] : 0.0);
+  double value = -INFINITY;                      // of the group that this lane holds
+  for (int j = 0; j < n; ++j) {                  // its largest
+    const double v = __shfl_sync(kAll, key, j);
+    if (__shfl_sync(kAll, mine, j) == held && v > value) value = v;
+  }
+  if (a.pair) {
+    double second = -INFINITY;
+    bool met = false;                            // the largest itself, once
+    for (int j = 0; j < n; ++j) {
+      const double v = __shfl_sync(kAll, key, j);
+      if (__shfl_sync(kAll, mine, j) != held) continue;
+      if (v == value && !met) met = true;
+      else if (v > second) second = v;
+    }
+    if (second > -INFINITY) value += second;
+  }
+  int ahead = 0;
+  for (int j = 0; j < close; ++j) {
+    const double v = __shfl_sync(kAll, value, j);
+    ahead += (v > value || (v == value && j < lane)) ? 1 : 0;
+  }
+  // the bits anew
+  for (int g0 = 0; g0 < G; g0 += 32) {
+    const int g = g0 + lane;
+    const unsigned word = __ballot_sync(kAll, g < G && row.value[g < G ? g : 0] > out + error);
+    if (lane == 0) row.kept[g0 >> 5] = word;
+  }
+  __syncwarp();
+  if (held >= 0 && ahead < open) atomicOr(&row.kept[held >> 5], 1u << (held & 31));
+  __syncwarp();
+  return true;
+}
+
 // Which groups compete (row.kept), from the keys in shared memory.  Several lanes share a
 // group, from places that differ by group so that they do not meet in a bank.  Returns
 // whether the last group in and the first one out are too close to tell.
-__device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRow& row, bool exact,
+__device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRow& row,
+                                              const float* logits, bool exact, bool sig,
                                               float error) {
   const int lane = threadIdx.x & 31, G = a.groups, size = a.group_size;
-  int share = 1;                             // lanes a group
-  while (2 * share * G <= 32 && 2 * share <= size) share *= 2;
-  const int per = (size + share - 1) / share, at_once = 32 / share;
-  for (int g0 = 0; g0 < G; g0 += at_once) {
-    const int g = g0 + lane / share, q = lane % share;
+  const int share = 1 << a.share_log2, per = (size + share - 1) >> a.share_log2;
+  const int q = lane & (share - 1);
+  for (int g = lane >> a.share_log2; g - (lane >> a.share_log2) < G; g += 32 >> a.share_log2) {
     float first = -INFINITY, second = -INFINITY;
     if (g < G) {
-      int j = g % per;
+      const float* const p = row.key + g * size + q;
+      int j = per == 8 ? g & 7 : g % per;
+#pragma unroll 8
       for (int n = 0; n < per; ++n) {
-        const int i = q + share * j;
-        const float v = i < size ? row.key[g * size + i] : -INFINITY;
+        const float v = q + (j << a.share_log2) < size ? p[j << a.share_log2] : -INFINITY;
         second = fmaxf(second, fminf(first, v));
         first = fmaxf(first, v);
         if (++j == per) j = 0;
@@ -293,8 +400,10 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
       second = fmaxf(fminf(first, f), fmaxf(second, s));
       first = fmaxf(first, f);
     }
-    if (g < G && q == 0)
+    if (g < G && q == 0) {
       row.value[g] = a.pair && second > -INFINITY ? first + second : first;
+      row.second[g] = second;
+    }
   }
   __syncwarp();
   uint32_t low = 0xFFFFFFFFu, high = 0u;     // of those that stay, of those that do not
@@ -304,6 +413,7 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
     if (g < G) {
       const float v = row.value[g];
       int ahead = 0;
+#pragma unroll 8
       for (int h = 0; h < G; ++h) {
         const float w = row.value[h];
         ahead += (w > v || (w == v && h < g)) ? 1 : 0;
@@ -315,12 +425,13 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
     const unsigned word = __ballot_sync(kAll, stays);
     if (lane == 0) row.kept[g0 >> 5] = word;
   }
-  low = __reduce_min_sync(kAll, low);
-  high = __reduce_max_sync(kAll, high);
   __syncwarp();
   if (exact) return false;
+  low = __reduce_min_sync(kAll, low);
+  high = __reduce_max_sync(kAll, high);
   const float in = order_value(low), out = order_value(high);
-  return in - out <= error;                             // infinities: NaN, not close
+  if (!(in - out <= error)) return false;               // (infinities: NaN, not close)
+  return !sig || !choose_close_groups(a, row, logits, in, out, error);
 }
 
 // Forward.  L = logits type, NV = slots of 32 experts, GROUPS: the choice within groups.
@@ -336,7 +447,7 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
 // Measured, both launches: one token 3.5 us, 8192 rows of 128 experts (k = 8) 11.4, 16411
 // rows of 250 bf16 logits (k = 6, sigmoid, bias, 2048 rows masked) 19.6.
 template <typename L, int NV, bool GROUPS>
-__global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
+__global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs a) {
   extern __shared__ float psum[];                 // [warps][NV * 32], GROUPS: and the keys
   __shared__ int cnt[kMaxE];
   __shared__ uint8_t sel_id[32][kMaxE];           // a warp's chosen experts, in order
@@ -347,7 +458,7 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
   const int E = a.E, k = a.k;
   float* const mine = psum + warp * (NV * 32);    // first the row's logits, by expert
   float* const keys = GROUPS ? psum + (nw + warp) * (NV * 32) : nullptr;
-  float* const values = GROUPS ? psum + 2 * nw * (NV * 32) + warp * a.groups : nullptr;
+  float* const values = GROUPS ? psum + 2 * nw * (NV * 32) + warp * 2 * a.groups : nullptr;
   for (int e = threadIdx.x; e < kMaxE; e += blockDim.x) cnt[e] = 0;
   __syncthreads();
   pdl_wait();
@@ -359,7 +470,11 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) bias[i] = a.bias && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
   float wide = 0.f;                               // the largest bias
+  uint64_t group_of = 0;                          // group of the expert in slot i, byte i
   if (GROUPS) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      group_of |= (uint64_t)((lane + 32 * i) / a.group_size) << (8 * i);
 #pragma unroll
     for (int i = 0; i < NV; ++i) wide = fmaxf(wide, fabsf(bias[i]));
     wide = warp_max(wide);
@@ -397,20 +512,23 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
       nan |= l[i] != l[i];
     }
     int count = k;
-    bool close = false;
+    bool close = false, groups_close = false;
     float error = 0.f;
+    const bool weighed = GROUPS && (a.bias != nullptr || a.pair);
     if (GROUPS) {
       mx = warp_max(mx);
       float largest = 0.f;
       const bool keyed = a.bias != nullptr;
-      if (keyed || a.pair) {
-        // fp32 keys of scores
-        float s[NV], sum = 0.f;
+      if (weighed) {
+        // fp32 keys of scores; the weights take the logits' place
+        float sum = 0.f;
+        uint32_t off = 0;                        // bit i: a logit of -inf
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const float x = expf(sig ? -l[i] : l[i] - mx);
-          s[i] = sig ? __fdiv_rn(1.f, 1.f + x) : lane + 32 * i < E ? x : 0.f;
-          sum += s[i];
+          const float x = __expf(sig ? -l[i] : l[i] - mx);
+          off |= (l[i] == -INFINITY ? 1u : 0u) << i;
+          l[i] = lane + 32 * i >= E ? 0.f : sig ? __fdividef(1.f, 1.f + x) : x;
+          sum += l[i];
         }
         if (!sig) {
           sum = warp_sum(sum);
@@ -419,8 +537,8 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int e = lane + 32 * i;
-          if (!sig) s[i] = __fdiv_rn(s[i], sum);
-          const float v = l[i] == -INFINITY ? -INFINITY : s[i] + bias[i];
+          const float s = sig ? l[i] : l[i] * largest;
+          const float v = (off >> i) & 1u ? -INFINITY : s + bias[i];
           if (keyed) key[i] = e < E ? order_key(v) : 0u;
           keys[e] = v == v ? v : -INFINITY;
         }
@@ -431,11 +549,11 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
       __syncwarp();
       error = key_error(sig, largest, wide);
       if (a.top_groups < a.groups) {
-        const GroupRow row = {keys, values, kept[warp]};
-        close = choose_groups(a, row, !keyed && !a.pair, error);
+        const GroupRow row = {keys, values, values + a.groups, kept[warp]};
+        close = groups_close = choose_groups(a, row, mine, !keyed && !a.pair, sig, error);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const int g = (lane + 32 * i) / a.group_size;
+          const int g = (int)(group_of >> (8 * i)) & 255;
           if (lane + 32 * i < E && !((kept[warp][g >> 5] >> (g & 31)) & 1u)) key[i] = 0u;
         }
       }
@@ -477,7 +595,8 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     }
     if (GROUPS && close) {
       __syncwarp();
-      choose_slowly<NV>(a, mine, kept[warp], sel_id[warp]);
+      if (groups_close || !sig || !choose_among<NV>(a, mine, keys, kept[warp], sel_id[warp], error))
+        choose_slowly<NV>(a, mine, kept[warp], sel_id[warp]);
     }
     mx = warp_max(mx);
     nan = __any_sync(kAll, nan);
@@ -495,11 +614,15 @@ __global__ void __launch_bounds__(1024) k_router(const RouterArgs a) {
     live_rows += 1;
     const float top = shift_of(mx, sig);
     float total = 0.f;
+    if (!weighed || (sig && top != 0.f)) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      l[i] = lane + 32 * i < E ? weight(l[i], top, sig) : 0.f;
-      total += l[i];
+      for (int i = 0; i < NV; ++i) {
+        const int e = lane + 32 * i;
+        l[i] = e < E ? weight(weighed ? mine[e] : l[i], top, sig) : 0.f;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) total += l[i];
     total = warp_sum(total);
     const float inv = 1.f / total;
 #pragma unroll
@@ -768,24 +891,32 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
 
 // Up to a row per warp one CTA does all, the sums too (32 rows of 128 experts 4.8 us).
 // More rows are spread, and a second launch adds the sums: 64 rows 6.6 us against 7.8
-// on one CTA.
-constexpr int kOneCtaRows = 32;
+// on one CTA.  With groups a CTA has 16 warps, whose threads keep all in registers (8192
+// rows of 256 experts 31.5 us against 32.9 on 32 warps, one row 6.8 against 8.8).
+int most_warps(bool groups) { return groups ? 16 : 32; }
 
 // warps of a CTA: its chosen experts and per-warp sums take shared memory
-int forward_warps(int T, int grid) { return grid > 1 ? 32 : T > 8 ? 32 : 8; }
+int forward_warps(int T, int grid, bool groups) {
+  return grid > 1 || T > 8 ? most_warps(groups) : 8;
+}
 
-int forward_grid(int T) {
-  if (T <= kOneCtaRows) return 1;
-  const int want = (T - 1) / 32 + 1, cap = num_sms();      // T + 31 may pass INT_MAX
+int forward_grid(int T, bool groups) {
+  const int rows = most_warps(groups);
+  if (T <= rows) return 1;
+  const int want = (T - 1) / rows + 1, cap = num_sms();      // T + 31 may pass INT_MAX
   return want < cap ? want : cap;
+}
+
+size_t workspace_bytes_of(const moe_router_desc* s, int T, bool groups) {
+  return (size_t)forward_grid(T, groups) * (2 * s->E + 2) * 4;
 }
 
 template <typename L, int NV, bool GROUPS>
 cudaError_t launch_forward_nv(const RouterArgs& a, int grid, cudaStream_t st) {
-  const int warps = forward_warps(a.T, grid);
+  const int warps = forward_warps(a.T, grid, GROUPS);
   // with groups: the keys too, and the groups' values (256 at most)
-  const int a_warp = GROUPS ? 2 * NV * 32 + a.groups : NV * 32;
-  constexpr int most = 32 * (GROUPS ? 2 * NV * 32 + kMaxE : NV * 32) * (int)sizeof(float);
+  const int a_warp = GROUPS ? 2 * NV * 32 + 2 * a.groups : NV * 32;
+  constexpr int most = 32 * (GROUPS ? 2 * NV * 32 + 2 * kMaxE : NV * 32) * (int)sizeof(float);
   static std::atomic<unsigned long long> done{0};
   const cudaError_t e = smem_optin_once(k_router<L, NV, GROUPS>, most, done);
   if (e != cudaSuccess) return e;
@@ -800,6 +931,8 @@ cudaError_t launch_forward(const RouterArgs& a, int grid, cudaStream_t st) {
     case 2: return launch_forward_nv<L, 2, GROUPS>(a, grid, st);
     case 3: return launch_forward_nv<L, 3, GROUPS>(a, grid, st);
     case 4: return launch_forward_nv<L, 4, GROUPS>(a, grid, st);
+    case 5: return launch_forward_nv<L, GROUPS ? 5 : 8, GROUPS>(a, grid, st);
+    case 6: return launch_forward_nv<L, GROUPS ? 6 : 8, GROUPS>(a, grid, st);
     default: return launch_forward_nv<L, 8, GROUPS>(a, grid, st);
   }
 }
@@ -857,7 +990,7 @@ using namespace moe;
 
 extern "C" size_t moe_router_workspace_bytes(const moe_router_desc* s, int T) {
   if (!sizes_ok(s, T)) return 0;
-  return (size_t)forward_grid(T) * (2 * s->E + 2) * 4;
+  return workspace_bytes_of(s, T, false);
 }
 
 namespace moe {
@@ -876,14 +1009,15 @@ int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, con
   if (!aligned(bias, 4) || !aligned(ids, 4) || !aligned(scores, 4) || !aligned(counts, 4) ||
       !aligned(prob_sum, 4) || !aligned(losses, 4) || !aligned(row_stat, 4))
     return MOE_ERR_INVALID_ARG;
-  const int grid = forward_grid(T);
+  const int grid = forward_grid(T, g != nullptr);
   RouterArgs a = {};
   a.T = T; a.E = s->E; a.k = s->k; a.scoring = s->scoring; a.scale = s->scale;
   a.logits = logits; a.ld = ld; a.bias = bias; a.mask = token_mask;
   a.ids = ids; a.scores = scores; a.counts = counts; a.prob_sum = prob_sum; a.losses = losses;
   a.row_stat = row_stat;
   if (grid > 1) {
-    if (!workspace || workspace_bytes < moe_router_workspace_bytes(s, T)) return MOE_ERR_WORKSPACE;
+    if (!workspace || workspace_bytes < workspace_bytes_of(s, T, g != nullptr))
+      return MOE_ERR_WORKSPACE;
     if (!aligned(workspace, 16)) return MOE_ERR_INVALID_ARG;
     a.part_prob = static_cast<float*>(workspace);
     a.part_count = reinterpret_cast<int32_t*>(a.part_prob + (size_t)grid * a.E);
@@ -896,6 +1030,8 @@ int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, con
   if (g) {
     a.groups = g->groups; a.top_groups = g->top_groups; a.group_size = s->E / g->groups;
     a.pair = g->group_score == MOE_GROUP_TOP2 && a.group_size > 1;
+    while ((2 << a.share_log2) * a.groups <= 32 && (2 << a.share_log2) <= a.group_size)
+      a.share_log2 += 1;
     e = f32 ? launch_forward<float, true>(a, grid, st) : launch_forward<uint16_t, true>(a, grid, st);
   } else {
     e = f32 ? launch_forward<float, false>(a, grid, st)
@@ -942,7 +1078,7 @@ extern "C" int moe_router_forward(const moe_router_desc* s, int T, const void* l
 }
 
 extern "C" size_t moe_group_router_workspace_bytes(const moe_group_router_desc* g, int T) {
-  return group_desc_ok(g) ? moe_router_workspace_bytes(&g->router, T) : 0;
+  return group_desc_ok(g) && sizes_ok(&g->router, T) ? workspace_bytes_of(&g->router, T, true) : 0;
 }
 
 extern "C" int moe_group_router_forward(const moe_group_router_desc* g, int T, const void* logits,
