@@ -271,6 +271,19 @@ __device__ __forceinline__ void sum_rows(const Fp8GemmArgs& args, const Tile& ti
   constexpr int WIDE = S::WIDE, CH = 32;         // CH: columns a load
   const int row = quarter * 32 + lane, r = ti.m0 + row, c0 = ti.n0 + group * WIDE;
   const bool row_in = r < ti.m1;
+  if (ti.m0 + quarter * 32 >= ti.m1) {           // rows of nobody: only the rings go on
+    for (int b = ti.b0; b < ti.b1; ++b) {
+      rd.wait_sums();
+      rd.free_sums(lane);
+      rd.next_buf<S::NBUF>();
+      if ((b - ti.b0) % S::GROUP == S::GROUP - 1 || b + 1 == ti.b1) {
+        rd.wait_scales();
+        rd.free_scales(lane);
+        rd.next_slot<S::SLOTS>();
+      }
+    }
+    return;
+  }
   uint64_t acc[WIDE / 2];
 #pragma unroll
   for (int i = 0; i < WIDE / 2; ++i) acc[i] = 0;
@@ -751,6 +764,17 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
       ld_as < M || ld_c < s->N || !aligned(a_scales, 4) || !aligned(b_scales, 4) ||
       !aligned(c, es) || !aligned(offsets, 4) || ld_b >= (1LL << 39) / s->N)
     return MOE_ERR_INVALID_ARG;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  // Few rows, so few weights that they are units of one wave of the streaming kernel (eight
+  // rows of A a unit): M = 1, N = K = 4096 8.2 us against 10.1 on tiles, N = 300, K = 500 2.0
+  // against 4.2; beyond a wave tiles are ahead (one token's eight experts of N = 1536, K =
+  // 2048, 768 units, 12.7 against 10.2; M = 16, N = K = 4096 13.5 against 10.2).
+  if (M <= 32 && (long long)(M < s->E ? M : s->E) * ((s->N + 15) / 16) * ((M + 7) / 8) <=
+                     2 * num_sms()) {
+    const Fp8FewCall f = {M, s->N, s->K, s->E, a, ld_a, a_scales, ld_as, b, ld_b, b_scales,
+                          offsets, c, ld_c, es == 4, static_cast<DevError*>(status)};
+    return cuda_result(launch_fp8_few(f, st), "moe_fp8_gemm");
+  }
   Fp8GemmArgs g = {};
   g.M = M; g.N = s->N; g.K = s->K; g.E = s->E;
   g.sa = a_scales; g.ld_sa = ld_as; g.sb = b_scales;
@@ -758,11 +782,15 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
   g.f32 = es == 4;
   g.wide = aligned(c, 32) && ld_c * es % 32 == 0;
   g.err = static_cast<DevError*>(status);
-  // 128 columns a tile where 256 leave SMs without one (experts count with half a tile each
-  // beside their rows).  One wave of M = 1003, N = 1537, K = 2047: 10.2 us against 15.4; many
-  // waves (M = 65536, N = 1536, K = 2048 on 128 experts) 253 us against 205.
+  // 128 columns a tile, and four parts of tensor memory, where 256 leave SMs without a tile
+  // (experts count with half a tile each beside their rows).  One wave of M = 1003, N = 1537,
+  // K = 2047: 10.0 us against 15.4, M = 16, N = K = 4096 10.2 against 13.9; many waves (M =
+  // 65536, N = 1536, K = 2048 on 128 experts) 253 against 205.  A few rows on experts wait for
+  // the weights either way, in more and smaller copies with 128 (one token's eight experts
+  // 11.6 against 10.3).
   const long long rows = (M + 127) / 128 + (offsets ? (M < s->E ? M : s->E) / 2 : 0);
-  const bool narrow = s->N <= 128 || rows * ((s->N + 255) / 256) <= num_sms();
+  const bool narrow = s->N <= 128 || ((!offsets || M >= 128) &&
+                                      rows * ((s->N + 255) / 256) <= num_sms());
   const long long n_tiles = (s->N + (narrow ? 127 : 255)) / (narrow ? 128 : 256);
   const long long most = ((M + 127LL * (offsets ? s->E : 1)) / 128) * n_tiles;
   if (most > (1LL << 30)) return MOE_ERR_INVALID_ARG;
@@ -771,7 +799,6 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
       encode_tmap_codes(&tb, b, s->E, s->N, s->K, ld_b, narrow ? 128 : 256) != MOE_OK)
     return MOE_ERR_CUDA;
   const int grid = (int)(most < num_sms() ? most : num_sms());
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
   return cuda_result(narrow ? launch<128, false>(ta, tb, g, grid, st)
                             : launch<256, false>(ta, tb, g, grid, st), "moe_fp8_gemm");
 }

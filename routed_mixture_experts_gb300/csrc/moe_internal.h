@@ -243,6 +243,19 @@ int encode_tmap_u8(CUtensorMap* map, const void* base, long long rows, long long
 // beyond the extents, 128-byte swizzle.
 int encode_tmap_codes(CUtensorMap* map, const void* base, long long batch, long long rows,
                       long long cols, long long ld, int box_rows);
+// The 8-bit block product of a few rows (moe_fp8_few.cu).
+struct Fp8FewCall {
+  int M, N, K, E;
+  const uint8_t* a;  long long ld_a;
+  const float* sa;  long long ld_sa;
+  const uint8_t* b;  long long ld_b;
+  const float* sb;
+  const int32_t* offsets;    // NULL: one segment
+  void* c;  long long ld_c;
+  int f32;
+  DevError* err;
+};
+cudaError_t launch_fp8_few(const Fp8FewCall& a, cudaStream_t stream);
 // W13 [E, 2I, cols] (bf16, or E4M3 bytes) as (cols, I, 2E): a box of box_rows gate
 // rows of expert e followed by the same rows of its up half (coordinates
 // (k, row within the half, 2e)), one 128-byte swizzled K chunk wide
