@@ -217,6 +217,71 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   return r;
 }
 
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// The larger magnitudes of two pairs of bf16 (a NaN stays: all ones below the sign).
+__device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+  const __nv_bfloat162 v = __hmax2_nan(__habs2(*reinterpret_cast<const __nv_bfloat162*>(&a)),
+                                       __habs2(*reinterpret_cast<const __nv_bfloat162*>(&b)));
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+// Four neighbours as two pairs.
+__device__ __forceinline__ void pairs_of(uint2 q, uint64_t (&v)[2]) {
+  v[0] = pair(__uint_as_float(q.x << 16), __uint_as_float(q.x & 0xFFFF0000u));
+  v[1] = pair(__uint_as_float(q.y << 16), __uint_as_float(q.y & 0xFFFF0000u));
+}
+__device__ __forceinline__ void load_pairs(const uint16_t* p, uint64_t (&v)[2]) {
+  pairs_of(__ldg(reinterpret_cast<const uint2*>(p)), v);
+}
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
+  const float4 q = __ldg(reinterpret_cast<const float4*>(p));
+  v[0] = pair(q.x, q.y);
+  v[1] = pair(q.z, q.w);
+}
+// Sigmoids of two values, as sigmoid() has them.
+__device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
+  float a, b;
+  unpair(mul2(g, pair(-1.44269504f, -1.44269504f)), a, b);
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("ex2.approx.ftz.f32 %0, %0;" : "+f"(b));
+  unpair(add2(pair(a, b), pair(1.f, 1.f)), a, b);
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rcp.approx.ftz.f32 %0, %0;" : "+f"(b));
+  return pair(a, b);
+}
+
+// SwiGLU's gradient of four neighbours, at up or at the gate.  t = dh s: t c, t u (1 + c - c s).
+// Outside the limits the factor is 0 and not the gradient, so that a NaN passes.
+__device__ __forceinline__ void gradient2(uint64_t (&g)[2], uint64_t (&u)[2], uint64_t (&d)[2],
+                                          float clamp, bool at_up, uint64_t (&v)[2]) {
+  const uint64_t one = pair(1.f, 1.f);
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    if (clamp > 0.f) {
+      float x, y, p, q, e, f;
+      unpair(g[j], x, y);
+      unpair(u[j], p, q);
+      unpair(d[j], e, f);
+      e = fabsf(at_up ? p : x) > clamp ? e * 0.f : e;
+      f = fabsf(at_up ? q : y) > clamp ? f * 0.f : f;
+      g[j] = pair(clip(x, clamp), clip(y, clamp));
+      u[j] = pair(clip(p, clamp), clip(q, clamp));
+      d[j] = pair(e, f);
+    }
+    const uint64_t s = sigmoid2(g[j]), t = mul2(d[j], s);
+    v[j] = at_up ? mul2(t, g[j])
+                 : mul2(mul2(t, u[j]), fma2(g[j] ^ 0x8000000080000000ull, s, add2(one, g[j])));
+  }
+}
+
 // Asynchronous copy of BYTES (8 or 16) into shared memory, zeros where `there` is false.
 template <int BYTES>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -284,25 +349,31 @@ __device__ __forceinline__ void advance(const QuantArgs& a, const Segments& seg,
 }
 
 // Operands that v is made of, and whether a thread's share of them is copied ahead into
-// shared memory (64 KB a CTA at most, so that two fit an SM).
+// shared memory: 64 KB a CTA at most where two are to fit an SM; the gradient's three bf16
+// operands take 96 KB and a CTA an SM, whose threads have registers for both its halves
+// (65536 x 1536 134 us against 167 without).
 template <int SRC, typename T, bool VEC>
 struct Share {
   static constexpr int OPS = SRC == MOE_FP8_ROWS ? 1 : SRC + 1;
   static constexpr int PIECE = 4 * (int)sizeof(T);
-  static constexpr bool AHEAD = VEC && OPS * sizeof(T) <= 4;
+  static constexpr bool AHEAD = VEC && OPS * sizeof(T) <= 6;
   static constexpr int BYTES = AHEAD ? OPS * 8 * PIECE * kThreads : 0;
+  static constexpr int PER_SM = AHEAD && OPS == 3 ? 1 : 2;
 };
 
 // SRC: what v is.  COLS: codes along the columns are wanted.  BLOCKS: one scale a tile (weights, E matrices of M rows); else one a
 // row and one a column of the tile.
 template <int SRC, typename T, bool VEC, bool BLOCKS, bool COLS>
-__global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
+__global__ void __launch_bounds__(kThreads, (Share<SRC, T, VEC>::PER_SM))
+    k_fp8_quant(const QuantArgs a) {
   using S = Share<SRC, T, VEC>;
   constexpr bool AHEAD = S::AHEAD;
   constexpr bool PACKED = SRC == MOE_FP8_ROWS && VEC && sizeof(T) == 2;   // v are bf16 words
   constexpr int OPS = S::OPS, PIECE = S::PIECE;
   // the gradient's two halves from one reading, where a block lies on one side
   const int passes = a.run_blocks < a.col_blocks ? 2 : 1;
+  constexpr bool GRAD = SRC == MOE_FP8_SWIGLU_GRAD;
+  const bool in_ring = AHEAD && (!GRAD || passes == 2);
   extern __shared__ uint4 ring[];                // [row of the warp][operand][thread]
   __shared__ Segments seg;
   // the warps' largest magnitudes of the columns; a row 32 (16) bytes longer than it is
@@ -320,9 +391,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
   const uint32_t my_ring = smem_u32(ring) + threadIdx.x * PIECE;
   auto copy = [&](const Place& p) {
     const int col = (p.cb << 7) + 4 * lane;
-    const bool in = col < a.width;
+    const bool in = col < (GRAD ? a.C : a.width);
     const T* x = static_cast<const T*>(a.x) + (BLOCKS ? (long long)p.e * a.M * a.ld_x : 0LL) +
                  (in ? col : 0);
+    const T* const dh = static_cast<const T*>(a.dh) + (in ? col : 0);
     // (all there in all but the last blocks: no tests then)
     if (__all_sync(kAll, in && (lane >= 8 || p.source >= 0))) {
 #pragma unroll
@@ -331,6 +403,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
         copy_async<PIECE>(my_ring + (i * OPS) * (kThreads * PIECE), q);
         if (SRC != MOE_FP8_ROWS)
           copy_async<PIECE>(my_ring + (i * OPS + 1) * (kThreads * PIECE), q + a.C);
+        if (GRAD)
+          copy_async<PIECE>(my_ring + (i * OPS + 2) * (kThreads * PIECE),
+                            dh + (long long)(p.row0 + i) * a.ld_dh);
       }
     } else {
 #pragma unroll
@@ -341,6 +416,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
         copy_async<PIECE>(my_ring + (i * OPS) * (kThreads * PIECE), q, there);
         if (SRC != MOE_FP8_ROWS)
           copy_async<PIECE>(my_ring + (i * OPS + 1) * (kThreads * PIECE), q + a.C, there);
+        if (GRAD)
+          copy_async<PIECE>(my_ring + (i * OPS + 2) * (kThreads * PIECE),
+                            dh + (long long)(there ? p.row0 + i : 0) * a.ld_dh, there);
       }
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
@@ -350,18 +428,42 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
   next.unit = blockIdx.x;
   if (next.unit < units) {
     decode<BLOCKS>(a, seg, next);
-    if (AHEAD) copy(next);
+    if (in_ring) copy(next);
   }
   while (next.unit < units) {
     const Place t = next;
     advance<BLOCKS>(a, seg, units, next);
+    uint2 held[GRAD && AHEAD ? 8 : 1][3];         // gate, up, dh of both halves
     for (int pass = 0; pass < passes; ++pass) {
     const int cb = t.cb + pass * a.run_blocks;
     const int col = (cb << 7) + 4 * lane;
     const int n = a.width - col;                 // columns of this lane that are there
     uint64_t v[8][2];                            // two neighbours a word
     uint2 raw[PACKED ? 8 : 1];                   // four bf16
-    if (AHEAD) {
+    if (GRAD && in_ring) {
+      if constexpr (GRAD && AHEAD) {
+        if (pass == 0) {
+          asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 3; ++j)
+              held[i][j] = *reinterpret_cast<const uint2*>(
+                  reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
+                  (size_t)(i * OPS + j) * (kThreads * PIECE));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          uint64_t g[2], u[2], d[2];
+          pairs_of(held[i][0], g);
+          pairs_of(held[i][1], u);
+          pairs_of(held[i][2], d);
+          gradient2(g, u, d, a.clamp, pass == 1, v[i]);
+        }
+        // (what was read has been used: the next block's share may take its place)
+        if (pass == 0 && next.unit < units) copy(next);
+      }
+    } else if (in_ring) {
       asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -371,30 +473,44 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
           raw[i] = *reinterpret_cast<const uint2*>(p);
           v[i][0] = pair(__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xFFFF0000u));
           v[i][1] = pair(__uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xFFFF0000u));
+        } else if (SRC == MOE_FP8_ROWS) {
+          const float4 q = *reinterpret_cast<const float4*>(p);
+          v[i][0] = pair(q.x, q.y);
+          v[i][1] = pair(q.z, q.w);
         } else {
-          float f[4];
-          if (SRC == MOE_FP8_ROWS) {
-            const float4 q = *reinterpret_cast<const float4*>(p);
-            f[0] = q.x; f[1] = q.y; f[2] = q.z; f[3] = q.w;
-          } else {
-            const uint2 g = *reinterpret_cast<const uint2*>(p);
-            const uint2 u = *reinterpret_cast<const uint2*>(p + kThreads * PIECE);
-            const float gf[4] = {__uint_as_float(g.x << 16), __uint_as_float(g.x & 0xFFFF0000u),
-                                 __uint_as_float(g.y << 16), __uint_as_float(g.y & 0xFFFF0000u)};
-            const float uf[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                                 __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u)};
+          uint64_t g[2], u[2];
+          pairs_of(*reinterpret_cast<const uint2*>(p), g);
+          pairs_of(*reinterpret_cast<const uint2*>(p + kThreads * PIECE), u);
+          if (a.clamp > 0.f) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float c = clip(gf[j], a.clamp);
-              f[j] = c * sigmoid(c) * clip(uf[j], a.clamp);
+            for (int j = 0; j < 2; ++j) {
+              float x, y;
+              unpair(g[j], x, y);
+              g[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
+              unpair(u[j], x, y);
+              u[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
             }
           }
-          v[i][0] = pair(f[0], f[1]);
-          v[i][1] = pair(f[2], f[3]);
+#pragma unroll
+          for (int j = 0; j < 2; ++j) v[i][j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
         }
       }
       // the next block's share arrives while this one is worked on
       if (next.unit < units) copy(next);
+    } else if (GRAD && VEC && passes == 2) {
+      const int c0 = (t.cb << 7) + 4 * lane;       // column of the operands
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[i][0] = v[i][1] = 0;
+        if (i < t.rows && n > 0) {
+          const T* const x = static_cast<const T*>(a.x) + (long long)(t.row0 + i) * a.ld_x + c0;
+          uint64_t g[2], u[2], d[2];
+          load_pairs(x, g);
+          load_pairs(x + a.C, u);
+          load_pairs(static_cast<const T*>(a.dh) + (long long)(t.row0 + i) * a.ld_dh + c0, d);
+          gradient2(g, u, d, a.clamp, pass == 1, v[i]);
+        }
+      }
     } else {
       const long long base = BLOCKS ? (long long)t.e * a.M : 0LL;
 #pragma unroll
@@ -420,12 +536,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_fp8_quant(const QuantArgs a) {
         uint32_t r[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const uint32_t p = raw[i + j].x & 0x7FFF7FFFu, q = raw[i + j].y & 0x7FFF7FFFu;
           if (COLS) {
-            m.x = __vmaxu2(m.x, p);
-            m.y = __vmaxu2(m.y, q);
+            m.x = larger(m.x, raw[i + j].x);
+            m.y = larger(m.y, raw[i + j].y);
           }
-          r[j] = __vmaxu2(p, q);
+          r[j] = larger(raw[i + j].x, raw[i + j].y);
         }
         w[i >> 1] = __vmaxu2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[0], r[1], 0x7632));
       }
@@ -612,7 +727,7 @@ cudaError_t launch_with(const QuantArgs& a, dim3 g, dim3 b, cudaStream_t st) {
 
 template <int SRC, typename T, bool BLOCKS>
 cudaError_t launch(QuantArgs a, bool vec, cudaStream_t st) {
-  const int most = 2 * num_sms();
+  const int most = (vec ? Share<SRC, T, true>::PER_SM : 2) * num_sms();
   a.run_blocks = SRC == MOE_FP8_SWIGLU_GRAD && vec && a.C % 128 == 0 ? a.C / 128 : a.col_blocks;
   // runs as long as leave every CTA some six of them
   const long long each = (long long)a.row_blocks * a.run_blocks / (6LL * most);
