@@ -27,7 +27,7 @@ struct Fp8GemmArgs {
   const int32_t* offsets;            // [E+1] or NULL: one segment
   void* c;  long long ld_c;
   int row_blocks;                    // weights: blocks of 128 that the codes have
-  int f32, accumulate, wide;         // wide: 32-byte stores (weights: 8-byte)
+  int f32, accumulate, wide;         // wide: 16-byte stores (weights: 8-byte)
   DevError* err;
 };
 
@@ -141,12 +141,6 @@ __device__ __forceinline__ void arrive_lane0(uint32_t bar, int lane) {
       : "memory");
 }
 
-__device__ __forceinline__ void st_global_32B(void* p, const uint32_t (&w)[8]) {
-  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
-               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
-               : "memory");
-}
-
 // Asynchronous copy of 4 bytes into shared memory, zero where `there` is false.
 __device__ __forceinline__ void copy4(uint32_t dst, const float* src, bool there) {
   const int n = there ? 4 : 0;
@@ -167,7 +161,7 @@ struct Shape {
                 "what the first warps give up is all that there is");
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int TURN = WGRAD ? 0 : SUM_WARPS * 32 * 9 * 4;   // narrow stores, a warp 32 x 8
+  static constexpr int TURN = WGRAD ? 0 : SUM_WARPS * 32 * 80;   // a warp's 32 rows x 64 bytes
   // scales of GROUP blocks: of each its 128 rows', then (weights) BN columns' or the two
   // weight blocks'
   static constexpr int GROUP = 4, SLOTS = 4, BLOCK = 512 + (WGRAD ? BN * 4 : 16);
@@ -266,7 +260,7 @@ struct Reader {
 template <int BN>
 __device__ __forceinline__ void sum_rows(const Fp8GemmArgs& args, const Tile& ti, Reader& rd,
                                          uint32_t lane_base, int quarter, int group, int lane,
-                                         float* turn) {
+                                         uint8_t* turn) {
   using S = Shape<BN, false>;
   constexpr int WIDE = S::WIDE, CH = 32;         // CH: columns a load
   const int row = quarter * 32 + lane, r = ti.m0 + row, c0 = ti.n0 + group * WIDE;
@@ -324,65 +318,64 @@ __device__ __forceinline__ void sum_rows(const Fp8GemmArgs& args, const Tile& ti
     }
   }
   // ---- out ----
+  // 64 bytes of each of the warp's rows at a time are turned in shared memory (rows 80 bytes
+  // apart, so that neither side meets in a bank), and four lanes write a row's, or all of
+  // them its single elements where rows are not aligned (N = 4095 118 us, N = 4096 107).
   const int n_here = min(WIDE, args.N - c0);     // columns of this warp
   if (n_here <= 0) return;
-  if (args.wide && n_here == WIDE) {
-    if (!row_in) return;
-    if (args.f32) {
-      float* p = static_cast<float*>(args.c) + r * args.ld_c + c0;
+  const int rows_here = min(32, ti.m1 - ti.m0 - quarter * 32);
+  const long long row0 = r - lane;               // the warp's first row
+  auto put = [&](auto type, const uint32_t (&w)[16], int first) {
+    using T = decltype(type);
+    constexpr int COLS = 64 / (int)sizeof(T), EACH = 16 / (int)sizeof(T);
+    __syncwarp();
 #pragma unroll
-      for (int i = 0; i < WIDE / 8; ++i) {
-        uint32_t w[8];
+    for (int q = 0; q < 4; ++q)
+      *reinterpret_cast<uint4*>(turn + lane * 80 + 16 * q) =
+          make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]);
+    __syncwarp();
+    T* const out = static_cast<T*>(args.c) + row0 * args.ld_c + c0 + first;
+    if (args.wide && first + COLS <= n_here) {
+      const int q = lane & 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float x, y;
-          unpair(acc[4 * i + j], x, y);
-          w[2 * j] = __float_as_uint(x);
-          w[2 * j + 1] = __float_as_uint(y);
-        }
-        st_global_32B(p + 8 * i, w);
+      for (int i = 0; i < 4; ++i) {
+        const int k = 8 * i + (lane >> 2);
+        if (k < rows_here)
+          *reinterpret_cast<uint4*>(out + k * args.ld_c + EACH * q) =
+              *reinterpret_cast<const uint4*>(turn + k * 80 + 16 * q);
       }
     } else {
-      uint16_t* p = static_cast<uint16_t*>(args.c) + r * args.ld_c + c0;
-#pragma unroll
-      for (int i = 0; i < WIDE / 16; ++i) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float x, y;
-          unpair(acc[8 * i + j], x, y);
-          w[j] = pack_bf2(x, y);
-        }
-        st_global_32B(p + 16 * i, w);
-      }
+      constexpr int AT_ONCE = 32 / COLS;         // rows
+      const int c = lane % COLS;
+      if (first + c < n_here)
+        for (int k = lane / COLS; k < rows_here; k += AT_ONCE)
+          out[k * args.ld_c + c] = *reinterpret_cast<const T*>(turn + k * 80 + c * sizeof(T));
     }
-    return;
-  }
-  // rows of any width: 8 columns at a time turned, so that a quarter of a warp writes a row's
-  // neighbours
-  const int rows_here = min(32, ti.m1 - ti.m0 - quarter * 32);
-  const int q0 = lane >> 3, c = lane & 7;
+  };
+  if (args.f32) {
 #pragma unroll
-  for (int i = 0; i < WIDE / 8; ++i) {
-    __syncwarp();
+    for (int i = 0; i < WIDE / 16; ++i) {
+      uint32_t w[16];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float x, y;
-      unpair(acc[4 * i + j], x, y);
-      turn[lane * 9 + 2 * j] = x;
-      turn[lane * 9 + 2 * j + 1] = y;
-    }
-    __syncwarp();
-    if (8 * i + c < n_here) {
-      const long long at0 = (long long)(r - lane) * args.ld_c + c0 + 8 * i + c;
-      for (int q = q0; q < rows_here; q += 4) {
-        const float v = turn[q * 9 + c];
-        const long long at = at0 + q * args.ld_c;
-        if (args.f32)
-          static_cast<float*>(args.c)[at] = v;
-        else
-          static_cast<uint16_t*>(args.c)[at] = f2bf(v);
+      for (int j = 0; j < 8; ++j) {
+        float x, y;
+        unpair(acc[8 * i + j], x, y);
+        w[2 * j] = __float_as_uint(x);
+        w[2 * j + 1] = __float_as_uint(y);
       }
+      put(float(), w, 16 * i);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < WIDE / 32; ++i) {
+      uint32_t w[16];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        float x, y;
+        unpair(acc[16 * i + j], x, y);
+        w[j] = pack_bf2(x, y);
+      }
+      put(uint16_t(), w, 32 * i);
     }
   }
   __syncwarp();
@@ -491,8 +484,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
-  float* const turn_all = reinterpret_cast<float*>(smem + STAGES * S::STAGE);
-  float* const slots = turn_all + S::TURN / 4;
+  uint8_t* const turn_all = smem + STAGES * S::STAGE;
+  float* const slots = reinterpret_cast<float*>(turn_all + S::TURN);
   const uint32_t bar0 = smem_u32(slots + SLOTS * S::SLOT / 4);
   auto full_bar = [&](int s) { return bar0 + 8u * s; };
   auto empty_bar = [&](int s) { return bar0 + 8u * (STAGES + s); };
@@ -698,7 +691,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
         sum_weights<BN>(args, ti, rd, lane_base, quarter, group, lane);
       else
         sum_rows<BN>(args, ti, rd, lane_base, quarter, group, lane,
-                     turn_all + (warp - 4) * 32 * 9);
+                     turn_all + (warp - 4) * 32 * 80);
       // after a wait that gave up nothing waits any more, and the tile's end leaves
       rd.ok = __all_sync(0xffffffffu, rd.ok);
       if (!rd.ok) break;
@@ -780,7 +773,7 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
   g.sa = a_scales; g.ld_sa = ld_as; g.sb = b_scales;
   g.offsets = offsets; g.c = c; g.ld_c = ld_c;
   g.f32 = es == 4;
-  g.wide = aligned(c, 32) && ld_c * es % 32 == 0;
+  g.wide = aligned(c, 16) && ld_c * es % 16 == 0;
   g.err = static_cast<DevError*>(status);
   // 128 columns a tile, and four parts of tensor memory, where 256 leave SMs without a tile
   // (experts count with half a tile each beside their rows).  One wave of M = 1003, N = 1537,
