@@ -575,7 +575,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     }
     for (int s = 0; s < STAGES && ok; ++s) {     // every stage has been released
       if (elect_one()) ok = mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 2);
-      __syncwarp();
+      ok = __all_sync(0xffffffffu, ok);
       if (++stage == STAGES) {
         stage = 0;
         phase ^= 1u;
@@ -588,6 +588,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     __syncwarp();
   } else if (warp == 1) {
     // ---------------- MMA: a block of 128 a time ----------------
+    // (the whole warp walks the loop, so that its values are uniform; one lane issues)
     {
       const uint64_t a0 = smem_desc_sw128(stage0, 16, 1024);
       const uint64_t b0 = smem_desc_sw128(stage0 + S::A_BYTES, 16, 1024);

@@ -256,6 +256,63 @@ def test_experts(moe, counts, N, K, dtype):
     assert lin.check() == (moe.MOE_OK, 0)
 
 
+@pytest.mark.parametrize("counts", [[1], [8], [9], [0, 1, 0, 20, 3], [32], [0, 0, 17, 8, 1, 5],
+                                    [1] * 31, [0] * 6])
+@pytest.mark.parametrize("N,K", [(16, 128), (40, 3001), (33, 17), (8, 20000)])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_few_rows_of_experts(moe, counts, N, K, dtype):
+    """Up to 32 rows, 32 of one expert among them, and more blocks than are on their way."""
+    E, used = len(counts), sum(counts)
+    first = min(1, 32 - used)
+    M = max(used + first, 1)
+    q, wq, _, x, w = operands(moe, M, N, K, E, N + used)
+    offsets = offsets_of(counts) + first
+    lin = moe.MoeFp8Linear(N, K, E, dtype=TYPES[dtype])
+    out = torch.full((M, N + 1), 7.0, dtype=TYPES[dtype]).cuda()
+    lin.forward(q, wq, offsets=offsets.cuda(), out=out[:, :N])
+    got, at = f32(out), offsets.tolist()
+    for e in range(E):
+        rows = slice(at[e], at[e + 1])
+        ref.check_product(got[rows, :N], x[rows], w[e], "expert %d" % e, bf16=dtype == "bf16")
+    assert (got[:first] == 7).all() and (got[at[-1]:] == 7).all() and (got[:, N:] == 7).all()
+    assert lin.check() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("N,K", [(1500, 1300), (1501, 257)])
+def test_more_tiles_than_processors(moe, N, K):
+    """Every CTA takes several tiles, with all of its rings going round."""
+    M = 7000
+    q, wq, _, x, w = operands(moe, M, N, K, 1, 31)
+    y = moe.MoeFp8Linear(N, K, dtype=torch.float32).forward(q, wq)
+    ref.check_product(f32(y), x, w[0], "y")
+    E, counts = 6, [700, 0, 130, 1, 900, 300]
+    offsets = offsets_of(counts)
+    both = dict(offsets=offsets.cuda(), by_row=False, by_column=True)
+    g = gen(32)
+    _, dy = moe.quantize_fp8(torch.randn(sum(counts), N, generator=g).cuda(), **both)
+    _, xt = moe.quantize_fp8(torch.randn(sum(counts), K, generator=g).cuda(), **both)
+    dw = f32(moe.MoeFp8Linear(N, K, E).grad_weight(dy, xt, offsets=offsets.cuda()))
+    n, _ = ref.columns(offsets.tolist(), sum(counts))
+    a, b = (ref.values(bytes_of(m.codes)[:, :n[-1]], f32(m.scales)[:n[-1] // 128])
+            for m in (dy, xt))
+    for e in range(E):
+        cols = slice(n[e], n[e + 1])
+        ref.check_product(dw[e], a[:, cols], b[:, cols], "dw %d" % e)
+
+
+def test_every_significand(moe):
+    """Scales of all 2^23 significands are the rounded quotients."""
+    top = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(0x3F800000)).view(np.float32)
+    q, _ = moe.quantize_fp8(torch.from_numpy(top)[:, None].cuda())
+    assert np.array_equal(f32(q.scales)[0], top / np.float32(448))
+    # and the factors: 300 / x times x / 300 of a second element lands on a code's border or
+    # on one side of it as the rounded product says
+    x = np.stack([top, top * np.float32(0.0390625)], 1)       # codes of 17.5, between 17 and 18
+    q, _ = moe.quantize_fp8(torch.from_numpy(x).cuda())
+    want = ref.e4m3(x * (np.float32(448) / top)[:, None])
+    assert np.array_equal(bytes_of(q.codes), want)
+
+
 def test_many_experts(moe):
     g = gen(11)
     E, N, K = 256, 192, 384
