@@ -2,6 +2,7 @@
 
 import collections
 import ctypes
+import functools
 import os
 import threading
 
@@ -840,18 +841,33 @@ class MoeBlockNorm:
 Fp8Matrix = collections.namedtuple("Fp8Matrix", "codes scales")
 
 
+class _Types:
+    """What of torch the calls below look up, found at its first use (an import statement in
+    each of them costs a tenth of a small call)."""
+
+    def __getattr__(self, name):
+        import torch
+
+        self.f8, self.f32, self.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        self.code = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
+        self.empty, self.zeros = torch.empty, torch.zeros
+        return self.__dict__[name]
+
+
+_types = _Types()
+
+
 def _codes(t, what, shape, dev):
     """t: E4M3 codes [..., width] whose rows lie a multiple of 16 bytes apart (address, row
     distance); a batch's matrices follow one another."""
-    import torch
-
-    if t.dtype is torch.float8_e4m3fn and t.shape == shape and t.get_device() == dev:
-        if t.is_contiguous() and shape[-1] % 16 == 0:
-            return t.data_ptr(), shape[-1]
+    if t.dtype is _types.f8 and t.shape == shape and t.get_device() == dev:
+        width = shape[-1]
+        if width % 16 == 0 and t.is_contiguous():
+            return t.data_ptr(), width
         st = t.stride()
         ld = st[-2] if shape[-2] > 1 else (st[-3] if len(shape) == 3 and shape[0] > 1
-                                           else (shape[-1] + 15) // 16 * 16)
-        if ((st[-1] == 1 or shape[-1] == 1) and ld % 16 == 0 and ld >= shape[-1] and
+                                           else (width + 15) // 16 * 16)
+        if ((st[-1] == 1 or width == 1) and ld % 16 == 0 and ld >= width and
                 (len(shape) == 2 or shape[0] == 1 or st[0] == shape[1] * ld)):
             return t.data_ptr(), ld
     raise MoeError(MOE_ERR_INVALID_ARG, "%s: want float8_e4m3fn %s on the current GPU (%d), rows a "
@@ -861,23 +877,28 @@ def _codes(t, what, shape, dev):
 
 def _new_codes(lead, width, device):
     """Codes [*lead, width] with rows a multiple of 16 bytes apart."""
-    import torch
-
-    ld = (width + 15) // 16 * 16
-    return torch.empty((*lead, ld), dtype=torch.float8_e4m3fn, device=device)[..., :width]
+    if width % 16 == 0:
+        return _types.empty((*lead, width), dtype=_types.f8, device=device)
+    return _types.empty((*lead, (width + 15) // 16 * 16), dtype=_types.f8,
+                        device=device)[..., :width]
 
 
 def _offsets(offsets, E, dev):
     """Address of the offsets and the number of segments."""
-    import torch
-
     if offsets is None:
         if E not in (None, 1):
             raise MoeError(MOE_ERR_INVALID_ARG, "%d experts need offsets" % E)
         return None, 1
     if E is None:
         E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
-    return _want(offsets, "offsets", torch.int32, (E + 1,), dev), E
+    return _want(offsets, "offsets", _types.i32, (E + 1,), dev), E
+
+
+@functools.lru_cache(maxsize=256)
+def _quant_desc(source, C, dtype, E, clamp, flags):
+    """A description and its address."""
+    desc = Fp8QuantDesc(source, C, dtype, E, clamp, flags)
+    return desc, ctypes.addressof(desc)
 
 
 def fp8_columns(M, E=1, offsets=True):
@@ -888,39 +909,48 @@ def fp8_columns(M, E=1, offsets=True):
 
 def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_column, out, out_t,
                   what):
-    import torch
-
-    _rows_fit(max(M, x.shape[0]), what)
     if not (by_row or by_column) or (out is not None and not by_row) or (
             out_t is not None and not by_column):
         raise MoeError(MOE_ERR_INVALID_ARG, "%s: out goes with by_row, out_t with by_column, and "
                        "one of them is needed" % what)
-    dev, at, f32 = _device(), x.device, torch.float32
-    dtype = _dtype_code(x.dtype, what)
+    L = _lib if _lib is not None else lib()
+    n_src = x.shape[0]
+    _rows_fit(M if M > n_src else n_src, what)
+    dev, f32, dtype = _device(), _types.f32, x.dtype
+    code = _types.code.get(dtype)
+    if code is None:
+        code = _dtype_code(dtype, what)
     width = 2 * C if source == MOE_FP8_SWIGLU_GRAD else C
-    xp, ld_x = _rows(x, "x", x.dtype, (x.shape[0], C if source == MOE_FP8_ROWS else 2 * C), dev)
-    dp, ld_d = (None, 0) if dh is None else _rows(dh, "dh", x.dtype, (M, C), dev)
-    rp = _maybe(rows, "rows", torch.int32, (M,), dev)
-    fp, E = _offsets(offsets, None, dev)
-    cp = sp = tp = up = None
-    ld_c = ld_s = ld_t = ld_u = R = 0
+    blocks = (width + 127) // 128
+    xp, ld_x = _rows(x, "x", dtype, (n_src, C if source == MOE_FP8_ROWS else 2 * C), dev)
+    dp = rp = fp = cp = sp = tp = up = None
+    ld_d = ld_c = ld_s = ld_t = ld_u = R = 0
+    E = 1
+    if dh is not None:
+        dp, ld_d = _rows(dh, "dh", dtype, (M, C), dev)
+    if rows is not None:
+        rp = _want(rows, "rows", _types.i32, (M,), dev)
+    if offsets is not None:
+        fp, E = _offsets(offsets, None, dev)
     if by_row:
         if out is None:
-            out = Fp8Matrix(_new_codes((M,), width, at),
-                            torch.empty(((width + 127) // 128, M), dtype=f32, device=at))
+            out = Fp8Matrix(_new_codes((M,), width, x.device),
+                            _types.empty((blocks, M), dtype=f32, device=x.device))
         cp, ld_c = _codes(out[0], "codes", (M, width), dev)
-        sp, ld_s = _rows(out[1], "scales", f32, ((width + 127) // 128, M), dev)
+        sp, ld_s = _rows(out[1], "scales", f32, (blocks, M), dev)
     if by_column:
         if out_t is None:
             R = fp8_columns(M, E, offsets is not None)
-            out_t = Fp8Matrix(torch.empty((width, R), dtype=torch.float8_e4m3fn, device=at),
-                              torch.empty((R // 128, width), dtype=f32, device=at))
+            out_t = Fp8Matrix(_new_codes((width,), R, x.device),
+                              _types.empty((R // 128, width), dtype=f32, device=x.device))
         R = out_t[0].shape[-1]
         tp, ld_t = _codes(out_t[0], "codes_t", (width, R), dev)
         up, ld_u = _rows(out_t[1], "scales_t", f32, (R // 128, width), dev)
-    desc = Fp8QuantDesc(source, C, dtype, E, clamp, MOE_FP8_POW2 if pow2 else 0)
-    _check(_lib.moe_fp8_quantize(ctypes.addressof(desc), M, xp, ld_x, x.shape[0], dp, ld_d, rp, fp,
-                                 cp, ld_c, sp, ld_s, tp, ld_t, R, up, ld_u, _raw_stream(dev)), what)
+    rc = L.moe_fp8_quantize(_quant_desc(source, C, code, E, clamp, MOE_FP8_POW2 if pow2 else 0)[1],
+                            M, xp, ld_x, n_src, dp, ld_d, rp, fp, cp, ld_c, sp, ld_s, tp, ld_t, R,
+                            up, ld_u, _raw_stream(dev))
+    if rc:
+        _check(rc, what)
     return (Fp8Matrix(*out) if by_row else None), (Fp8Matrix(*out_t) if by_column else None)
 
 
@@ -931,12 +961,11 @@ def quantize_fp8(x, rows=None, offsets=None, pow2=False, by_row=True, by_column=
     rows [M] int32 gathers (zeros where it is out of range); offsets [E+1] int32 are the
     experts' rows.  -> (by row: Fp8Matrix(codes [M, C], scales [ceil(C/128), M]) or None,
     by column: Fp8Matrix(codes [C, R], scales [R/128, C]) or None)."""
-    import torch
-
     if stream is not None:               # the outputs then belong to that stream too
+        import torch
+
         with torch.cuda.stream(stream):
             return quantize_fp8(x, rows, offsets, pow2, by_row, by_column, out, out_t)
-    lib()
     M = x.shape[0] if rows is None else rows.shape[0]
     return _quantize_fp8(MOE_FP8_ROWS, x, x.shape[1], M, None, rows, offsets, 0.0, pow2, by_row,
                          by_column, out, out_t, "quantize_fp8")
@@ -945,12 +974,11 @@ def quantize_fp8(x, rows=None, offsets=None, pow2=False, by_row=True, by_column=
 def swiglu_fp8(a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=False, out=None,
                out_t=None, stream=None):
     """Codes of silu(g) * u for a = [g | u] [M, 2C], as quantize_fp8."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return swiglu_fp8(a, clamp, offsets, pow2, by_row, by_column, out, out_t)
-    lib()
     return _quantize_fp8(MOE_FP8_SWIGLU, a, a.shape[1] // 2, a.shape[0], None, None, offsets,
                          clamp, pow2, by_row, by_column, out, out_t, "swiglu_fp8")
 
@@ -958,12 +986,11 @@ def swiglu_fp8(a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=Fa
 def swiglu_grad_fp8(dh, a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=False,
                     out=None, out_t=None, stream=None):
     """Codes of the gradient [M, 2C] at a = [g | u] from dh [M, C], as quantize_fp8."""
-    import torch
-
     if stream is not None:
+        import torch
+
         with torch.cuda.stream(stream):
             return swiglu_grad_fp8(dh, a, clamp, offsets, pow2, by_row, by_column, out, out_t)
-    lib()
     return _quantize_fp8(MOE_FP8_SWIGLU_GRAD, a, a.shape[1] // 2, a.shape[0], dh, None, offsets,
                          clamp, pow2, by_row, by_column, out, out_t, "swiglu_grad_fp8")
 
@@ -1011,77 +1038,91 @@ class MoeFp8Linear:
         code = _dtype_code(self.dtype, "MoeFp8Linear")
         if not (0 < N <= MOE_FP8_MAX_WIDTH and 0 < K <= MOE_FP8_MAX_WIDTH and 0 < E <= 256):
             raise MoeError(MOE_ERR_INVALID_ARG, "MoeFp8Linear(%d,%d,%d)" % (N, K, E))
-        self.desc = Fp8GemmDesc(N, K, E, code)
-        self._desc_t = Fp8GemmDesc(K, N, E, code)
+        self._ahead, self._back = self._side(N, K, E, code), self._side(K, N, E, code)
         self.status = torch.zeros(4, dtype=torch.int32, device=device)
 
-    def _product(self, desc, x, w, offsets, out, what):
-        import torch
+    @staticmethod
+    def _side(N, K, E, code):
+        """A description, its address and the shapes that go with it."""
+        desc = Fp8GemmDesc(N, K, E, code)
+        return (desc, ctypes.addressof(desc), N, K, (K + 127) // 128, (E, N, K),
+                (E, (N + 127) // 128, (K + 127) // 128))
 
-        N, K, E = desc.N, desc.K, desc.E
-        dev, f32 = _device(), torch.float32
+    def _product(self, side, x, w, offsets, out, what):
+        _, desc, N, K, blocks, w_shape, s_shape = side
+        x, scales = x
+        w, w_scales = w
+        dev, f32 = _device(), _types.f32
         _scratch_on(self.status, dev)
-        M = x[0].shape[0]
+        M = x.shape[0]
         _rows_fit(M, what)
-        ap, ld_a = _codes(x[0], "codes", (M, K), dev)
-        sp, ld_s = _rows(x[1], "scales", f32, ((K + 127) // 128, M), dev)
-        wc = w[0] if w[0].dim() == 3 else w[0][None]
-        bp, ld_b = _codes(wc, "weights' codes", (E, N, K), dev)
-        ws = w[1] if w[1].dim() == 3 else w[1][None]
-        wp = _want(ws, "weights' scales", f32, (E, (N + 127) // 128, (K + 127) // 128), dev)
-        fp, _ = _offsets(offsets, E, dev)
+        ap, ld_a = _codes(x, "codes", (M, K), dev)
+        sp, ld_s = _rows(scales, "scales", f32, (blocks, M), dev)
+        if w.dim() == 2:
+            w, w_scales = w[None], w_scales[None]
+        bp, ld_b = _codes(w, "weights' codes", w_shape, dev)
+        wp = _want(w_scales, "weights' scales", f32, s_shape, dev)
+        fp = _offsets(offsets, w_shape[0], dev)[0]
         if out is None:
-            out = torch.empty((M, N), dtype=self.dtype, device=x[0].device)
+            out = _types.empty((M, N), dtype=self.dtype, device=x.device)
             op, ld_o = out.data_ptr(), N
         else:
             op, ld_o = _rows(out, "out", self.dtype, (M, N), dev)
-        _check(_lib.moe_fp8_gemm(ctypes.addressof(desc), M, ap, ld_a, sp, ld_s, bp, ld_b, wp, fp,
-                                 op, ld_o, self.status.data_ptr(), _raw_stream(dev)), what)
+        rc = _lib.moe_fp8_gemm(desc, M, ap, ld_a, sp, ld_s, bp, ld_b, wp, fp, op, ld_o,
+                               self.status.data_ptr(), _raw_stream(dev))
+        if rc:
+            _check(rc, what)
         return out
 
     def forward(self, x, w, offsets=None, out=None, stream=None):
         """y [M, N] = x w[e]^T of x by rows [M, K] and weights w; rows of no segment are not
         written."""
-        import torch
-
         if stream is not None:
+            import torch
+
             with torch.cuda.stream(stream):
                 return self.forward(x, w, offsets, out)
-        return self._product(self.desc, x, w, offsets, out, "fp8 forward")
+        return self._product(self._ahead, x, w, offsets, out, "fp8 forward")
 
     def grad_input(self, dy, w_t, offsets=None, out=None, stream=None):
         """dx [M, K] = dy w[e] of dy by rows [M, N] and the transposed weights w_t."""
-        import torch
-
         if stream is not None:
+            import torch
+
             with torch.cuda.stream(stream):
                 return self.grad_input(dy, w_t, offsets, out)
-        return self._product(self._desc_t, dy, w_t, offsets, out, "fp8 grad_input")
+        return self._product(self._back, dy, w_t, offsets, out, "fp8 grad_input")
 
     def grad_weight(self, dy_t, x_t, offsets=None, dw=None, accumulate=False, stream=None):
         """dw [E, N, K] fp32 = dy^T x of each expert's rows, of dy and x by columns [N, R],
         [K, R]; accumulate adds to the given dw."""
-        import torch
-
         if stream is not None:
+            import torch
+
             with torch.cuda.stream(stream):
                 return self.grad_weight(dy_t, x_t, offsets, dw, accumulate)
         N, K, E = self.N, self.K, self.E
-        dev, f32 = _device(), torch.float32
+        dy, dy_scales = dy_t
+        x, x_scales = x_t
+        dev, f32 = _device(), _types.f32
         _scratch_on(self.status, dev)
-        R = x_t[0].shape[-1]
-        yp, ld_y = _codes(dy_t[0], "dy's codes", (N, R), dev)
-        xp, ld_x = _codes(x_t[0], "x's codes", (K, R), dev)
-        sp, ld_sy = _rows(dy_t[1], "dy's scales", f32, (R // 128, N), dev)
-        tp, ld_sx = _rows(x_t[1], "x's scales", f32, (R // 128, K), dev)
-        fp, _ = _offsets(offsets, E, dev)
+        R = x.shape[-1]
+        yp, ld_y = _codes(dy, "dy's codes", (N, R), dev)
+        xp, ld_x = _codes(x, "x's codes", (K, R), dev)
+        sp, ld_sy = _rows(dy_scales, "dy's scales", f32, (R // 128, N), dev)
+        tp, ld_sx = _rows(x_scales, "x's scales", f32, (R // 128, K), dev)
+        fp = _offsets(offsets, E, dev)[0]
         if dw is None:
-            new = torch.zeros if accumulate else torch.empty
-            dw = new((E, N, K), dtype=f32, device=x_t[0].device)
-        _check(_lib.moe_fp8_gemm_wgrad(
-            ctypes.addressof(self.desc), R, yp, ld_y, sp, ld_sy, xp, ld_x, tp, ld_sx, fp,
-            _want(dw, "dw", f32, (E, N, K), dev), 1 if accumulate else 0, self.status.data_ptr(),
-            _raw_stream(dev)), "fp8 grad_weight")
+            new = _types.zeros if accumulate else _types.empty
+            dw = new((E, N, K), dtype=f32, device=x.device)
+            wp = dw.data_ptr()
+        else:
+            wp = _want(dw, "dw", f32, (E, N, K), dev)
+        rc = _lib.moe_fp8_gemm_wgrad(
+            self._ahead[1], R, yp, ld_y, sp, ld_sy, xp, ld_x, tp, ld_sx, fp, wp,
+            1 if accumulate else 0, self.status.data_ptr(), _raw_stream(dev))
+        if rc:
+            _check(rc, "fp8 grad_weight")
         return dw
 
     def check(self):

@@ -239,7 +239,7 @@ def test_python_calls_refuse(B, on_gpu_0):
 
     h = object.__new__(B.MoeFp8Linear)
     h.N, h.K, h.E, h.dtype = N, K, E, bf16
-    h.desc, h._desc_t = B.Fp8GemmDesc(N, K, E, 0), B.Fp8GemmDesc(K, N, E, 0)
+    h._ahead, h._back = h._side(N, K, E, 0), h._side(K, N, E, 0)
 
     def forward(t):
         h.status = t["status"]
