@@ -7,8 +7,20 @@
 //
 // The scales change with every block of 128, so the tensor core's sum ends there: the
 // 128 products of a block go to tensor memory in fp32 (four K = 32 instructions), are read
-// back, and join the running sum in registers with one fused multiply-add an element, all
-// fp32.  tcgen05.mma writes one part of tensor memory while eight warps read the other.
+// back, and join the running sum in registers with one fused multiply-add an element (two
+// multiplications for the weights, whose columns have scales of their own), all fp32.
+//
+// A tile is 128 x 256: the widest whose sums fit the registers, and a part of tensor memory
+// that leaves a second one, which tcgen05.mma writes while the warps read the first; 48 KB
+// of codes a block and four of them on their way.  Narrower tiles (128 columns, four parts)
+// serve shapes of a single wave.
+//
+// Bound by the way of the sums: from the last MMA of a block until its part is free again
+// some 900 cycles pass a block (barriers, tensor memory loads of 46 cycles and more, additions),
+// where its MMAs take 512 and its copies, at the 64 bytes a cycle an SM gets from L2, 768.
+// Dense 8192 x 4096 x 4096 106 us (2.6 PFLOP/s), M = 65536, N = 1536, K = 2048 on 128 experts
+// 206 (2.0), its weight gradient on 32 experts 329 (1.25); 512 rows on the 128 experts 60, the
+// weights' bytes at a copy's rate.
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
