@@ -563,27 +563,65 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
       // the next one too, to see how close it comes
       if (keyed && k < a.top_groups * a.group_size) count = k + 1;
     }
-    // the largest key k times; slots are searched in order and lanes within a slot,
-    // so equal keys go to the lowest expert.  A chosen key becomes 0.
-    for (int j = 0; j < count; ++j) {
-      uint32_t best = key[0];
+    if (GROUPS) {
+      // Each lane sorts its keys (Batcher's network; equal ones by slot), and of the lanes'
+      // first ones the largest is taken, of equal ones the lowest expert.
+      uint32_t slot[NV];
 #pragma unroll
-      for (int i = 1; i < NV; ++i) best = max(best, key[i]);
-      const uint32_t top = __reduce_max_sync(kAll, best);
-      bool open = true;
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-        if (open) {
-          const unsigned has = __ballot_sync(kAll, key[i] == top);
-          if (has) {
-            const int at = __ffs(has) - 1;
-            if (lane == at) {
-              key[i] = 0u;
-              sel_id[warp][j] = (uint8_t)(32 * i + at);
-            }
-            open = false;
-          }
+      for (int i = 0; i < NV; ++i) slot[i] = i;
+      auto order = [&](int i, int j) {
+        if (j < NV) {
+          const bool swap = key[j] > key[i] || (key[j] == key[i] && slot[j] < slot[i]);
+          const uint32_t ki = key[i], si = slot[i];
+          key[i] = swap ? key[j] : ki;
+          slot[i] = swap ? slot[j] : si;
+          key[j] = swap ? ki : key[j];
+          slot[j] = swap ? si : slot[j];
         }
+      };
+      order(0, 1); order(2, 3); order(4, 5); order(6, 7);
+      order(0, 2); order(1, 3); order(4, 6); order(5, 7);
+      order(1, 2); order(5, 6);
+      order(0, 4); order(1, 5); order(2, 6); order(3, 7);
+      order(2, 4); order(3, 5);
+      order(1, 2); order(3, 4); order(5, 6);
+      uint32_t slots = 0;                        // four bits each
+#pragma unroll
+      for (int i = 0; i < NV; ++i) slots |= slot[i] << (4 * i);
+      for (int j = 0; j < count; ++j) {
+        const uint32_t top = __reduce_max_sync(kAll, key[0]);
+        const uint32_t e = __reduce_min_sync(
+            kAll, key[0] == top ? (slots & 15u) * 32u + (uint32_t)lane : 0xFFFFu);
+        if (lane == 0) sel_id[warp][j] = (uint8_t)e;
+        const bool took = (e & 31u) == (uint32_t)lane;
+#pragma unroll
+        for (int i = 0; i + 1 < NV; ++i) key[i] = took ? key[i + 1] : key[i];
+        key[NV - 1] = took ? 0u : key[NV - 1];
+        slots = took ? slots >> 4 : slots;
+      }
+    } else {
+      // the largest key k times; slots are searched in order and lanes within a slot,
+      // so equal keys go to the lowest expert.  A chosen key becomes 0.
+      for (int j = 0; j < k; ++j) {
+        uint32_t best = key[0];
+#pragma unroll
+        for (int i = 1; i < NV; ++i) best = max(best, key[i]);
+        const uint32_t top = __reduce_max_sync(kAll, best);
+        bool open = true;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+          if (open) {
+            const unsigned has = __ballot_sync(kAll, key[i] == top);
+            if (has) {
+              const int at = __ffs(has) - 1;
+              if (lane == at) {
+                key[i] = 0u;
+                sel_id[warp][j] = (uint8_t)(32 * i + at);
+              }
+              open = false;
+            }
+          }
+      }
     }
     if (GROUPS && !close && a.bias) {
       __syncwarp();
