@@ -459,6 +459,8 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
   __shared__ uint32_t kept[GROUPS ? 32 : 1][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
   const int E = a.E, k = a.k;
+  // whether slot i of this lane is an expert (with groups NV is the fewest slots)
+  auto there = [&](int i) { return (GROUPS && i + 1 < NV) || lane + 32 * i < E; };
   float* const mine = psum + warp * (NV * 32);    // first the row's logits, by expert
   float* const keys = GROUPS ? psum + (nw + warp) * (NV * 32) : nullptr;
   float* const values = GROUPS ? psum + 2 * nw * (NV * 32) + warp * 2 * a.groups : nullptr;
@@ -471,7 +473,7 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
   for (int i = 0; i < NV; ++i) ps[i] = 0.f;
   float bias[NV];
 #pragma unroll
-  for (int i = 0; i < NV; ++i) bias[i] = a.bias && lane + 32 * i < E ? a.bias[lane + 32 * i] : 0.f;
+  for (int i = 0; i < NV; ++i) bias[i] = a.bias && there(i) ? a.bias[lane + 32 * i] : 0.f;
   float wide = 0.f;                               // the largest bias
   uint64_t group_of = 0;                          // group of the expert in slot i, byte i
   if (GROUPS) {
@@ -484,7 +486,10 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
   }
   float z = 0.f;
   int live_rows = 0;
-  for (long long t = (long long)blockIdx.x * nw + warp; t < a.T; t += (long long)gridDim.x * nw) {
+  // with groups a row's work is large enough for the last ones to be spread over the SMs
+  const long long first = GROUPS ? (long long)warp * gridDim.x + blockIdx.x
+                                 : (long long)blockIdx.x * nw + warp;
+  for (long long t = first; t < a.T; t += (long long)gridDim.x * nw) {
     const L* row = static_cast<const L*>(a.logits) + t * a.ld;
     int32_t* ids = a.ids + t * k;
     float* scores = a.scores + t * k;
@@ -497,53 +502,59 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
       if (lane == 0) a.row_stat[t] = -INFINITY;
       continue;
     }
+    const bool weighed = GROUPS && (a.bias != nullptr || a.pair);
     float l[NV];
     uint32_t key[NV];
     float mx = -INFINITY;
     bool nan = false;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      l[i] = e < E ? load_logit(row + e) : -INFINITY;
+      l[i] = there(i) ? load_logit(row + lane + 32 * i) : -INFINITY;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int e = lane + 32 * i;
-      key[i] = e < E ? order_key(l[i] + bias[i]) : 0u;
-      mine[e] = l[i];
+      if (!weighed) key[i] = there(i) ? order_key(l[i] + bias[i]) : 0u;
+      mine[lane + 32 * i] = l[i];
       mx = fmaxf(mx, l[i]);
       nan |= l[i] != l[i];
     }
     int count = k;
     bool close = false, groups_close = false;
     float error = 0.f;
-    const bool weighed = GROUPS && (a.bias != nullptr || a.pair);
     if (GROUPS) {
       mx = warp_max(mx);
       float largest = 0.f;
       const bool keyed = a.bias != nullptr;
       if (weighed) {
-        // fp32 keys of scores; the weights take the logits' place
-        float sum = 0.f;
+        // fp32 keys of scores; the weights take the logits' place.  Without a bias the
+        // logits order the experts.
+        if (!keyed) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) key[i] = there(i) ? order_key(l[i]) : 0u;
+        }
         uint32_t off = 0;                        // bit i: a logit of -inf
+        if (sig) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            off |= (l[i] == -INFINITY ? 1u : 0u) << i;
+            l[i] = there(i) ? __fdividef(1.f, 1.f + __expf(-l[i])) : 0.f;
+          }
+        } else {
+          float sum = 0.f;
+#pragma unroll
+          for (int i = 0; i < NV; ++i) {
+            off |= (l[i] == -INFINITY ? 1u : 0u) << i;
+            l[i] = there(i) ? __expf(l[i] - mx) : 0.f;
+            sum += l[i];
+          }
+          largest = 1.f / warp_sum(sum);
+        }
+        const float share = sig ? 1.f : largest;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-          const float x = __expf(sig ? -l[i] : l[i] - mx);
-          off |= (l[i] == -INFINITY ? 1u : 0u) << i;
-          l[i] = lane + 32 * i >= E ? 0.f : sig ? __fdividef(1.f, 1.f + x) : x;
-          sum += l[i];
-        }
-        if (!sig) {
-          sum = warp_sum(sum);
-          largest = 1.f / sum;
-        }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int e = lane + 32 * i;
-          const float s = sig ? l[i] : l[i] * largest;
-          const float v = (off >> i) & 1u ? -INFINITY : s + bias[i];
-          if (keyed) key[i] = e < E ? order_key(v) : 0u;
-          keys[e] = v == v ? v : -INFINITY;
+          const float v = (off >> i) & 1u ? -INFINITY : fmaf(l[i], share, bias[i]);
+          if (keyed) key[i] = there(i) ? order_key(v) : 0u;
+          keys[lane + 32 * i] = v == v ? v : -INFINITY;
         }
       } else {
 #pragma unroll
@@ -557,7 +568,7 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int g = (int)(group_of >> (8 * i)) & 255;
-          if (lane + 32 * i < E && !((kept[warp][g >> 5] >> (g & 31)) & 1u)) key[i] = 0u;
+          if (!((kept[warp][g >> 5] >> (g & 31)) & 1u)) key[i] = 0u;
         }
       }
       // the next one too, to see how close it comes
@@ -639,7 +650,7 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
       if (groups_close || !sig || !choose_among<NV>(a, mine, keys, kept[warp], sel_id[warp], error))
         choose_slowly<NV>(a, mine, kept[warp], sel_id[warp]);
     }
-    mx = warp_max(mx);
+    if (!GROUPS) mx = warp_max(mx);
     nan = __any_sync(kAll, nan);
     __syncwarp();                          // sel_id and the row's logits are written
     if (!nan && mx == -INFINITY) {         // nothing to choose
@@ -658,8 +669,7 @@ __global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs
     if (!weighed || (sig && top != 0.f)) {
 #pragma unroll
       for (int i = 0; i < NV; ++i) {
-        const int e = lane + 32 * i;
-        l[i] = e < E ? weight(weighed ? mine[e] : l[i], top, sig) : 0.f;
+        l[i] = there(i) ? weight(weighed ? mine[lane + 32 * i] : l[i], top, sig) : 0.f;
       }
     }
 #pragma unroll
@@ -974,6 +984,7 @@ cudaError_t launch_forward(const RouterArgs& a, int grid, cudaStream_t st) {
     case 4: return launch_forward_nv<L, 4, GROUPS>(a, grid, st);
     case 5: return launch_forward_nv<L, GROUPS ? 5 : 8, GROUPS>(a, grid, st);
     case 6: return launch_forward_nv<L, GROUPS ? 6 : 8, GROUPS>(a, grid, st);
+    case 7: return launch_forward_nv<L, GROUPS ? 7 : 8, GROUPS>(a, grid, st);
     default: return launch_forward_nv<L, 8, GROUPS>(a, grid, st);
   }
 }
