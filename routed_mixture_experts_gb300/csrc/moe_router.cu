@@ -153,7 +153,7 @@ __device__ __forceinline__ uint64_t warp_max64(uint64_t v) {
 
 // The choice of one row on 64-bit keys, by one warp (logits by expert in shared memory).
 template <int NV>
-__device__ __noinline__ void choose_slowly(const RouterArgs& a, const float* logits,
+__device__ __forceinline__ void choose_slowly(const RouterArgs& a, const float* logits,
                                            uint32_t* kept, uint8_t* chosen) {
   const int lane = threadIdx.x & 31, E = a.E;
   const bool sig = a.scoring == MOE_ROUTER_SIGMOID;
@@ -272,7 +272,7 @@ __device__ __noinline__ void choose_slowly(const RouterArgs& a, const float* log
 // bits costs a warp some 1000 cycles, and choose_slowly eight of them.  False where there
 // are more of them than lanes.
 template <int NV>
-__device__ __noinline__ bool choose_among(const RouterArgs& a, const float* logits,
+__device__ __forceinline__ bool choose_among(const RouterArgs& a, const float* logits,
                                           const float* keys, const uint32_t* kept,
                                           uint8_t* chosen, float error) {
   const int lane = threadIdx.x & 31;
@@ -309,7 +309,7 @@ __device__ __noinline__ bool choose_among(const RouterArgs& a, const float* logi
 // that make them: those within `error` of a group's second (or largest) key, a lane each.
 // Chooses among them so that top_groups compete.  False where there are more than lanes.
 // (Sigmoid keys: a softmax key needs the whole row in 64 bits.)
-__device__ __noinline__ bool choose_close_groups(const RouterArgs& a, const GroupRow& row,
+__device__ __forceinline__ bool choose_close_groups(const RouterArgs& a, const GroupRow& row,
                                                  const float* logits, float in, float out,
                                                  float error) {
   const int lane = threadIdx.x & 31, G = a.groups;
@@ -382,17 +382,30 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
   const int lane = threadIdx.x & 31, G = a.groups, size = a.group_size;
   const int share = 1 << a.share_log2, per = (size + share - 1) >> a.share_log2;
   const int q = lane & (share - 1);
+  const bool even = size == per << a.share_log2 && (per & (per - 1)) == 0;
   for (int g = lane >> a.share_log2; g - (lane >> a.share_log2) < G; g += 32 >> a.share_log2) {
     float first = -INFINITY, second = -INFINITY;
     if (g < G) {
       const float* const p = row.key + g * size + q;
-      int j = per == 8 ? g & 7 : g % per;
+      if (even && a.pair) {
 #pragma unroll 8
-      for (int n = 0; n < per; ++n) {
-        const float v = q + (j << a.share_log2) < size ? p[j << a.share_log2] : -INFINITY;
-        second = fmaxf(second, fminf(first, v));
-        first = fmaxf(first, v);
-        if (++j == per) j = 0;
+        for (int n = 0; n < per; ++n) {
+          const float v = p[(n ^ (g & (per - 1))) << a.share_log2];
+          second = fmaxf(second, fminf(first, v));
+          first = fmaxf(first, v);
+        }
+      } else if (even) {
+#pragma unroll 8
+        for (int n = 0; n < per; ++n)
+          first = fmaxf(first, p[(n ^ (g & (per - 1))) << a.share_log2]);
+      } else {
+        int j = g % per;
+        for (int n = 0; n < per; ++n) {
+          const float v = q + (j << a.share_log2) < size ? p[j << a.share_log2] : -INFINITY;
+          second = fmaxf(second, fminf(first, v));
+          first = fmaxf(first, v);
+          if (++j == per) j = 0;
+        }
       }
     }
     for (int o = share >> 1; o > 0; o >>= 1) {
@@ -445,12 +458,16 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
 // registers over all their rows, so that no atomic adds floating-point values and the
 // results do not depend on the order in which warps run.
 // With groups the chain has the groups' values before it (their largest keys found by up to
-// 32 lanes, their places by counting those ahead): 8192 rows of 256 experts in 8 groups 31 us,
-// 16411 rows of 160 experts in 20 (bf16, 2048 rows masked) 27, one row 6.4.
+// 32 lanes, their places by counting those ahead), and the choice takes the lanes' largest
+// keys from lists that each lane has sorted: 8192 rows of 256 experts in 8 groups 24.3 us,
+// 16411 rows of 160 experts in 20 (bf16, 2048 rows masked) 23.0, one row 5.3.  The sorted
+// lists took 31.1 us, with a search over all slots a step, to 28.5.  The rare choices on
+// 64-bit keys are inlined: called, they kept the loop's registers in memory (26.3 us against
+// 25.2).  Two thirds of the instructions' rate are used; the rest is the chain's waits.
 // Measured, both launches: one token 3.5 us, 8192 rows of 128 experts (k = 8) 11.4, 16411
 // rows of 250 bf16 logits (k = 6, sigmoid, bias, 2048 rows masked) 19.6.
 template <typename L, int NV, bool GROUPS>
-__global__ void __launch_bounds__(GROUPS ? 512 : 1024) k_router(const RouterArgs a) {
+__global__ void __launch_bounds__(GROUPS ? 640 : 1024) k_router(const RouterArgs a) {
   extern __shared__ float psum[];                 // [warps][NV * 32], GROUPS: and the keys
   __shared__ int cnt[kMaxE];
   __shared__ uint8_t sel_id[32][kMaxE];           // a warp's chosen experts, in order
@@ -942,9 +959,10 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
 
 // Up to a row per warp one CTA does all, the sums too (32 rows of 128 experts 4.8 us).
 // More rows are spread, and a second launch adds the sums: 64 rows 6.6 us against 7.8
-// on one CTA.  With groups a CTA has 16 warps, whose threads keep all in registers (8192
-// rows of 256 experts 31.5 us against 32.9 on 32 warps, one row 6.8 against 8.8).
-int most_warps(bool groups) { return groups ? 16 : 32; }
+// on one CTA.  With groups a CTA has 20 warps, whose threads keep nearly all in registers
+// (8192 rows of 256 experts 24.3 us against 25.2 on 16 warps, before the last steps 32.9
+// on 32 and 31.5 on 16; 64 rows 10.3 against 9.9).
+int most_warps(bool groups) { return groups ? 20 : 32; }
 
 // warps of a CTA: its chosen experts and per-warp sums take shared memory
 int forward_warps(int T, int grid, bool groups) {
