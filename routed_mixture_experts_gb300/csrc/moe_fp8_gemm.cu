@@ -195,15 +195,20 @@ struct Tile {
   int b0, b1;          // blocks along the depth
 };
 
-// Persistent: tiles in turn over the CTAs, every role walking the same sequence.
+// Persistent: tiles in turn over the CTAs, every role walking the same sequence.  Weights' tiles
+// are as deep as their expert has rows: the deepest experts come first (order), and the CTAs
+// are dealt tiles forwards and backwards by turns (65536 rows on 32 experts, 6 to 56 blocks
+// each: the deepest CTA has 340 blocks where the experts' order gives 379, and the mean is
+// 333; 302 us against 329).
 template <int BN, bool WGRAD>
-__device__ __forceinline__ Tile tile_of(const Fp8GemmArgs& a, const Segments& seg, int t,
-                                        int n_tiles) {
+__device__ __forceinline__ Tile tile_of(const Fp8GemmArgs& a, const Segments& seg,
+                                        const uint8_t* order, int t, int n_tiles) {
   Tile r;
   if (WGRAD) {
     const int m_tiles = (a.N + 127) >> 7, per = m_tiles * n_tiles;
-    r.e = t / per;
-    const int q = t - r.e * per;
+    const int place = t / per;
+    const int q = t - place * per;
+    r.e = order[place];
     r.m0 = (q / n_tiles) << 7;
     r.m1 = min(r.m0 + 128, a.N);
     r.n0 = (q % n_tiles) * BN;
@@ -491,6 +496,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
   static_assert(S::SMEM + 3584 <= 232448, "shared memory");
   extern __shared__ uint8_t smem_raw[];
   __shared__ Segments seg;
+  __shared__ uint8_t order[WGRAD ? kMaxSegments : 1];
   __shared__ uint32_t tmem_holder;
   __shared__ volatile int abort_s;
 
@@ -541,6 +547,22 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
             : (args.offsets ? seg.first[args.E] : (args.M + 127) >> 7) * n_tiles);
   if ((int)blockIdx.x >= num_tiles || (WGRAD && args.offsets && seg.bad)) return;
 
+  if (WGRAD && threadIdx.x < args.E) {           // (without offsets the one expert)
+    const int mine = args.offsets ? seg.first[threadIdx.x + 1] - seg.first[threadIdx.x] : 0;
+    int ahead = 0;
+    if (args.offsets) {
+      int begin = 0;
+      for (int f = 0; f < args.E; ++f) {
+        const int end = seg.first[f + 1], blocks = end - begin;
+        ahead += (blocks > mine || (blocks == mine && f < (int)threadIdx.x)) ? 1 : 0;
+        begin = end;
+      }
+    }
+    order[ahead] = (uint8_t)threadIdx.x;
+  }
+  const int step = WGRAD ? 2 * gridDim.x - 1 - 2 * blockIdx.x : gridDim.x;
+  auto next_step = [&](int d) { return WGRAD ? 2 * (int)gridDim.x - d : d; };
+
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_holder), 512);
     tmem_relinquish();
@@ -560,8 +582,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     uint32_t issued = 0;                         // bit s: stage s has been filled
     uint32_t parity = 0;                         // bit s: in which phase last
     bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-      const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+    for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
+      const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
       for (int b = ti.b0; b < ti.b1; ++b) {
         if (elect_one()) {
           ok = ok && mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 1);
@@ -608,8 +630,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
       int stage = 0, buf = 0;
       uint32_t phase = 0, buf_phase = 0;
       bool ok = true;
-      for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-        const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+      for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
+        const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
         for (int b = ti.b0; b < ti.b1; ++b) {
           ok = ok && mbar_wait(tempty_bar(buf), buf_phase ^ 1u, &abort_s, args.err, 3) &&
                mbar_wait(full_bar(stage), phase, &abort_s, args.err, 4);
@@ -650,8 +672,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     int slot = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (int t = blockIdx.x; t < num_tiles && ok; t += gridDim.x) {
-      const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+    for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
+      const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
       const float* const pb = WGRAD ? args.sb + ti.n0
                                     : args.sb + ((long long)ti.e * nb_all + (ti.n0 >> 7)) * k_blocks;
       for (int g = ti.b0; g < ti.b1; g += S::GROUP) {
@@ -698,8 +720,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
         tmem_base + ((uint32_t)(quarter * 32) << 16) + (uint32_t)(group * WIDE);
     Reader rd = {slots, sfull_bar(0), sempty_bar(0), tfull_bar(0), tempty_bar(0), 0, 0, 0u, 0u,
                  true, &abort_s, args.err};
-    for (int t = blockIdx.x; t < num_tiles; t += gridDim.x) {
-      const Tile ti = tile_of<BN, WGRAD>(args, seg, t, n_tiles);
+    for (int t = blockIdx.x, d = step; t < num_tiles; t += d, d = next_step(d)) {
+      const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
       if constexpr (WGRAD)
         sum_weights<BN>(args, ti, rd, lane_base, quarter, group, lane);
       else
