@@ -300,6 +300,30 @@ def test_more_tiles_than_processors(moe, N, K):
         ref.check_product(dw[e], a[:, cols], b[:, cols], "dw %d" % e)
 
 
+@pytest.mark.parametrize("E,N,K", [(256, 300, 520), (97, 129, 1300), (256, 100, 60)])
+def test_weight_gradient_of_many_experts(moe, E, N, K):
+    """Experts of every depth, none and the same as another's among them, whose tiles are
+    dealt to the CTAs several times round."""
+    counts = np.random.default_rng(E + N).integers(0, 520, E)
+    counts[::7], counts[3::11] = 0, 256
+    offsets = offsets_of(counts.tolist())
+    R = int(counts.sum())
+    both = dict(offsets=offsets.cuda(), by_row=False, by_column=True)
+    g = gen(41)
+    _, dy = moe.quantize_fp8(torch.randn(R, N, generator=g).cuda(), **both)
+    _, xt = moe.quantize_fp8(torch.randn(R, K, generator=g).cuda(), **both)
+    linear = moe.MoeFp8Linear(N, K, E)
+    dw = linear.grad_weight(dy, xt, offsets=offsets.cuda())
+    n, _ = ref.columns(offsets.tolist(), R)
+    a, b = (ref.values(bytes_of(m.codes)[:, :n[-1]], f32(m.scales)[:n[-1] // 128])
+            for m in (dy, xt))
+    got = f32(dw)
+    for e in range(E):
+        cols = slice(n[e], n[e + 1])
+        ref.check_product(got[e], a[:, cols], b[:, cols], "dw %d" % e)
+    assert torch.equal(dw, linear.grad_weight(dy, xt, offsets=offsets.cuda()))
+
+
 def test_every_significand(moe):
     """Scales of all 2^23 significands are the rounded quotients."""
     top = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(0x3F800000)).view(np.float32)
