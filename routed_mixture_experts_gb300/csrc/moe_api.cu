@@ -204,6 +204,20 @@ int encode_tmap_codes(CUtensorMap* map, const void* base, long long batch, long 
   return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
 }
 
+int encode_tmap_f32_weights(CUtensorMap* map, const void* base, long long batch, long long rows,
+                            long long cols) {
+  PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_detail::encode_fn();
+  if (!fn) return MOE_ERR_CUDA;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)batch};
+  const cuuint64_t strides[2] = {(cuuint64_t)(4 * cols), (cuuint64_t)(4 * rows * cols)};
+  const cuuint32_t box[3] = {32, 32, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3, const_cast<void*>(base), dims, strides,
+                  box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? MOE_OK : MOE_ERR_CUDA;
+}
+
 int encode_tmap_gate_up(CUtensorMap* map, bool fp8, const void* base, long long E, long long I,
                         long long cols, int box_rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = tmap_detail::encode_fn();

@@ -39,7 +39,7 @@ struct Fp8GemmArgs {
   const int32_t* offsets;            // [E+1] or NULL: one segment
   void* c;  long long ld_c;
   int row_blocks;                    // weights: blocks of 128 that the codes have
-  int f32, accumulate, wide;         // wide: 16-byte stores (weights: 8-byte)
+  int f32, accumulate, wide;         // wide: 16-byte stores (weights: 2, 8-byte; 4, copies)
   DevError* err;
 };
 
@@ -173,10 +173,11 @@ struct Shape {
                 "what the first warps give up is all that there is");
   static constexpr int A_BYTES = 128 * 128, B_BYTES = BN * 128;
   static constexpr int STAGE = A_BYTES + B_BYTES;
-  static constexpr int TURN = WGRAD ? 0 : SUM_WARPS * 32 * 80;   // a warp's 32 rows x 64 bytes
+  // on the way out: a warp's 32 rows x 64 bytes, 80 apart (weights: x 128)
+  static constexpr int TURN = SUM_WARPS * 32 * (WGRAD ? 128 : 80);
   // scales of GROUP blocks: of each its 128 rows', then (weights) BN columns' or the two
   // weight blocks'
-  static constexpr int GROUP = 4, SLOTS = 4, BLOCK = 512 + (WGRAD ? BN * 4 : 16);
+  static constexpr int GROUP = 4, SLOTS = WGRAD ? 2 : 4, BLOCK = 512 + (WGRAD ? BN * 4 : 16);
   static constexpr int SLOT = GROUP * BLOCK;
   static constexpr int REST = TURN + SLOTS * SLOT + 512;
   static constexpr int FIT = (226 * 1024 - 3584 - REST) / STAGE;
@@ -405,7 +406,7 @@ __device__ __forceinline__ void sum_rows(const Fp8GemmArgs& args, const Tile& ti
 template <int BN>
 __device__ __forceinline__ void sum_weights(const Fp8GemmArgs& args, const Tile& ti, Reader& rd,
                                             uint32_t lane_base, int quarter, int group,
-                                            int lane) {
+                                            int lane, uint32_t turn, const CUtensorMap* out_map) {
   using S = Shape<BN, true>;
   constexpr int WIDE = S::WIDE, CH = 16;         // CH: columns a load
   const int row = quarter * 32 + (lane >> 2), pair0 = 2 * (lane & 3);
@@ -459,6 +460,45 @@ __device__ __forceinline__ void sum_weights(const Fp8GemmArgs& args, const Tile&
   if (args.accumulate && ti.b0 == ti.b1) return;
   float* const out = static_cast<float*>(args.c) + (long long)ti.e * args.N * args.K;
   const int c0 = ti.n0 + group * WIDE + pair0;
+  if (args.wide == 4) {
+    // 32 x 32 at a time through shared memory, whose copies out go on beside the next tile's
+    // sums: written from registers, a tile of 128 KB kept the warps for a third of their time.
+#pragma unroll
+    for (int h = 0; h < WIDE / 32; ++h) {
+      if (lane == 0) bulk_wait_read<0>();        // of what was there before
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = ti.m0 + row + 8 * j;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int c = c0 + 32 * h + 8 * i;
+          float x, y;
+          unpair(acc[4 * h + i][j], x, y);
+          if (args.accumulate && r < ti.m1 && c < args.K) {
+            const float2 v = *reinterpret_cast<const float2*>(out + (long long)r * args.K + c);
+            x += v.x;
+            y += v.y;
+          }
+          // rows of 128 bytes whose 16-byte pieces are turned by the row (lane / 4 of eight)
+          const uint32_t piece = (uint32_t)(2 * i + ((lane & 3) >> 1)) ^ (uint32_t)(lane >> 2);
+          asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(
+                           turn + (uint32_t)(((lane >> 2) + 8 * j) * 128 + 8 * (lane & 1)) +
+                           16u * piece),
+                       "f"(x), "f"(y)
+                       : "memory");
+        }
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        const int c = ti.n0 + group * WIDE + 32 * h, r = ti.m0 + quarter * 32;
+        if (c < args.K && r < ti.m1) tma_store_3d(out_map, turn, c, r, ti.e);
+        bulk_commit();
+      }
+    }
+    return;
+  }
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int r = ti.m0 + row + 8 * j;
@@ -490,7 +530,7 @@ __device__ __forceinline__ void sum_weights(const Fp8GemmArgs& args, const Tile&
 template <int BN, bool WGRAD>
 __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     k_fp8_gemm(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const Fp8GemmArgs args) {
+               const __grid_constant__ CUtensorMap tmC, const Fp8GemmArgs args) {
   using S = Shape<BN, WGRAD>;
   constexpr int STAGES = S::STAGES, NBUF = S::NBUF, SLOTS = S::SLOTS, WIDE = S::WIDE;
   static_assert(S::SMEM + 3584 <= 232448, "shared memory");
@@ -723,7 +763,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     for (int t = blockIdx.x, d = step; t < num_tiles; t += d, d = next_step(d)) {
       const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
       if constexpr (WGRAD)
-        sum_weights<BN>(args, ti, rd, lane_base, quarter, group, lane);
+        sum_weights<BN>(args, ti, rd, lane_base, quarter, group, lane,
+                        smem_u32(turn_all) + (uint32_t)(warp - 4) * 4096u, &tmC);
       else
         sum_rows<BN>(args, ti, rd, lane_base, quarter, group, lane,
                      turn_all + (warp - 4) * 32 * 80);
@@ -731,6 +772,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
       rd.ok = __all_sync(0xffffffffu, rd.ok);
       if (!rd.ok) break;
     }
+    if (WGRAD && lane == 0) bulk_wait_all();     // the last copies out
   }
   pdl_trigger();
   tc_fence_before();
@@ -742,8 +784,8 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
 }
 
 template <int BN, bool WGRAD>
-cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmArgs& a, int grid,
-                   cudaStream_t st) {
+cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
+                   const Fp8GemmArgs& a, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};
   const cudaError_t e = smem_optin_once(k_fp8_gemm<BN, WGRAD>, (Shape<BN, WGRAD>::SMEM), configured);
   if (e != cudaSuccess) return e;
@@ -757,7 +799,7 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const Fp8GemmAr
   }
   if (regs.load(std::memory_order_relaxed) != Shape<BN, WGRAD>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
   return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(Shape<BN, WGRAD>::THREADS), (Shape<BN, WGRAD>::SMEM), st, ta, tb,
-                    a);
+                    tc, a);
 }
 
 bool aligned(const void* p, int bytes) {
@@ -827,8 +869,8 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
       encode_tmap_codes(&tb, b, s->E, s->N, s->K, ld_b, narrow ? 128 : 256) != MOE_OK)
     return MOE_ERR_CUDA;
   const int grid = (int)(most < num_sms() ? most : num_sms());
-  return cuda_result(narrow ? launch<128, false>(ta, tb, g, grid, st)
-                            : launch<256, false>(ta, tb, g, grid, st), "moe_fp8_gemm");
+  return cuda_result(narrow ? launch<128, false>(ta, tb, ta, g, grid, st)
+                            : launch<256, false>(ta, tb, ta, g, grid, st), "moe_fp8_gemm");
 }
 
 extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const uint8_t* dyt,
@@ -856,7 +898,9 @@ extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const
   g.row_blocks = (int)(R / 128);
   g.f32 = 1;
   g.accumulate = accumulate != 0;
-  g.wide = aligned(dw, 8) && s->K % 2 == 0;
+  g.wide = aligned(dw, 16) && s->K % 4 == 0 && (long long)s->N * s->K < (1LL << 37)
+               ? 4
+               : aligned(dw, 8) && s->K % 2 == 0 ? 2 : 0;
   g.err = static_cast<DevError*>(status);
   // as in moe_fp8_gemm: N = 777, K = 1111 over 1003 rows 8.6 us against 14.4
   const bool narrow = s->K <= 128 || (long long)s->E * ((s->N + 127) / 128) *
@@ -868,9 +912,12 @@ extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const
   if (encode_tmap_codes(&ta, dyt, 0, s->N, R, ld_dyt, 128) != MOE_OK ||
       encode_tmap_codes(&tb, xt, 0, s->K, R, ld_xt, narrow ? 128 : 256) != MOE_OK)
     return MOE_ERR_CUDA;
+  CUtensorMap tc = ta;                           // (read where rows are aligned)
+  if (g.wide == 4 && encode_tmap_f32_weights(&tc, dw, s->E, s->N, s->K) != MOE_OK)
+    return MOE_ERR_CUDA;
   const int grid = (int)(tiles < num_sms() ? tiles : num_sms());
-  return cuda_result(narrow ? launch<128, true>(ta, tb, g, grid, st)
-                            : launch<256, true>(ta, tb, g, grid, st), "moe_fp8_gemm_wgrad");
+  return cuda_result(narrow ? launch<128, true>(ta, tb, tc, g, grid, st)
+                            : launch<256, true>(ta, tb, tc, g, grid, st), "moe_fp8_gemm_wgrad");
 }
 
 extern "C" int moe_fp8_check(void* status, int* where) {

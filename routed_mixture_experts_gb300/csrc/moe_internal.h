@@ -243,6 +243,9 @@ int encode_tmap_u8(CUtensorMap* map, const void* base, long long rows, long long
 // beyond the extents, 128-byte swizzle.
 int encode_tmap_codes(CUtensorMap* map, const void* base, long long batch, long long rows,
                       long long cols, long long ld, int box_rows);
+// fp32 weights [batch, rows, cols] that a box of 32 x 32 is stored to (128-byte swizzle).
+int encode_tmap_f32_weights(CUtensorMap* map, const void* base, long long batch, long long rows,
+                            long long cols);
 // The 8-bit block product of a few rows (moe_fp8_few.cu).
 struct Fp8FewCall {
   int M, N, K, E;
