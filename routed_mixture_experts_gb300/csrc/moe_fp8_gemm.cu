@@ -12,14 +12,15 @@
 //
 // A tile is 128 x 256: the widest whose sums fit the registers, and a part of tensor memory
 // that leaves a second one, which tcgen05.mma writes while the warps read the first; 48 KB
-// of codes a block and four of them on their way.  Narrower tiles (128 columns, four parts)
-// serve shapes of a single wave.
+// of codes a block and four of them on their way (weights: three, which leaves room for tiles
+// on their way out; before those had any, 4 / 3 / 2 took 302 / 290 / 320 us).  Narrower tiles
+// (128 columns, four parts) serve shapes of a single wave.
 //
 // Bound by the way of the sums: from the last MMA of a block until its part is free again
 // some 900 cycles pass a block (barriers, tensor memory loads of 46 cycles and more, additions),
 // where its MMAs take 512 and its copies, at the 64 bytes a cycle an SM gets from L2, 768.
 // Dense 8192 x 4096 x 4096 106 us (2.6 PFLOP/s), M = 65536, N = 1536, K = 2048 on 128 experts
-// 206 (2.0), its weight gradient on 32 experts 329 (1.25); 512 rows on the 128 experts 60, the
+// 206 (2.0), its weight gradient on 32 experts 267 (1.54); 512 rows on the 128 experts 60, the
 // weights' bytes at a copy's rate.
 
 #include "../../include/moe.h"
@@ -200,7 +201,7 @@ struct Tile {
 // are as deep as their expert has rows: the deepest experts come first (order), and the CTAs
 // are dealt tiles forwards and backwards by turns (65536 rows on 32 experts, 6 to 56 blocks
 // each: the deepest CTA has 340 blocks where the experts' order gives 379, and the mean is
-// 333; 302 us against 329).
+// 333; 302 us against 329, before the tiles left by copies).
 template <int BN, bool WGRAD>
 __device__ __forceinline__ Tile tile_of(const Fp8GemmArgs& a, const Segments& seg,
                                         const uint8_t* order, int t, int n_tiles) {
@@ -434,18 +435,17 @@ __device__ __forceinline__ void sum_weights(const Fp8GemmArgs& args, const Tile&
       uint32_t d[2][8];                          // rows 0..15, rows 16..31
       tmem_ld_16x256b_x2(at, d[0]);
       tmem_ld_16x256b_x2(at + (16u << 16), d[1]);
-      float2 x[2];
+      uint64_t x2[2];                            // (as pairs: put together they are moved)
 #pragma unroll
-      for (int g = 0; g < 2; ++g) x[g] = *reinterpret_cast<const float2*>(cs + CH * c + 8 * g);
+      for (int g = 0; g < 2; ++g) x2[g] = *reinterpret_cast<const uint64_t*>(cs + CH * c + 8 * g);
       tmem_wait(d[0], d[1]);
       if (c + 1 == WIDE / CH) rd.free_sums(lane);
 #pragma unroll
       for (int g = 0; g < 2; ++g) {
-        const uint64_t x2 = pair(x[g].x, x[g].y);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const uint32_t* const q = d[j >> 1] + 4 * g + 2 * (j & 1);
-          acc[2 * c + g][j] = fma2(mul2(pair_u(q[0], q[1]), x2), s2[j], acc[2 * c + g][j]);
+          acc[2 * c + g][j] = fma2(mul2(pair_u(q[0], q[1]), x2[g]), s2[j], acc[2 * c + g][j]);
         }
       }
     }
@@ -462,7 +462,7 @@ __device__ __forceinline__ void sum_weights(const Fp8GemmArgs& args, const Tile&
   const int c0 = ti.n0 + group * WIDE + pair0;
   if (args.wide == 4) {
     // 32 x 32 at a time through shared memory, whose copies out go on beside the next tile's
-    // sums: written from registers, a tile of 128 KB kept the warps for a third of their time.
+    // sums (279 us; written from registers, a tile of 128 KB kept the warps: 290).
 #pragma unroll
     for (int h = 0; h < WIDE / 32; ++h) {
       if (lane == 0) bulk_wait_read<0>();        // of what was there before
