@@ -587,6 +587,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
             : (args.offsets ? seg.first[args.E] : (args.M + 127) >> 7) * n_tiles);
   if ((int)blockIdx.x >= num_tiles || (WGRAD && args.offsets && seg.bad)) return;
 
+  // the experts by depth; those as deep as another in their order
   if (WGRAD && threadIdx.x < args.E) {           // (without offsets the one expert)
     const int mine = args.offsets ? seg.first[threadIdx.x + 1] - seg.first[threadIdx.x] : 0;
     int ahead = 0;
@@ -615,77 +616,28 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(S::COPY_REGS));
-  if (warp == 0) {
-    // ---------------- copies ----------------
-    int stage = 0;
-    uint32_t phase = 0;
-    uint32_t issued = 0;                         // bit s: stage s has been filled
-    uint32_t parity = 0;                         // bit s: in which phase last
-    bool ok = true;
-    for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
-      const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
-      for (int b = ti.b0; b < ti.b1; ++b) {
-        if (elect_one()) {
-          ok = ok && mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 1);
-          if (ok) {
-            const uint32_t fb = full_bar(stage), sa = stage0 + stage * S::STAGE;
-            mbar_arrive_expect_tx(fb, S::STAGE);
-            tma_load_2d(sa, &tmA, b << 7, ti.m0, fb);
-            if (WGRAD)
-              tma_load_2d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, fb);
-            else
-              tma_load_3d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, ti.e, fb);
-            issued |= 1u << stage;
-            parity = (parity & ~(1u << stage)) | (phase << stage);
-          }
-        }
-        __syncwarp();
-        if (++stage == STAGES) {
-          stage = 0;
-          phase ^= 1u;
-        }
-      }
-      ok = __all_sync(0xffffffffu, ok);
-    }
-    for (int s = 0; s < STAGES && ok; ++s) {     // every stage has been released
-      if (elect_one()) ok = mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 2);
-      ok = __all_sync(0xffffffffu, ok);
-      if (++stage == STAGES) {
-        stage = 0;
-        phase ^= 1u;
-      }
-    }
-    if (abort_s) {                               // let the copies in flight land
-      for (int s = 0; s < STAGES; ++s)
-        if ((issued >> s) & 1u) gemm::mbar_wait_drain(full_bar(s), (parity >> s) & 1u);
-    }
-    __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- MMA: a block of 128 a time ----------------
-    // (the whole warp walks the loop, so that its values are uniform; one lane issues)
-    {
-      const uint64_t a0 = smem_desc_sw128(stage0, 16, 1024);
-      const uint64_t b0 = smem_desc_sw128(stage0 + S::A_BYTES, 16, 1024);
-      constexpr uint32_t IDESC = idesc_f8(128, BN);
-      int stage = 0, buf = 0;
-      uint32_t phase = 0, buf_phase = 0;
+    if (warp == 0) {
+      // ---------------- copies ----------------
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t issued = 0;                         // bit s: stage s has been filled
+      uint32_t parity = 0;                         // bit s: in which phase last
       bool ok = true;
       for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
         const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
         for (int b = ti.b0; b < ti.b1; ++b) {
-          ok = ok && mbar_wait(tempty_bar(buf), buf_phase ^ 1u, &abort_s, args.err, 3) &&
-               mbar_wait(full_bar(stage), phase, &abort_s, args.err, 4);
-          __syncwarp();
           if (elect_one()) {
+            ok = ok && mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 1);
             if (ok) {
-              tc_fence_after();
-              const uint64_t off = (uint64_t)((uint32_t)(stage * S::STAGE) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_f8(tmem_base + (uint32_t)(buf * BN), a0 + off + 2 * k, b0 + off + 2 * k, IDESC,
-                        k != 0);
-              umma_commit(empty_bar(stage));
-              umma_commit(tfull_bar(buf));
+              const uint32_t fb = full_bar(stage), sa = stage0 + stage * S::STAGE;
+              mbar_arrive_expect_tx(fb, S::STAGE);
+              tma_load_2d(sa, &tmA, b << 7, ti.m0, fb);
+              if (WGRAD)
+                tma_load_2d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, fb);
+              else
+                tma_load_3d(sa + S::A_BYTES, &tmB, b << 7, ti.n0, ti.e, fb);
+              issued |= 1u << stage;
+              parity = (parity & ~(1u << stage)) | (phase << stage);
             }
           }
           __syncwarp();
@@ -693,65 +645,115 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
             stage = 0;
             phase ^= 1u;
           }
-          if (++buf == NBUF) {
-            buf = 0;
-            buf_phase ^= 1u;
-          }
         }
         ok = __all_sync(0xffffffffu, ok);
       }
-      if (abort_s && elect_one()) {
-        umma_commit(drain_bar);                  // every MMA issued so far has completed
-        gemm::mbar_wait_drain(drain_bar, 0);
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---------------- scales of a block, as far ahead as there are slots ----------------
-    const int nb_all = (args.N + 127) >> 7, k_blocks = (args.K + 127) >> 7;
-    int slot = 0;
-    uint32_t phase = 0;
-    bool ok = true;
-    for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
-      const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
-      const float* const pb = WGRAD ? args.sb + ti.n0
-                                    : args.sb + ((long long)ti.e * nb_all + (ti.n0 >> 7)) * k_blocks;
-      for (int g = ti.b0; g < ti.b1; g += S::GROUP) {
-        if (lane == 0) ok = mbar_wait(sempty_bar(slot), phase ^ 1u, &abort_s, args.err, 6);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        const int end = min(g + S::GROUP, ti.b1);
-        for (int b = g; b < end; ++b) {
-          const uint32_t to = smem_u32(slots) + slot * S::SLOT + (b - g) * S::BLOCK;
-          const float* const pa = args.sa + b * args.ld_sa + ti.m0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int r = 32 * i + lane;
-            const bool there = ti.m0 + r < ti.m1;
-            copy4(to + 4 * r, pa + (there ? r : 0), there);
-          }
-          if (WGRAD) {
-#pragma unroll
-            for (int i = 0; i < BN / 32; ++i) {
-              const int c = 32 * i + lane;
-              const bool there = ti.n0 + c < args.K;
-              copy4(to + 512 + 4 * c, pb + b * args.ld_sb + (there ? c : 0), there);
-            }
-          } else if (lane < BN / 128) {
-            const bool there = (ti.n0 >> 7) + lane < nb_all;
-            copy4(to + 512 + 4 * lane, pb + b + (there ? lane * k_blocks : 0), there);
-          }
-        }
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull_bar(slot))
-                     : "memory");
-        if (++slot == SLOTS) {
-          slot = 0;
+      for (int s = 0; s < STAGES && ok; ++s) {     // every stage has been released
+        if (elect_one()) ok = mbar_wait(empty_bar(stage), phase ^ 1u, &abort_s, args.err, 2);
+        ok = __all_sync(0xffffffffu, ok);
+        if (++stage == STAGES) {
+          stage = 0;
           phase ^= 1u;
         }
       }
+      if (abort_s) {                               // let the copies in flight land
+        for (int s = 0; s < STAGES; ++s)
+          if ((issued >> s) & 1u) gemm::mbar_wait_drain(full_bar(s), (parity >> s) & 1u);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ---------------- MMA: a block of 128 a time ----------------
+      // (the whole warp walks the loop, so that its values are uniform; one lane issues)
+      {
+        const uint64_t a0 = smem_desc_sw128(stage0, 16, 1024);
+        const uint64_t b0 = smem_desc_sw128(stage0 + S::A_BYTES, 16, 1024);
+        constexpr uint32_t IDESC = idesc_f8(128, BN);
+        int stage = 0, buf = 0;
+        uint32_t phase = 0, buf_phase = 0;
+        bool ok = true;
+        for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
+          const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
+          for (int b = ti.b0; b < ti.b1; ++b) {
+            ok = ok && mbar_wait(tempty_bar(buf), buf_phase ^ 1u, &abort_s, args.err, 3) &&
+                 mbar_wait(full_bar(stage), phase, &abort_s, args.err, 4);
+            __syncwarp();
+            if (elect_one()) {
+              if (ok) {
+                tc_fence_after();
+                const uint64_t off = (uint64_t)((uint32_t)(stage * S::STAGE) >> 4);
+  #pragma unroll
+                for (int k = 0; k < 4; ++k)
+                  umma_f8(tmem_base + (uint32_t)(buf * BN), a0 + off + 2 * k, b0 + off + 2 * k,
+                          IDESC, k != 0);
+                umma_commit(empty_bar(stage));
+                umma_commit(tfull_bar(buf));
+              }
+            }
+            __syncwarp();
+            if (++stage == STAGES) {
+              stage = 0;
+              phase ^= 1u;
+            }
+            if (++buf == NBUF) {
+              buf = 0;
+              buf_phase ^= 1u;
+            }
+          }
+          ok = __all_sync(0xffffffffu, ok);
+        }
+        if (abort_s && elect_one()) {
+          umma_commit(drain_bar);                  // every MMA issued so far has completed
+          gemm::mbar_wait_drain(drain_bar, 0);
+        }
+      }
+      __syncwarp();
+    } else if (warp == 2) {
+      // ---------------- scales of a block, as far ahead as there are slots ----------------
+      const int nb_all = (args.N + 127) >> 7, k_blocks = (args.K + 127) >> 7;
+      int slot = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int t = blockIdx.x, d = step; t < num_tiles && ok; t += d, d = next_step(d)) {
+        const Tile ti = tile_of<BN, WGRAD>(args, seg, order, t, n_tiles);
+        const float* const pb =
+            WGRAD ? args.sb + ti.n0
+                  : args.sb + ((long long)ti.e * nb_all + (ti.n0 >> 7)) * k_blocks;
+        for (int g = ti.b0; g < ti.b1; g += S::GROUP) {
+          if (lane == 0) ok = mbar_wait(sempty_bar(slot), phase ^ 1u, &abort_s, args.err, 6);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const int end = min(g + S::GROUP, ti.b1);
+          for (int b = g; b < end; ++b) {
+            const uint32_t to = smem_u32(slots) + slot * S::SLOT + (b - g) * S::BLOCK;
+            const float* const pa = args.sa + b * args.ld_sa + ti.m0;
+  #pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = 32 * i + lane;
+              const bool there = ti.m0 + r < ti.m1;
+              copy4(to + 4 * r, pa + (there ? r : 0), there);
+            }
+            if (WGRAD) {
+  #pragma unroll
+              for (int i = 0; i < BN / 32; ++i) {
+                const int c = 32 * i + lane;
+                const bool there = ti.n0 + c < args.K;
+                copy4(to + 512 + 4 * c, pb + b * args.ld_sb + (there ? c : 0), there);
+              }
+            } else if (lane < BN / 128) {
+              const bool there = (ti.n0 >> 7) + lane < nb_all;
+              copy4(to + 512 + 4 * lane, pb + b + (there ? lane * k_blocks : 0), there);
+            }
+          }
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sfull_bar(slot))
+                       : "memory");
+          if (++slot == SLOTS) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        }
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-  }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(S::SUM_REGS));
     // ---------------- sums ----------------
@@ -797,9 +799,10 @@ cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorM
     if (q != cudaSuccess) return q;
     regs.store(at.numRegs, std::memory_order_relaxed);
   }
-  if (regs.load(std::memory_order_relaxed) != Shape<BN, WGRAD>::LAUNCH_REGS) return cudaErrorInvalidConfiguration;
-  return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(Shape<BN, WGRAD>::THREADS), (Shape<BN, WGRAD>::SMEM), st, ta, tb,
-                    tc, a);
+  if (regs.load(std::memory_order_relaxed) != Shape<BN, WGRAD>::LAUNCH_REGS)
+    return cudaErrorInvalidConfiguration;
+  return launch_pdl(k_fp8_gemm<BN, WGRAD>, dim3(grid), dim3(Shape<BN, WGRAD>::THREADS),
+                    (Shape<BN, WGRAD>::SMEM), st, ta, tb, tc, a);
 }
 
 bool aligned(const void* p, int bytes) {
