@@ -324,6 +324,29 @@ def test_weight_gradient_of_many_experts(moe, E, N, K):
     assert torch.equal(dw, linear.grad_weight(dy, xt, offsets=offsets.cuda()))
 
 
+@pytest.mark.parametrize("shift", [0, 1, 2, 4])
+@pytest.mark.parametrize("N,K", [(130, 260), (33, 36), (200, 1028)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_in_place(moe, shift, N, K, accumulate):
+    """Weights at 16-byte boundaries and between them, alike to the bit, and nothing written
+    beside them."""
+    E, offsets = 3, offsets_of([140, 0, 300])
+    both = dict(offsets=offsets.cuda(), by_row=False, by_column=True)
+    g = gen(51)
+    _, dy = moe.quantize_fp8(torch.randn(440, N, generator=g).cuda(), **both)
+    _, xt = moe.quantize_fp8(torch.randn(440, K, generator=g).cuda(), **both)
+    linear = moe.MoeFp8Linear(N, K, E)
+    want = linear.grad_weight(dy, xt, offsets=offsets.cuda())
+    room = torch.randn(shift + E * N * K + 64, generator=g).cuda()
+    before = room.clone()
+    dw = room[shift:shift + E * N * K].view(E, N, K)
+    linear.grad_weight(dy, xt, offsets=offsets.cuda(), dw=dw, accumulate=accumulate)
+    old = before[shift:shift + E * N * K].view(E, N, K)
+    assert torch.equal(dw, old + want if accumulate else want)
+    assert torch.equal(room[:shift], before[:shift])
+    assert torch.equal(room[shift + E * N * K:], before[shift + E * N * K:])
+
+
 def test_every_significand(moe):
     """Scales of all 2^23 significands are the rounded quotients."""
     top = (np.arange(1 << 23, dtype=np.uint32) | np.uint32(0x3F800000)).view(np.float32)
