@@ -870,7 +870,9 @@ int moe_fp8_gemm(const moe_fp8_gemm_desc* desc, int M, const uint8_t* a, long lo
  * dw[e, n, k] = sum over expert e's rows of dy[r, n] * x[r, k], added to dw with
  * accumulate = 1: dy and x by columns (dyt [N, R], xt [K, R]), with the offsets that
  * they were quantised with.  dw [E, N, K] fp32, dense.  Without accumulate the dw of an
- * expert without rows is 0.  desc->out_dtype is not looked at beyond its range.
+ * expert without rows is 0.  Without offsets the sum goes over all R columns.  Offsets whose
+ * blocks do not fit into R columns are bad ones: recorded, and nothing is written.
+ * desc->out_dtype is not looked at beyond its range.
  */
 int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* desc, long long R, const uint8_t* dyt,
                        long long ld_dyt, const float* dyt_scales, long long ld_dys,

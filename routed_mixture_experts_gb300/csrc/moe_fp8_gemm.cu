@@ -214,8 +214,8 @@ __device__ __forceinline__ Tile tile_of(const Fp8GemmArgs& a, const Segments& se
     r.m0 = (q / n_tiles) << 7;
     r.m1 = min(r.m0 + 128, a.N);
     r.n0 = (q % n_tiles) * BN;
-    r.b0 = a.offsets ? min(seg.first[r.e], a.row_blocks) : 0;
-    r.b1 = a.offsets ? min(seg.first[r.e + 1], a.row_blocks) : a.row_blocks;
+    r.b0 = a.offsets ? seg.first[r.e] : 0;       // (within row_blocks: checked)
+    r.b1 = a.offsets ? seg.first[r.e + 1] : a.row_blocks;
   } else {
     const int b = t / n_tiles;
     r.n0 = (t - b * n_tiles) * BN;
@@ -576,16 +576,18 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
     tma_prefetch_desc(&tmB);
   }
   pdl_wait();                        // the previous kernel of the stream has completed
+  bool bad = false;
   if (args.offsets) {
     seg.init<S::THREADS>(args.offsets, args.E, WGRAD ? 0x7FFFFFFF : args.M);
-    if (seg.bad && blockIdx.x == 0 && threadIdx.x == 0)
+    bad = seg.bad || (WGRAD && seg.first[args.E] > args.row_blocks);   // more than the codes have
+    if (bad && blockIdx.x == 0 && threadIdx.x == 0)
       record_error(args.err, MOE_ERR_INVALID_ARG, 0);
   }
   const int n_tiles = ((WGRAD ? args.K : args.N) + BN - 1) / BN;
   const int num_tiles = uniform(
       WGRAD ? args.E * ((args.N + 127) >> 7) * n_tiles
             : (args.offsets ? seg.first[args.E] : (args.M + 127) >> 7) * n_tiles);
-  if ((int)blockIdx.x >= num_tiles || (WGRAD && args.offsets && seg.bad)) return;
+  if ((int)blockIdx.x >= num_tiles || bad) return;
 
   // the experts by depth; those as deep as another in their order
   if (WGRAD && threadIdx.x < args.E) {           // (without offsets the one expert)
@@ -785,6 +787,22 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
   }
 }
 
+// Weight gradient on no columns: 0 (nothing is added), unless some expert has rows.
+__global__ void __launch_bounds__(256) k_fp8_no_rows(float* dw, long long n, int accumulate,
+                                                     const int32_t* offsets, int E,
+                                                     DevError* err) {
+  pdl_wait();
+  const int t = threadIdx.x;
+  if (__syncthreads_or(offsets && t < E && (offsets[t] < 0 || offsets[t + 1] != offsets[t]))) {
+    if (blockIdx.x == 0 && t == 0) record_error(err, MOE_ERR_INVALID_ARG, 0);
+    return;
+  }
+  if (!accumulate)
+    for (long long i = (long long)blockIdx.x * 256 + t; i < n; i += (long long)gridDim.x * 256)
+      dw[i] = 0.f;
+  pdl_trigger();
+}
+
 template <int BN, bool WGRAD>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                    const Fp8GemmArgs& a, int grid, cudaStream_t st) {
@@ -886,9 +904,13 @@ extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (R == 0) {
-    if (accumulate) return MOE_OK;
-    return cuda_result(cudaMemsetAsync(dw, 0, 4ull * s->E * s->N * s->K, st),
-                       "moe_fp8_gemm_wgrad");
+    if (!aligned(offsets, 4)) return MOE_ERR_INVALID_ARG;
+    if (!offsets && accumulate) return MOE_OK;
+    const long long all = (long long)s->E * s->N * s->K, ctas = (all + 1023) / 1024;
+    const int most = 8 * num_sms();
+    return cuda_result(launch_pdl(k_fp8_no_rows, dim3((unsigned)(ctas < most ? ctas : most)),
+                                  dim3(256), 0, st, dw, all, accumulate != 0, offsets, s->E,
+                                  static_cast<DevError*>(status)), "moe_fp8_gemm_wgrad");
   }
   if (!codes_ok(dyt, ld_dyt, R) || !codes_ok(xt, ld_xt, R) || !dyt_scales || !xt_scales ||
       ld_dys < s->N || ld_xs < s->K || !aligned(dyt_scales, 4) || !aligned(xt_scales, 4) ||

@@ -1,0 +1,64 @@
+"""The 8-bit block operators where offsets, buffers and magnitudes reach their limits."""
+
+import numpy as np
+import pytest
+import torch
+
+import fp8_refs as ref
+from test_gpu_fp8 import F8, TYPES, bytes_of, f32, gen, moe, offsets_of, wide_rows  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(values):
+    return torch.tensor(values, dtype=torch.int32).cuda()
+
+
+def codes_of(codes, scales, offsets):
+    """64-bit values of the columns that the segments take."""
+    n, _ = ref.columns(offsets, offsets[-1])
+    return n, ref.values(bytes_of(codes)[:, :n[-1]], f32(scales)[:n[-1] // 128])
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_of_more_rows_than_its_codes(moe, accumulate):
+    """Offsets that need a block more than the codes have are refused as a whole, and recorded."""
+    N, K, E = 70, 300, 3
+    fits, longer = [0, 128, 200, 328], [0, 129, 201, 329]         # 3 and 5 blocks
+    g = gen(61)
+    both = dict(offsets=i32(fits), by_row=False, by_column=True)
+    _, dy = moe.quantize_fp8(torch.randn(328, N, generator=g).cuda(), **both)
+    _, x = moe.quantize_fp8(torch.randn(328, K, generator=g).cuda(), **both)
+    cut = lambda m: moe.Fp8Matrix(m.codes[:, :384], m.scales[:3])
+    dy, x = cut(dy), cut(x)
+    lin = moe.MoeFp8Linear(N, K, E)
+    for bad in (longer, [0, 0, 0, 385], [0, 128, 128, 385]):
+        dw = torch.full((E, N, K), 7.0).cuda()
+        lin.grad_weight(dy, x, offsets=i32(bad), dw=dw, accumulate=accumulate)
+        assert (dw == 7).all(), bad
+        assert lin.check()[0] == moe.MOE_ERR_INVALID_ARG and lin.check()[0] == moe.MOE_OK
+    dw = torch.zeros(E, N, K).cuda()
+    lin.grad_weight(dy, x, offsets=i32(fits), dw=dw, accumulate=accumulate)
+    (n, a), (_, b) = codes_of(*dy, fits), codes_of(*x, fits)
+    for e in range(E):
+        cols = slice(n[e], n[e + 1])
+        ref.check_product(f32(dw)[e], a[:, cols], b[:, cols], "dw %d" % e)
+    assert lin.check() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_weight_gradient_of_no_columns(moe, accumulate):
+    """Codes without columns: 0 where no expert has rows, refused where one has."""
+    N, K, E = 33, 1100, 3
+    none = lambda n: (torch.zeros(n, 0, dtype=torch.uint8).cuda().view(F8), torch.zeros(0, n).cuda())
+    lin = moe.MoeFp8Linear(N, K, E)
+    for offsets, ok in (([0, 0, 0, 0], True), ([9, 9, 9, 9], True), ([0, 0, 1, 1], False),
+                        ([0, 4, 2, 4], False), ([-1, -1, -1, -1], False)):
+        dw = torch.full((E, N, K), 7.0).cuda()
+        lin.grad_weight(none(N), none(K), offsets=i32(offsets), dw=dw, accumulate=accumulate)
+        assert (dw == (0.0 if ok and not accumulate else 7.0)).all(), offsets
+        assert lin.check()[0] == (moe.MOE_OK if ok else moe.MOE_ERR_INVALID_ARG)
+    dense = moe.MoeFp8Linear(N, K)
+    dw = torch.full((1, N, K), 7.0).cuda()
+    dense.grad_weight(none(N), none(K), dw=dw, accumulate=accumulate)
+    assert (dw == (7.0 if accumulate else 0.0)).all() and dense.check() == (moe.MOE_OK, 0)
