@@ -847,7 +847,8 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
                             const float* a_scales, long long ld_as, const uint8_t* b,
                             long long ld_b, const float* b_scales, const int32_t* offsets, void* c,
                             long long ld_c, void* status, void* stream) {
-  if (!desc_ok(s) || M < 0 || (s->E > 1 && !offsets) || !status || !aligned(status, 16))
+  if (!desc_ok(s) || M < 0 || M > 0x7FFFFF80 ||  // (rounded up to blocks: an int)
+      (s->E > 1 && !offsets) || !status || !aligned(status, 16))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;
   const int es = s->out_dtype == MOE_DTYPE_FP32 ? 4 : 2;

@@ -286,3 +286,12 @@ def test_columns_hold_any_segments(B):
         used = (worst - 1) * 128 + (rows + 127) // 128 * 128 if worst else 0
         assert R % 128 == 0 and R >= used
     assert B.fp8_columns(129, 1, offsets=False) == 256
+
+
+def test_product_of_rows_that_32_bits_cannot_round_up(B):
+    """The last 127 row counts below 2^31, whose blocks of 128 would be counted beyond it."""
+    L = B.lib()
+    d = B.Fp8GemmDesc(16, 16, 1, 0)
+    for M in (0x7FFFFF81, 0x7FFFFFFF):
+        assert L.moe_fp8_gemm(ctypes.addressof(d), M, A, 16, A, M, A, 16, A, None, A, 16, A,
+                              None) == INVALID
