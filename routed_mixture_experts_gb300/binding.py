@@ -946,9 +946,10 @@ def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_co
         R = out_t[0].shape[-1]
         tp, ld_t = _codes(out_t[0], "codes_t", (width, R), dev)
         up, ld_u = _rows(out_t[1], "scales_t", f32, (R // 128, width), dev)
-    rc = L.moe_fp8_quantize(_quant_desc(source, C, code, E, clamp, MOE_FP8_POW2 if pow2 else 0)[1],
-                            M, xp, ld_x, n_src, dp, ld_d, rp, fp, cp, ld_c, sp, ld_s, tp, ld_t, R,
-                            up, ld_u, _raw_stream(dev))
+    # (held: another thread's calls may drop it from the table during this one)
+    desc = _quant_desc(source, C, code, E, clamp, MOE_FP8_POW2 if pow2 else 0)
+    rc = L.moe_fp8_quantize(desc[1], M, xp, ld_x, n_src, dp, ld_d, rp, fp, cp, ld_c, sp, ld_s, tp,
+                            ld_t, R, up, ld_u, _raw_stream(dev))
     if rc:
         _check(rc, what)
     return (Fp8Matrix(*out) if by_row else None), (Fp8Matrix(*out_t) if by_column else None)

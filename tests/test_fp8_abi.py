@@ -295,3 +295,39 @@ def test_product_of_rows_that_32_bits_cannot_round_up(B):
     for M in (0x7FFFFF81, 0x7FFFFFFF):
         assert L.moe_fp8_gemm(ctypes.addressof(d), M, A, 16, A, M, A, 16, A, None, A, 16, A,
                               None) == INVALID
+
+
+def test_descriptions_outlive_their_calls(B, on_gpu_0, monkeypatch):
+    """A call's description stays while the library has its address, whatever other threads'
+    calls bring into the table of descriptions meanwhile."""
+    import gc
+    import weakref
+
+    import torch
+
+    made = []
+
+    class Desc(B.Fp8QuantDesc):
+        def __init__(self, *values):
+            super().__init__(*values)
+            made.append(weakref.ref(self))
+
+    monkeypatch.setattr(B, "Fp8QuantDesc", Desc)
+    B._quant_desc.cache_clear()
+
+    def quantize(at, *rest):
+        (desc,) = [d for d in (r() for r in made) if d is not None and ctypes.addressof(d) == at]
+        del desc
+        for C in range(1000, 1400):                # as many as the table holds, and more
+            B._quant_desc(0, C, 0, 1, 0.0, 0)
+        gc.collect()
+        assert any(d is not None and ctypes.addressof(d) == at for d in (r() for r in made[:1]))
+        seen.append(at)
+        return OK
+
+    seen = []
+    on_gpu_0.moe_fp8_quantize = quantize
+    bf16, f8, f32 = torch.bfloat16, torch.float8_e4m3fn, torch.float32
+    B.quantize_fp8(OnGpu(bf16, (8, 256)), out=(OnGpu(f8, (8, 256)), OnGpu(f32, (2, 8))))
+    assert seen
+    B._quant_desc.cache_clear()
