@@ -265,7 +265,8 @@ __device__ __forceinline__ uint64_t sigmoid2(uint64_t g) {
   return pair(a, b);
 }
 
-// SwiGLU's gradient of four neighbours, at up or at the gate.  t = dh s: t c, t u (1 + c - c s).
+// SwiGLU's gradient of four neighbours, at up or at the gate.  t = dh s: t c, t u (1 + c (1 - s)),
+// whose 1 - s is 0 at large gates (1 + c - c s loses the 1 from c = 2^24 on).
 // Outside the limits the factor is 0 and not the gradient, so that a NaN passes.
 __device__ __forceinline__ void gradient2(uint64_t (&g)[2], uint64_t (&u)[2], uint64_t (&d)[2],
                                           float clamp, bool at_up, uint64_t (&v)[2]) {
@@ -285,7 +286,8 @@ __device__ __forceinline__ void gradient2(uint64_t (&g)[2], uint64_t (&u)[2], ui
     }
     const uint64_t s = sigmoid2(g[j]), t = mul2(d[j], s);
     v[j] = at_up ? mul2(t, g[j])
-                 : mul2(mul2(t, u[j]), fma2(g[j] ^ 0x8000000080000000ull, s, add2(one, g[j])));
+                 : mul2(mul2(t, u[j]),
+                        fma2(g[j], add2(one, s ^ 0x8000000080000000ull), one));
   }
 }
 

@@ -62,3 +62,28 @@ def test_weight_gradient_of_no_columns(moe, accumulate):
     dw = torch.full((1, N, K), 7.0).cuda()
     dense.grad_weight(none(N), none(K), dw=dw, accumulate=accumulate)
     assert (dw == (7.0 if accumulate else 0.0)).all() and dense.check() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("C", [128, 100, 130, 384])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_swiglu_gradient_at_large_gates(moe, C, dtype):
+    """Gates of either sign up to 2^30, where the sigmoid is 0 or 1 and dsilu with it.  (One
+    row has one gate, so that the blocks at the gate have magnitudes of their own.)"""
+    gates = [s * 2.0 ** e * m for e in range(0, 31) for m in (1.0, 1.25) for s in (1.0, -1.0)]
+    M = len(gates)
+    a = torch.ones(M, 2 * C)
+    a[:, :C] = torch.tensor(gates)[:, None]
+    a[:, C:] = torch.randn(M, C, generator=gen(62))
+    dh = torch.randn(M, C, generator=gen(63))
+    a, dh = a.to(TYPES[dtype]), dh.to(TYPES[dtype])
+    q, _ = moe.swiglu_grad_fp8(dh.cuda(), a.cuda())
+    want, _ = ref.swiglu_grad(f32(dh), f32(a))
+    # fp32: a dozen roundings, and the sigmoid's exponent |g| 2^-24 off where it is not 0 or 1
+    g = np.array(gates)[:, None]
+    mag = np.abs(want) + np.where(np.abs(g) < 110, np.concatenate(
+        [np.abs(f32(dh) * f32(a)[:, C:]) * ref.ref.sigmoid(g) * (1 + np.abs(g)) ** 2,
+         np.abs(want[:, C:]) * (1 + np.abs(g))], 1), 0.0)
+    # (sigmoids below 2^-126 count as 0)
+    mag = mag + 2.0 ** -126 / ref.FP32 * np.abs(g) ** 2 * (1 + np.abs(np.concatenate(
+        [f32(dh) * f32(a)[:, C:], f32(dh)], 1)))
+    ref.check_codes(bytes_of(q.codes), f32(q.scales), want, mag, "rows")
