@@ -440,6 +440,7 @@ __device__ __forceinline__ bool choose_groups(const RouterArgs& a, const GroupRo
   }
   __syncwarp();
   if (exact) return false;
+  if (!(error < INFINITY)) return true;
   low = __reduce_min_sync(kAll, low);
   high = __reduce_max_sync(kAll, high);
   const float in = order_value(low), out = order_value(high);
@@ -500,6 +501,8 @@ __global__ void __launch_bounds__(GROUPS ? 640 : 1024) k_router(const RouterArgs
 #pragma unroll
     for (int i = 0; i < NV; ++i) wide = fmaxf(wide, fabsf(bias[i]));
     wide = warp_max(wide);
+    // sums of two such keys are beyond fp32: no comparison of them tells
+    if (wide >= 0x1p126f) wide = INFINITY;
   }
   float z = 0.f;
   int live_rows = 0;

@@ -202,3 +202,27 @@ def test_many_rows_repeat_and_replay(moe):
     torch.cuda.synchronize()
     for x, y, z in zip(a, b, out):
         assert torch.equal(x, y) and torch.equal(x, z)
+
+
+@pytest.mark.parametrize("scoring", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("pair", [False, True])
+@pytest.mark.parametrize("T,E,k,groups,top", [(40, 64, 6, 8, 3), (9, 8, 1, 8, 1), (30, 48, 4, 12, 2),
+                                              (50, 256, 8, 8, 4)])
+def test_biases_of_any_size(moe, T, E, k, groups, top, scoring, pair):
+    """Experts switched off or forced by their bias, and keys whose sums pass fp32's range."""
+    g = torch.Generator().manual_seed(T + E)
+    logits = (torch.randn(T, E, generator=g) * 1.5).cuda()
+    for off in (-1e9, -INF, 1e9, INF, 3e38, -3e38):
+        for n in (1, 2, E // 2):
+            bias = torch.randn(E, generator=g) * 0.1
+            bias[torch.randperm(E, generator=g)[:n]] = off
+            check(make(moe, T, E, k, groups, top, scoring, pair), logits, scoring, pair,
+                  bias=bias.cuda())
+    # two groups whose sums fp32 holds for infinite: the second is larger
+    if pair and E > groups:
+        size = E // groups
+        bias = torch.zeros(E)
+        bias[0], bias[1] = 2e38, 2e38
+        bias[size], bias[size + 1] = 3e38, 1.5e38
+        check(make(moe, T, E, 1, groups, 1, scoring, pair), logits, scoring, pair,
+              bias=bias.cuda())
