@@ -771,7 +771,7 @@ extern "C" int moe_fp8_quantize(const moe_fp8_quant_desc* s, int M, const void* 
     return MOE_ERR_INVALID_ARG;
   const bool grad = s->source == MOE_FP8_SWIGLU_GRAD, plain = s->source == MOE_FP8_ROWS;
   const int width = grad ? 2 * s->C : s->C, in_width = plain ? s->C : 2 * s->C;
-  if ((!codes && !codes_t) || (s->E > 1 && !offsets) || (rows && !plain) ||
+  if ((!codes && !codes_t && M > 0) || (s->E > 1 && !offsets) || (rows && !plain) ||
       (rows && x_rows < 0) || (grad != (dh != nullptr) && M > 0) || (plain && s->clamp > 0.f))
     return MOE_ERR_INVALID_ARG;
   if (M == 0) return MOE_OK;

@@ -331,3 +331,18 @@ def test_descriptions_outlive_their_calls(B, on_gpu_0, monkeypatch):
     B.quantize_fp8(OnGpu(bf16, (8, 256)), out=(OnGpu(f8, (8, 256)), OnGpu(f32, (2, 8))))
     assert seen
     B._quant_desc.cache_clear()
+
+
+def test_no_rows_are_no_mistake(B):
+    """Codes of no rows have no address; the other checks hold for them too."""
+    L = B.lib()
+
+    def call(source, M=0, E=1, C=64, offsets=None):
+        d = B.Fp8QuantDesc(source, C, 0, E, 0.0, 0)
+        return L.moe_fp8_quantize(ctypes.addressof(d), M, None, 2 * C, 0, None, C, None, offsets,
+                                  None, 2 * C, None, M, None, 0, 0, None, 0, None)
+
+    for source in (0, 1, 2):
+        assert call(source) == OK and call(source, E=3, offsets=A) == OK
+        assert call(source, M=1) == INVALID
+        assert call(source, E=3) == INVALID and call(source, C=0) == INVALID

@@ -87,3 +87,29 @@ def test_swiglu_gradient_at_large_gates(moe, C, dtype):
     mag = mag + 2.0 ** -126 / ref.FP32 * np.abs(g) ** 2 * (1 + np.abs(np.concatenate(
         [f32(dh) * f32(a)[:, C:], f32(dh)], 1)))
     ref.check_codes(bytes_of(q.codes), f32(q.scales), want, mag, "rows")
+
+
+def test_no_rows(moe):
+    """Every quantiser of no rows, either way, and what the products make of them."""
+    C, N, E = 64, 48, 3
+    none = torch.zeros(0, 2 * C).cuda()
+    for offsets in (None, i32([0, 0, 0, 0])):
+        for both in (dict(), dict(by_column=True), dict(by_row=False, by_column=True)):
+            for q, t in (moe.quantize_fp8(none[:, :C], offsets=offsets, **both),
+                         moe.quantize_fp8(torch.ones(5, C).cuda(), rows=i32([]), offsets=offsets,
+                                          **both),
+                         moe.swiglu_fp8(none, offsets=offsets, **both),
+                         moe.swiglu_grad_fp8(none[:, :C], none, offsets=offsets, **both)):
+                if both.get("by_row", True):
+                    assert q.codes.shape[0] == 0
+                if both:
+                    assert t.codes.shape[1] == moe.fp8_columns(0, E if offsets is not None else 1,
+                                                               offsets is not None)
+    lin = moe.MoeFp8Linear(N, C)
+    q, t = moe.quantize_fp8(none[:, :C], by_column=True)
+    w, wt = moe.quantize_fp8_weights(torch.randn(N, C).cuda(), transposed=True)
+    assert lin.forward(q, w).shape == (0, N)
+    dy, dyt = moe.quantize_fp8(torch.zeros(0, N).cuda(), by_column=True)
+    assert lin.grad_input(dy, wt).shape == (0, C)
+    assert (lin.grad_weight(dyt, t) == 0).all()
+    assert lin.check() == (moe.MOE_OK, 0)
