@@ -798,7 +798,9 @@ int moe_block_norm_backward(const moe_block_norm_desc* desc, int T, const void* 
  *               columns from 128 * sum_{i<e} ceil(rows_i / 128) on, the codes of the rest
  *               of its last block are 0, and blocks beyond the last segment's are
  *               neither written nor read.  R is a multiple of 128; with offsets M + 127 E,
- *               rounded down to such, always holds all of it.
+ *               rounded down to such, always holds all of it.  Without offsets all of
+ *               the R columns are written (by a call with M > 0) and read: those beyond
+ *               the rows are 0.
  * Codes start at 16-byte boundaries with row distances that are multiples of 16; the
  * codes' own rows may have any width.
  */

@@ -849,6 +849,7 @@ class _Types:
         import torch
 
         self.f8, self.f32, self.i32 = torch.float8_e4m3fn, torch.float32, torch.int32
+        self.u8 = torch.uint8
         self.code = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_FP32}
         self.empty, self.zeros = torch.empty, torch.zeros
         return self.__dict__[name]
@@ -946,6 +947,9 @@ def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_co
         R = out_t[0].shape[-1]
         tp, ld_t = _codes(out_t[0], "codes_t", (width, R), dev)
         up, ld_u = _rows(out_t[1], "scales_t", f32, (R // 128, width), dev)
+        if M == 0 and R and offsets is None:         # (the library writes nothing then)
+            out_t[0].view(_types.u8).zero_()
+            out_t[1].zero_()
     # (held: another thread's calls may drop it from the table during this one)
     desc = _quant_desc(source, C, code, E, clamp, MOE_FP8_POW2 if pow2 else 0)
     rc = L.moe_fp8_quantize(desc[1], M, xp, ld_x, n_src, dp, ld_d, rp, fp, cp, ld_c, sp, ld_s, tp,

@@ -788,8 +788,10 @@ extern "C" int moe_fp8_quantize(const moe_fp8_quant_desc* s, int M, const void* 
   if (codes_t) {
     const long long need = offsets ? 0 : blocks * 128;
     if (!scales_t || !aligned(codes_t, 16) || cols_t < need || cols_t % 128 ||
-        ld_codes_t < cols_t || ld_codes_t % 16 || !aligned(scales_t, 4) || ld_scales_t < width)
+        ld_codes_t < cols_t || ld_codes_t % 16 || !aligned(scales_t, 4) || ld_scales_t < width ||
+        (!offsets && cols_t > 0x7FFFFF80LL))
       return MOE_ERR_INVALID_ARG;
+    if (!offsets) blocks = cols_t / 128;         // those beyond the rows are zeros
   }
   // with offsets: every expert's last block may hold as little as one row
   if (offsets) blocks = ((long long)M + 127LL * s->E) / 128;

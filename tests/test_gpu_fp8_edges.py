@@ -113,3 +113,33 @@ def test_no_rows(moe):
     assert lin.grad_input(dy, wt).shape == (0, C)
     assert (lin.grad_weight(dyt, t) == 0).all()
     assert lin.check() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("M", [0, 1, 128, 200])
+@pytest.mark.parametrize("source", ["rows", "swiglu", "swiglu_grad"])
+@pytest.mark.parametrize("C", [128, 90])
+def test_columns_beyond_the_rows_without_offsets(moe, M, source, C):
+    """A buffer kept for more rows than there are: its last columns are 0, and the weight
+    gradient over all of them is that of the rows."""
+    R, g = 512, gen(64)
+    width = 2 * C if source == "swiglu_grad" else C
+    a, dh = torch.randn(M, 2 * C, generator=g).cuda(), torch.randn(M, C, generator=g).cuda()
+
+    def run(**kw):
+        if source == "rows":
+            return moe.quantize_fp8(dh, by_column=True, **kw)
+        if source == "swiglu":
+            return moe.swiglu_fp8(a, by_column=True, **kw)
+        return moe.swiglu_grad_fp8(dh, a, by_column=True, **kw)
+
+    kept = moe.Fp8Matrix(torch.full((width, R), 0x7F, dtype=torch.uint8).cuda().view(F8),
+                         torch.full((R // 128, width), float("nan")).cuda())
+    q, t = run(out_t=kept)
+    alone, own = run()
+    n = own.codes.shape[1]
+    assert np.array_equal(bytes_of(q.codes), bytes_of(alone.codes))
+    assert np.array_equal(bytes_of(t.codes)[:, :n], bytes_of(own.codes))
+    assert torch.equal(t.scales[:n // 128], own.scales)
+    assert (bytes_of(t.codes)[:, n:] == 0).all() and torch.isfinite(t.scales).all()
+    lin = moe.MoeFp8Linear(width, width)
+    assert torch.equal(lin.grad_weight(t, t), lin.grad_weight(own, own))
