@@ -827,7 +827,8 @@ typedef struct moe_fp8_quant_desc {
  *         it is negative or not below x_rows (token_of of a dispatch gathers)
  *   dh    [M, C] gradient at h, with MOE_FP8_SWIGLU_GRAD
  * With offsets only the segments' rows are read and written.  codes or codes_t may be
- * NULL.  Columns that do not fit below cols_t = R are left out, of both layouts.
+ * NULL.  Blocks of columns that do not fit below cols_t = R are left out (the weight gradient
+ * refuses the offsets then); the codes by rows are whole.
  */
 int moe_fp8_quantize(const moe_fp8_quant_desc* desc, int M, const void* x, long long ld_x,
                      int x_rows, const void* dh, long long ld_dh, const int32_t* rows,

@@ -143,3 +143,38 @@ def test_columns_beyond_the_rows_without_offsets(moe, M, source, C):
     assert (bytes_of(t.codes)[:, n:] == 0).all() and torch.isfinite(t.scales).all()
     lin = moe.MoeFp8Linear(width, width)
     assert torch.equal(lin.grad_weight(t, t), lin.grad_weight(own, own))
+
+
+@pytest.mark.parametrize("source", ["rows", "swiglu_grad"])
+@pytest.mark.parametrize("dtype,C", [("bf16", 256), ("bf16", 70), ("fp32", 130)])
+@pytest.mark.parametrize("blocks", [0, 1, 3])
+def test_columns_that_do_not_fit(moe, source, dtype, C, blocks):
+    """Codes by columns as far as there is room, within a larger buffer of which nothing else
+    is written; codes by rows whole all the same."""
+    counts = [5, 0, 130, 1, 0, 64]                                 # five blocks
+    M, g, offsets = sum(counts), gen(65), offsets_of(counts).cuda()
+    width = 2 * C if source == "swiglu_grad" else C
+    a = torch.randn(M, 2 * C, generator=g).to(TYPES[dtype]).cuda()
+    dh = torch.randn(M, C, generator=g).to(TYPES[dtype]).cuda()
+
+    def run(**kw):
+        if source == "rows":
+            return moe.quantize_fp8(dh, offsets=offsets, **kw)
+        return moe.swiglu_grad_fp8(dh, a, offsets=offsets, **kw)
+
+    whole, columns = run(by_column=True)
+    room = torch.full((width + 3, 1024), 0x55, dtype=torch.uint8).cuda()
+    room_s = torch.full((blocks + 3, width + 5), -1.0).cuda()
+    n = 128 * blocks
+    for by_row in (True, False) if blocks else (True,):
+        room.fill_(0x55)
+        room_s.fill_(-1.0)
+        out_t = (room.view(F8)[1:width + 1, 128:128 + n], room_s[1:blocks + 1, 2:width + 2])
+        q, t = run(by_row=by_row, by_column=True, out_t=out_t)
+        if by_row:
+            assert np.array_equal(bytes_of(q.codes), bytes_of(whole.codes))
+            assert torch.equal(q.scales, whole.scales)
+        want, want_s = np.full(room.shape, 0x55, np.uint8), np.full(room_s.shape, -1.0, np.float32)
+        want[1:width + 1, 128:128 + n] = bytes_of(columns.codes)[:, :n]
+        want_s[1:blocks + 1, 2:width + 2] = f32(columns.scales)[:blocks]
+        assert np.array_equal(bytes_of(room), want) and np.array_equal(f32(room_s), want_s)
