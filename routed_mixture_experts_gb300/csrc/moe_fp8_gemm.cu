@@ -587,7 +587,7 @@ __global__ void __launch_bounds__((Shape<BN, WGRAD>::THREADS), 1)
   const int num_tiles = uniform(
       WGRAD ? args.E * ((args.N + 127) >> 7) * n_tiles
             : (args.offsets ? seg.first[args.E] : (args.M + 127) >> 7) * n_tiles);
-  if ((int)blockIdx.x >= num_tiles || bad) return;
+  if ((int)blockIdx.x >= num_tiles || (WGRAD && bad)) return;
 
   // the experts by depth; those as deep as another in their order
   if (WGRAD && threadIdx.x < args.E) {           // (without offsets the one expert)
@@ -857,10 +857,12 @@ extern "C" int moe_fp8_gemm(const moe_fp8_gemm_desc* s, int M, const uint8_t* a,
       !aligned(c, es) || !aligned(offsets, 4) || ld_b >= (1LL << 39) / s->N)
     return MOE_ERR_INVALID_ARG;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  // Few rows, so few weights that they are units of one wave of the streaming kernel (eight
-  // rows of A a unit): M = 1, N = K = 4096 8.2 us against 10.1 on tiles, N = 300, K = 500 2.0
-  // against 4.2; beyond a wave tiles are ahead (one token's eight experts of N = 1536, K =
-  // 2048, 768 units, 12.7 against 10.2; M = 16, N = K = 4096 13.5 against 10.2).
+  // Few rows, and so few weights that 16 rows of them a CTA are one wave of the streaming
+  // kernel (two CTAs an SM; every eight rows of A count, for they take the weights again): M = 1,
+  // N = K = 4096 6.9 us against 10.1 on tiles, N = 300, K = 500 2.0 against 4.2.  Beyond a wave
+  // neither is always ahead.  In units of 16 rows: 384 of one row each on four experts (K =
+  // 4096) 10.4 against 15.5, eight rows on 448 13.6 against 12.3, 32 rows on 320 12.4 against
+  // 11.5, one token's eight experts on 768 (K = 2048) 11.5 against 10.0.
   if (M <= 32 && (long long)(M < s->E ? M : s->E) * ((s->N + 15) / 16) * ((M + 7) / 8) <=
                      2 * num_sms()) {
     const Fp8FewCall f = {M, s->N, s->K, s->E, a, ld_a, a_scales, ld_as, b, ld_b, b_scales,

@@ -178,3 +178,45 @@ def test_columns_that_do_not_fit(moe, source, dtype, C, blocks):
         want[1:width + 1, 128:128 + n] = bytes_of(columns.codes)[:, :n]
         want_s[1:blocks + 1, 2:width + 2] = f32(columns.scales)[:blocks]
         assert np.array_equal(bytes_of(room), want) and np.array_equal(f32(room_s), want_s)
+
+
+BAD = [[0, 20, 10, 30], [-1, 10, 20, 30], [0, 10, 20, 33], [5, 2 ** 31 - 1, 7, 9], [2, 1, 0, 0]]
+
+
+@pytest.mark.parametrize("bad", BAD)
+def test_bad_offsets_of_few_rows(moe, bad):
+    """Nothing is written, and it is recorded; good offsets of the same call work after that."""
+    M, N, K = 32, 40, 300
+    g = gen(66)
+    q, _ = moe.quantize_fp8(torch.randn(M, K, generator=g).cuda())
+    w = moe.quantize_fp8_weights(torch.randn(3, N, K, generator=g).cuda())
+    lin = moe.MoeFp8Linear(N, K, 3, dtype=torch.float32)
+    y = torch.full((M, N), 7.0).cuda()
+    lin.forward(q, w, offsets=i32(bad), out=y)
+    assert (y == 7).all()
+    assert lin.check()[0] == moe.MOE_ERR_INVALID_ARG and lin.check()[0] == moe.MOE_OK
+    lin.forward(q, w, offsets=i32([0, 20, 20, 30]), out=y)
+    x, t = ref.values(bytes_of(q.codes), f32(q.scales)), ref.tile_values(bytes_of(w.codes),
+                                                                         f32(w.scales))
+    ref.check_product(f32(y)[:20], x[:20], t[0], "first")
+    ref.check_product(f32(y)[20:30], x[20:30], t[2], "last")
+    assert (y[30:] == 7).all() and lin.check() == (moe.MOE_OK, 0)
+
+
+@pytest.mark.parametrize("M,E", [(1, 1), (1, 256), (9, 9), (31, 256), (32, 2), (32, 200)])
+@pytest.mark.parametrize("N,K", [(16, 4000), (1, 1), (17, 1025), (300, 130)])
+def test_few_rows_anywhere(moe, M, E, N, K):
+    """Rows of any experts, one of them with most, on a CTA for each that may have some."""
+    g = np.random.default_rng(M * E + N)
+    counts = np.bincount(np.append(g.integers(0, E, M // 2), [E // 3] * (M - M // 2)), minlength=E)
+    offsets = offsets_of(counts.tolist())
+    q, _ = moe.quantize_fp8(torch.randn(M, K, generator=gen(67)).cuda())
+    w = moe.quantize_fp8_weights(torch.randn(E, N, K, generator=gen(68)).cuda())
+    lin = moe.MoeFp8Linear(N, K, E, dtype=torch.float32)
+    got, at = f32(lin.forward(q, w, offsets=offsets.cuda())), offsets.tolist()
+    x, t = ref.values(bytes_of(q.codes), f32(q.scales)), ref.tile_values(bytes_of(w.codes),
+                                                                         f32(w.scales))
+    for e in range(E):
+        rows = slice(at[e], at[e + 1])
+        ref.check_product(got[rows], x[rows], t[e], "expert %d" % e)
+    assert lin.check() == (moe.MOE_OK, 0)
