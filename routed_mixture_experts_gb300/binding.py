@@ -858,6 +858,11 @@ class _Types:
 _types = _Types()
 
 
+def _not_of(dims, t, what):
+    raise MoeError(MOE_ERR_INVALID_ARG, "%s: want %d dimensions, got %s" % (what, dims,
+                                                                            tuple(t.shape)))
+
+
 def _codes(t, what, shape, dev):
     """t: E4M3 codes [..., width] whose rows lie a multiple of 16 bytes apart (address, row
     distance); a batch's matrices follow one another."""
@@ -891,7 +896,9 @@ def _offsets(offsets, E, dev):
             raise MoeError(MOE_ERR_INVALID_ARG, "%d experts need offsets" % E)
         return None, 1
     if E is None:
-        E = offsets.shape[0] - 1 if offsets.dim() == 1 else 0
+        E = offsets.shape[0] - 1 if offsets.dim() == 1 else _not_of(1, offsets, "offsets")
+        if E < 1:
+            raise MoeError(MOE_ERR_INVALID_ARG, "offsets of no expert")
     return _want(offsets, "offsets", _types.i32, (E + 1,), dev), E
 
 
@@ -908,14 +915,14 @@ def fp8_columns(M, E=1, offsets=True):
     return (M + 127 * E) // 128 * 128 if offsets else (M + 127) // 128 * 128
 
 
-def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_column, out, out_t,
-                  what):
+def _quantize_fp8(source, x, shape, C, M, dh, rows, offsets, clamp, pow2, by_row, by_column, out,
+                  out_t, what):
     if not (by_row or by_column) or (out is not None and not by_row) or (
             out_t is not None and not by_column):
         raise MoeError(MOE_ERR_INVALID_ARG, "%s: out goes with by_row, out_t with by_column, and "
                        "one of them is needed" % what)
     L = _lib if _lib is not None else lib()
-    n_src = x.shape[0]
+    n_src = shape[0]
     _rows_fit(M if M > n_src else n_src, what)
     dev, f32, dtype = _device(), _types.f32, x.dtype
     code = _types.code.get(dtype)
@@ -944,7 +951,9 @@ def _quantize_fp8(source, x, C, M, dh, rows, offsets, clamp, pow2, by_row, by_co
             R = fp8_columns(M, E, offsets is not None)
             out_t = Fp8Matrix(_new_codes((width,), R, x.device),
                               _types.empty((R // 128, width), dtype=f32, device=x.device))
-        R = out_t[0].shape[-1]
+        if out_t[0].dim() != 2:
+            _not_of(2, out_t[0], "codes_t")
+        R = out_t[0].shape[1]
         tp, ld_t = _codes(out_t[0], "codes_t", (width, R), dev)
         up, ld_u = _rows(out_t[1], "scales_t", f32, (R // 128, width), dev)
         if M == 0 and R and offsets is None:         # (the library writes nothing then)
@@ -971,9 +980,12 @@ def quantize_fp8(x, rows=None, offsets=None, pow2=False, by_row=True, by_column=
 
         with torch.cuda.stream(stream):
             return quantize_fp8(x, rows, offsets, pow2, by_row, by_column, out, out_t)
-    M = x.shape[0] if rows is None else rows.shape[0]
-    return _quantize_fp8(MOE_FP8_ROWS, x, x.shape[1], M, None, rows, offsets, 0.0, pow2, by_row,
-                         by_column, out, out_t, "quantize_fp8")
+    shape = x.shape if x.dim() == 2 else _not_of(2, x, "x")
+    M = shape[0]
+    if rows is not None:
+        M = rows.shape[0] if rows.dim() == 1 else _not_of(1, rows, "rows")
+    return _quantize_fp8(MOE_FP8_ROWS, x, shape, shape[1], M, None, rows, offsets, 0.0, pow2,
+                         by_row, by_column, out, out_t, "quantize_fp8")
 
 
 def swiglu_fp8(a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=False, out=None,
@@ -984,7 +996,8 @@ def swiglu_fp8(a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_column=Fa
 
         with torch.cuda.stream(stream):
             return swiglu_fp8(a, clamp, offsets, pow2, by_row, by_column, out, out_t)
-    return _quantize_fp8(MOE_FP8_SWIGLU, a, a.shape[1] // 2, a.shape[0], None, None, offsets,
+    shape = a.shape if a.dim() == 2 else _not_of(2, a, "a")
+    return _quantize_fp8(MOE_FP8_SWIGLU, a, shape, shape[1] // 2, shape[0], None, None, offsets,
                          clamp, pow2, by_row, by_column, out, out_t, "swiglu_fp8")
 
 
@@ -996,7 +1009,8 @@ def swiglu_grad_fp8(dh, a, clamp=0.0, offsets=None, pow2=False, by_row=True, by_
 
         with torch.cuda.stream(stream):
             return swiglu_grad_fp8(dh, a, clamp, offsets, pow2, by_row, by_column, out, out_t)
-    return _quantize_fp8(MOE_FP8_SWIGLU_GRAD, a, a.shape[1] // 2, a.shape[0], dh, None, offsets,
+    shape = a.shape if a.dim() == 2 else _not_of(2, a, "a")
+    return _quantize_fp8(MOE_FP8_SWIGLU_GRAD, a, shape, shape[1] // 2, shape[0], dh, None, offsets,
                          clamp, pow2, by_row, by_column, out, out_t, "swiglu_grad_fp8")
 
 
@@ -1012,7 +1026,7 @@ def quantize_fp8_weights(w, transposed=False, pow2=False, stream=None):
     L, dev, at = lib(), _device(), w.device
     if w.dim() == 2:
         w = w[None]
-    E, N, K = w.shape
+    E, N, K = w.shape if w.dim() == 3 else _not_of(3, w, "w")
     nb, kb = (N + 127) // 128, (K + 127) // 128
     wp = _want(w, "w", w.dtype, (E, N, K), dev)
     make = lambda rows, width, a, b: Fp8Matrix(
@@ -1059,7 +1073,7 @@ class MoeFp8Linear:
         w, w_scales = w
         dev, f32 = _device(), _types.f32
         _scratch_on(self.status, dev)
-        M = x.shape[0]
+        M = x.shape[0] if x.dim() == 2 else _not_of(2, x, "codes")
         _rows_fit(M, what)
         ap, ld_a = _codes(x, "codes", (M, K), dev)
         sp, ld_s = _rows(scales, "scales", f32, (blocks, M), dev)
@@ -1111,7 +1125,7 @@ class MoeFp8Linear:
         x, x_scales = x_t
         dev, f32 = _device(), _types.f32
         _scratch_on(self.status, dev)
-        R = x.shape[-1]
+        R = x.shape[1] if x.dim() == 2 else _not_of(2, x, "x's codes")
         yp, ld_y = _codes(dy, "dy's codes", (N, R), dev)
         xp, ld_x = _codes(x, "x's codes", (K, R), dev)
         sp, ld_sy = _rows(dy_scales, "dy's scales", f32, (R // 128, N), dev)
@@ -1133,5 +1147,6 @@ class MoeFp8Linear:
     def check(self):
         """Synchronise; (status, detail) of what the device recorded, which is cleared."""
         where = ctypes.c_int(0)
+        _scratch_on(self.status, _device())
         rc = _lib.moe_fp8_check(self.status.data_ptr(), ctypes.byref(where))
         return rc, where.value

@@ -346,3 +346,43 @@ def test_no_rows_are_no_mistake(B):
         assert call(source) == OK and call(source, E=3, offsets=A) == OK
         assert call(source, M=1) == INVALID
         assert call(source, E=3) == INVALID and call(source, C=0) == INVALID
+
+
+def test_shapes_are_refused_as_such(B, on_gpu_0):
+    """Tensors of too few dimensions, offsets of no expert, a status of another GPU: errors of
+    this library, before anything is called."""
+    import torch
+
+    f8, f32, bf16, i32 = torch.float8_e4m3fn, torch.float32, torch.bfloat16, torch.int32
+    x, codes, scales = OnGpu(bf16, (8, 256)), OnGpu(f8, (8, 256)), OnGpu(f32, (2, 8))
+    wide, out_t = OnGpu(bf16, (8, 512)), (OnGpu(f8, (256, 128)), OnGpu(f32, (1, 256)))
+    bad = [lambda: B.quantize_fp8(OnGpu(bf16, (256,)), out=(codes, scales)),
+           lambda: B.quantize_fp8(OnGpu(bf16, ()), out=(codes, scales)),
+           lambda: B.quantize_fp8(x, rows=OnGpu(i32, ()), out=(codes, scales)),
+           lambda: B.quantize_fp8(x, offsets=OnGpu(i32, (0,)), out=(codes, scales)),
+           lambda: B.quantize_fp8(x, offsets=OnGpu(i32, (1,)), by_column=True, out=(codes, scales),
+                                  out_t=out_t),
+           lambda: B.quantize_fp8(x, by_row=False, by_column=True, out_t=(OnGpu(f8, ()), scales)),
+           lambda: B.swiglu_fp8(OnGpu(bf16, (512,)), out=(codes, scales)),
+           lambda: B.swiglu_grad_fp8(x, OnGpu(bf16, (512,)), out=(codes, scales)),
+           lambda: B.swiglu_grad_fp8(OnGpu(bf16, ()), wide, out=(codes, scales)),
+           lambda: B.quantize_fp8_weights(OnGpu(bf16, (256,))),
+           lambda: B.quantize_fp8_weights(OnGpu(bf16, (2, 3, 4, 5)))]
+    h = object.__new__(B.MoeFp8Linear)
+    h.N, h.K, h.E, h.dtype, h.status = 48, 256, 1, bf16, OnGpu(i32, (4,))
+    h._ahead, h._back = h._side(48, 256, 1, 0), h._side(256, 48, 1, 0)
+    w = (OnGpu(f8, (1, 48, 256)), OnGpu(f32, (1, 1, 2)))
+    y = OnGpu(bf16, (8, 48))
+    bad += [lambda: h.forward((OnGpu(f8, ()), scales), w, out=y),
+            lambda: h.forward((codes, scales), (OnGpu(f8, (48,)), w[1]), out=y),
+            lambda: h.forward((codes, scales), w, offsets=OnGpu(i32, ()), out=y),
+            lambda: h.grad_weight((OnGpu(f8, ()), scales), (OnGpu(f8, ()), scales))]
+    before = on_gpu_0.calls
+    for i, call in enumerate(bad):
+        with pytest.raises(B.MoeError) as e:
+            call()
+        assert e.value.code == INVALID, i
+    h.status = OnGpu(i32, (4,), dev=1)
+    with pytest.raises(B.MoeError):
+        h.check()
+    assert on_gpu_0.calls == before
