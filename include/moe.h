@@ -860,9 +860,9 @@ typedef struct moe_fp8_gemm_desc {
 /*
  * c[r, n] = sum_k a[r, k] * b[e, n, k], e the expert of row r: a by rows [M, K], b weights;
  * products and sums fp32 (each block of 128 summed by the tensor core, then scaled and
- * added in order), rounded once.  c [M, N], M <= 2^31 - 128, rows ld_c elements apart; rows of no segment
- * are left as they are.  With b the transposed weights and N, K exchanged this is the
- * gradient at the inputs.
+ * added in order), rounded once.  c [M, N], M <= 2^31 - 128, rows ld_c elements apart; rows
+ * of no segment are left as they are.  With b the transposed weights and N, K exchanged this
+ * is the gradient at the inputs.
  */
 int moe_fp8_gemm(const moe_fp8_gemm_desc* desc, int M, const uint8_t* a, long long ld_a,
                  const float* a_scales, long long ld_as, const uint8_t* b, long long ld_b,

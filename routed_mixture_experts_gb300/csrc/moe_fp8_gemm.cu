@@ -20,8 +20,8 @@
 // some 900 cycles pass a block (barriers, tensor memory loads of 46 cycles and more, additions),
 // where its MMAs take 512 and its copies, at the 64 bytes a cycle an SM gets from L2, 768.
 // Dense 8192 x 4096 x 4096 106 us (2.6 PFLOP/s), M = 65536, N = 1536, K = 2048 on 128 experts
-// 206 (2.0), its weight gradient on 32 experts 267 (1.54); 512 rows on the 128 experts 60, the
-// weights' bytes at a copy's rate.
+// 206 (2.0), or up to 242 (1.7) where the power limit lowers the clocks, its weight gradient on
+// 32 experts 267 (1.54); 512 rows on the 128 experts 60, the weights' bytes at a copy's rate.
 
 #include "../../include/moe.h"
 #include "moe_device.cuh"
@@ -283,7 +283,6 @@ __device__ __forceinline__ void sum_rows(const Fp8GemmArgs& args, const Tile& ti
   using S = Shape<BN, false>;
   constexpr int WIDE = S::WIDE, CH = 32;         // CH: columns a load
   const int row = quarter * 32 + lane, r = ti.m0 + row, c0 = ti.n0 + group * WIDE;
-  const bool row_in = r < ti.m1;
   if (ti.m0 + quarter * 32 >= ti.m1) {           // rows of nobody: only the rings go on
     for (int b = ti.b0; b < ti.b1; ++b) {
       rd.wait_sums();
@@ -807,7 +806,8 @@ template <int BN, bool WGRAD>
 cudaError_t launch(const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& tc,
                    const Fp8GemmArgs& a, int grid, cudaStream_t st) {
   static std::atomic<unsigned long long> configured{0};
-  const cudaError_t e = smem_optin_once(k_fp8_gemm<BN, WGRAD>, (Shape<BN, WGRAD>::SMEM), configured);
+  const cudaError_t e =
+      smem_optin_once(k_fp8_gemm<BN, WGRAD>, (Shape<BN, WGRAD>::SMEM), configured);
   if (e != cudaSuccess) return e;
   // the shares above are of what a thread is launched with
   static std::atomic<int> regs{0};
@@ -930,7 +930,7 @@ extern "C" int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* s, long long R, const
                ? 4
                : aligned(dw, 8) && s->K % 2 == 0 ? 2 : 0;
   g.err = static_cast<DevError*>(status);
-  // as in moe_fp8_gemm: N = 777, K = 1111 over 1003 rows 8.6 us against 14.4
+  // as in moe_fp8_gemm: N = 777, K = 1111 over 1003 rows 10.1 us against 15.4
   const bool narrow = s->K <= 128 || (long long)s->E * ((s->N + 127) / 128) *
                                          ((s->K + 255) / 256) <= num_sms();
   const long long tiles = (long long)s->E * ((s->N + 127) / 128) *

@@ -370,8 +370,8 @@ struct Share {
   static constexpr int PER_SM = AHEAD && OPS == 3 ? 1 : 2;
 };
 
-// SRC: what v is.  COLS: codes along the columns are wanted.  BLOCKS: one scale a tile (weights, E matrices of M rows); else one a
-// row and one a column of the tile.
+// SRC: what v is.  COLS: codes along the columns are wanted.  BLOCKS: one scale a tile
+// (weights, E matrices of M rows); else one a row and one a column of the tile.
 template <int SRC, typename T, bool VEC, bool BLOCKS, bool COLS>
 __global__ void __launch_bounds__(kThreads, (Share<SRC, T, VEC>::PER_SM))
     k_fp8_quant(const QuantArgs a) {
@@ -444,274 +444,275 @@ __global__ void __launch_bounds__(kThreads, (Share<SRC, T, VEC>::PER_SM))
     advance<BLOCKS>(a, seg, units, next);
     uint2 held[GRAD && AHEAD ? 8 : 1][3];         // gate, up, dh of both halves
     for (int pass = 0; pass < passes; ++pass) {
-    const int cb = t.cb + pass * a.run_blocks;
-    const int col = (cb << 7) + 4 * lane;
-    const int n = a.width - col;                 // columns of this lane that are there
-    uint64_t v[8][2];                            // two neighbours a word
-    uint2 raw[PACKED ? 8 : 1];                   // four bf16
-    if (GRAD && in_ring) {
-      if constexpr (GRAD && AHEAD) {
-        if (pass == 0) {
-          asm volatile("cp.async.wait_group 0;" ::: "memory");
+      const int cb = t.cb + pass * a.run_blocks;
+      const int col = (cb << 7) + 4 * lane;
+      const int n = a.width - col;                 // columns of this lane that are there
+      uint64_t v[8][2];                            // two neighbours a word
+      uint2 raw[PACKED ? 8 : 1];                   // four bf16
+      if (GRAD && in_ring) {
+        if constexpr (GRAD && AHEAD) {
+          if (pass == 0) {
+            asm volatile("cp.async.wait_group 0;" ::: "memory");
 #pragma unroll
-          for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 3; ++j)
-              held[i][j] = *reinterpret_cast<const uint2*>(
-                  reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
-                  (size_t)(i * OPS + j) * (kThreads * PIECE));
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint64_t g[2], u[2], d[2];
-          pairs_of(held[i][0], g);
-          pairs_of(held[i][1], u);
-          pairs_of(held[i][2], d);
-          gradient2(g, u, d, a.clamp, pass == 1, v[i]);
-        }
-        // (what was read has been used: the next block's share may take its place)
-        if (pass == 0 && next.unit < units) copy(next);
-      }
-    } else if (in_ring) {
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const uint8_t* p = reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
-                           (size_t)(i * OPS) * (kThreads * PIECE);
-        if (PACKED) {
-          raw[i] = *reinterpret_cast<const uint2*>(p);
-          v[i][0] = pair(__uint_as_float(raw[i].x << 16), __uint_as_float(raw[i].x & 0xFFFF0000u));
-          v[i][1] = pair(__uint_as_float(raw[i].y << 16), __uint_as_float(raw[i].y & 0xFFFF0000u));
-        } else if (SRC == MOE_FP8_ROWS) {
-          const float4 q = *reinterpret_cast<const float4*>(p);
-          v[i][0] = pair(q.x, q.y);
-          v[i][1] = pair(q.z, q.w);
-        } else {
-          uint64_t g[2], u[2];
-          pairs_of(*reinterpret_cast<const uint2*>(p), g);
-          pairs_of(*reinterpret_cast<const uint2*>(p + kThreads * PIECE), u);
-          if (a.clamp > 0.f) {
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float x, y;
-              unpair(g[j], x, y);
-              g[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
-              unpair(u[j], x, y);
-              u[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
-            }
-          }
-#pragma unroll
-          for (int j = 0; j < 2; ++j) v[i][j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
-        }
-      }
-      // the next block's share arrives while this one is worked on
-      if (next.unit < units) copy(next);
-    } else if (GRAD && VEC && passes == 2) {
-      const int c0 = (t.cb << 7) + 4 * lane;       // column of the operands
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i][0] = v[i][1] = 0;
-        if (i < t.rows && n > 0) {
-          const T* const x = static_cast<const T*>(a.x) + (long long)(t.row0 + i) * a.ld_x + c0;
-          uint64_t g[2], u[2], d[2];
-          load_pairs(x, g);
-          load_pairs(x + a.C, u);
-          load_pairs(static_cast<const T*>(a.dh) + (long long)(t.row0 + i) * a.ld_dh + c0, d);
-          gradient2(g, u, d, a.clamp, pass == 1, v[i]);
-        }
-      }
-    } else {
-      const long long base = BLOCKS ? (long long)t.e * a.M : 0LL;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int src = __shfl_sync(kAll, t.source, i);
-        float f[4] = {0.f, 0.f, 0.f, 0.f};
-        if (src >= 0 && n > 0) source4<SRC, VEC, T>(a, base + src, col, n, f);
-        v[i][0] = pair(f[0], f[1]);
-        v[i][1] = pair(f[2], f[3]);
-      }
-    }
-    auto four = [&](int i, float (&f)[4]) {
-      unpair(v[i][0], f[0], f[1]);
-      unpair(v[i][1], f[2], f[3]);
-    };
-    // ---- largest magnitudes: of the columns, over this warp's rows; of the rows ----
-    uint4 m = make_uint4(0u, 0u, 0u, 0u);         // (PACKED: two 16-bit magnitudes a word)
-    uint32_t top;                                 // of row lane / 4
-    if (PACKED) {
-      uint32_t w[4];                              // two rows a word
-#pragma unroll
-      for (int i = 0; i < 8; i += 2) {
-        uint32_t r[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          if (COLS) {
-            m.x = larger(m.x, raw[i + j].x);
-            m.y = larger(m.y, raw[i + j].y);
-          }
-          r[j] = larger(raw[i + j].x, raw[i + j].y);
-        }
-        w[i >> 1] = __vmaxu2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[0], r[1], 0x7632));
-      }
-      // lanes exchange rows: half of them each time, until a lane has two
-      const bool a16 = lane & 16, a8 = lane & 8;
-      const uint32_t k0 = __vmaxu2(a16 ? w[2] : w[0], __shfl_xor_sync(kAll, a16 ? w[0] : w[2], 16));
-      const uint32_t k1 = __vmaxu2(a16 ? w[3] : w[1], __shfl_xor_sync(kAll, a16 ? w[1] : w[3], 16));
-      uint32_t k = __vmaxu2(a8 ? k1 : k0, __shfl_xor_sync(kAll, a8 ? k0 : k1, 8));
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) k = __vmaxu2(k, __shfl_xor_sync(kAll, k, o));
-      top = (lane & 4) ? k & 0xFFFF0000u : k << 16;
-    } else {
-      uint32_t w[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float f[4];
-        four(i, f);
-        const uint32_t b[4] = {magnitude(f[0]), magnitude(f[1]), magnitude(f[2]),
-                               magnitude(f[3])};
-        if (COLS) {
-          m.x = max(m.x, b[0]);
-          m.y = max(m.y, b[1]);
-          m.z = max(m.z, b[2]);
-          m.w = max(m.w, b[3]);
-        }
-        w[i] = max(max(b[0], b[1]), max(b[2], b[3]));
-      }
-      // lanes exchange rows: half of them each time, until a lane has one
-#pragma unroll
-      for (int n = 4; n > 0; n >>= 1) {
-        const bool hi = lane & (4 * n);
-#pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const uint32_t send = hi ? w[i] : w[i + n], keep = hi ? w[i + n] : w[i];
-          w[i] = max(keep, __shfl_xor_sync(kAll, send, 4 * n));
-        }
-      }
-      top = w[0];
-      top = max(top, __shfl_xor_sync(kAll, top, 2));
-      top = max(top, __shfl_xor_sync(kAll, top, 1));
-    }
-    float scale = 0.f, factor = 0.f;
-    if (BLOCKS) {
-      top = __reduce_max_sync(kAll, top);
-      if (lane == 0) colmax[warp].x = top;
-      __syncthreads();
-      top = __reduce_max_sync(kAll, lane < kWarps ? colmax[lane].x : 0u);
-      block_scale(top, a.pow2, scale, factor);
-      if (threadIdx.x == 0) {
-        const int nb = (a.M + 127) >> 7, b = t.rb - t.e * nb;
-        if (a.scales) a.scales[((long long)t.e * nb + b) * a.col_blocks + cb] = scale;
-        if (a.scales_t) a.scales_t[((long long)t.e * a.col_blocks + cb) * nb + b] = scale;
-      }
-    } else {
-      // one reckoning for both: lanes 4 i take row i, lanes 4 i + 1 this warp's column i
-      if (COLS) {
-        uint8_t* const at = reinterpret_cast<uint8_t*>(colmax) + warp * COLMAX_ROW;
-        if (PACKED)
-          reinterpret_cast<uint2*>(at)[lane] = make_uint2(m.x, m.y);
-        else
-          reinterpret_cast<uint4*>(at)[lane] = m;
-        __syncthreads();
-        uint32_t c = 0;                           // column 8 warp + lane % 8
-#pragma unroll
-        for (int j = 0; j < kWarps; j += 4) {
-          const uint8_t* const q =
-              reinterpret_cast<const uint8_t*>(colmax) + ((lane >> 3) + j) * COLMAX_ROW;
-          const int i = 8 * warp + (lane & 7);
-          c = max(c, PACKED ? (uint32_t)reinterpret_cast<const uint16_t*>(q)[i] << 16
-                            : reinterpret_cast<const uint32_t*>(q)[i]);
-        }
-        c = max(c, __shfl_xor_sync(kAll, c, 8));
-        c = max(c, __shfl_xor_sync(kAll, c, 16));
-        c = __shfl_sync(kAll, c, lane >> 2);
-        if (lane & 1) top = c;
-      }
-      block_scale(top, a.pow2, scale, factor);
-      const int i = lane >> 2;
-      if (a.codes && (lane & 3) == 0 && i < t.rows)
-        a.scales[(long long)cb * a.ld_scales + t.row0 + i] = scale;
-      if (COLS && (lane & 3) == 1) {
-        const int c = (cb << 7) + 8 * warp + i;
-        reinterpret_cast<float*>(factors)[8 * warp + i] = factor;
-        if (c < a.width) a.scales_t[(long long)t.rb * a.ld_scales_t + c] = scale;
-      }
-    }
-    // ---- codes along the rows ----
-    if (a.codes) {
-      uint8_t* const p =
-          a.codes + ((BLOCKS ? (long long)t.e * a.M : 0LL) + t.row0) * a.ld_codes + col;
-      const int rows = n > 0 ? t.rows : 0;
-      auto code_rows = [&](auto full) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float s = BLOCKS ? factor : __shfl_sync(kAll, factor, 4 * i);
-          const uint64_t s2 = pair(s, s);
-          float f[4];
-          unpair(mul2(v[i][0], s2), f[0], f[1]);
-          unpair(mul2(v[i][1], s2), f[2], f[3]);
-          const uint32_t w = codes4(f[0], f[1], f[2], f[3]);
-          if (decltype(full)::value || i < rows) {
-            uint8_t* const q = p + (long long)i * a.ld_codes;
-            if (VEC || n >= 4) {
-              *reinterpret_cast<uint32_t*>(q) = w;
-            } else {
+            for (int i = 0; i < 8; ++i)
 #pragma unroll
               for (int j = 0; j < 3; ++j)
-                if (j < n) q[j] = (uint8_t)(w >> (8 * j));
+                held[i][j] = *reinterpret_cast<const uint2*>(
+                    reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
+                    (size_t)(i * OPS + j) * (kThreads * PIECE));
+          }
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            uint64_t g[2], u[2], d[2];
+            pairs_of(held[i][0], g);
+            pairs_of(held[i][1], u);
+            pairs_of(held[i][2], d);
+            gradient2(g, u, d, a.clamp, pass == 1, v[i]);
+          }
+          // (what was read has been used: the next block's share may take its place)
+          if (pass == 0 && next.unit < units) copy(next);
+        }
+      } else if (in_ring) {
+        asm volatile("cp.async.wait_group 0;" ::: "memory");
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint8_t* p = reinterpret_cast<const uint8_t*>(ring) + threadIdx.x * PIECE +
+                             (size_t)(i * OPS) * (kThreads * PIECE);
+          if (PACKED) {
+            raw[i] = *reinterpret_cast<const uint2*>(p);
+            pairs_of(raw[i], v[i]);
+          } else if (SRC == MOE_FP8_ROWS) {
+            const float4 q = *reinterpret_cast<const float4*>(p);
+            v[i][0] = pair(q.x, q.y);
+            v[i][1] = pair(q.z, q.w);
+          } else {
+            uint64_t g[2], u[2];
+            pairs_of(*reinterpret_cast<const uint2*>(p), g);
+            pairs_of(*reinterpret_cast<const uint2*>(p + kThreads * PIECE), u);
+            if (a.clamp > 0.f) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                float x, y;
+                unpair(g[j], x, y);
+                g[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
+                unpair(u[j], x, y);
+                u[j] = pair(clip(x, a.clamp), clip(y, a.clamp));
+              }
             }
+#pragma unroll
+            for (int j = 0; j < 2; ++j) v[i][j] = mul2(mul2(g[j], sigmoid2(g[j])), u[j]);
           }
         }
-      };
-      if (VEC && __all_sync(kAll, rows == 8))
-        code_rows(std::true_type{});
-      else
-        code_rows(std::false_type{});
-    }
-    if (!COLS) {
-      if (BLOCKS) __syncthreads();                // colmax has been read
-      continue;
-    }
-    // ---- codes along the columns ----
-    float4 f = make_float4(factor, factor, factor, factor);
-    if (!BLOCKS) {
-      __syncthreads();
-      f = factors[lane];
-    }
-    {
-      const uint64_t f2[2] = {pair(f.x, f.y), pair(f.z, f.w)};
-      // rows 8 warp.. of a column: half `warp & 1` of piece warp / 2
-      const int piece = (warp >> 1) ^ (lane & 7), side = (warp & 1) ^ ((lane >> 3) & 1);
+        // the next block's share arrives while this one is worked on
+        if (next.unit < units) copy(next);
+      } else if (GRAD && VEC && passes == 2) {
+        const int c0 = (t.cb << 7) + 4 * lane;       // column of the operands
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x[8], y[8];
+        for (int i = 0; i < 8; ++i) {
+          v[i][0] = v[i][1] = 0;
+          if (i < t.rows && n > 0) {
+            const T* const x = static_cast<const T*>(a.x) + (long long)(t.row0 + i) * a.ld_x + c0;
+            uint64_t g[2], u[2], d[2];
+            load_pairs(x, g);
+            load_pairs(x + a.C, u);
+            load_pairs(static_cast<const T*>(a.dh) + (long long)(t.row0 + i) * a.ld_dh + c0, d);
+            gradient2(g, u, d, a.clamp, pass == 1, v[i]);
+          }
+        }
+      } else {
+        const long long base = BLOCKS ? (long long)t.e * a.M : 0LL;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) unpair(mul2(v[i][h], f2[h]), x[i], y[i]);
-        reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h][piece])[side] =
-            make_uint2(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]));
-        reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h + 1][piece])[side] =
-            make_uint2(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
+        for (int i = 0; i < 8; ++i) {
+          const int src = __shfl_sync(kAll, t.source, i);
+          float f[4] = {0.f, 0.f, 0.f, 0.f};
+          if (src >= 0 && n > 0) source4<SRC, VEC, T>(a, base + src, col, n, f);
+          v[i][0] = pair(f[0], f[1]);
+          v[i][1] = pair(f[2], f[3]);
+        }
       }
-    }
-    __syncthreads();
-    // first column of codes_t, and how many there are
-    const int at_t = BLOCKS ? (t.rb - t.e * ((a.M + 127) >> 7)) << 7 : t.rb << 7;
-    const int n_t = BLOCKS ? a.M - at_t : 128;
+      auto four = [&](int i, float (&f)[4]) {
+        unpair(v[i][0], f[0], f[1]);
+        unpair(v[i][1], f[2], f[3]);
+      };
+      // ---- largest magnitudes: of the columns, over this warp's rows; of the rows ----
+      uint4 m = make_uint4(0u, 0u, 0u, 0u);         // (PACKED: two 16-bit magnitudes a word)
+      uint32_t top;                                 // of row lane / 4
+      if (PACKED) {
+        uint32_t w[4];                              // two rows a word
 #pragma unroll
-    for (int q = threadIdx.x; q < 1024; q += kThreads) {
-      const int c = q >> 3, piece = q & 7, group = c >> 2;
-      if ((cb << 7) + c >= a.width || 16 * piece >= n_t) continue;
-      uint4 w = turned[c][piece ^ (group & 7)];
-      if ((group >> 3) & 1) w = make_uint4(w.z, w.w, w.x, w.y);
-      const long long row = (BLOCKS ? (long long)t.e * a.width : 0LL) + (cb << 7) + c;
-      uint8_t* p = a.codes_t + row * a.ld_codes_t + at_t + 16 * piece;
-      if (BLOCKS)
-        store_codes16(p, w, n_t - 16 * piece);
-      else
-        *reinterpret_cast<uint4*>(p) = w;
-    }
-    // (between two barriers only: the next block writes colmax before its first, when this
-    // one's has been read, factors before its second, turned after that)
-    if (BLOCKS) __syncthreads();
+        for (int i = 0; i < 8; i += 2) {
+          uint32_t r[2];
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            if (COLS) {
+              m.x = larger(m.x, raw[i + j].x);
+              m.y = larger(m.y, raw[i + j].y);
+            }
+            r[j] = larger(raw[i + j].x, raw[i + j].y);
+          }
+          w[i >> 1] = __vmaxu2(__byte_perm(r[0], r[1], 0x5410), __byte_perm(r[0], r[1], 0x7632));
+        }
+        // lanes exchange rows: half of them each time, until a lane has two
+        const bool a16 = lane & 16, a8 = lane & 8;
+        const uint32_t k0 =
+            __vmaxu2(a16 ? w[2] : w[0], __shfl_xor_sync(kAll, a16 ? w[0] : w[2], 16));
+        const uint32_t k1 =
+            __vmaxu2(a16 ? w[3] : w[1], __shfl_xor_sync(kAll, a16 ? w[1] : w[3], 16));
+        uint32_t k = __vmaxu2(a8 ? k1 : k0, __shfl_xor_sync(kAll, a8 ? k0 : k1, 8));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) k = __vmaxu2(k, __shfl_xor_sync(kAll, k, o));
+        top = (lane & 4) ? k & 0xFFFF0000u : k << 16;
+      } else {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          float f[4];
+          four(i, f);
+          const uint32_t b[4] = {magnitude(f[0]), magnitude(f[1]), magnitude(f[2]),
+                                 magnitude(f[3])};
+          if (COLS) {
+            m.x = max(m.x, b[0]);
+            m.y = max(m.y, b[1]);
+            m.z = max(m.z, b[2]);
+            m.w = max(m.w, b[3]);
+          }
+          w[i] = max(max(b[0], b[1]), max(b[2], b[3]));
+        }
+        // lanes exchange rows: half of them each time, until a lane has one
+#pragma unroll
+        for (int n = 4; n > 0; n >>= 1) {
+          const bool hi = lane & (4 * n);
+#pragma unroll
+          for (int i = 0; i < n; ++i) {
+            const uint32_t send = hi ? w[i] : w[i + n], keep = hi ? w[i + n] : w[i];
+            w[i] = max(keep, __shfl_xor_sync(kAll, send, 4 * n));
+          }
+        }
+        top = w[0];
+        top = max(top, __shfl_xor_sync(kAll, top, 2));
+        top = max(top, __shfl_xor_sync(kAll, top, 1));
+      }
+      float scale = 0.f, factor = 0.f;
+      if (BLOCKS) {
+        top = __reduce_max_sync(kAll, top);
+        if (lane == 0) colmax[warp].x = top;
+        __syncthreads();
+        top = __reduce_max_sync(kAll, lane < kWarps ? colmax[lane].x : 0u);
+        block_scale(top, a.pow2, scale, factor);
+        if (threadIdx.x == 0) {
+          const int nb = (a.M + 127) >> 7, b = t.rb - t.e * nb;
+          if (a.scales) a.scales[((long long)t.e * nb + b) * a.col_blocks + cb] = scale;
+          if (a.scales_t) a.scales_t[((long long)t.e * a.col_blocks + cb) * nb + b] = scale;
+        }
+      } else {
+        // one reckoning for both: lanes 4 i take row i, lanes 4 i + 1 this warp's column i
+        if (COLS) {
+          uint8_t* const at = reinterpret_cast<uint8_t*>(colmax) + warp * COLMAX_ROW;
+          if (PACKED)
+            reinterpret_cast<uint2*>(at)[lane] = make_uint2(m.x, m.y);
+          else
+            reinterpret_cast<uint4*>(at)[lane] = m;
+          __syncthreads();
+          uint32_t c = 0;                           // column 8 warp + lane % 8
+#pragma unroll
+          for (int j = 0; j < kWarps; j += 4) {
+            const uint8_t* const q =
+                reinterpret_cast<const uint8_t*>(colmax) + ((lane >> 3) + j) * COLMAX_ROW;
+            const int i = 8 * warp + (lane & 7);
+            c = max(c, PACKED ? (uint32_t)reinterpret_cast<const uint16_t*>(q)[i] << 16
+                              : reinterpret_cast<const uint32_t*>(q)[i]);
+          }
+          c = max(c, __shfl_xor_sync(kAll, c, 8));
+          c = max(c, __shfl_xor_sync(kAll, c, 16));
+          c = __shfl_sync(kAll, c, lane >> 2);
+          if (lane & 1) top = c;
+        }
+        block_scale(top, a.pow2, scale, factor);
+        const int i = lane >> 2;
+        if (a.codes && (lane & 3) == 0 && i < t.rows)
+          a.scales[(long long)cb * a.ld_scales + t.row0 + i] = scale;
+        if (COLS && (lane & 3) == 1) {
+          const int c = (cb << 7) + 8 * warp + i;
+          reinterpret_cast<float*>(factors)[8 * warp + i] = factor;
+          if (c < a.width) a.scales_t[(long long)t.rb * a.ld_scales_t + c] = scale;
+        }
+      }
+      // ---- codes along the rows ----
+      if (a.codes) {
+        uint8_t* const p =
+            a.codes + ((BLOCKS ? (long long)t.e * a.M : 0LL) + t.row0) * a.ld_codes + col;
+        const int rows = n > 0 ? t.rows : 0;
+        auto code_rows = [&](auto full) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float s = BLOCKS ? factor : __shfl_sync(kAll, factor, 4 * i);
+            const uint64_t s2 = pair(s, s);
+            float f[4];
+            unpair(mul2(v[i][0], s2), f[0], f[1]);
+            unpair(mul2(v[i][1], s2), f[2], f[3]);
+            const uint32_t w = codes4(f[0], f[1], f[2], f[3]);
+            if (decltype(full)::value || i < rows) {
+              uint8_t* const q = p + (long long)i * a.ld_codes;
+              if (VEC || n >= 4) {
+                *reinterpret_cast<uint32_t*>(q) = w;
+              } else {
+#pragma unroll
+                for (int j = 0; j < 3; ++j)
+                  if (j < n) q[j] = (uint8_t)(w >> (8 * j));
+              }
+            }
+          }
+        };
+        if (VEC && __all_sync(kAll, rows == 8))
+          code_rows(std::true_type{});
+        else
+          code_rows(std::false_type{});
+      }
+      if (!COLS) {
+        if (BLOCKS) __syncthreads();                // colmax has been read
+        continue;
+      }
+      // ---- codes along the columns ----
+      float4 f = make_float4(factor, factor, factor, factor);
+      if (!BLOCKS) {
+        __syncthreads();
+        f = factors[lane];
+      }
+      {
+        const uint64_t f2[2] = {pair(f.x, f.y), pair(f.z, f.w)};
+        // rows 8 warp.. of a column: half `warp & 1` of piece warp / 2
+        const int piece = (warp >> 1) ^ (lane & 7), side = (warp & 1) ^ ((lane >> 3) & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x[8], y[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) unpair(mul2(v[i][h], f2[h]), x[i], y[i]);
+          reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h][piece])[side] =
+              make_uint2(codes4(x[0], x[1], x[2], x[3]), codes4(x[4], x[5], x[6], x[7]));
+          reinterpret_cast<uint2*>(&turned[4 * lane + 2 * h + 1][piece])[side] =
+              make_uint2(codes4(y[0], y[1], y[2], y[3]), codes4(y[4], y[5], y[6], y[7]));
+        }
+      }
+      __syncthreads();
+      // first column of codes_t, and how many there are
+      const int at_t = BLOCKS ? (t.rb - t.e * ((a.M + 127) >> 7)) << 7 : t.rb << 7;
+      const int n_t = BLOCKS ? a.M - at_t : 128;
+#pragma unroll
+      for (int q = threadIdx.x; q < 1024; q += kThreads) {
+        const int c = q >> 3, piece = q & 7, group = c >> 2;
+        if ((cb << 7) + c >= a.width || 16 * piece >= n_t) continue;
+        uint4 w = turned[c][piece ^ (group & 7)];
+        if ((group >> 3) & 1) w = make_uint4(w.z, w.w, w.x, w.y);
+        const long long row = (BLOCKS ? (long long)t.e * a.width : 0LL) + (cb << 7) + c;
+        uint8_t* p = a.codes_t + row * a.ld_codes_t + at_t + 16 * piece;
+        if (BLOCKS)
+          store_codes16(p, w, n_t - 16 * piece);
+        else
+          *reinterpret_cast<uint4*>(p) = w;
+      }
+      // (between two barriers only: the next block writes colmax before its first, when this
+      // one's has been read, factors before its second, turned after that)
+      if (BLOCKS) __syncthreads();
     }
   }
   pdl_trigger();

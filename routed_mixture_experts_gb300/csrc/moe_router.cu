@@ -962,8 +962,8 @@ __global__ void __launch_bounds__(kGradWarps * 32) k_router_grad(const RouterArg
 
 // Up to a row per warp one CTA does all, the sums too (32 rows of 128 experts 4.8 us).
 // More rows are spread, and a second launch adds the sums: 64 rows 6.6 us against 7.8
-// on one CTA.  With groups a CTA has 20 warps, whose threads keep nearly all in registers
-// (8192 rows of 256 experts 24.3 us against 25.2 on 16 warps, before the last steps 32.9
+// on one CTA.  With groups a CTA has 20 warps, whose threads keep all but 156 bytes (of 256
+// experts; 76 of 224, and with fewer all) in registers (8192 rows of 256 experts 24.3 us against 25.2 on 16 warps, before the last steps 32.9
 // on 32 and 31.5 on 16; 64 rows 10.3 against 9.9).
 int most_warps(bool groups) { return groups ? 20 : 32; }
 
@@ -1071,8 +1071,8 @@ namespace moe {
 namespace {
 
 // Both forwards; g: the choice within groups (NULL: among all experts).
-int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, const void* logits, long long ld, const float* bias,
-            const uint8_t* token_mask, int32_t* ids, float* scores, int32_t* counts,
+int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, const void* logits,
+            long long ld, const float* bias, const uint8_t* token_mask, int32_t* ids, float* scores, int32_t* counts,
             float* prob_sum, float* losses, float* row_stat, void* workspace,
             size_t workspace_bytes, void* stream) {
   if (!sizes_ok(s, T) || !counts || !prob_sum || !losses) return MOE_ERR_INVALID_ARG;
@@ -1105,7 +1105,8 @@ int forward(const moe_router_desc* s, const moe_group_router_desc* g, int T, con
     a.pair = g->group_score == MOE_GROUP_TOP2 && a.group_size > 1;
     while ((2 << a.share_log2) * a.groups <= 32 && (2 << a.share_log2) <= a.group_size)
       a.share_log2 += 1;
-    e = f32 ? launch_forward<float, true>(a, grid, st) : launch_forward<uint16_t, true>(a, grid, st);
+    e = f32 ? launch_forward<float, true>(a, grid, st)
+            : launch_forward<uint16_t, true>(a, grid, st);
   } else {
     e = f32 ? launch_forward<float, false>(a, grid, st)
             : launch_forward<uint16_t, false>(a, grid, st);

@@ -50,7 +50,8 @@ def test_weight_gradient_of_more_rows_than_its_codes(moe, accumulate):
 def test_weight_gradient_of_no_columns(moe, accumulate):
     """Codes without columns: 0 where no expert has rows, refused where one has."""
     N, K, E = 33, 1100, 3
-    none = lambda n: (torch.zeros(n, 0, dtype=torch.uint8).cuda().view(F8), torch.zeros(0, n).cuda())
+    none = lambda n: (torch.zeros(n, 0, dtype=torch.uint8).cuda().view(F8),
+                      torch.zeros(0, n).cuda())
     lin = moe.MoeFp8Linear(N, K, E)
     for offsets, ok in (([0, 0, 0, 0], True), ([9, 9, 9, 9], True), ([0, 0, 1, 1], False),
                         ([0, 4, 2, 4], False), ([-1, -1, -1, -1], False)):

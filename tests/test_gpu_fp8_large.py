@@ -51,7 +51,8 @@ def quantise(moe, source, x, **kw):
 @pytest.mark.parametrize("source,M,C", [("rows", 128 * 300, 300), ("rows", 128 * 70, 2048 + 8),
                                         ("rows", 128 * 600, 2048), ("rows", 128 * 200, 515),
                                         ("swiglu", 128 * 300, 384), ("swiglu", 128 * 200, 130),
-                                        ("swiglu", 128 * 900, 1000), ("swiglu_grad", 128 * 300, 256),
+                                        ("swiglu", 128 * 900, 1000),
+                                        ("swiglu_grad", 128 * 300, 256),
                                         ("swiglu_grad", 128 * 900, 768),
                                         ("swiglu_grad", 128 * 200, 388),
                                         ("swiglu_grad", 128 * 150, 133)])
@@ -293,10 +294,11 @@ def test_on_the_tables_of_a_dispatch(moe):
     scores = torch.rand(T, k, generator=g).cuda()
     cap = (T * k + E * 127) // 128 * 128
     e32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")
-    m_indptr, off_pad, row_of, token_of, status = e32(E + 1), e32(E + 1), e32(T * k), e32(cap), e32(2)
+    m_indptr, off_pad, row_of, token_of = e32(E + 1), e32(E + 1), e32(T * k), e32(cap)
+    status = e32(2)
     score_of = torch.empty(cap, device="cuda")
     vp, n = ctypes.c_void_p, ctypes.c_int
-    L.moe_dispatch_static.argtypes = [vp, vp, n, n, n, vp, vp, vp, vp, vp, ctypes.c_longlong, vp, vp]
+    L.moe_dispatch_static.argtypes = [vp, vp, n, n, n] + [vp] * 5 + [ctypes.c_longlong, vp, vp]
     L.moe_dispatch_static.restype = n
     p = lambda t: t.data_ptr()
     assert L.moe_dispatch_static(p(ids), p(scores), T, k, E, p(m_indptr), p(off_pad), p(row_of),
