@@ -874,7 +874,9 @@ int moe_fp8_gemm(const moe_fp8_gemm_desc* desc, int M, const uint8_t* a, long lo
  * accumulate = 1: dy and x by columns (dyt [N, R], xt [K, R]), with the offsets that
  * they were quantised with.  dw [E, N, K] fp32, dense.  Without accumulate the dw of an
  * expert without rows is 0.  Without offsets the sum goes over all R columns.  Offsets whose
- * blocks do not fit into R columns are bad ones: recorded, and nothing is written.
+ * blocks do not fit into R columns are bad ones: recorded, and nothing is written.  (R is all
+ * that it has to go by: offsets that left the M rows when these were quantised, so that no
+ * codes were written, are not found here, but by the quantised rows' product.)
  * desc->out_dtype is not looked at beyond its range.
  */
 int moe_fp8_gemm_wgrad(const moe_fp8_gemm_desc* desc, long long R, const uint8_t* dyt,

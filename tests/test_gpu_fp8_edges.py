@@ -221,3 +221,77 @@ def test_few_rows_anywhere(moe, M, E, N, K):
         rows = slice(at[e], at[e + 1])
         ref.check_product(got[rows], x[rows], t[e], "expert %d" % e)
     assert lin.check() == (moe.MOE_OK, 0)
+
+
+def layer(moe, M, N, K, E, seed):
+    """A step of one layer of experts as a closure over its offsets, outputs kept."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x, dy = (torch.randn(M, w, generator=g, device="cuda") for w in (K, N))
+    w, wt = moe.quantize_fp8_weights(torch.randn(E, N, K, generator=g, device="cuda"),
+                                     transposed=True)
+    lin = moe.MoeFp8Linear(N, K, E, dtype=torch.float32)
+    out = [torch.zeros(M, N, device="cuda"), torch.zeros(M, K, device="cuda"),
+           torch.zeros(E, N, K, device="cuda")]
+
+    def step(offsets):
+        for t in out:
+            t.zero_()
+        xq, xc = moe.quantize_fp8(x, offsets=offsets, by_column=True)
+        yq, yc = moe.quantize_fp8(dy, offsets=offsets, by_column=True)
+        lin.forward(xq, w, offsets=offsets, out=out[0])
+        lin.grad_input(yq, wt, offsets=offsets, out=out[1])
+        lin.grad_weight(yc, xc, offsets=offsets, dw=out[2], accumulate=True)
+        return out
+
+    return lin, step
+
+
+@pytest.mark.parametrize("M,N,K", [(700, 384, 520), (30, 40, 300)])
+def test_replays_follow_the_offsets(moe, M, N, K):
+    """One captured step, replayed on other offsets than it was captured with, bad ones among
+    them: the same bits as without capture."""
+    E = 4
+    lin, step = layer(moe, M, N, K, E, 81)
+    offsets = i32([0, M // 2, M // 2, M - 5, M])
+    step(offsets)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(offsets)
+    for at in ([0, 0, 0, 0, M], [3, 10, M // 3, M // 3 + 1, M - 1], [0, 0, 0, 0, 0],
+               [0, 9, 8, M, M], [0, 1, 2, 3, M + 1], [0, M // 4, M // 2, M - 7, M]):
+        offsets.copy_(i32(at))
+        graph.replay()
+        got = [t.clone() for t in out]
+        code = lin.check()[0]
+        want = step(offsets)
+        assert lin.check()[0] == code, at
+        assert code == (moe.MOE_ERR_INVALID_ARG if at[1] > at[2] or at[-1] > M else moe.MOE_OK)
+        # (beyond M nothing was quantised, and the weight gradient, which has the codes' columns
+        # to go by and not M, added what the codes held)
+        known = 3 if at[-1] <= M else 2
+        for a, b in zip(got[:known], want):
+            assert torch.equal(a, b), at
+
+
+def test_steps_on_two_streams_at_once(moe):
+    """Two layers' steps, of few rows and of many, at the same time on streams of their own."""
+    sizes = ((3000, 1030, 700, 8, 82), (24, 48, 900, 8, 83))
+    steps, offsets, want = [], [], []
+    for M, N, K, E, seed in sizes:
+        lin, step = layer(moe, M, N, K, E, seed)
+        off = i32(np.linspace(0, M, E + 1).astype(int).tolist())
+        steps.append((lin, step))
+        offsets.append(off)
+        want.append([t.clone() for t in step(off)])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in sizes]
+    got = [[], []]
+    for _ in range(20):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append([t.clone() for t in steps[i][1](offsets[i])])
+    torch.cuda.synchronize()
+    for i in range(2):
+        for out in got[i]:
+            assert all(torch.equal(a, b) for a, b in zip(out, want[i]))
+        assert steps[i][0].check() == (moe.MOE_OK, 0)
